@@ -134,7 +134,9 @@ typedef struct {
 
 /* Which call a workspace is sized for. */
 typedef enum { MOE_CALL_PERMUTE = 0, MOE_CALL_GATE_UP = 1, MOE_CALL_DOWN = 2,
-               MOE_CALL_FORWARD = 3, MOE_CALL_ROUTE = 4 } moe_call_t;
+               MOE_CALL_FORWARD = 3, MOE_CALL_ROUTE = 4,
+               /* of moe_linear_workspace_bytes only */
+               MOE_CALL_LINEAR = 5, MOE_CALL_LINEAR_BACKWARD = 6 } moe_call_t;
 
 /* Human-readable name of a status.  Never NULL. */
 const char* moe_status_string(moe_status_t status);
@@ -317,6 +319,143 @@ moe_status_t moe_forward_noalloc(const moe_shape_t* shape, const void* x, const 
                                  const void* w2_scale, void* y, int32_t* topk_ids_out,
                                  float* topk_weights_out, int32_t* expert_counts_out,
                                  uint8_t* drop_mask_out, float* logits_out, void* stream);
+
+/* ---- scored routing ----
+ * The general router of fine-grained layers, on given logits: moe_route_topk's
+ * place is taken by a product for the logits (moe_linear with fp32 output) and
+ * moe_route_scored; its ids, weights and next_ids go to moe_permute, moe_combine
+ * and moe_forward_routed like moe_route_topk's. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+typedef struct {
+  int32_t score;        /* moe_score_t: s = softmax(logits) over all E experts, or sigmoid(logits) */
+  int32_t n_groups;     /* groups of n_experts / n_groups consecutive experts, 1..64 (1: no groups) */
+  int32_t topk_groups;  /* groups a token may choose from, 1..n_groups */
+  int32_t group_top;    /* a group's score is the sum of its 1 or 2 largest choices */
+  int32_t renormalize;  /* 1: weights divided by the sum of the chosen scores; 0: not */
+  float scale;          /* weights are multiplied by this (finite) */
+} moe_router_t;
+
+/* Scored top-k selection.  Uses T, n_experts, top_k of the shape.
+ * Pages: "How Mixtral 8x7B uses mixture of experts", the simplified forward pass
+ * (softmax over all experts, top-k, renormalise); "Mixtral 8x7B" interview page,
+ * section on how MoE design changed since Mixtral.
+ *   logits       [T, E] fp32
+ *   balance_bias [E] fp32 or NULL: added to the scores for the choice only,
+ *                c = s + balance_bias
+ *   topk_ids     [T, k] int32 out: the k largest c among the experts of the
+ *                topk_groups best groups, in descending order, ties -> lower
+ *                index (groups likewise)
+ *   topk_weights [T, k] fp32 out: scale * s_j, divided by the sum of the k
+ *                chosen s with renormalize
+ *   scores       [T, E] fp32 out or NULL: s
+ *   next_ids     [T, 2] int32 out or NULL: the experts ranked k+1 and k+2 among
+ *                the same groups' experts, -1 where there are no more
+ * The order is that of the scores of the given logits as fp64 arithmetic has
+ * them (without a balance bias: that of the logits), whatever fp32 rounding would
+ * make of them, so it depends on nothing but the row.
+ * Logits may be -inf (a masked expert: score 0; a row of nothing else gets zero
+ * weights) and balance_bias -inf (never chosen while another candidate is left);
+ * NaN ranks below -inf.  The ids of a row are distinct and in [0, E) whatever
+ * the contents.
+ * Errors: MOE_ERR_INVALID_ARG for a router value outside its range, n_groups
+ * that does not divide n_experts, group_top above the group's size, or fewer
+ * than top_k experts in topk_groups groups; MOE_ERR_UNSUPPORTED above 64 groups.
+ * No workspace. */
+moe_status_t moe_route_scored(const moe_shape_t* shape, const moe_router_t* router, const float* logits,
+                              const float* balance_bias, int32_t* topk_ids, float* topk_weights,
+                              float* scores, int32_t* next_ids, void* stream);
+
+/* Gradient of moe_route_scored at the logits (the choice itself has none).
+ *   logits, topk_ids  as given to / written by moe_route_scored (the ids of a
+ *                row distinct; one outside [0, E) adds nothing)
+ *   dweights     [T, k] fp32: gradient at topk_weights
+ *   dscores      [T, E] fp32 or NULL: gradient that arrives at the scores from
+ *                elsewhere (a balance loss)
+ *   dlogits      [T, E] fp32 out
+ * No workspace. */
+moe_status_t moe_route_scored_backward(const moe_shape_t* shape, const moe_router_t* router,
+                                       const float* logits, const int32_t* topk_ids,
+                                       const float* dweights, const float* dscores, float* dlogits,
+                                       void* stream);
+
+/* Gradient of moe_combine.
+ *   dy           [T, d] act dtype: gradient at y
+ *   y_perm, slot_to_row, topk_weights as given to moe_combine (y_perm may be NULL
+ *                when dweights is)
+ *   dy_perm      [R, d] act dtype out, or NULL: gradient at y_perm, w[t, s] * dy[t]
+ *                (shared expert: dy[t]) in row slot_to_row of each kept slot; rows
+ *                no slot points to are left as they were
+ *   dweights     [T, k] fp32 out, or NULL: <dy[t], y_perm[row]>, summed in fp64; 0
+ *                for a dropped slot
+ * At least one output must be given.  No workspace. */
+moe_status_t moe_combine_backward(const moe_shape_t* shape, const void* dy, const float* y_perm,
+                                  const int32_t* slot_to_row, const float* topk_weights, void* dy_perm,
+                                  float* dweights, void* stream);
+
+/* moe_forward from a given routing (moe_route_scored's, or any other) instead of
+ * its own router: permute -> gate/up -> down -> combine, bit for bit the staged
+ * calls on the same ids and weights.
+ *   topk_ids [T, k], topk_weights [T, k]; next_ids [T, 2], required with a
+ *   capacity and MOE_OVERFLOW_NEXT_BEST, else ignored (may be NULL); the ids of a
+ *   token distinct, in [0, E)
+ *   other arguments as for moe_forward
+ * Workspace: moe_workspace_bytes(MOE_CALL_FORWARD). */
+moe_status_t moe_forward_routed(const moe_shape_t* shape, const void* x, const int32_t* topk_ids,
+                                const float* topk_weights, const int32_t* next_ids, const void* w1,
+                                const void* w3, const void* w2, const void* w1_scale,
+                                const void* w3_scale, const void* w2_scale, void* y,
+                                int32_t* expert_counts_out, uint8_t* drop_mask_out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* ---- dense product ----
+ *   y = act(x . w^T + bias) + residual
+ * The router's product (fp32 logits) and the dense projections around the
+ * experts (Pages: "Mixtral" study notes, nn.Linear of MixtralMoE and
+ * MixtralBlock). */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2,
+               MOE_ACT_GELU = 3,        /* p Phi(p), with erf */
+               MOE_ACT_GELU_TANH = 4    /* its tanh form, sqrt(2/pi) (p + 0.044715 p^3) */
+} moe_act_t;
+
+typedef struct {
+  int32_t M;        /* rows (tokens), 0..2^24 */
+  int32_t N;        /* output channels: a multiple of 8, at most 2^18 */
+  int32_t K;        /* input channels: a multiple of 8, at most 2^18 */
+  int32_t dtype;    /* x, w, pre, dx, dw: MOE_BF16 (MOE_F32: MOE_ERR_UNSUPPORTED) */
+  int32_t y_dtype;  /* y, residual, dy: MOE_BF16 or MOE_F32 */
+  int32_t act;      /* moe_act_t */
+} moe_linear_t;
+
+/* Bytes of device workspace moe_linear (MOE_CALL_LINEAR) or moe_linear_backward
+ * (MOE_CALL_LINEAR_BACKWARD) needs; 0 is possible (a NULL workspace is accepted
+ * then).  Two calls that share a workspace must not run concurrently. */
+moe_status_t moe_linear_workspace_bytes(const moe_linear_t* linear, moe_call_t call, size_t* bytes);
+
+/*   x        [M, K] dtype;  w [N, K] dtype (nn.Linear [out, in] layout)
+ *   bias     [N] fp32 or NULL;  residual [M, N] y_dtype or NULL
+ *   y        [M, N] y_dtype out; may be the residual's memory, else overlaps no input
+ *   pre      [M, N] dtype out, or NULL: x . w^T + bias, kept for the backward pass
+ * fp32 accumulation; bias, activation and residual in fp32, one rounding to
+ * y_dtype (the activation sees the unrounded pre).  A row's result depends on M
+ * only through which kernel runs. */
+moe_status_t moe_linear(const moe_linear_t* linear, const void* x, const void* w, const float* bias,
+                        const void* residual, void* y, void* pre, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Gradients of moe_linear.  With dpre = dy * act'(pre):
+ *   dx       [M, K] dtype out or NULL:  dpre . w        (needs w)
+ *   dw       [N, K] dtype out or NULL:  dpre^T . x      (needs x)
+ *   dbias    [N] fp32 out or NULL:      column sums of dpre, from its fp32 values
+ *   dy       [M, N] y_dtype;  pre [M, N] dtype as written by moe_linear, required
+ *            unless act is MOE_ACT_NONE (then ignored); the residual's gradient
+ *            is dy itself
+ * dpre is rounded to dtype for the two products (their matrix-core operand), which
+ * accumulate in fp32.  relu'(0) = 0.  Outputs overlap no input and are fully
+ * written, with M = 0 too (dw and dbias are then zero). */
+moe_status_t moe_linear_backward(const moe_linear_t* linear, const void* dy, const void* pre,
+                                 const void* x, const void* w, void* dx, void* dw, float* dbias,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

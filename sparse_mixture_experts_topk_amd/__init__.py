@@ -16,16 +16,27 @@ import torch
 from . import _lib
 from ._lib import (MOE_BF16, MOE_CALL_DOWN, MOE_CALL_FORWARD, MOE_CALL_GATE_UP,
                    MOE_CALL_PERMUTE, MOE_CALL_ROUTE, MOE_DROPLESS, MOE_F32, MOE_FP8_E4M3, MOE_MXFP4,
-                   MOE_NOALLOC_SCRATCH_BYTES, MOE_OVERFLOW_DROP, MOE_OVERFLOW_NEXT_BEST, MoeShape)
+                   MOE_NOALLOC_SCRATCH_BYTES, MOE_OVERFLOW_DROP, MOE_OVERFLOW_NEXT_BEST, MoeShape,
+                   MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU,
+                   MOE_CALL_LINEAR, MOE_CALL_LINEAR_BACKWARD, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
+                   MoeLinear, MoeRouter)
 
 __all__ = ["MoEError", "MoeShape", "make_shape", "moe_status_string", "moe_version",
            "moe_workspace_bytes", "moe_route_topk", "moe_permute", "moe_expert_gemm_gate_up",
            "moe_expert_gemm_down", "moe_combine", "moe_forward", "moe_forward_noalloc",
            "MOE_NOALLOC_SCRATCH_BYTES", "MOE_F32", "MOE_BF16",
            "MOE_FP8_E4M3", "MOE_MXFP4", "MOE_DROPLESS", "MOE_CALL_PERMUTE", "MOE_CALL_GATE_UP",
-           "MOE_CALL_DOWN", "MOE_CALL_FORWARD", "MOE_CALL_ROUTE", "MOE_OVERFLOW_DROP", "MOE_OVERFLOW_NEXT_BEST"]
+           "MOE_CALL_DOWN", "MOE_CALL_FORWARD", "MOE_CALL_ROUTE", "MOE_OVERFLOW_DROP", "MOE_OVERFLOW_NEXT_BEST",
+           "MoeRouter", "MoeLinear", "make_router", "make_linear", "moe_route_scored",
+           "moe_route_scored_backward", "moe_combine_backward", "moe_forward_routed", "moe_linear",
+           "moe_linear_backward", "moe_linear_workspace_bytes", "MOE_CALL_LINEAR",
+           "MOE_CALL_LINEAR_BACKWARD", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_ACT_NONE",
+           "MOE_ACT_RELU", "MOE_ACT_SILU", "MOE_ACT_GELU", "MOE_ACT_GELU_TANH"]
 
 _DT = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8_e4m3": MOE_FP8_E4M3, "mxfp4": MOE_MXFP4}
+_SCORE = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_ACT = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU,
+        "gelu_tanh": MOE_ACT_GELU_TANH}
 _OVF = {"drop": MOE_OVERFLOW_DROP, "next_best": MOE_OVERFLOW_NEXT_BEST}
 
 
@@ -150,3 +161,144 @@ def moe_forward_noalloc(shape, x, w_gate, router_bias, w1, w3, w2, w1_scale, w3_
         _p(w1_scale), _p(w3_scale), _p(w2_scale), _p(y), _p(topk_ids_out),
         _p(topk_weights_out), _p(expert_counts_out), _p(drop_mask_out), _p(logits_out),
         _stream(stream)))
+
+
+# ---- scored routing, gradients of the gate, dense products ----
+
+_TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+class _Args:
+    """Pointers of one call's tensors, checked against the descriptor: element type, at least so
+    many elements, contiguous, all on one device.  The call runs on that device's current stream
+    unless it is given one."""
+
+    def __init__(self, fn: str):
+        self.fn, self.device = fn, None
+
+    def __call__(self, name: str, t, dtype, numel: int):
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            return int(t)
+        if not t.is_cuda:
+            raise ValueError(f"{self.fn}: {name} must live in device memory")
+        if dtype is not None and t.dtype is not dtype:
+            raise ValueError(f"{self.fn}: {name} must be {dtype}, got {t.dtype}")
+        if t.numel() < numel:
+            raise ValueError(f"{self.fn}: {name} needs {numel} elements, got {t.numel()}")
+        if not t.is_contiguous():
+            raise ValueError(f"{self.fn}: {name} must be contiguous (row-major)")
+        d = t.get_device()
+        if self.device is None:
+            self.device = d
+        elif self.device != d:
+            raise ValueError(f"{self.fn}: {name} is on another device than the other tensors")
+        return t.data_ptr()
+
+    def workspace(self, t):
+        """(pointer, bytes) of a workspace tensor or None."""
+        if t is None:
+            return None, 0
+        return self("workspace", t, None, 0), t.numel() * t.element_size()
+
+    def run(self, call, stream):
+        if self.device is None or self.device == torch.cuda.current_device():
+            _check(self.fn, call(_stream(stream)))
+            return
+        with torch.cuda.device(self.device):      # the launches go to the tensors' device
+            _check(self.fn, call(_stream(stream)))
+
+
+def make_router(score="softmax", n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+                renormalize: bool = True, scale: float = 1.0) -> MoeRouter:
+    return MoeRouter(_SCORE.get(score, score), n_groups, topk_groups, group_top, int(renormalize), scale)
+
+
+def make_linear(M: int, N: int, K: int, dtype="bf16", y_dtype="bf16", act="none") -> MoeLinear:
+    return MoeLinear(M, N, K, _DT.get(dtype, dtype), _DT.get(y_dtype, y_dtype), _ACT.get(act, act))
+
+
+def moe_linear_workspace_bytes(linear: MoeLinear, call: int = MOE_CALL_LINEAR) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_linear_workspace_bytes", _lib.load().moe_linear_workspace_bytes(
+        ctypes.byref(linear), call, ctypes.byref(n)))
+    return n.value
+
+
+def moe_linear(linear, x, w, bias, residual, y, pre=None, workspace=None, stream=None):
+    a = _Args("moe_linear")
+    M, N, K = linear.M, linear.N, linear.K
+    dt, ydt = _TORCH.get(linear.dtype), _TORCH.get(linear.y_dtype)
+    p = (a("x", x, dt, M * K), a("w", w, dt, N * K), a("bias", bias, torch.float32, N),
+         a("residual", residual, ydt, M * N), a("y", y, ydt, M * N), a("pre", pre, dt, M * N),
+         *a.workspace(workspace))
+    a.run(lambda st: _lib.load().moe_linear(ctypes.byref(linear), *p, st), stream)
+
+
+def moe_linear_backward(linear, dy, pre, x, w, dx, dw, dbias, workspace=None, stream=None):
+    a = _Args("moe_linear_backward")
+    M, N, K = linear.M, linear.N, linear.K
+    dt, ydt = _TORCH.get(linear.dtype), _TORCH.get(linear.y_dtype)
+    p = (a("dy", dy, ydt, M * N), a("pre", pre, dt, M * N), a("x", x, dt, M * K),
+         a("w", w, dt, N * K), a("dx", dx, dt, M * K), a("dw", dw, dt, N * K),
+         a("dbias", dbias, torch.float32, N), *a.workspace(workspace))
+    a.run(lambda st: _lib.load().moe_linear_backward(ctypes.byref(linear), *p, st), stream)
+
+
+def moe_route_scored(shape, router, logits, balance_bias, topk_ids, topk_weights, scores=None,
+                     next_ids=None, stream=None):
+    a = _Args("moe_route_scored")
+    T, E, k = shape.T, shape.n_experts, shape.top_k
+    f32, i32 = torch.float32, torch.int32
+    p = (a("logits", logits, f32, T * E), a("balance_bias", balance_bias, f32, E),
+         a("topk_ids", topk_ids, i32, T * k), a("topk_weights", topk_weights, f32, T * k),
+         a("scores", scores, f32, T * E), a("next_ids", next_ids, i32, T * 2))
+    a.run(lambda st: _lib.load().moe_route_scored(ctypes.byref(shape), ctypes.byref(router), *p, st), stream)
+
+
+def moe_route_scored_backward(shape, router, logits, topk_ids, dweights, dscores, dlogits, stream=None):
+    a = _Args("moe_route_scored_backward")
+    T, E, k = shape.T, shape.n_experts, shape.top_k
+    f32 = torch.float32
+    p = (a("logits", logits, f32, T * E), a("topk_ids", topk_ids, torch.int32, T * k),
+         a("dweights", dweights, f32, T * k), a("dscores", dscores, f32, T * E),
+         a("dlogits", dlogits, f32, T * E))
+    a.run(lambda st: _lib.load().moe_route_scored_backward(ctypes.byref(shape), ctypes.byref(router), *p, st),
+          stream)
+
+
+def moe_combine_backward(shape, dy, y_perm, slot_to_row, topk_weights, dy_perm, dweights, stream=None):
+    a = _Args("moe_combine_backward")
+    T, d, k = shape.T, shape.d_model, shape.top_k
+    R = T * (k + shape.n_shared)
+    dt = _TORCH.get(shape.act_dtype)
+    p = (a("dy", dy, dt, T * d), a("y_perm", y_perm, torch.float32, R * d),
+         a("slot_to_row", slot_to_row, torch.int32, R), a("topk_weights", topk_weights, torch.float32, T * k),
+         a("dy_perm", dy_perm, dt, R * d), a("dweights", dweights, torch.float32, T * k))
+    a.run(lambda st: _lib.load().moe_combine_backward(ctypes.byref(shape), *p, st), stream)
+
+
+def moe_forward_routed(shape, x, topk_ids, topk_weights, next_ids, w1, w3, w2, w1_scale, w3_scale,
+                       w2_scale, y, expert_counts_out=None, drop_mask_out=None, workspace=None,
+                       stream=None):
+    a = _Args("moe_forward_routed")
+    T, d, k, G = shape.T, shape.d_model, shape.top_k, shape.n_experts + shape.n_shared
+    dt, i32 = _TORCH.get(shape.act_dtype), torch.int32
+    # expert weights in their storage type: 1 byte (fp8), half a byte (MXFP4) or the activations'
+    per_matrix = G * d * shape.d_ff // (2 if shape.w_dtype == MOE_MXFP4 else 1)
+    wt = _TORCH.get(shape.w_dtype)
+    if shape.w_dtype == MOE_FP8_E4M3:
+        st, n_up, n_down = torch.float32, G * shape.d_ff, G * d
+    elif shape.w_dtype == MOE_MXFP4:
+        st, n_up, n_down = torch.uint8, G * shape.d_ff * d // 32, G * d * shape.d_ff // 32
+    else:                       # no scales
+        st, n_up, n_down = None, 0, 0
+    p = (a("x", x, dt, T * d), a("topk_ids", topk_ids, i32, T * k),
+         a("topk_weights", topk_weights, torch.float32, T * k), a("next_ids", next_ids, i32, T * 2),
+         a("w1", w1, wt, per_matrix), a("w3", w3, wt, per_matrix), a("w2", w2, wt, per_matrix),
+         a("w1_scale", w1_scale, st, n_up), a("w3_scale", w3_scale, st, n_up),
+         a("w2_scale", w2_scale, st, n_down), a("y", y, dt, T * d),
+         a("expert_counts_out", expert_counts_out, i32, G),
+         a("drop_mask_out", drop_mask_out, torch.uint8, T * k), *a.workspace(workspace))
+    a.run(lambda st: _lib.load().moe_forward_routed(ctypes.byref(shape), *p, st), stream)

@@ -11,12 +11,17 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4 = 0, 1, 2, 3
 MOE_DROPLESS = -1
 MOE_OVERFLOW_DROP, MOE_OVERFLOW_NEXT_BEST = 0, 1
 MOE_CALL_PERMUTE, MOE_CALL_GATE_UP, MOE_CALL_DOWN, MOE_CALL_FORWARD, MOE_CALL_ROUTE = range(5)
+MOE_CALL_LINEAR, MOE_CALL_LINEAR_BACKWARD = 5, 6
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 # Every symbol include/moe.h declares.
 EXPORTS = ("moe_status_string", "moe_version", "moe_workspace_bytes", "moe_route_topk",
            "moe_permute", "moe_expert_gemm_gate_up", "moe_expert_gemm_down", "moe_combine",
-           "moe_forward", "moe_forward_noalloc")
+           "moe_forward", "moe_forward_noalloc", "moe_forward_routed", "moe_route_scored",
+           "moe_route_scored_backward", "moe_combine_backward", "moe_linear_workspace_bytes",
+           "moe_linear", "moe_linear_backward")
 
 
 class MoeShape(ctypes.Structure):
@@ -27,10 +32,23 @@ class MoeShape(ctypes.Structure):
                 ("n_shared", ctypes.c_int32)]
 
 
+class MoeRouter(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MoeLinear(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 SZ = ctypes.c_size_t
 SHAPE = ctypes.POINTER(MoeShape)
+ROUTER = ctypes.POINTER(MoeRouter)
+LINEAR = ctypes.POINTER(MoeLinear)
 
 _SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [I32]),
@@ -43,6 +61,13 @@ _SIGNATURES = {
     "moe_combine": (I32, [SHAPE, P, P, P, P, P]),
     "moe_forward": (I32, [SHAPE, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
     "moe_forward_noalloc": (I32, [SHAPE, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P]),
+    "moe_forward_routed": (I32, [SHAPE, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+    "moe_route_scored": (I32, [SHAPE, ROUTER, P, P, P, P, P, P, P]),
+    "moe_route_scored_backward": (I32, [SHAPE, ROUTER, P, P, P, P, P, P]),
+    "moe_combine_backward": (I32, [SHAPE, P, P, P, P, P, P, P]),
+    "moe_linear_workspace_bytes": (I32, [LINEAR, I32, ctypes.POINTER(SZ)]),
+    "moe_linear": (I32, [LINEAR, P, P, P, P, P, P, P, SZ, P]),
+    "moe_linear_backward": (I32, [LINEAR, P, P, P, P, P, P, P, P, SZ, P]),
 }
 
 _lib = None

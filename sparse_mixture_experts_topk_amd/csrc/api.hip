@@ -2,6 +2,7 @@
 // Every public function validates on the host before enqueueing anything.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -177,11 +178,47 @@ ForwardLayout forward_layout(const moe_shape_t& s) {
   return L;
 }
 
+// Shape limits that T, n_experts and top_k alone decide, and the router's own.
+moe_status_t validate_router(const moe_shape_t* s, const moe_router_t* r) {
+  moe_status_t v = validate_shape(s);
+  if (v != MOE_OK) return v;
+  if (r == nullptr) return MOE_ERR_INVALID_ARG;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (r->n_groups < 1 || r->n_groups > s->n_experts || s->n_experts % r->n_groups != 0) return MOE_ERR_INVALID_ARG;
+  const int group_size = s->n_experts / r->n_groups;
+  if (r->topk_groups < 1 || r->topk_groups > r->n_groups) return MOE_ERR_INVALID_ARG;
+  if (r->group_top < 1 || r->group_top > 2 || r->group_top > group_size) return MOE_ERR_INVALID_ARG;
+  if (r->topk_groups * group_size < s->top_k) return MOE_ERR_INVALID_ARG;
+  if (r->renormalize != 0 && r->renormalize != 1) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(r->scale)) return MOE_ERR_INVALID_ARG;
+  if (r->n_groups > moe::kMaxRouterGroups) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t validate_linear(const moe_linear_t* l) {
+  if (l == nullptr) return MOE_ERR_INVALID_ARG;
+  if (l->M < 0 || l->M > (1 << 24) || l->N <= 0 || l->K <= 0) return MOE_ERR_INVALID_ARG;
+  if (l->dtype < MOE_F32 || l->dtype > MOE_MXFP4 || l->y_dtype < MOE_F32 || l->y_dtype > MOE_MXFP4)
+    return MOE_ERR_INVALID_ARG;
+  if (l->act < MOE_ACT_NONE || l->act > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+  if (l->dtype != MOE_BF16 || (l->y_dtype != MOE_BF16 && l->y_dtype != MOE_F32)) return MOE_ERR_UNSUPPORTED;
+  if (l->N % 8 != 0 || l->K % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (l->N > moe::kMaxLinearWidth || l->K > moe::kMaxLinearWidth) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 template <typename T>
 T* at(void* base, size_t off) { return reinterpret_cast<T*>(static_cast<uint8_t*>(base) + off); }
 
+// Routing handed in by the caller instead of computed from w_gate.
+struct GivenRouting {
+  const int32_t* ids;
+  const float* weights;
+  const int32_t* next_ids;
+};
+
 moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_gate,
-                          const float* router_bias, const void* w1, const void* w3, const void* w2,
+                          const float* router_bias, const GivenRouting* given, const void* w1, const void* w3, const void* w2,
                           const void* w1_scale, const void* w3_scale, const void* w2_scale,
                           void* y, int32_t* topk_ids_out, float* topk_weights_out,
                           int32_t* expert_counts_out, uint8_t* drop_mask_out, float* logits_out,
@@ -189,7 +226,13 @@ moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_gat
   moe_status_t v = validate_shape(s);
   if (v != MOE_OK) return v;
   if (s->T == 0) return MOE_OK;
-  if ((v = check_ptrs({x, w_gate, w1, w3, w2, y},
+  if (given != nullptr) {
+    if ((v = check_ptrs({given->ids, given->weights}, {given->next_ids})) != MOE_OK) return v;
+    if (fallback_on(*s) && given->next_ids == nullptr) return MOE_ERR_INVALID_ARG;
+  } else if ((v = check_ptrs({w_gate}, {})) != MOE_OK) {
+    return v;
+  }
+  if ((v = check_ptrs({x, w1, w3, w2, y},
                       {router_bias, topk_ids_out, topk_weights_out, expert_counts_out,
                        drop_mask_out, logits_out, w1_scale, w3_scale, w2_scale})) != MOE_OK)
     return v;
@@ -202,8 +245,10 @@ moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_gat
     return MOE_ERR_WORKSPACE;
 
   hipStream_t st = static_cast<hipStream_t>(stream);
-  int32_t* ids = topk_ids_out ? topk_ids_out : at<int32_t>(workspace, L.ids);
-  float* gw = topk_weights_out ? topk_weights_out : at<float>(workspace, L.weights);
+  int32_t* ids_out = topk_ids_out ? topk_ids_out : at<int32_t>(workspace, L.ids);
+  float* gw_out = topk_weights_out ? topk_weights_out : at<float>(workspace, L.weights);
+  const int32_t* ids = given != nullptr ? given->ids : ids_out;
+  const float* gw = given != nullptr ? given->weights : gw_out;
   int32_t* counts = expert_counts_out ? expert_counts_out : at<int32_t>(workspace, L.counts);
   int32_t* offsets = at<int32_t>(workspace, L.offsets);
   int32_t* perm_src = at<int32_t>(workspace, L.perm_src);
@@ -214,13 +259,14 @@ moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_gat
   void* h = at<void>(workspace, L.h);
   uint8_t* h_scale = fp8 ? at<uint8_t>(workspace, L.h_scale) : nullptr;
   float* y_perm = at<float>(workspace, L.y_perm);
-  int32_t* next = fallback_on(*s) ? at<int32_t>(workspace, L.next_ids) : nullptr;
+  int32_t* next_out = fallback_on(*s) ? at<int32_t>(workspace, L.next_ids) : nullptr;
+  const int32_t* next = given != nullptr && fallback_on(*s) ? given->next_ids : next_out;
 
   hipError_t e = hipSuccess;
-  if (moe::route_index_fused(*s) && (s->w_dtype == MOE_BF16 || s->w_dtype == MOE_MXFP4)) {
+  if (given == nullptr && moe::route_index_fused(*s) && (s->w_dtype == MOE_BF16 || s->w_dtype == MOE_MXFP4)) {
     // decode: router partial sums over eight workgroups, then selection + grouping in
     // one; gate/up reads x through perm_src
-    e = moe::launch_route_index(*s, x, w_gate, router_bias, ids, gw, logits_out, counts, offsets, perm_src,
+    e = moe::launch_route_index(*s, x, w_gate, router_bias, ids_out, gw_out, logits_out, counts, offsets, perm_src,
                                 slot_to_row, at<void>(workspace, L.route_part), st);
     if (e == hipSuccess && drop_mask_out != nullptr)
       e = launch_fill_u8(drop_mask_out, (int64_t)s->T * s->top_k, 0, st);
@@ -234,8 +280,9 @@ moe_status_t forward_impl(const moe_shape_t* s, const void* x, const void* w_gat
                                            static_cast<const uint8_t*>(w3), static_cast<const uint8_t*>(w3_scale),
                                            static_cast<uint16_t*>(h), st);
   } else {
-    e = moe::launch_route_topk(*s, x, w_gate, router_bias, ids, gw, logits_out, next,
-                               at<void>(workspace, L.route_logits), st);
+    if (given == nullptr)
+      e = moe::launch_route_topk(*s, x, w_gate, router_bias, ids_out, gw_out, logits_out, next_out,
+                                 at<void>(workspace, L.route_logits), st);
     const uint8_t* drop_in = nullptr;
     if (e == hipSuccess) {
       if (s->capacity >= 0) {
@@ -452,9 +499,108 @@ moe_status_t moe_forward(const moe_shape_t* s, const void* x, const void* w_gate
                          void* y, int32_t* topk_ids_out, float* topk_weights_out,
                          int32_t* expert_counts_out, uint8_t* drop_mask_out, float* logits_out,
                          void* workspace, size_t workspace_bytes, void* stream) {
-  return forward_impl(s, x, w_gate, router_bias, w1, w3, w2, w1_scale, w3_scale, w2_scale, y,
+  return forward_impl(s, x, w_gate, router_bias, nullptr, w1, w3, w2, w1_scale, w3_scale, w2_scale, y,
                       topk_ids_out, topk_weights_out, expert_counts_out, drop_mask_out, logits_out,
                       workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_forward_routed(const moe_shape_t* s, const void* x, const int32_t* topk_ids,
+                                const float* topk_weights, const int32_t* next_ids, const void* w1,
+                                const void* w3, const void* w2, const void* w1_scale,
+                                const void* w3_scale, const void* w2_scale, void* y,
+                                int32_t* expert_counts_out, uint8_t* drop_mask_out, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  const GivenRouting given{topk_ids, topk_weights, next_ids};
+  return forward_impl(s, x, nullptr, nullptr, &given, w1, w3, w2, w1_scale, w3_scale, w2_scale, y, nullptr,
+                      nullptr, expert_counts_out, drop_mask_out, nullptr, workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_route_scored(const moe_shape_t* s, const moe_router_t* r, const float* logits,
+                              const float* balance_bias, int32_t* topk_ids, float* topk_weights,
+                              float* scores, int32_t* next_ids, void* stream) {
+  moe_status_t v = validate_router(s, r);
+  if (v != MOE_OK) return v;
+  if (s->T == 0) return MOE_OK;
+  if ((v = check_ptrs({logits, topk_ids, topk_weights}, {balance_bias, scores, next_ids})) != MOE_OK) return v;
+  return from_hip(moe::launch_route_scored(*s, *r, logits, balance_bias, topk_ids, topk_weights, scores,
+                                           next_ids, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_route_scored_backward(const moe_shape_t* s, const moe_router_t* r, const float* logits,
+                                       const int32_t* topk_ids, const float* dweights, const float* dscores,
+                                       float* dlogits, void* stream) {
+  moe_status_t v = validate_router(s, r);
+  if (v != MOE_OK) return v;
+  if (s->T == 0) return MOE_OK;
+  if ((v = check_ptrs({logits, topk_ids, dweights, dlogits}, {dscores})) != MOE_OK) return v;
+  return from_hip(moe::launch_route_scored_backward(*s, *r, logits, topk_ids, dweights, dscores, dlogits,
+                                                    static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_combine_backward(const moe_shape_t* s, const void* dy, const float* y_perm,
+                                  const int32_t* slot_to_row, const float* topk_weights, void* dy_perm,
+                                  float* dweights, void* stream) {
+  moe_status_t v = validate_shape(s);
+  if (v != MOE_OK) return v;
+  if (dy_perm == nullptr && dweights == nullptr) return MOE_ERR_INVALID_ARG;
+  if (s->T == 0) return MOE_OK;
+  if ((v = check_ptrs({dy, slot_to_row, topk_weights}, {y_perm, dy_perm, dweights})) != MOE_OK) return v;
+  if (dweights != nullptr && y_perm == nullptr) return MOE_ERR_INVALID_ARG;
+  return from_hip(moe::launch_combine_backward(*s, dy, y_perm, slot_to_row, topk_weights, dy_perm, dweights,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_linear_workspace_bytes(const moe_linear_t* l, moe_call_t call, size_t* bytes) {
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  moe_status_t v = validate_linear(l);
+  if (v != MOE_OK) return v;
+  if (call == MOE_CALL_LINEAR) *bytes = moe::linear_workspace_bytes(*l);
+  else if (call == MOE_CALL_LINEAR_BACKWARD) *bytes = moe::linear_backward_workspace_bytes(*l);
+  else return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status_t moe_linear(const moe_linear_t* l, const void* x, const void* w, const float* bias,
+                        const void* residual, void* y, void* pre, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  moe_status_t v = validate_linear(l);
+  if (v != MOE_OK) return v;
+  if (l->M == 0) return MOE_OK;
+  if ((v = check_ptrs({x, w, y}, {bias, residual, pre})) != MOE_OK) return v;
+  const size_t need = moe::linear_workspace_bytes(*l);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
+    return MOE_ERR_WORKSPACE;
+  return from_hip(moe::launch_linear(*l, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), bias,
+                                     residual, y, static_cast<uint16_t*>(pre), need > 0 ? workspace : nullptr,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_linear_backward(const moe_linear_t* l, const void* dy, const void* pre,
+                                 const void* x, const void* w, void* dx, void* dw, float* dbias,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  moe_status_t v = validate_linear(l);
+  if (v != MOE_OK) return v;
+  if (dx == nullptr && dw == nullptr && dbias == nullptr) return MOE_ERR_INVALID_ARG;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (l->M == 0) {   // the sums over no rows
+    if ((v = check_ptrs({}, {dw, dbias})) != MOE_OK) return v;
+    hipError_t e = hipSuccess;
+    if (dw != nullptr) e = launch_fill_u8(static_cast<uint8_t*>(dw), (int64_t)l->N * l->K * 2, 0, st);
+    if (e == hipSuccess && dbias != nullptr)
+      e = launch_fill_u8(reinterpret_cast<uint8_t*>(dbias), (int64_t)l->N * 4, 0, st);
+    return from_hip(e);
+  }
+  if ((v = check_ptrs({dy}, {pre, x, w, dx, dw, dbias})) != MOE_OK) return v;
+  if ((dx != nullptr && w == nullptr) || (dw != nullptr && x == nullptr) ||
+      (l->act != MOE_ACT_NONE && pre == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::linear_backward_workspace_bytes(*l);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
+    return MOE_ERR_WORKSPACE;
+  return from_hip(moe::launch_linear_backward(*l, dy, static_cast<const uint16_t*>(pre),
+                                              static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w),
+                                              static_cast<uint16_t*>(dx), static_cast<uint16_t*>(dw), dbias,
+                                              need > 0 ? workspace : nullptr, st));
 }
 
 moe_status_t moe_forward_noalloc(const moe_shape_t* s, const void* x, const void* w_gate,
@@ -479,7 +625,7 @@ moe_status_t moe_forward_noalloc(const moe_shape_t* s, const void* x, const void
   }
   void* ws = nullptr;
   if (scratch_address(dev, &ws) != hipSuccess) return MOE_ERR_HIP;
-  return forward_impl(s, x, w_gate, router_bias, w1, w3, w2, w1_scale, w3_scale, w2_scale, y,
+  return forward_impl(s, x, w_gate, router_bias, nullptr, w1, w3, w2, w1_scale, w3_scale, w2_scale, y,
                       topk_ids_out, topk_weights_out, expert_counts_out, drop_mask_out, logits_out,
                       ws, MOE_NOALLOC_SCRATCH_BYTES, stream);
 }

@@ -146,6 +146,29 @@ hipError_t launch_down_mxfp4(const moe_shape_t& s, const uint16_t* h, const int3
                              const uint8_t* w2, const uint8_t* w2_scale, float* y_perm,
                              hipStream_t st);
 
+// Scored routing from logits and its gradient (moe_route_scored).
+constexpr int kMaxRouterGroups = 64;   // one lane at least per group
+hipError_t launch_route_scored(const moe_shape_t& s, const moe_router_t& r, const float* logits, const float* bias,
+                               int32_t* ids, float* weights, float* scores, int32_t* next_ids, hipStream_t st);
+hipError_t launch_route_scored_backward(const moe_shape_t& s, const moe_router_t& r, const float* logits,
+                                        const int32_t* ids, const float* dweights, const float* dscores,
+                                        float* dlogits, hipStream_t st);
+
+// Gradient of the combine (either output may be NULL).
+hipError_t launch_combine_backward(const moe_shape_t& s, const void* dy, const float* y_perm,
+                                   const int32_t* slot_to_row, const float* weights, void* dy_perm,
+                                   float* dweights, hipStream_t st);
+
+// Dense product with bias, activation and residual, and its gradients.
+constexpr int kMaxLinearWidth = 1 << 18;
+size_t linear_workspace_bytes(const moe_linear_t& l);
+size_t linear_backward_workspace_bytes(const moe_linear_t& l);
+hipError_t launch_linear(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const float* bias,
+                         const void* residual, void* y, uint16_t* pre, void* workspace, hipStream_t st);
+hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const uint16_t* pre, const uint16_t* x,
+                                  const uint16_t* w, uint16_t* dx, uint16_t* dw, float* dbias, void* workspace,
+                                  hipStream_t st);
+
 // Largest number of rows any routed expert can receive: each token picks an expert at most once.
 inline int64_t max_rows_per_routed_expert(const moe_shape_t& s) {
   int64_t m = s.T;

@@ -1,0 +1,470 @@
+// Scored top-k routing from given logits, and its gradient at the logits.
+//
+// Pages: "How Mixtral 8x7B uses mixture of experts", the simplified forward
+// pass (softmax over all experts, top-k, renormalise); "Mixtral 8x7B"
+// interview page, section on how MoE design changed since Mixtral (256
+// fine-grained experts, balanced without an auxiliary loss).
+//
+// Forward, per token: scores s = softmax(l) or sigmoid(l); choice c = s + b
+// (b the balance bias); the score of a group of consecutive experts is its
+// largest c or the sum of its two largest; the best `topk_groups` groups stay
+// open and the k largest c of their experts are chosen, ties to the lower
+// index.  The weights come from s alone: w_j = scale * s_j, or scale * s_j /
+// (sum of the chosen s), the latter formed as e^(l_j - m) / sum e^(l_i - m)
+// (softmax) or with every e^l taken relative to the largest chosen one
+// (sigmoid), so that it holds where every score underflows.
+//
+// One wavefront per token.  The 64 lanes are cut into as many equal parts as
+// there are groups (rounded up to a power of two), a group's experts lying in
+// index order over its part's lanes, PER to a lane: a lane position, then a
+// position within the lane, orders experts by index, so "the lowest lane that
+// holds the maximum" settles ties.  Keys are the choices mapped to ordered
+// unsigned integers (0: not a candidate), which also orders -inf (an expert
+// that is only chosen when nothing else is left) and NaN (below -inf), so k
+// distinct experts always come out.
+//
+// The choice must not depend on how fp32 rounds the scores.  Without a
+// balance bias the order of c is that of the logits and the keys are the
+// logits themselves.  Otherwise the wavefront works in fp32 and looks at
+// every gap that decided something (between consecutive chosen experts, the
+// last chosen and the first left out, any two groups): one within the fp32
+// error of the two values (kScoreErr of the largest score, kSumErr of the
+// choice) sends the token through the same steps in fp64, where scores of
+// distinct fp32 logits are distinct until they saturate.  With 256 experts
+// and N(0,1) logits about one token in 500 goes that way.
+#include <type_traits>
+
+#include "device_common.hpp"
+#include "launch.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kRouteWaves = 4;     // tokens per workgroup
+// fp32 softmax or sigmoid: under 1e-6 of the largest score (expf and the sum
+// over at most 256 terms); a difference of two has twice that.  c = s + b and
+// the sum of two choices round once more, 2^-24 of the value each.
+constexpr float kScoreErr = 4e-6f;
+constexpr float kSumErr = 5e-7f;
+
+// Order-preserving map to unsigned integers; 0 is kept for "no candidate".
+__device__ __forceinline__ uint32_t ordered(float v) {
+  if (v != v) return 1u;
+  const uint32_t b = __float_as_uint(v + 0.0f);          // -0 -> +0
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t ordered(double v) {
+  if (v != v) return 1ull;
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, false);
+}
+// Largest key of the wavefront, uniform.  DPP row shifts within 16 lanes, then
+// the two row broadcasts, leave it in lane 63.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp_or_zero<0x111, 0xF>(v));
+  v = max(v, dpp_or_zero<0x112, 0xF>(v));
+  v = max(v, dpp_or_zero<0x114, 0xF>(v));
+  v = max(v, dpp_or_zero<0x118, 0xF>(v));
+  v = max(v, dpp_or_zero<0x142, 0xA>(v));
+  v = max(v, dpp_or_zero<0x143, 0xC>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const uint64_t o = (uint64_t)__shfl_xor((long long)v, m);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+template <class R>
+__device__ __forceinline__ R wave_sum(R v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+template <class R>
+__device__ __forceinline__ R wave_max_value(R v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const R o = __shfl_xor(v, m);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ float exp_r(float v) { return expf(v); }
+__device__ __forceinline__ double exp_r(double v) { return exp(v); }
+
+// sigmoid(l) without overflow: e^min(l,0) / (1 + e^-|l|)
+template <class R>
+__device__ __forceinline__ R sigmoid(R l) {
+  const R e = exp_r(l < 0 ? l : -l);
+  return (l < 0 ? e : R(1)) / (R(1) + e);
+}
+
+struct RouteArgs {
+  int T, E, k;
+  int n_groups, group_size, lanes_per_group, topk_groups, group_top;
+  bool softmax, renormalize;
+  float scale;
+  const float* logits;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  float* scores;
+  int32_t* next_ids;
+};
+
+// Scores of the lane's experts (0 at positions past the group), in R.
+template <class R, int PER>
+__device__ __forceinline__ void lane_scores(const RouteArgs& a, const float (&l)[PER], const bool (&in)[PER],
+                                            float lmax, R (&s)[PER]) {
+  R z = 0;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    if (a.softmax) s[p] = in[p] ? exp_r((R)l[p] - (R)lmax) : R(0);
+    else s[p] = in[p] ? sigmoid<R>((R)l[p]) : R(0);
+    z += s[p];
+  }
+  if (a.softmax) {
+    z = wave_sum(z);
+    const R inv = z > 0 ? R(1) / z : R(0);       // every logit -inf: no score
+#pragma unroll
+    for (int p = 0; p < PER; ++p) s[p] *= inv;
+  }
+}
+
+// The `rounds` best experts of the open groups into lanes 0 .. rounds - 1 of
+// `chosen` (-1: no candidate left).  Returns whether fp32 could have decided
+// any step wrongly (always false in fp64).
+template <class R, int PER>
+__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER], const bool (&in)[PER],
+                                       const float (&b)[PER], float lmax, bool need_scores, int lane, int rounds,
+                                       R (&s)[PER], int& chosen) {
+  using Key = std::conditional_t<sizeof(R) == 4, uint32_t, uint64_t>;
+  constexpr bool CHECK = sizeof(R) == 4;
+  const int lig = lane & (a.lanes_per_group - 1), grp = lane / a.lanes_per_group;
+  if (need_scores) lane_scores<R, PER>(a, l, in, lmax, s);
+  const bool by_logit = a.bias == nullptr;
+  bool near = false;
+  float score_tol = 0;
+  if constexpr (CHECK) {
+    if (need_scores && (!by_logit || a.n_groups > 1)) {
+      float m = 0;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) m = fmaxf(m, (float)s[p]);
+      score_tol = kScoreErr * __uint_as_float(wave_max(__float_as_uint(m)));   // s >= 0: ordered as integers
+    }
+  }
+  bool open = grp < a.n_groups;
+  if (a.n_groups > 1) {
+    // the group's score: its two largest values merged over the part's lanes
+    const R none = -(R)INFINITY;
+    R g1 = none, g2 = none;
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      R v = none;
+      if (in[p]) {
+        if (a.group_top == 1 && by_logit) v = (R)l[p];
+        else v = s[p] + (by_logit ? R(0) : (R)b[p]);
+        if (v != v) v = none;
+      }
+      g2 = v > g1 ? g1 : (v > g2 ? v : g2);
+      g1 = v > g1 ? v : g1;
+    }
+    for (int m = 1; m < a.lanes_per_group; m <<= 1) {
+      const R o1 = __shfl_xor(g1, m), o2 = __shfl_xor(g2, m);
+      const R lo = o1 > g1 ? g1 : o1;
+      g1 = o1 > g1 ? o1 : g1;
+      const R hi2 = o2 > g2 ? o2 : g2;
+      g2 = lo > hi2 ? lo : hi2;
+    }
+    const R gs = a.group_top == 1 ? g1 : g1 + g2;
+    int rank = 0;
+    for (int o = 0; o < a.n_groups; ++o) {
+      const R os = __shfl(gs, o * a.lanes_per_group);
+      rank += (os > gs || (os == gs && o < grp)) ? 1 : 0;
+      if constexpr (CHECK) {
+        if (!(a.group_top == 1 && by_logit) && open && o != grp)
+          near |= !(fabsf(os - gs) > 2 * score_tol + 2 * kSumErr * fabsf(gs));
+      }
+    }
+    open = open && rank < a.topk_groups;
+  }
+  Key key[PER], best = 0;
+  int bp = 0;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    key[p] = !(open && in[p]) ? Key(0) : by_logit ? ordered((R)l[p]) : ordered(s[p] + (R)b[p]);
+    if (key[p] > best) { best = key[p]; bp = p; }
+  }
+  chosen = -1;
+  float prev = 0;
+  for (int r = 0; r < rounds; ++r) {
+    const Key top = wave_max(best);
+    if (top == 0) break;                                   // uniform: no candidate left
+    const int owner = __builtin_amdgcn_readfirstlane((int)__builtin_ctzll(__ballot(best == top)));
+    const int e = __builtin_amdgcn_readlane(grp * a.group_size + lig * PER + bp, owner);
+    if constexpr (CHECK) {
+      if (!by_logit) {
+        const float v = from_ordered(top);
+        if (r > 0) near |= !(prev - v > score_tol + kSumErr * fmaxf(fabsf(prev), fabsf(v)));
+        prev = v;
+      }
+    }
+    chosen = lane == r ? e : chosen;
+    if (lane == owner) {
+      best = 0;
+      const int taken = bp;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) {
+        if (p == taken) key[p] = 0;
+        if (key[p] > best) { best = key[p]; bp = p; }
+      }
+    }
+  }
+  return CHECK && __ballot(near) != 0;
+}
+
+// HBM-bound in principle (4 E bytes per token in, 8 k out); in practice the
+// k + 1 selection rounds of each wavefront bound it.
+template <int PER>
+__global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const RouteArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= a.T) return;
+  const int lig = lane & (a.lanes_per_group - 1), grp = lane / a.lanes_per_group;
+  const int first = grp * a.group_size + lig * PER;          // the lane's first expert
+  const float* row = a.logits + (int64_t)t * a.E;
+  float l[PER], b[PER];
+  bool in[PER];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    in[p] = grp < a.n_groups && lig * PER + p < a.group_size;
+    l[p] = in[p] ? row[first + p] : -INFINITY;
+    b[p] = in[p] && a.bias != nullptr ? a.bias[first + p] : 0.0f;
+  }
+  // the softmax of all experts is not needed where the weights are
+  // renormalised over the chosen ones and nothing else looks at scores
+  const bool need_scores = a.bias != nullptr || (a.n_groups > 1 && a.group_top > 1) || a.scores != nullptr ||
+                           (a.softmax && !a.renormalize);
+  float lmax = -INFINITY;
+  if (a.softmax && need_scores) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p) lmax = fmaxf(lmax, l[p]);
+    lmax = fmaxf(wave_max_value(lmax), -3.402823466e38f);    // all -inf: every term e^-inf
+  }
+  const int want = a.k + (a.next_ids != nullptr ? 2 : 0);
+  float s[PER];
+  int chosen;
+  if (choose<float, PER>(a, l, in, b, lmax, need_scores, lane, want + 1, s, chosen)) {
+    double s64[PER];
+    choose<double, PER>(a, l, in, b, lmax, need_scores, lane, want, s64, chosen);
+  }
+  if (a.scores != nullptr) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      if (in[p]) a.scores[(int64_t)t * a.E + first + p] = s[p];
+  }
+  // weights: lane j < k holds the j-th chosen expert
+  const bool mine = lane < a.k;
+  const float lj = mine ? row[chosen] : -INFINITY;
+  float w;
+  if (a.renormalize) {
+    float m = lj;
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    m = fmaxf(m, -3.402823466e38f);
+    if (a.softmax) {
+      w = expf(lj - m);
+    } else {
+      m = fminf(m, 0.0f);
+      w = expf(fminf(lj, 0.0f) - m) / (1.0f + expf(-fabsf(lj)));
+    }
+    if (!mine) w = 0.0f;
+    float sum = w;
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor(sum, d);
+    w = sum > 0.0f ? w / sum : 0.0f;
+  } else if (a.softmax) {
+    // the token's softmax, its denominator from the lanes' experts again
+    float z = 0;
+#pragma unroll
+    for (int p = 0; p < PER; ++p) z += in[p] ? expf(l[p] - lmax) : 0.0f;
+    z = wave_sum(z);
+    w = z > 0.0f ? expf(lj - lmax) / z : 0.0f;
+  } else {
+    w = sigmoid(lj);
+  }
+  if (mine) {
+    a.ids[(int64_t)t * a.k + lane] = chosen;
+    a.weights[(int64_t)t * a.k + lane] = w * a.scale;
+  }
+  if (a.next_ids != nullptr && lane >= a.k && lane < a.k + 2)
+    a.next_ids[(int64_t)t * 2 + lane - a.k] = chosen;
+}
+
+struct RouteBackArgs {
+  int T, E, k;
+  bool softmax, renormalize;
+  float scale;
+  const float* logits;
+  const int32_t* ids;
+  const float* dweights;
+  const float* dscores;
+  float* dlogits;
+};
+
+// Gradient at the logits, one wavefront per token.  With D the gradient that
+// arrives at the scores (0 without one), g the one at the weights and, when
+// renormalised, w' = s / (sum of the chosen s) and
+//   q_j = scale w'_j sum_i w'_i (g_j - g_i),
+//   softmax:  dl_e = q_e + s_e (D_e - sum_i D_i s_i)
+//   sigmoid:  dl_e = q_e (1 - s_e) + D_e s_e (1 - s_e)
+// else, with a_e = D_e + scale g_e,
+//   softmax:  dl_e = s_e (a_e - sum_i a_i s_i)
+//   sigmoid:  dl_e = a_e s_e (1 - s_e).
+// The differences g_j - g_i are taken before they are weighted: they hold
+// where the g are near each other.  1 - sigmoid(l) is sigmoid(-l).
+// HBM-bound: reads 4 E bytes (8 E with D) and writes 4 E per token.
+template <int PER>
+__global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_kernel(const RouteBackArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= a.T) return;
+  const int64_t base = (int64_t)t * a.E;
+  float l[PER], d[PER];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int e = lane * PER + p;
+    l[p] = e < a.E ? a.logits[base + e] : -INFINITY;
+    d[p] = e < a.E && a.dscores != nullptr ? a.dscores[base + e] : 0.0f;
+  }
+  // lanes j < k: the j-th chosen expert (an id outside the row adds nothing)
+  int id = lane < a.k ? a.ids[(int64_t)t * a.k + lane] : -1;
+  if (id >= a.E) id = -1;
+  const float g = id >= 0 ? a.dweights[(int64_t)t * a.k + lane] : 0.0f;
+  float q = a.scale * g;
+  if (a.renormalize) {
+    const float lj = id >= 0 ? a.logits[base + id] : -INFINITY;
+    float m = lj;
+#pragma unroll
+    for (int x = 1; x < 8; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+    m = fmaxf(m, -3.402823466e38f);
+    float w;
+    if (a.softmax) {
+      w = expf(lj - m);
+    } else {
+      m = fminf(m, 0.0f);
+      w = expf(fminf(lj, 0.0f) - m) / (1.0f + expf(-fabsf(lj)));
+    }
+    if (id < 0) w = 0.0f;
+    float sum = w;
+#pragma unroll
+    for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor(sum, x);
+    w = sum > 0.0f ? w / sum : 0.0f;
+    float c = 0.0f;
+#pragma unroll
+    for (int x = 1; x < 8; ++x) c += __shfl_xor(w, x) * (g - __shfl_xor(g, x));
+    q = a.scale * w * c;
+  }
+  float sel[PER];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) sel[p] = 0.0f;
+  for (int j = 0; j < a.k; ++j) {
+    const int ej = __builtin_amdgcn_readlane(id, j);
+    const float qj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(q), j));
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      if (lane * PER + p == ej) sel[p] += qj;
+  }
+  float out[PER];
+  if (a.softmax) {
+    const bool need = !a.renormalize || a.dscores != nullptr;
+    if (need) {
+      float lmax = -INFINITY;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) lmax = fmaxf(lmax, l[p]);
+      lmax = fmaxf(wave_max_value(lmax), -3.402823466e38f);
+      float s[PER], z = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) {
+        s[p] = expf(l[p] - lmax);
+        z += s[p];
+        if (!a.renormalize) d[p] += sel[p];
+        dot += d[p] * s[p];
+      }
+      z = wave_sum(z);
+      dot = wave_sum(dot);
+      const float inv = z > 0.0f ? 1.0f / z : 0.0f;
+#pragma unroll
+      for (int p = 0; p < PER; ++p)
+        out[p] = (a.renormalize ? sel[p] : 0.0f) + s[p] * inv * (d[p] - dot * inv);
+    } else {
+#pragma unroll
+      for (int p = 0; p < PER; ++p) out[p] = sel[p];
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const float below = sigmoid(-l[p]);                      // 1 - s
+      const float s = sigmoid(l[p]);
+      out[p] = a.renormalize ? sel[p] * below + d[p] * s * below : (d[p] + sel[p]) * s * below;
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int e = lane * PER + p;
+    if (e < a.E) a.dlogits[base + e] = out[p];
+  }
+}
+
+}  // namespace
+
+hipError_t launch_route_scored(const moe_shape_t& s, const moe_router_t& r, const float* logits, const float* bias,
+                               int32_t* ids, float* weights, float* scores, int32_t* next_ids, hipStream_t st) {
+  RouteArgs a{};
+  a.T = s.T; a.E = s.n_experts; a.k = s.top_k;
+  a.n_groups = r.n_groups;
+  a.group_size = s.n_experts / r.n_groups;
+  int parts = 1;
+  while (parts < r.n_groups) parts *= 2;
+  a.lanes_per_group = kWave / parts;
+  // every group open: groups decide nothing
+  a.topk_groups = r.topk_groups;
+  a.group_top = r.group_top;
+  a.softmax = r.score == MOE_SCORE_SOFTMAX;
+  a.renormalize = r.renormalize != 0;
+  a.scale = r.scale;
+  a.logits = logits; a.bias = bias; a.ids = ids; a.weights = weights; a.scores = scores; a.next_ids = next_ids;
+  const int per = (a.group_size + a.lanes_per_group - 1) / a.lanes_per_group;
+  const dim3 grid((unsigned)((s.T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
+  if (per <= 1) hipLaunchKernelGGL(route_scored_kernel<1>, grid, block, 0, st, a);
+  else if (per <= 2) hipLaunchKernelGGL(route_scored_kernel<2>, grid, block, 0, st, a);
+  else if (per <= 4) hipLaunchKernelGGL(route_scored_kernel<4>, grid, block, 0, st, a);
+  else hipLaunchKernelGGL(route_scored_kernel<8>, grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_route_scored_backward(const moe_shape_t& s, const moe_router_t& r, const float* logits,
+                                        const int32_t* ids, const float* dweights, const float* dscores,
+                                        float* dlogits, hipStream_t st) {
+  RouteBackArgs a{s.T, s.n_experts, s.top_k, r.score == MOE_SCORE_SOFTMAX, r.renormalize != 0, r.scale,
+                  logits, ids, dweights, dscores, dlogits};
+  const dim3 grid((unsigned)((s.T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
+  if (a.E <= 64) hipLaunchKernelGGL(route_scored_backward_kernel<1>, grid, block, 0, st, a);
+  else if (a.E <= 128) hipLaunchKernelGGL(route_scored_backward_kernel<2>, grid, block, 0, st, a);
+  else hipLaunchKernelGGL(route_scored_backward_kernel<4>, grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace moe

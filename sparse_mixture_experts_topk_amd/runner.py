@@ -3,6 +3,10 @@
 ``DeviceInputs`` moves a synthetic.MoEInputs to the GPU; ``forward`` runs the
 fused ``moe_forward``; ``staged`` runs the five boundary calls one after the
 other and returns every intermediate, so each step can be checked on its own.
+Given a ``MoeRouter``, both route by ``scored_routing`` (``moe_linear`` for the
+logits, ``moe_route_scored`` for the choice) instead of the library's top-k
+softmax router, and ``gate_backward`` takes the gradient at y of such a staged
+pass back to x and the router's weights (the experts' weights held fixed).
 """
 from __future__ import annotations
 
@@ -11,9 +15,12 @@ from typing import Optional
 
 import torch
 
-from . import (moe_combine, moe_expert_gemm_down, moe_expert_gemm_gate_up, moe_forward,
-               moe_permute, moe_route_topk, moe_workspace_bytes, shape_of, MOE_CALL_DOWN,
-               MOE_CALL_FORWARD, MOE_CALL_ROUTE)
+from . import (make_linear, moe_combine, moe_combine_backward, moe_expert_gemm_down,
+               moe_expert_gemm_gate_up, moe_forward, moe_forward_routed, moe_linear,
+               moe_linear_backward, moe_linear_workspace_bytes, moe_permute, moe_route_scored,
+               moe_route_scored_backward, moe_route_topk, moe_workspace_bytes, shape_of,
+               MOE_CALL_DOWN, MOE_CALL_FORWARD, MOE_CALL_LINEAR, MOE_CALL_LINEAR_BACKWARD,
+               MOE_CALL_ROUTE)
 
 
 def _dev(t: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
@@ -83,18 +90,75 @@ def alloc_forward(cfg, device="cuda", with_outputs=True) -> ForwardBuffers:
                           torch.empty(T, E, dtype=torch.float32, device=device), ws)
 
 
-def forward(di: DeviceInputs, buf: Optional[ForwardBuffers] = None, stream=None) -> ForwardBuffers:
+def _bytes(n: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def scored_routing(di: DeviceInputs, router, balance_bias=None, stream=None, out: Optional[dict] = None,
+                   scores: bool = False) -> dict:
+    """logits = x . w_gate^T (+ router_bias) in fp32, then moe_route_scored: the buffers of both
+    (``out`` holds ones to use: logits, topk_ids, topk_weights, next_ids, scores, linear_ws)."""
+    cfg, dev = di.cfg, di.x.device
+    T, E, k = cfg.T, cfg.n_experts, cfg.top_k
+    lin = make_linear(T, E, cfg.d_model, dtype=cfg.act_dtype, y_dtype="f32")
+    o = {} if out is None else out
+    for name, shape, dtype in (("topk_ids", (T, k), torch.int32), ("topk_weights", (T, k), torch.float32),
+                               ("logits", (T, E), torch.float32), ("next_ids", (T, 2), torch.int32),
+                               ("scores", (T, E) if scores else None, torch.float32)):
+        if o.get(name) is None:
+            o[name] = None if shape is None else torch.empty(*shape, dtype=dtype, device=dev)
+    if o.get("linear_ws") is None:
+        o["linear_ws"] = _bytes(moe_linear_workspace_bytes(lin, MOE_CALL_LINEAR), dev)
+    moe_linear(lin, di.x, di.w_gate, di.router_bias, None, o["logits"], None, o["linear_ws"], stream)
+    moe_route_scored(shape_of(cfg), router, o["logits"], balance_bias, o["topk_ids"], o["topk_weights"],
+                     o["scores"], o["next_ids"], stream)
+    return o
+
+
+def gate_backward(di: DeviceInputs, st: dict, router, dy: torch.Tensor, dscores=None, stream=None) -> dict:
+    """Gradients of the gate from the gradient ``dy`` at y: ``st`` is the result of ``staged`` with
+    the same router.  dy_perm is the gradient at the experts' rows; dx and dw_gate, dbias are those
+    of the router's product alone (the path through the gate weights)."""
+    cfg, dev = di.cfg, di.x.device
+    T, d, E, k = cfg.T, cfg.d_model, cfg.n_experts, cfg.top_k
+    shape = shape_of(cfg)
+    o = {"dy_perm": torch.empty(T * (k + cfg.n_shared), d, dtype=_act_dtype(cfg), device=dev),
+         "dweights": torch.empty(T, k, device=dev), "dlogits": torch.empty(T, E, device=dev),
+         "dx": torch.empty(T, d, dtype=_act_dtype(cfg), device=dev),
+         "dw_gate": torch.empty(E, d, dtype=_act_dtype(cfg), device=dev),
+         "dbias": torch.empty(E, device=dev) if di.router_bias is not None else None}
+    moe_combine_backward(shape, dy, st["y_perm"], st["slot_to_row"], st["topk_weights"], o["dy_perm"],
+                         o["dweights"], stream)
+    moe_route_scored_backward(shape, router, st["logits"], st["topk_ids"], o["dweights"], dscores,
+                              o["dlogits"], stream)
+    lin = make_linear(T, E, d, dtype=cfg.act_dtype, y_dtype="f32")
+    o["ws"] = _bytes(moe_linear_workspace_bytes(lin, MOE_CALL_LINEAR_BACKWARD), dev)
+    moe_linear_backward(lin, o["dlogits"], None, di.x, di.w_gate, o["dx"], o["dw_gate"], o["dbias"], o["ws"],
+                        stream)
+    return o
+
+
+def forward(di: DeviceInputs, buf: Optional[ForwardBuffers] = None, stream=None, router=None,
+            balance_bias=None) -> ForwardBuffers:
     cfg = di.cfg
     if buf is None:
         buf = alloc_forward(cfg, di.x.device)
+    if router is not None:
+        r = scored_routing(di, router, balance_bias, stream,
+                           {"topk_ids": buf.topk_ids, "topk_weights": buf.topk_weights, "logits": buf.logits})
+        moe_forward_routed(shape_of(cfg), di.x, r["topk_ids"], r["topk_weights"], r["next_ids"], di.w1, di.w3,
+                           di.w2, di.w1_scale, di.w3_scale, di.w2_scale, buf.y, buf.expert_counts,
+                           buf.drop_mask, buf.workspace, stream)
+        return buf
     moe_forward(shape_of(cfg), di.x, di.w_gate, di.router_bias, di.w1, di.w3, di.w2, di.w1_scale,
                 di.w3_scale, di.w2_scale, buf.y, buf.topk_ids, buf.topk_weights,
                 buf.expert_counts, buf.drop_mask, buf.logits, buf.workspace, stream)
     return buf
 
 
-def staged(di: DeviceInputs, stream=None) -> dict:
-    """The five boundary calls in sequence; returns every intermediate buffer."""
+def staged(di: DeviceInputs, stream=None, router=None, balance_bias=None) -> dict:
+    """The five boundary calls in sequence (with a router: scored_routing in place of
+    moe_route_topk); returns every intermediate buffer."""
     cfg = di.cfg
     dev = di.x.device
     T, d, F, E, k, S = cfg.T, cfg.d_model, cfg.d_ff, cfg.n_experts, cfg.top_k, cfg.n_shared
@@ -103,14 +167,17 @@ def staged(di: DeviceInputs, stream=None) -> dict:
     shape = shape_of(cfg)
     fp8 = cfg.w_dtype == "fp8_e4m3"
     o = {}
-    o["topk_ids"] = torch.empty(T, k, dtype=torch.int32, device=dev)
-    o["topk_weights"] = torch.empty(T, k, dtype=torch.float32, device=dev)
-    o["logits"] = torch.empty(T, E, dtype=torch.float32, device=dev)
-    o["next_ids"] = torch.empty(T, 2, dtype=torch.int32, device=dev)
-    route_ws = moe_workspace_bytes(shape, MOE_CALL_ROUTE)   # used when no logits buffer is passed
-    o["route_ws"] = torch.empty(route_ws, dtype=torch.uint8, device=dev) if route_ws else None
-    moe_route_topk(shape, di.x, di.w_gate, di.router_bias, o["topk_ids"], o["topk_weights"],
-                   o["logits"], o["next_ids"], None, stream)
+    if router is not None:
+        scored_routing(di, router, balance_bias, stream, o, scores=True)
+    else:
+        o["topk_ids"] = torch.empty(T, k, dtype=torch.int32, device=dev)
+        o["topk_weights"] = torch.empty(T, k, dtype=torch.float32, device=dev)
+        o["logits"] = torch.empty(T, E, dtype=torch.float32, device=dev)
+        o["next_ids"] = torch.empty(T, 2, dtype=torch.int32, device=dev)
+        route_ws = moe_workspace_bytes(shape, MOE_CALL_ROUTE)   # used when no logits buffer is passed
+        o["route_ws"] = _bytes(route_ws, dev)
+        moe_route_topk(shape, di.x, di.w_gate, di.router_bias, o["topk_ids"], o["topk_weights"],
+                       o["logits"], o["next_ids"], None, stream)
     o["expert_counts"] = torch.empty(E + S, dtype=torch.int32, device=dev)
     o["expert_offsets"] = torch.empty(E + S + 1, dtype=torch.int32, device=dev)
     o["perm_src"] = torch.full((R,), -7, dtype=torch.int32, device=dev)

@@ -1,0 +1,741 @@
+"""GPU parity of the scored router, the dense product and the gate's gradients with the fp64
+reference, through the public entry points.
+
+Tolerances.  h(t) is half a step of a type, relative to the value: bf16 2^-8, fp32 2^-24.
+A dot product of n terms on the matrix cores, whose adder may truncate, is held to
+(n + 4) 2^-23 sum |a b|; each activation and its derivative to 2^-19 (1 + |p|) (a few roundings,
+the hardware's exp2 and reciprocal, and the rounding of an argument up to 1.6 |p| (1 + |p|^2 / 22)
+whose slope dies out as that grows)."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_mixture_experts_topk_amd as moe
+from oracle import operators as ref
+from sparse_mixture_experts_topk_amd import runner, synthetic
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = 2.0 ** -8, 2.0 ** -24
+DEV = "cuda"
+
+
+def say(msg):
+    print(f"\n[case] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def normal(g, *shape, std=1.0, dtype=torch.float32):
+    return (torch.randn(*shape, generator=g) * std).to(dtype)
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def cuda(t):
+    return None if t is None else t.to(DEV)
+
+
+GUARD = 32      # elements behind an output that must stay as they were
+
+
+class Out:
+    """A device output with a guard behind it."""
+
+    def __init__(self, *shape, dtype=torch.float32, fill=-7.0):
+        n = int(np.prod(shape))
+        self.flat = torch.full((n + GUARD,), fill, dtype=dtype, device=DEV)
+        self.fill, self.n = fill, n
+        self.t = self.flat[:n].view(*shape)
+
+    def np(self):
+        guard = self.flat[self.n:].cpu().float().numpy()
+        assert (guard == self.fill).all(), "written past the end"
+        return f64(self.t)
+
+
+def close(got, want, tol, what):
+    assert got.shape == want.shape
+    assert np.isfinite(got).all(), f"{what}: not finite"
+    off = np.abs(got - want) - tol
+    at = np.unravel_index(off.argmax(), off.shape)
+    assert off.max() <= 0, f"{what}{at}: {got[at]} against {want[at]}, allowed {np.broadcast_to(tol, got.shape)[at]}"
+
+
+# ---- scored routing ----
+
+def route_case(T, E, k, kind="sigmoid", n_groups=1, topk_groups=1, group_top=1, renormalize=True, scale=1.0,
+               bias=True, seed=0, logits=None, next_ids=True, scores=True):
+    say(f"route T={T} E={E} k={k} {kind} groups={topk_groups}/{n_groups} top{group_top} renorm={renormalize} "
+        f"bias={bias} seed={seed}")
+    g = gen(seed)
+    x = normal(g, T, E) if logits is None else logits
+    b = normal(g, E, std=0.05 if kind == "sigmoid" else 0.2 / E) if bias is True else bias if bias is not False else None
+    r = moe.make_router(kind, n_groups, topk_groups, group_top, renormalize, scale)
+    s = moe.make_shape(T, 64, 64, E, k)
+    ids, w = Out(T, k, dtype=torch.int32, fill=-77), Out(T, k)
+    sc = Out(T, E) if scores else None
+    nx = Out(T, 2, dtype=torch.int32, fill=-77) if next_ids else None
+    moe.moe_route_scored(s, r, cuda(x), cuda(b), ids.t, w.t, sc.t if sc else None, nx.t if nx else None)
+    torch.cuda.synchronize()
+    want = ref.route_scored(f64(x), f64(b), k, kind, n_groups, topk_groups, group_top, renormalize, scale)
+    assert np.array_equal(ids.np(), want[0]), "ids"
+    if nx:
+        assert np.array_equal(nx.np(), want[3]), "next ids"
+    # exp's argument is rounded (up to its size in half steps), then some ten roundings
+    # and the rounding of a sum of at most E terms
+    span = np.ptp(np.where(np.isfinite(f64(x)), f64(x), 0.0), axis=1, keepdims=True) + 24
+    close(w.np(), want[1], span * 2 * F32 * want[1] + 1e-37, "weights")
+    if sc:
+        close(sc.np(), want[2], span * 2 * F32 * want[2] + 1e-37, "scores")
+    return ids, w
+
+
+ROUTES = [
+    # T, E, k, groups, kept, top: one token, few and odd experts, groups of odd size, the largest
+    (1, 2, 1, 1, 1, 1), (1, 8, 2, 1, 1, 1), (3, 8, 8, 1, 1, 1), (5, 3, 2, 1, 1, 1), (61, 60, 4, 1, 1, 1),
+    (64, 64, 6, 4, 2, 1), (33, 65, 8, 1, 1, 1), (257, 160, 6, 8, 3, 1), (19, 200, 5, 10, 4, 2),
+    (128, 128, 7, 16, 5, 2), (300, 256, 8, 8, 4, 2), (17, 256, 8, 64, 9, 2), (9, 64, 8, 64, 11, 1),
+    (7, 256, 8, 2, 1, 2), (4, 250, 3, 5, 2, 2), (11, 6, 2, 3, 1, 2), (1021, 256, 8, 1, 1, 1),
+    (6, 66, 2, 33, 2, 2), (6, 231, 2, 33, 2, 2),
+]
+
+
+@pytest.mark.parametrize("case", ROUTES)
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route(case, kind, bias):
+    T, E, k, n, kept, top = case
+    route_case(T, E, k, kind, n, kept, top, renormalize=True, scale=2.5, bias=bias, seed=E + k)
+    route_case(T, E, k, kind, n, kept, top, renormalize=False, bias=bias, seed=E + k + 1, next_ids=False,
+               scores=False)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (8, 4, 2), (8, 3, 1)])
+def test_route_ties_go_to_the_lower_index(kind, groups):
+    g = gen(3)
+    x = torch.randint(-2, 3, (64, 128), generator=g).float() * 0.5        # many equal logits
+    x[0] = 0.0                                                            # all equal
+    x[1, 5], x[1, 9] = 0.0, -0.0                                          # zeros of either sign are equal
+    route_case(64, 128, 8, kind, *groups, bias=False, logits=x)
+    b = torch.randint(0, 3, (128,), generator=g).float() * 0.25
+    route_case(64, 128, 8, kind, *groups, bias=b, logits=x)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_is_decided_by_the_scores_not_their_rounding(kind):
+    """Logits one fp32 step apart with a balance bias: in fp32 the choices are equal."""
+    T, E = 32, 64
+    base = torch.linspace(0.5, 1.5, T)[:, None].expand(T, E).contiguous()
+    step = torch.zeros(E, dtype=torch.int32)
+    step[torch.randperm(E, generator=gen(4))] = torch.arange(E, dtype=torch.int32)
+    x = (base.view(torch.int32) + step).view(torch.float32).contiguous()
+    for bias in (torch.zeros(E), torch.full((E,), 3.0)):
+        route_case(T, E, 8, kind, bias=bias, logits=x)
+        route_case(T, E, 8, kind, 8, 3, 2, bias=bias, logits=x)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_masked_logits_and_biases(kind, renorm):
+    T, E, k = 12, 32, 4
+    x = normal(gen(8), T, E)
+    x[0, :] = -float("inf")                                # nothing left: zero weights
+    x[1, 3:] = -float("inf")                               # three experts left for four places
+    x[2, ::2] = -float("inf")
+    x[3, :] = torch.finfo(torch.float32).min               # the type's lowest value everywhere
+    x[4, 1:] = torch.finfo(torch.float32).min
+    x[5] -= 200.0                                          # every sigmoid underflows in fp32
+    x[6] += 90.0
+    x[7] *= 30.0
+    b = torch.zeros(E)
+    b[5] = -float("inf")
+    b[7] = 40.0
+    say(f"masked rows {kind} renorm={renorm}")
+    r = moe.make_router(kind, renormalize=renorm)
+    s = moe.make_shape(T, 64, 64, E, k)
+    for bias in (None, b):
+        ids, w, sc = Out(T, k, dtype=torch.int32, fill=-77), Out(T, k), Out(T, E)
+        moe.moe_route_scored(s, r, cuda(x), cuda(bias), ids.t, w.t, sc.t)
+        torch.cuda.synchronize()
+        got, gw, gs = ids.np(), w.np(), sc.np()
+        want = ref.route_scored(f64(x), f64(bias), k, kind, renormalize=renorm)
+        # rows whose scores are distinct in fp64: the reference's ids; others: the lowest indices, distinct
+        for t in range(T):
+            assert len(set(got[t])) == k and got[t].min() >= 0 and got[t].max() < E
+        rows = [t for t in range(T) if bias is None or t not in (6, 7)]
+        assert np.array_equal(got[rows], want[0][rows])
+        # 90 + fp32 argument rounding of exp at arguments up to 200
+        close(gw[rows], want[1][rows], 256 * 2 * F32 * want[1][rows] + 1e-37, "weights")
+        close(gs[rows], want[2][rows], 256 * 2 * F32 * want[2][rows] + 1e-37, "scores")
+        assert (gw[0] == 0).all() and (gs[0] == 0).all()
+
+
+def test_route_nan_and_infinite_logits_still_give_distinct_ids():
+    T, E, k = 8, 40, 8
+    x = normal(gen(9), T, E)
+    x[0] = float("nan")
+    x[1, ::3] = float("nan")
+    x[2] = float("inf")
+    x[3, 4] = float("inf")
+    x[4, 5], x[4, 6] = float("nan"), -float("inf")
+    for kind in ("softmax", "sigmoid"):
+        for groups in ((1, 1, 1), (8, 4, 2)):
+            for bias in (None, torch.zeros(E)):
+                say(f"nan {kind} {groups} bias={bias is not None}")
+                ids, w = Out(T, k, dtype=torch.int32, fill=-77), Out(T, k)
+                moe.moe_route_scored(moe.make_shape(T, 64, 64, E, k), moe.make_router(kind, *groups), cuda(x),
+                                     cuda(bias), ids.t, w.t)
+                torch.cuda.synchronize()
+                got = ids.np()
+                for t in range(T):
+                    assert len(set(got[t])) == k and got[t].min() >= 0 and got[t].max() < E, (t, got[t])
+
+
+def test_route_rows_do_not_depend_on_the_batch():
+    x = normal(gen(10), 777, 256)
+    s, r = moe.make_shape, moe.make_router("sigmoid", 8, 4, 2, True, 2.5)
+    b = cuda(normal(gen(11), 256, std=0.05))
+    whole, ww = Out(777, 8, dtype=torch.int32, fill=-77), Out(777, 8)
+    moe.moe_route_scored(s(777, 64, 64, 256, 8), r, cuda(x), b, whole.t, ww.t)
+    part, pw = Out(5, 8, dtype=torch.int32, fill=-77), Out(5, 8)
+    moe.moe_route_scored(s(5, 64, 64, 256, 8), r, cuda(x[700:705].contiguous()), b, part.t, pw.t)
+    torch.cuda.synchronize()
+    assert np.array_equal(whole.np()[700:705], part.np()) and np.array_equal(ww.np()[700:705], pw.np())
+
+
+def route_backward_case(T, E, k, kind, renorm, dscores, scale=1.5, seed=0, logits=None):
+    say(f"route backward T={T} E={E} k={k} {kind} renorm={renorm} dscores={dscores}")
+    g = gen(seed)
+    x = normal(g, T, E) if logits is None else logits
+    ids = x.topk(k, 1).indices.to(torch.int32)
+    dw = normal(g, T, k)
+    D = normal(g, T, E) if dscores else None
+    out = Out(T, E)
+    moe.moe_route_scored_backward(moe.make_shape(T, 64, 64, E, k),
+                                  moe.make_router(kind, renormalize=renorm, scale=scale), cuda(x), cuda(ids),
+                                  cuda(dw), cuda(D), out.t)
+    torch.cuda.synchronize()
+    want = ref.route_scored_backward(f64(x), ids.numpy(), f64(dw), f64(D), kind, renorm, scale)
+    # each factor: some ten roundings, exp's argument (up to the logits' span in half steps), a sum of
+    # at most E terms below 1 in weight; the gradients' size bounds the terms
+    size = scale * np.abs(f64(dw)).max(1, keepdims=True) * (2 if renorm else 1)
+    size = size + (np.abs(f64(D)).max(1, keepdims=True) if dscores else 0)
+    span = np.ptp(np.where(np.isfinite(f64(x)), f64(x), 0.0), axis=1, keepdims=True) + 32
+    close(out.np(), want, span * 2 * F32 * 2 * size, "dlogits")
+    return out.np(), want
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 2, 1), (1, 8, 2), (5, 3, 3), (61, 60, 4), (65, 64, 8), (33, 65, 5),
+                                   (130, 129, 6), (257, 256, 8), (1021, 160, 7)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_backward(T, E, k, kind, renorm):
+    for dscores in (False, True):
+        route_backward_case(T, E, k, kind, renorm, dscores, seed=T + E)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_backward_of_masked_rows(kind, renorm):
+    x = normal(gen(20), 6, 32)
+    x[0, 4:] = -float("inf")
+    x[1] = -float("inf")
+    x[2] -= 200.0
+    x[3] += 60.0
+    x[4] = torch.finfo(torch.float32).min
+    for dscores in (False, True):
+        got, _ = route_backward_case(6, 32, 4, kind, renorm, dscores, logits=x, seed=21)
+        assert (got[1] == 0).all() and (got[0, 4:] == 0).all()
+
+
+def test_route_backward_of_equal_gate_gradients_is_zero():
+    """Renormalised weights sum to a constant: a gradient that is the same for all of them has no effect."""
+    x = cuda(normal(gen(22), 9, 64))
+    ids = x.topk(6, 1).indices.to(torch.int32).contiguous()
+    out = Out(9, 64)
+    for kind in ("softmax", "sigmoid"):
+        moe.moe_route_scored_backward(moe.make_shape(9, 64, 64, 64, 6), moe.make_router(kind), x, ids,
+                                      torch.full((9, 6), 1e4, device=DEV), None, out.t)
+        torch.cuda.synchronize()
+        assert (out.np() == 0).all()
+
+
+def test_route_backward_ignores_ids_outside_the_row():
+    x = normal(gen(23), 4, 16)
+    ids = x.topk(3, 1).indices.to(torch.int32)
+    bad = ids.clone()
+    bad[1, 2], bad[2, 0] = -1, 16
+    dw = normal(gen(24), 4, 3)
+    out = Out(4, 16)
+    moe.moe_route_scored_backward(moe.make_shape(4, 64, 64, 16, 3), moe.make_router("sigmoid", renormalize=False),
+                                  cuda(x), cuda(bad), cuda(dw), None, out.t)
+    torch.cuda.synchronize()
+    d2 = dw.clone()
+    d2[1, 2] = d2[2, 0] = 0
+    want = ref.route_scored_backward(f64(x), ids.numpy(), f64(d2), None, "sigmoid", False)
+    close(out.np(), want, 64 * F32 * 4, "dlogits")
+
+
+# ---- combine ----
+
+def rows_of(T, E, k, S, drop, seed):
+    g = gen(seed)
+    ids = torch.rand(T, E, generator=g).topk(k, 1).indices.flatten()
+    dropped = torch.rand(T * k, generator=g) < drop
+    order = torch.sort(torch.where(dropped, E, ids), stable=True).indices
+    row = torch.empty(T * k, dtype=torch.int64)
+    row[order] = torch.arange(T * k)
+    kept = int((~dropped).sum())
+    row[dropped] = -1
+    if S:
+        row = torch.cat((row, kept + torch.arange(T)))
+    return row.to(torch.int32), kept + S * T
+
+
+@pytest.mark.parametrize("T,d,k,S", [(1, 64, 1, 0), (1, 4096, 2, 0), (7, 128, 2, 1), (61, 4096, 2, 0),
+                                     (33, 2112, 8, 1), (5, 192, 3, 0), (9, 320, 4, 1), (6, 64, 5, 0), (6, 64, 6, 1),
+                                     (6, 576, 7, 0), (300, 1024, 8, 0), (16, 65536, 1, 1)])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("drop", [0.0, 0.4, 1.0])
+def test_combine_backward(T, d, k, S, act, drop):
+    say(f"combine backward T={T} d={d} k={k} S={S} {act} drop={drop}")
+    dt = torch.bfloat16 if act == "bf16" else torch.float32
+    g = gen(T + d)
+    s2r, used = rows_of(T, 16, k, S, drop, T + k)
+    R = T * (k + S)
+    y, dy, w = normal(g, R, d), normal(g, T, d, dtype=dt), torch.rand(T, k, generator=g)
+    y[used:] = float("nan")                                  # rows that no slot points to are not read
+    if used == 0:
+        y[0] = 1.0
+    shape = moe.make_shape(T, d, 64, 16, k, n_shared=S, act_dtype=act, w_dtype=act)
+    want_rows, want_dw = ref.combine_backward(f64(dy), f64(y), s2r.numpy(), f64(w), k, S)
+    for want_outputs in ((True, True), (True, False), (False, True)):
+        dyp, dw = Out(R, d, dtype=dt), Out(T, k)
+        moe.moe_combine_backward(shape, cuda(dy), cuda(y), cuda(s2r), cuda(w), dyp.t if want_outputs[0] else None,
+                                 dw.t if want_outputs[1] else None)
+        torch.cuda.synchronize()
+        got, gdw = dyp.np(), dw.np()
+        if want_outputs[0]:
+            want = np.full((R, d), -7.0)                     # other rows stay as they were
+            for r, v in want_rows.items():
+                want[r] = v
+            close(got, want, (BF16 + 2 * F32 if act == "bf16" else F32) * np.abs(want), "dy_perm")
+        else:
+            assert (got == -7.0).all()
+        if want_outputs[1]:
+            size = np.zeros((T, k))
+            for t in range(T):
+                for j in range(k):
+                    r = s2r[t * k + j]
+                    size[t, j] = (np.abs(f64(dy[t])) * np.abs(f64(y[r]))).sum() if r >= 0 else 0.0
+            close(gdw, want_dw, F32 * np.abs(want_dw) + d * 2.0 ** -52 * size, "dweights")
+        else:
+            assert (gdw == -7.0).all()
+
+
+# ---- dense product ----
+
+def linear_case(M, N, K, act="none", out="bf16", bias=True, residual=False, pre=False, seed=0, std=1.0):
+    say(f"linear M={M} N={N} K={K} {act} {out} bias={bias} residual={residual} pre={pre}")
+    g = gen(seed + M + N + K)
+    odt = torch.bfloat16 if out == "bf16" else torch.float32
+    x = normal(g, M, K, std=std, dtype=torch.bfloat16)
+    w = normal(g, N, K, std=K ** -0.5, dtype=torch.bfloat16)
+    b = normal(g, N) if bias else None
+    r = normal(g, M, N, dtype=odt) if residual else None
+    lin = moe.make_linear(M, N, K, y_dtype=out, act=act)
+    n = moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR)
+    ws = Out(n, dtype=torch.uint8, fill=77) if n else None
+    if ws:
+        ws.t.fill_(0xFF)                                     # NaN patterns: no content is counted on
+    y, p = Out(M, N, dtype=odt), Out(M, N, dtype=torch.bfloat16) if pre else None
+    moe.moe_linear(lin, cuda(x), cuda(w), cuda(b), cuda(r), y.t, p.t if p else None, ws.t if ws else None)
+    torch.cuda.synchronize()
+    wy, wp = ref.linear(f64(x), f64(w), f64(b), f64(r), act)
+    dot = (K + 4) * 2.0 ** -23 * (np.abs(f64(x)) @ np.abs(f64(w)).T + (np.abs(f64(b)) if bias else 0))
+    step = BF16 if out == "bf16" else 2 * F32
+    tol = 1.13 * dot + (2.0 ** -19 * (1 + np.abs(wp)) if act not in ("none", "relu") else 0) + step * np.abs(wy)
+    if residual:
+        tol = tol + 2 * F32 * np.abs(f64(r))
+    close(y.np(), wy, tol * (1 + BF16), "y")
+    if p:
+        close(p.np(), wp, (dot + BF16 * np.abs(wp)) * (1 + BF16), "pre")
+    if ws:
+        ws.np()                                              # nothing past the workspace
+    return y.t.clone()
+
+
+LINEARS = [(1, 8, 8), (1, 64, 64), (1, 4096, 1024), (2, 264, 136), (3, 8, 4096), (15, 200, 72), (16, 256, 4096),
+           (16, 1000, 264), (17, 72, 520), (31, 64, 2048), (33, 256, 256), (64, 128, 64), (65, 136, 200),
+           (100, 320, 1160), (127, 1024, 512), (128, 384, 96), (129, 640, 24), (255, 2048, 64), (256, 256, 2056),
+           (257, 264, 1032), (300, 8, 16), (509, 1024, 2048), (700, 3000, 128), (1025, 520, 392), (2049, 256, 512)]
+
+
+@pytest.mark.parametrize("dims", LINEARS)
+def test_linear(dims):
+    M, N, K = dims
+    linear_case(M, N, K, "none", "f32", bias=False)
+    linear_case(M, N, K, "silu", "bf16", bias=True, pre=True)
+    linear_case(M, N, K, "gelu_tanh", "bf16", bias=True, residual=True)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("dims", [(5, 72, 136), (300, 200, 264)])
+def test_linear_activations(act, out, dims):
+    linear_case(*dims, act, out, bias=True, residual=True, pre=True, std=3.0)
+    linear_case(*dims, act, out, bias=False, residual=False, pre=False, std=0.1)
+
+
+@pytest.mark.parametrize("dims", [(3, 256, 512), (300, 264, 520)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_residual_in_place(dims, out):
+    M, N, K = dims
+    odt = torch.bfloat16 if out == "bf16" else torch.float32
+    g = gen(40)
+    x, w = cuda(normal(g, M, K, dtype=torch.bfloat16)), cuda(normal(g, N, K, std=0.05, dtype=torch.bfloat16))
+    r = cuda(normal(g, M, N, dtype=odt))
+    lin = moe.make_linear(M, N, K, y_dtype=out, act="relu")
+    ws = runner._bytes(moe.moe_linear_workspace_bytes(lin), DEV)
+    y = torch.empty_like(r)
+    moe.moe_linear(lin, x, w, None, r, y, None, ws)
+    moe.moe_linear(lin, x, w, None, r, r, None, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(r, y)
+
+
+def test_linear_infinite_operand_stays_in_its_row():
+    """Rows and channels next to each other share loads, never values."""
+    for M, N, K in ((5, 72, 136), (70, 136, 264), (300, 264, 200)):
+        say(f"infinite row M={M} N={N} K={K}")
+        g = gen(41)
+        x, w = normal(g, M, K, dtype=torch.bfloat16), normal(g, N, K, std=0.1, dtype=torch.bfloat16)
+        clean = x.clone()
+        x[1] = float("inf")
+        lin = moe.make_linear(M, N, K, y_dtype="f32")
+        ws = runner._bytes(moe.moe_linear_workspace_bytes(lin), DEV)
+        a, b = Out(M, N), Out(M, N)
+        moe.moe_linear(lin, cuda(x), cuda(w), None, None, a.t, None, ws)
+        moe.moe_linear(lin, cuda(clean), cuda(w), None, None, b.t, None, ws)
+        torch.cuda.synchronize()
+        keep = [i for i in range(M) if i != 1]
+        assert torch.equal(a.t[keep], b.t[keep])
+        w[3] = float("nan")
+        moe.moe_linear(lin, cuda(clean), cuda(w), None, None, a.t, None, ws)
+        torch.cuda.synchronize()
+        keep = [i for i in range(N) if i != 3]
+        assert torch.equal(a.t[:, keep], b.t[:, keep]) and torch.isnan(a.t[:, 3]).all()
+
+
+def linear_backward_case(M, N, K, act="none", out="bf16", seed=0, outputs=(True, True, True), std=1.0):
+    say(f"linear backward M={M} N={N} K={K} {act} {out} outputs={outputs}")
+    g = gen(seed + M + N + K)
+    odt = torch.bfloat16 if out == "bf16" else torch.float32
+    dy, x = normal(g, M, N, dtype=odt), normal(g, M, K, dtype=torch.bfloat16)
+    w = normal(g, N, K, dtype=torch.bfloat16)
+    pre = normal(g, M, N, std=std, dtype=torch.bfloat16) if act != "none" else None
+    lin = moe.make_linear(M, N, K, y_dtype=out, act=act)
+    n = moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR_BACKWARD)
+    ws = Out(n, dtype=torch.uint8, fill=77) if n else None
+    if ws:
+        ws.t.fill_(0xFF)
+    dx, dw, db = Out(M, K, dtype=torch.bfloat16), Out(N, K, dtype=torch.bfloat16), Out(N)
+    moe.moe_linear_backward(lin, cuda(dy), cuda(pre), cuda(x) if outputs[1] else None,
+                            cuda(w) if outputs[0] else None, dx.t if outputs[0] else None,
+                            dw.t if outputs[1] else None, db.t if outputs[2] else None, ws.t if ws else None)
+    torch.cuda.synchronize()
+    wdx, wdw, wdb, d = ref.linear_backward(f64(dy), f64(pre), f64(x), f64(w), act)
+    # the derivative's error, and the rounding of dpre to the products' operand type
+    slope = np.abs(f64(dy)) * 2.0 ** -19 * (1 + np.abs(f64(pre))) if act not in ("none", "relu") else 0.0 * d
+    copied = act != "none" or out == "f32"
+    e = slope + (BF16 * np.abs(d) if copied else 0)
+    a = np.abs(d) + e
+    got = dx.np()
+    if outputs[0]:
+        aw = np.abs(f64(w))
+        tol = e @ aw + (N + 4) * 2.0 ** -23 * (a @ aw)
+        close(got, wdx, tol * (1 + BF16) + BF16 * np.abs(wdx), "dx")
+    else:
+        assert (got == -7.0).all()
+    got = dw.np()
+    if outputs[1]:
+        ax = np.abs(f64(x))
+        tol = e.T @ ax + (M + 4) * 2.0 ** -23 * (a.T @ ax)
+        close(got, wdw, tol * (1 + BF16) + BF16 * np.abs(wdw), "dw")
+    else:
+        assert (got == -7.0).all()
+    got = db.np()
+    if outputs[2]:
+        tol = slope.sum(0) + (M + 4) * F32 * np.abs(d).sum(0)
+        close(got, wdb, tol, "dbias")
+    else:
+        assert (got == -7.0).all()
+    if ws:
+        ws.np()
+
+
+@pytest.mark.parametrize("dims", LINEARS)
+def test_linear_backward(dims):
+    M, N, K = dims
+    linear_backward_case(M, N, K, "none", "f32")
+    linear_backward_case(M, N, K, "silu", "bf16")
+    linear_backward_case(M, N, K, "none", "bf16")
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_backward_activations(act, out):
+    linear_backward_case(37, 136, 72, act, out, std=3.0)
+    for outputs in ((True, False, False), (False, True, False), (False, False, True), (True, False, True)):
+        linear_backward_case(37, 136, 72, act, out, outputs=outputs)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_linear_of_large_pre_activations_is_finite(act):
+    """Pre-activations whose cube overflows fp32: slope 0 or 1, value 0 or p."""
+    M, N, K = 8, 64, 64
+    pre = torch.tensor([-3e38, -1e20, -3e4, -40.0, 40.0, 3e4, 1e20, 3e38]).view(8, 1).expand(8, N)
+    pre = pre.to(torch.bfloat16).contiguous()
+    dy = torch.ones(M, N, dtype=torch.bfloat16)
+    lin = moe.make_linear(M, N, K, act=act)
+    ws = runner._bytes(moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR_BACKWARD), DEV)
+    w = torch.eye(64, dtype=torch.bfloat16)
+    dx = Out(M, K, dtype=torch.bfloat16)
+    moe.moe_linear_backward(lin, cuda(dy), cuda(pre), None, cuda(w), dx.t, None, None, ws)
+    torch.cuda.synchronize()
+    want = np.zeros((M, K))
+    want[4:] = 1.0
+    close(dx.np(), want, 2.0 ** -40, "dx")
+
+
+def test_linear_backward_of_no_rows_is_zero():
+    lin = moe.make_linear(0, 72, 64)
+    dw, db = Out(72, 64, dtype=torch.bfloat16), Out(72)
+    e = torch.empty(0, device=DEV, dtype=torch.bfloat16)
+    moe.moe_linear_backward(lin, e, None, e, torch.zeros(72, 64, device=DEV, dtype=torch.bfloat16), e, dw.t, db.t)
+    torch.cuda.synchronize()
+    assert (dw.np() == 0).all() and (db.np() == 0).all()
+
+
+# ---- streams, graphs, calls side by side ----
+
+def _linear_setup(M, N, K, seed, act="gelu"):
+    g = gen(seed)
+    lin = moe.make_linear(M, N, K, act=act)
+    t = dict(x=cuda(normal(g, M, K, dtype=torch.bfloat16)), w=cuda(normal(g, N, K, std=0.05, dtype=torch.bfloat16)),
+             b=cuda(normal(g, N)), dy=cuda(normal(g, M, N, dtype=torch.bfloat16)))
+    e = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=DEV)    # noqa: E731
+    t.update(y=e(M, N), pre=e(M, N), dx=e(M, K), dw=e(N, K), db=e(N, dt=torch.float32),
+             ws=runner._bytes(moe.moe_linear_workspace_bytes(lin), DEV),
+             wsb=runner._bytes(moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR_BACKWARD), DEV))
+
+    def run(stream=None):
+        moe.moe_linear(lin, t["x"], t["w"], t["b"], None, t["y"], t["pre"], t["ws"], stream)
+        moe.moe_linear_backward(lin, t["dy"], t["pre"], t["x"], t["w"], t["dx"], t["dw"], t["db"], t["wsb"], stream)
+    return t, run
+
+
+OUTPUTS = ("y", "pre", "dx", "dw", "db")
+
+
+@pytest.mark.parametrize("dims", [(16, 512, 1024), (500, 768, 512)])
+def test_linear_captured_and_replayed(dims):
+    t, run = _linear_setup(*dims, seed=50)
+    run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run()
+    for i in range(3):
+        t["x"].normal_()
+        t["dy"].normal_()
+        run()
+        torch.cuda.synchronize()
+        want = [t[n].clone() for n in OUTPUTS]
+        for n in OUTPUTS:
+            t[n].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t[n], w) for n, w in zip(OUTPUTS, want)), f"replay {i}"
+
+
+def test_linear_on_two_streams_at_once():
+    a, run_a = _linear_setup(700, 1024, 512, seed=60)
+    b, run_b = _linear_setup(16, 2048, 1024, seed=61)
+    run_a()
+    run_b()
+    torch.cuda.synchronize()
+    want = [a[n].clone() for n in OUTPUTS] + [b[n].clone() for n in OUTPUTS]
+    for t in (a, b):
+        for n in OUTPUTS:
+            t[n].zero_()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        run_a(s1)
+        run_b(s2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip([a[n] for n in OUTPUTS] + [b[n] for n in OUTPUTS], want))
+
+
+# ---- together, as used ----
+
+def layer(T=96, E=32, k=4, shared=1, **kw):
+    cfg = synthetic.MoEConfig(name="scored", T=T, d_model=256, d_ff=192, n_experts=E, top_k=k, n_shared=shared,
+                              wg_std=256 ** -0.5, w13_std=0.05, w2_std=0.05, seed=11, **kw)
+    inp = synthetic.make_inputs(cfg)
+    inp.router_bias = normal(gen(70), E, std=0.3)
+    return cfg, inp, normal(gen(71), E, std=0.05)
+
+
+LAYERS = [dict(), dict(T=16, E=8, k=2, shared=0), dict(T=1, E=8, k=2, shared=0), dict(T=700, E=8, k=2, shared=0),
+          dict(capacity=9), dict(T=200, E=8, k=2, shared=0, capacity=30, overflow="next_best")]
+ROUTER = dict(score="sigmoid", n_groups=4, topk_groups=2, group_top=2, renormalize=True, scale=2.5)
+
+
+@pytest.mark.parametrize("kw", LAYERS)
+def test_scored_layer_and_its_gate_gradient(kw):
+    cfg, inp, balance = layer(**kw)
+    say(f"scored layer {kw}")
+    di = runner.DeviceInputs.from_host(inp)
+    router = moe.make_router(**ROUTER)
+    b = cuda(balance)
+    st = runner.staged(di, router=router, balance_bias=b)
+    buf = runner.forward(di, router=router, balance_bias=b)
+    torch.cuda.synchronize()
+    # one call and the staged calls agree bit for bit
+    assert torch.equal(buf.topk_ids, st["topk_ids"]) and torch.equal(buf.topk_weights, st["topk_weights"])
+    assert torch.equal(buf.y, st["y"]) and torch.equal(buf.drop_mask, st["drop_mask"])
+    assert torch.equal(buf.expert_counts, st["expert_counts"])
+    # the routing is the reference's on the very logits, and the logits are the product
+    T, E, k, S = cfg.T, cfg.n_experts, cfg.top_k, cfg.n_shared
+    args = (ROUTER["score"], ROUTER["n_groups"], ROUTER["topk_groups"], ROUTER["group_top"], True, ROUTER["scale"])
+    logits = f64(st["logits"])
+    ids, w, s, nxt = ref.route_scored(logits, f64(balance), k, *args)
+    assert np.array_equal(f64(st["topk_ids"]), ids) and np.array_equal(f64(st["next_ids"]), nxt)
+    wl = f64(inp.x) @ f64(inp.w_gate).T + f64(inp.router_bias)
+    close(logits, wl, 260 * 2.0 ** -23 * (np.abs(f64(inp.x)) @ np.abs(f64(inp.w_gate)).T + 2), "logits")
+    # y from the experts' rows
+    rows, y_perm, s2r = st["slot_to_row"].cpu().numpy(), f64(st["y_perm"]), st["slot_to_row"].cpu().numpy()
+    want = np.zeros((T, cfg.d_model))
+    size = np.zeros_like(want)
+    for t in range(T):
+        for j in range(k):
+            if rows[t * k + j] >= 0:
+                want[t] += w[t, j] * y_perm[rows[t * k + j]]
+                size[t] += np.abs(w[t, j] * y_perm[rows[t * k + j]])
+        if S:
+            want[t] += y_perm[rows[T * k + t]]
+    close(f64(st["y"]), want, BF16 * np.abs(want) + 128 * F32 * (size + np.abs(want)), "y")
+    # and the gradient of <dy, y> + <D, scores> back to x and the router's weights
+    dy, D = normal(gen(72), T, cfg.d_model, dtype=torch.bfloat16), normal(gen(73), T, E, std=0.1)
+    g = runner.gate_backward(di, st, router, cuda(dy), cuda(D))
+    torch.cuda.synchronize()
+    want_rows, want_dw = ref.combine_backward(f64(dy), y_perm, s2r, w, k, S)
+    wsize = np.array([[np.abs(f64(dy[t]) * y_perm[max(rows[t * k + j], 0)]).sum() for j in range(k)] for t in range(T)])
+    close(f64(g["dweights"]), want_dw, F32 * np.abs(want_dw) + 1e-12 * wsize, "dweights")
+    for r, v in want_rows.items():
+        close(f64(g["dy_perm"][r]), v, BF16 * np.abs(v) + 128 * F32 * np.abs(v), "dy_perm")
+    dl = ref.route_scored_backward(logits, ids, want_dw, f64(D), "sigmoid", True, ROUTER["scale"])
+    mag = ROUTER["scale"] * 2 * np.abs(want_dw).max(1, keepdims=True) + np.abs(f64(D)).max(1, keepdims=True)
+    e_dl = 64 * F32 * mag
+    close(f64(g["dlogits"]), dl, e_dl, "dlogits")
+    wdx, wdw, wdb, _ = ref.linear_backward(dl, None, f64(inp.x), f64(inp.w_gate), "none")
+    e = e_dl + BF16 * np.abs(dl) + 0 * dl
+    a = np.abs(dl) + e
+    tol = e @ np.abs(f64(inp.w_gate)) + (E + 4) * 2.0 ** -23 * (a @ np.abs(f64(inp.w_gate)))
+    close(f64(g["dx"]), wdx, tol * (1 + BF16) + BF16 * np.abs(wdx), "dx")
+    tol = e.T @ np.abs(f64(inp.x)) + (T + 4) * 2.0 ** -23 * (a.T @ np.abs(f64(inp.x)))
+    close(f64(g["dw_gate"]), wdw, tol * (1 + BF16) + BF16 * np.abs(wdw), "dw_gate")
+    close(f64(g["dbias"]), wdb, e_dl.sum(0) + (T + 4) * F32 * a.sum(0), "dbias")
+
+
+def test_gate_gradient_is_the_difference_quotient():
+    """d<dy, y> / d logit from the GPU's gradients against differences of the fp64 combine of the
+    same experts' rows."""
+    cfg, inp, balance = layer(T=5, E=8, k=3, shared=0)
+    di = runner.DeviceInputs.from_host(inp)
+    for score, renorm in (("sigmoid", True), ("softmax", True), ("softmax", False), ("sigmoid", False)):
+        router = moe.make_router(score, renormalize=renorm, scale=1.5)
+        st = runner.staged(di, router=router, balance_bias=cuda(balance))
+        dy = normal(gen(80), 5, cfg.d_model, dtype=torch.bfloat16)
+        g = runner.gate_backward(di, st, router, cuda(dy))
+        torch.cuda.synchronize()
+        x, ids, rows = f64(st["logits"]), st["topk_ids"].cpu().numpy(), st["slot_to_row"].cpu().numpy()
+        dots = np.array([[f64(dy[t]) @ f64(st["y_perm"][rows[t * 3 + j]]) for j in range(3)] for t in range(5)])
+
+        def loss(z):
+            s = np.take_along_axis(ref.scores(z, score), ids, 1)
+            return float((dots * 1.5 * (s / s.sum(1, keepdims=True) if renorm else s)).sum())
+
+        h = 1e-6
+        got = f64(g["dlogits"])
+        for t, e in np.ndindex(5, 8):
+            p, m = x.copy(), x.copy()
+            p[t, e] += h
+            m[t, e] -= h
+            q = (loss(p) - loss(m)) / (2 * h)
+            assert abs(q - got[t, e]) <= 1e-6 * (1 + np.abs(dots).max()), (score, renorm, t, e)
+
+
+@pytest.mark.parametrize("fmt", ["fp8_e4m3", "mxfp4"])
+def test_routed_layer_with_quantised_experts(fmt):
+    cfg = synthetic.MoEConfig(name="scored_q", T=40, d_model=256, d_ff=256, n_experts=8, wg_std=1 / 16,
+                              w13_std=0.05, w2_std=0.05, w_dtype=fmt, seed=12)
+    di = runner.DeviceInputs.from_host(synthetic.make_inputs(cfg))
+    router = moe.make_router("softmax")
+    st = runner.staged(di, router=router)
+    buf = runner.forward(di, router=router)
+    torch.cuda.synchronize()
+    assert torch.equal(buf.y, st["y"])
+    # softmax of the kept logits is the library's own router: the same layer either way
+    own = runner.staged(di)
+    torch.cuda.synchronize()
+    if torch.equal(own["topk_ids"], st["topk_ids"]):
+        # the gate weights differ by their roundings only, y by those and its own rounding
+        a, b = f64(own["y"]), f64(st["y"])
+        assert np.abs(a - b).max() <= 2.0 ** -7 * np.abs(a).max()
+
+
+def test_scored_layer_captured_and_replayed():
+    cfg, inp, balance = layer(T=16, E=8, k=2, shared=0)
+    di = runner.DeviceInputs.from_host(inp)
+    router, b = moe.make_router(**ROUTER), cuda(balance)
+    buf = runner.alloc_forward(cfg, DEV)
+    T, E, k = cfg.T, cfg.n_experts, cfg.top_k
+    r = {"topk_ids": buf.topk_ids, "topk_weights": buf.topk_weights, "logits": buf.logits,
+         "next_ids": torch.empty(T, 2, dtype=torch.int32, device=DEV), "scores": None}
+    dw, dl = torch.randn(T, k, device=DEV), torch.empty(T, E, device=DEV)
+    shape = moe.shape_of(cfg)
+
+    def run():
+        runner.scored_routing(di, router, b, None, r)
+        moe.moe_forward_routed(shape, di.x, r["topk_ids"], r["topk_weights"], None, di.w1, di.w3, di.w2, None, None,
+                               None, buf.y, buf.expert_counts, buf.drop_mask, buf.workspace)
+        moe.moe_route_scored_backward(shape, router, r["logits"], r["topk_ids"], dw, None, dl)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i in range(3):
+        di.x.normal_()
+        run()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (buf.y, r["topk_ids"], r["topk_weights"], dl)]
+        for t in (buf.y, r["topk_ids"], r["topk_weights"], dl):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((buf.y, r["topk_ids"], r["topk_weights"], dl), want)), i
