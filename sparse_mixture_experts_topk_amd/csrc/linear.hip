@@ -10,74 +10,77 @@
 // All three products are out[r][c] = sum_t P(r, t) Q(c, t); an operand is
 // stored with its contraction index contiguous ([r][t]) or as the slow index
 // ([t][r], dx: Q = w; dw: P = dpre, Q = x).
+#include <algorithm>
+
 #include "device_common.hpp"
 #include "launch.hpp"
-#include "linear_epilogue.hpp"
+#include "linear_tiles.hpp"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kStep = 32, kPad = 8;
+// Tile shapes.
+struct Big { static constexpr int NS = 2, WR = 2, WC = 4, WA = 4, WB = 2; };     // 256 x 256
+struct Mid { static constexpr int NS = 5, WR = 2, WC = 2, WA = 2, WB = 2; };     // 128 x 128
+template <class C> using GeomOf = ProductGeom<64, C::NS, C::WR, C::WC, C::WA, C::WB>;
 
-// One operand's tile slice (64 rows x 32 of the contraction) into LDS [row][t].
-template <bool SLOW>
-__device__ __forceinline__ void load_slice(const uint16_t* __restrict__ p, int64_t ld, int r0, int rows, int t0,
-                                           int len, uint16_t (*lds)[kStep + kPad]) {
-  const int i = threadIdx.x;
-  if constexpr (!SLOW) {
-    const int r = i >> 2, t = t0 + (i & 3) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r0 + r < rows && t < len) v = *reinterpret_cast<const uint4*>(p + (int64_t)(r0 + r) * ld + t);
-    *reinterpret_cast<uint4*>(&lds[r][(i & 3) * 8]) = v;
-  } else {
-    const int t = i >> 3, r = (i & 7) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (t0 + t < len && r0 + r < rows) v = *reinterpret_cast<const uint4*>(p + (int64_t)(t0 + t) * ld + r0 + r);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int q = 0; q < 8; ++q) lds[r + q][t] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
-  }
-}
-
-template <bool PSLOW, bool QSLOW>
-__global__ __launch_bounds__(256) void linear_tile_kernel(const uint16_t* __restrict__ P, int64_t ldp,
-                                                          const uint16_t* __restrict__ Q, int64_t ldq, int rows,
-                                                          int cols, int len, int col_tiles, const Epilogue ep) {
-  __shared__ __attribute__((aligned(16))) uint16_t ps[kTile][kStep + kPad];
-  __shared__ __attribute__((aligned(16))) uint16_t qs[kTile][kStep + kPad];
-  const int r0 = (blockIdx.x / col_tiles) * kTile, c0 = (blockIdx.x % col_tiles) * kTile;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int fi = lane & 31, fg = lane >> 5;
-  const int wr = (wave >> 1) * 32, wc = (wave & 1) * 32;
-  f32x16_t acc = {};
-  for (int t = 0; t < len; t += kStep) {
-    load_slice<PSLOW>(P, ldp, r0, rows, t, len, ps);
-    load_slice<QSLOW>(Q, ldq, c0, cols, t, len, qs);
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < kStep / 16; ++s) {
-      const uint4 a = *reinterpret_cast<const uint4*>(&qs[wc + fi][s * 16 + fg * 8]);
-      const uint4 b = *reinterpret_cast<const uint4*>(&ps[wr + fi][s * 16 + fg * 8]);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(b), acc, 0, 0, 0);
+// Workgroups: one per CU at most, a multiple of the 8 XCDs, and no more than
+// give each at least kMinSlices slices of work.
+constexpr int kMinSlices = 4;
+template <class C>
+struct Plan {
+  int row_tiles, col_tiles, KT, grid;
+  bool split;
+  static Plan of(int rows, int cols, int len) {
+    using G = GeomOf<C>;
+    Plan p;
+    p.row_tiles = (rows + G::TB - 1) / G::TB;
+    p.col_tiles = (cols + G::TA - 1) / G::TA;
+    p.KT = (len + 63) / 64;
+    const int64_t work = (int64_t)p.row_tiles * p.col_tiles * p.KT;
+    const int64_t cus = std::min<int64_t>(device_cu_count(), kMaxPersistentGroups) / 8 * 8;
+    p.grid = (int)std::max<int64_t>(8, std::min<int64_t>(cus, work / kMinSlices / 8 * 8));
+    p.split = false;
+    for (int x = 0; x < 8; ++x) {
+      const TileSplit s = TileSplit::of(p.row_tiles * p.col_tiles, x, p.grid / 8, p.KT);
+      p.split |= s.tail > 0 && !s.whole_tail;
     }
-    __syncthreads();
+    return p;
   }
-  const int r = r0 + wr + fi;
-  if (r >= rows) return;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int c = c0 + wc + q * 8 + fg * 4;
-    if (c < cols) ep.store4(r, c, cols, make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]));
-  }
+  size_t workspace() const { return split ? (size_t)grid * 2 * GeomOf<C>::PARTIAL * 4 : 0; }
+};
+
+template <bool PSLOW, bool QSLOW, int ACT, class C>
+hipError_t launch_cfg(ProductArgs a, hipStream_t st) {
+  using G = GeomOf<C>;
+  const Plan<C> p = Plan<C>::of(a.rows, a.cols, a.len);
+  a.row_tiles = p.row_tiles;
+  a.col_tiles = p.col_tiles;
+  hipLaunchKernelGGL((linear_product_kernel<PSLOW, QSLOW, ACT, 64, C::NS, C::WR, C::WC, C::WA, C::WB>),
+                     dim3((unsigned)p.grid), dim3(G::THREADS), 0, st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !p.split) return e;
+  hipLaunchKernelGGL((linear_join_kernel<ACT, G::TA, G::TB>), dim3((unsigned)(p.grid * (G::TB / 32))), dim3(256), 0,
+                     st, a, p.grid / 8, p.KT);
+  return hipGetLastError();
 }
 
-template <bool PSLOW, bool QSLOW>
+bool use_big(int rows, int cols, int len) {
+  (void)len;
+  return (int64_t)((rows + 255) / 256) * ((cols + 255) / 256) >= 192;
+}
+
+size_t product_workspace(int rows, int cols, int len) {
+  return use_big(rows, cols, len) ? Plan<Big>::of(rows, cols, len).workspace()
+                                  : Plan<Mid>::of(rows, cols, len).workspace();
+}
+
+template <bool PSLOW, bool QSLOW, int ACT>
 hipError_t launch_product(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, int rows, int cols,
-                          int len, const Epilogue& ep, hipStream_t st) {
-  const int rt = (rows + kTile - 1) / kTile, ct = (cols + kTile - 1) / kTile;
-  hipLaunchKernelGGL((linear_tile_kernel<PSLOW, QSLOW>), dim3((unsigned)((int64_t)rt * ct)), dim3(256), 0, st, P,
-                     ldp, Q, ldq, rows, cols, len, ct, ep);
-  return hipGetLastError();
+                          int len, void* partials, const Epilogue& ep, hipStream_t st) {
+  ProductArgs a{P, Q, ldp, ldq, rows, cols, len, 0, 0, static_cast<float*>(partials), ep};
+  if (use_big(rows, cols, len)) return launch_cfg<PSLOW, QSLOW, ACT, Big>(a, st);
+  return launch_cfg<PSLOW, QSLOW, ACT, Mid>(a, st);
 }
 
 // ---- gradient at the pre-activation ----
@@ -150,19 +153,31 @@ bool dpre_copied(const moe_linear_t& l) { return l.act != MOE_ACT_NONE || l.y_dt
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 size_t dpre_bytes(const moe_linear_t& l) { return dpre_copied(l) ? round256((size_t)l.M * l.N * 2) : 0; }
 
+size_t part_bytes(const moe_linear_t& l) { return round256((size_t)prep_chunks(l) * l.N * 4); }
+
 }  // namespace
 
-size_t linear_workspace_bytes(const moe_linear_t&) { return 0; }
+size_t linear_workspace_bytes(const moe_linear_t& l) { return l.M == 0 ? 0 : product_workspace(l.M, l.N, l.K); }
 
 size_t linear_backward_workspace_bytes(const moe_linear_t& l) {
-  return dpre_bytes(l) + round256((size_t)prep_chunks(l) * l.N * 4);
+  if (l.M == 0) return 0;
+  return dpre_bytes(l) + part_bytes(l) +
+         std::max(product_workspace(l.M, l.K, l.N), product_workspace(l.N, l.K, l.M));
 }
 
 hipError_t launch_linear(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const float* bias,
                          const void* residual, void* y, uint16_t* pre, void* workspace, hipStream_t st) {
-  (void)workspace;
-  const Epilogue ep{bias, residual, y, pre, l.act, l.y_dtype == MOE_F32};
-  return launch_product<false, false>(x, l.K, w, l.K, l.M, l.N, l.K, ep, st);
+  const Epilogue ep{bias, residual, y, pre, l.y_dtype == MOE_F32};
+  auto run = [&](auto act) {
+    return launch_product<false, false, decltype(act)::value>(x, l.K, w, l.K, l.M, l.N, l.K, workspace, ep, st);
+  };
+  switch (l.act) {
+    case MOE_ACT_RELU: return run(std::integral_constant<int, MOE_ACT_RELU>{});
+    case MOE_ACT_SILU: return run(std::integral_constant<int, MOE_ACT_SILU>{});
+    case MOE_ACT_GELU: return run(std::integral_constant<int, MOE_ACT_GELU>{});
+    case MOE_ACT_GELU_TANH: return run(std::integral_constant<int, MOE_ACT_GELU_TANH>{});
+    default: return run(std::integral_constant<int, MOE_ACT_NONE>{});
+  }
 }
 
 hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const uint16_t* pre, const uint16_t* x,
@@ -187,10 +202,13 @@ hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const u
     e = hipGetLastError();
   }
   const uint16_t* d = copy != nullptr ? copy : static_cast<const uint16_t*>(dy);
+  void* partials = static_cast<uint8_t*>(workspace) + dpre_bytes(l) + part_bytes(l);
   if (e == hipSuccess && dx != nullptr)
-    e = launch_product<false, true>(d, l.N, w, l.K, l.M, l.K, l.N, Epilogue{nullptr, nullptr, dx, nullptr, 0, false}, st);
+    e = launch_product<false, true, MOE_ACT_NONE>(d, l.N, w, l.K, l.M, l.K, l.N, partials,
+                                                  Epilogue{nullptr, nullptr, dx, nullptr, false}, st);
   if (e == hipSuccess && dw != nullptr)
-    e = launch_product<true, true>(d, l.N, x, l.K, l.N, l.K, l.M, Epilogue{nullptr, nullptr, dw, nullptr, 0, false}, st);
+    e = launch_product<true, true, MOE_ACT_NONE>(d, l.N, x, l.K, l.N, l.K, l.M, partials,
+                                                 Epilogue{nullptr, nullptr, dw, nullptr, false}, st);
   return e;
 }
 

@@ -13,14 +13,13 @@ __device__ __forceinline__ float fast_sigmoid(float v) { return __builtin_amdgcn
 constexpr float kGeluA = 1.5957691216057308f;    // 2 sqrt(2 / pi): 0.5 (1 + tanh(u)) = sigmoid(2 u)
 constexpr float kGeluB = 0.044715f;
 
-__device__ __forceinline__ float act_value(float p, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return fmaxf(p, 0.0f);
-    case MOE_ACT_SILU: return p * fast_sigmoid(p);
-    case MOE_ACT_GELU: return 0.5f * p * erfcf(p * -0.7071067811865476f);   // erfc: exact in the left tail
-    case MOE_ACT_GELU_TANH: return p * fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));
-    default: return p;
-  }
+template <int ACT>
+__device__ __forceinline__ float act_value(float p) {
+  if constexpr (ACT == MOE_ACT_RELU) return fmaxf(p, 0.0f);
+  else if constexpr (ACT == MOE_ACT_SILU) return p * fast_sigmoid(p);
+  else if constexpr (ACT == MOE_ACT_GELU) return 0.5f * p * erfcf(p * -0.7071067811865476f);   // erfc: exact in the left tail
+  else if constexpr (ACT == MOE_ACT_GELU_TANH) return p * fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));
+  else return p;
 }
 
 __device__ __forceinline__ float act_grad(float p, int act) {
@@ -59,9 +58,9 @@ struct Epilogue {
   const void* residual;
   void* y;
   uint16_t* pre;
-  int act;
   bool f32;      // y and residual
 
+  template <int ACT>
   __device__ __forceinline__ void store4(int r, int c, int cols, float4 v) const {
     const int64_t at = (int64_t)r * cols + c;
     if (bias != nullptr) {
@@ -69,10 +68,8 @@ struct Epilogue {
       v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
     }
     if (pre != nullptr) *reinterpret_cast<uint2*>(pre + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    if (act != MOE_ACT_NONE) {
-      v.x = act_value(v.x, act); v.y = act_value(v.y, act);
-      v.z = act_value(v.z, act); v.w = act_value(v.w, act);
-    }
+    v.x = act_value<ACT>(v.x); v.y = act_value<ACT>(v.y);
+    v.z = act_value<ACT>(v.z); v.w = act_value<ACT>(v.w);
     if (f32) {
       if (residual != nullptr) {
         const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(residual) + at);
