@@ -20,9 +20,9 @@ namespace moe {
 namespace {
 
 // Tile shapes.
-struct Big { static constexpr int NS = 2, WR = 2, WC = 4, WA = 4, WB = 2; };     // 256 x 256
-struct Mid { static constexpr int NS = 5, WR = 2, WC = 2, WA = 2, WB = 2; };     // 128 x 128
-template <class C> using GeomOf = ProductGeom<64, C::NS, C::WR, C::WC, C::WA, C::WB>;
+struct Big { static constexpr int NS = 2, WR = 4, WC = 2, WA = 4, WB = 8; };     // 256 x 256, 8 wavefronts
+struct Mid { static constexpr int NS = 4, WR = 2, WC = 2, WA = 4, WB = 4; };     // 128 x 128, 4 wavefronts
+template <class C> using GeomOf = ProductGeom<C::NS, C::WR, C::WC, C::WA, C::WB>;
 
 // Workgroups: one per CU at most, a multiple of the 8 XCDs, and no more than
 // give each at least kMinSlices slices of work.
@@ -56,7 +56,7 @@ hipError_t launch_cfg(ProductArgs a, hipStream_t st) {
   const Plan<C> p = Plan<C>::of(a.rows, a.cols, a.len);
   a.row_tiles = p.row_tiles;
   a.col_tiles = p.col_tiles;
-  hipLaunchKernelGGL((linear_product_kernel<PSLOW, QSLOW, ACT, 64, C::NS, C::WR, C::WC, C::WA, C::WB>),
+  hipLaunchKernelGGL((linear_product_kernel<PSLOW, QSLOW, ACT, C::NS, C::WR, C::WC, C::WA, C::WB>),
                      dim3((unsigned)p.grid), dim3(G::THREADS), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.split) return e;

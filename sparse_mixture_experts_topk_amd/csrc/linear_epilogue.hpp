@@ -51,8 +51,17 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 
-// y = act(acc + bias) + residual, 4 channels of one row at a time (channel
-// counts are multiples of 8, so a group of 4 is in or out as a whole).
+__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8f(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// y = act(acc + bias) + residual, 8 channels of one row at a time (channel
+// counts are multiples of 8, so a group of 8 is in or out as a whole).
 struct Epilogue {
   const float* bias;
   const void* residual;
@@ -61,29 +70,25 @@ struct Epilogue {
   bool f32;      // y and residual
 
   template <int ACT>
-  __device__ __forceinline__ void store4(int r, int c, int cols, float4 v) const {
+  __device__ __forceinline__ void store8(int r, int c, int cols, float (&v)[8]) const {
     const int64_t at = (int64_t)r * cols + c;
+    float u[8];
     if (bias != nullptr) {
-      const float4 b = *reinterpret_cast<const float4*>(bias + c);
-      v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
+      load8f(bias + c, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += u[i];
     }
-    if (pre != nullptr) *reinterpret_cast<uint2*>(pre + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    v.x = act_value<ACT>(v.x); v.y = act_value<ACT>(v.y);
-    v.z = act_value<ACT>(v.z); v.w = act_value<ACT>(v.w);
-    if (f32) {
-      if (residual != nullptr) {
-        const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(residual) + at);
-        v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
-      }
-      *reinterpret_cast<float4*>(static_cast<float*>(y) + at) = v;
-    } else {
-      if (residual != nullptr) {
-        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(residual) + at);
-        v.x += bf16_lo(q.x); v.y += bf16_hi(q.x); v.z += bf16_lo(q.y); v.w += bf16_hi(q.y);
-      }
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) =
-          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    if (pre != nullptr) *reinterpret_cast<uint4*>(pre + at) = pack8(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_value<ACT>(v[i]);
+    if (residual != nullptr) {
+      if (f32) load8f(static_cast<const float*>(residual) + at, u);
+      else unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(residual) + at), u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += u[i];
     }
+    if (f32) store8f(static_cast<float*>(y) + at, v);
+    else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) = pack8(v);
   }
 };
 
