@@ -168,46 +168,55 @@ def moe_forward_noalloc(shape, x, w_gate, router_bias, w1, w3, w2, w1_scale, w3_
 _TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
 
 
-class _Args:
-    """Pointers of one call's tensors, checked against the descriptor: element type, at least so
-    many elements, contiguous, all on one device.  The call runs on that device's current stream
-    unless it is given one."""
-
-    def __init__(self, fn: str):
-        self.fn, self.device = fn, None
-
-    def __call__(self, name: str, t, dtype, numel: int):
-        if t is None:
-            return None
-        if not isinstance(t, torch.Tensor):
-            return int(t)
-        if not t.is_cuda:
-            raise ValueError(f"{self.fn}: {name} must live in device memory")
-        if dtype is not None and t.dtype is not dtype:
-            raise ValueError(f"{self.fn}: {name} must be {dtype}, got {t.dtype}")
-        if t.numel() < numel:
-            raise ValueError(f"{self.fn}: {name} needs {numel} elements, got {t.numel()}")
-        if not t.is_contiguous():
-            raise ValueError(f"{self.fn}: {name} must be contiguous (row-major)")
-        d = t.get_device()
-        if self.device is None:
-            self.device = d
-        elif self.device != d:
-            raise ValueError(f"{self.fn}: {name} is on another device than the other tensors")
+def _ptr(fn: str, name: str, t, dtype, numel: int, dev: Optional[int]):
+    """Address of one of a call's tensors, checked against the descriptor: element type, at least
+    `numel` elements, contiguous, on device `dev` (a raw address passes unchecked)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        return int(t)
+    if (t.get_device() == dev and (t.dtype is dtype or dtype is None) and t.numel() >= numel
+            and t.is_contiguous()):
         return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must live in device memory")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{fn}: {name} needs {numel} elements, got {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous (row-major)")
+    raise ValueError(f"{fn}: {name} is on device {t.get_device()}, another tensor on device {dev}")
 
-    def workspace(self, t):
-        """(pointer, bytes) of a workspace tensor or None."""
-        if t is None:
-            return None, 0
-        return self("workspace", t, None, 0), t.numel() * t.element_size()
 
-    def run(self, call, stream):
-        if self.device is None or self.device == torch.cuda.current_device():
-            _check(self.fn, call(_stream(stream)))
-            return
-        with torch.cuda.device(self.device):      # the launches go to the tensors' device
-            _check(self.fn, call(_stream(stream)))
+def _device(*tensors) -> Optional[int]:
+    """Index of the device of the first device tensor (None: raw addresses only)."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            return t.get_device()
+    return None
+
+
+def _workspace(fn: str, t, dev):
+    """(address, bytes) of a workspace tensor or None."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{fn}: the workspace must be a tensor (its size is passed on)")
+    return _ptr(fn, "workspace", t, None, 0, dev), t.numel() * t.element_size()
+
+
+def _run(fn: str, dev: Optional[int], stream, *args):
+    """The C call on `stream`, or on the current stream of the tensors' device; its launches go to that device."""
+    f = getattr(_lib.load(), fn)
+    if dev is None:
+        _check(fn, f(*args, _stream(stream)))
+    elif dev == torch.cuda.current_device():
+        st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+        _check(fn, f(*args, st))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, f(*args, _stream(stream)))
 
 
 def make_router(score="softmax", n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
@@ -227,78 +236,73 @@ def moe_linear_workspace_bytes(linear: MoeLinear, call: int = MOE_CALL_LINEAR) -
 
 
 def moe_linear(linear, x, w, bias, residual, y, pre=None, workspace=None, stream=None):
-    a = _Args("moe_linear")
+    fn = "moe_linear"
     M, N, K = linear.M, linear.N, linear.K
-    dt, ydt = _TORCH.get(linear.dtype), _TORCH.get(linear.y_dtype)
-    p = (a("x", x, dt, M * K), a("w", w, dt, N * K), a("bias", bias, torch.float32, N),
-         a("residual", residual, ydt, M * N), a("y", y, ydt, M * N), a("pre", pre, dt, M * N),
-         *a.workspace(workspace))
-    a.run(lambda st: _lib.load().moe_linear(ctypes.byref(linear), *p, st), stream)
+    dt, ydt, d = _TORCH.get(linear.dtype), _TORCH.get(linear.y_dtype), _device(x, w, y)
+    _run(fn, d, stream, ctypes.byref(linear), _ptr(fn, "x", x, dt, M * K, d), _ptr(fn, "w", w, dt, N * K, d),
+         _ptr(fn, "bias", bias, torch.float32, N, d), _ptr(fn, "residual", residual, ydt, M * N, d),
+         _ptr(fn, "y", y, ydt, M * N, d), _ptr(fn, "pre", pre, dt, M * N, d), *_workspace(fn, workspace, d))
 
 
 def moe_linear_backward(linear, dy, pre, x, w, dx, dw, dbias, workspace=None, stream=None):
-    a = _Args("moe_linear_backward")
+    fn = "moe_linear_backward"
     M, N, K = linear.M, linear.N, linear.K
-    dt, ydt = _TORCH.get(linear.dtype), _TORCH.get(linear.y_dtype)
-    p = (a("dy", dy, ydt, M * N), a("pre", pre, dt, M * N), a("x", x, dt, M * K),
-         a("w", w, dt, N * K), a("dx", dx, dt, M * K), a("dw", dw, dt, N * K),
-         a("dbias", dbias, torch.float32, N), *a.workspace(workspace))
-    a.run(lambda st: _lib.load().moe_linear_backward(ctypes.byref(linear), *p, st), stream)
+    dt, ydt, d = _TORCH.get(linear.dtype), _TORCH.get(linear.y_dtype), _device(dy, x, w, dx, dw, dbias)
+    _run(fn, d, stream, ctypes.byref(linear), _ptr(fn, "dy", dy, ydt, M * N, d),
+         _ptr(fn, "pre", pre, dt, M * N, d), _ptr(fn, "x", x, dt, M * K, d), _ptr(fn, "w", w, dt, N * K, d),
+         _ptr(fn, "dx", dx, dt, M * K, d), _ptr(fn, "dw", dw, dt, N * K, d),
+         _ptr(fn, "dbias", dbias, torch.float32, N, d), *_workspace(fn, workspace, d))
 
 
 def moe_route_scored(shape, router, logits, balance_bias, topk_ids, topk_weights, scores=None,
                      next_ids=None, stream=None):
-    a = _Args("moe_route_scored")
+    fn = "moe_route_scored"
     T, E, k = shape.T, shape.n_experts, shape.top_k
-    f32, i32 = torch.float32, torch.int32
-    p = (a("logits", logits, f32, T * E), a("balance_bias", balance_bias, f32, E),
-         a("topk_ids", topk_ids, i32, T * k), a("topk_weights", topk_weights, f32, T * k),
-         a("scores", scores, f32, T * E), a("next_ids", next_ids, i32, T * 2))
-    a.run(lambda st: _lib.load().moe_route_scored(ctypes.byref(shape), ctypes.byref(router), *p, st), stream)
+    f32, i32, d = torch.float32, torch.int32, _device(logits, topk_ids, topk_weights)
+    _run(fn, d, stream, ctypes.byref(shape), ctypes.byref(router), _ptr(fn, "logits", logits, f32, T * E, d),
+         _ptr(fn, "balance_bias", balance_bias, f32, E, d), _ptr(fn, "topk_ids", topk_ids, i32, T * k, d),
+         _ptr(fn, "topk_weights", topk_weights, f32, T * k, d), _ptr(fn, "scores", scores, f32, T * E, d),
+         _ptr(fn, "next_ids", next_ids, i32, T * 2, d))
 
 
 def moe_route_scored_backward(shape, router, logits, topk_ids, dweights, dscores, dlogits, stream=None):
-    a = _Args("moe_route_scored_backward")
+    fn = "moe_route_scored_backward"
     T, E, k = shape.T, shape.n_experts, shape.top_k
-    f32 = torch.float32
-    p = (a("logits", logits, f32, T * E), a("topk_ids", topk_ids, torch.int32, T * k),
-         a("dweights", dweights, f32, T * k), a("dscores", dscores, f32, T * E),
-         a("dlogits", dlogits, f32, T * E))
-    a.run(lambda st: _lib.load().moe_route_scored_backward(ctypes.byref(shape), ctypes.byref(router), *p, st),
-          stream)
+    f32, d = torch.float32, _device(logits, dweights, dlogits)
+    _run(fn, d, stream, ctypes.byref(shape), ctypes.byref(router), _ptr(fn, "logits", logits, f32, T * E, d),
+         _ptr(fn, "topk_ids", topk_ids, torch.int32, T * k, d), _ptr(fn, "dweights", dweights, f32, T * k, d),
+         _ptr(fn, "dscores", dscores, f32, T * E, d), _ptr(fn, "dlogits", dlogits, f32, T * E, d))
 
 
 def moe_combine_backward(shape, dy, y_perm, slot_to_row, topk_weights, dy_perm, dweights, stream=None):
-    a = _Args("moe_combine_backward")
-    T, d, k = shape.T, shape.d_model, shape.top_k
+    fn = "moe_combine_backward"
+    T, dm, k = shape.T, shape.d_model, shape.top_k
     R = T * (k + shape.n_shared)
-    dt = _TORCH.get(shape.act_dtype)
-    p = (a("dy", dy, dt, T * d), a("y_perm", y_perm, torch.float32, R * d),
-         a("slot_to_row", slot_to_row, torch.int32, R), a("topk_weights", topk_weights, torch.float32, T * k),
-         a("dy_perm", dy_perm, dt, R * d), a("dweights", dweights, torch.float32, T * k))
-    a.run(lambda st: _lib.load().moe_combine_backward(ctypes.byref(shape), *p, st), stream)
+    f32, dt, d = torch.float32, _TORCH.get(shape.act_dtype), _device(dy, slot_to_row, topk_weights)
+    _run(fn, d, stream, ctypes.byref(shape), _ptr(fn, "dy", dy, dt, T * dm, d),
+         _ptr(fn, "y_perm", y_perm, f32, R * dm, d), _ptr(fn, "slot_to_row", slot_to_row, torch.int32, R, d),
+         _ptr(fn, "topk_weights", topk_weights, f32, T * k, d), _ptr(fn, "dy_perm", dy_perm, dt, R * dm, d),
+         _ptr(fn, "dweights", dweights, f32, T * k, d))
 
 
 def moe_forward_routed(shape, x, topk_ids, topk_weights, next_ids, w1, w3, w2, w1_scale, w3_scale,
                        w2_scale, y, expert_counts_out=None, drop_mask_out=None, workspace=None,
                        stream=None):
-    a = _Args("moe_forward_routed")
-    T, d, k, G = shape.T, shape.d_model, shape.top_k, shape.n_experts + shape.n_shared
-    dt, i32 = _TORCH.get(shape.act_dtype), torch.int32
-    # expert weights in their storage type: 1 byte (fp8), half a byte (MXFP4) or the activations'
-    per_matrix = G * d * shape.d_ff // (2 if shape.w_dtype == MOE_MXFP4 else 1)
-    wt = _TORCH.get(shape.w_dtype)
+    fn = "moe_forward_routed"
+    T, dm, dff, k, G = shape.T, shape.d_model, shape.d_ff, shape.top_k, shape.n_experts + shape.n_shared
+    dt, i32, d = _TORCH.get(shape.act_dtype), torch.int32, _device(x, topk_ids, topk_weights, y)
+    # expert weights and scales in their storage types
+    wt, n_w, st, n_up, n_down = _TORCH.get(shape.w_dtype), G * dm * dff, None, 0, 0
     if shape.w_dtype == MOE_FP8_E4M3:
-        st, n_up, n_down = torch.float32, G * shape.d_ff, G * d
+        st, n_up, n_down = torch.float32, G * dff, G * dm
     elif shape.w_dtype == MOE_MXFP4:
-        st, n_up, n_down = torch.uint8, G * shape.d_ff * d // 32, G * d * shape.d_ff // 32
-    else:                       # no scales
-        st, n_up, n_down = None, 0, 0
-    p = (a("x", x, dt, T * d), a("topk_ids", topk_ids, i32, T * k),
-         a("topk_weights", topk_weights, torch.float32, T * k), a("next_ids", next_ids, i32, T * 2),
-         a("w1", w1, wt, per_matrix), a("w3", w3, wt, per_matrix), a("w2", w2, wt, per_matrix),
-         a("w1_scale", w1_scale, st, n_up), a("w3_scale", w3_scale, st, n_up),
-         a("w2_scale", w2_scale, st, n_down), a("y", y, dt, T * d),
-         a("expert_counts_out", expert_counts_out, i32, G),
-         a("drop_mask_out", drop_mask_out, torch.uint8, T * k), *a.workspace(workspace))
-    a.run(lambda st: _lib.load().moe_forward_routed(ctypes.byref(shape), *p, st), stream)
+        n_w, st, n_up, n_down = n_w // 2, torch.uint8, n_w // 32, n_w // 32
+    _run(fn, d, stream, ctypes.byref(shape), _ptr(fn, "x", x, dt, T * dm, d),
+         _ptr(fn, "topk_ids", topk_ids, i32, T * k, d),
+         _ptr(fn, "topk_weights", topk_weights, torch.float32, T * k, d),
+         _ptr(fn, "next_ids", next_ids, i32, T * 2, d), _ptr(fn, "w1", w1, wt, n_w, d),
+         _ptr(fn, "w3", w3, wt, n_w, d), _ptr(fn, "w2", w2, wt, n_w, d),
+         _ptr(fn, "w1_scale", w1_scale, st, n_up, d), _ptr(fn, "w3_scale", w3_scale, st, n_up, d),
+         _ptr(fn, "w2_scale", w2_scale, st, n_down, d), _ptr(fn, "y", y, dt, T * dm, d),
+         _ptr(fn, "expert_counts_out", expert_counts_out, i32, G, d),
+         _ptr(fn, "drop_mask_out", drop_mask_out, torch.uint8, T * k, d), *_workspace(fn, workspace, d))

@@ -157,7 +157,9 @@ size_t part_bytes(const moe_linear_t& l) { return round256((size_t)prep_chunks(l
 
 }  // namespace
 
-size_t linear_workspace_bytes(const moe_linear_t& l) { return l.M == 0 ? 0 : product_workspace(l.M, l.N, l.K); }
+size_t linear_workspace_bytes(const moe_linear_t& l) { 
+  return l.M <= kLinearDecodeRows ? 0 : product_workspace(l.M, l.N, l.K);
+}
 
 size_t linear_backward_workspace_bytes(const moe_linear_t& l) {
   if (l.M == 0) return 0;
@@ -168,6 +170,7 @@ size_t linear_backward_workspace_bytes(const moe_linear_t& l) {
 hipError_t launch_linear(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const float* bias,
                          const void* residual, void* y, uint16_t* pre, void* workspace, hipStream_t st) {
   const Epilogue ep{bias, residual, y, pre, l.y_dtype == MOE_F32};
+  if (l.M <= kLinearDecodeRows) return launch_linear_decode(l, x, w, ep, st);
   auto run = [&](auto act) {
     return launch_product<false, false, decltype(act)::value>(x, l.K, w, l.K, l.M, l.N, l.K, workspace, ep, st);
   };

@@ -1,0 +1,149 @@
+// Dense product for a few rows (decode): weight streaming.
+//
+// y = act(x w^T + bias) + residual with M <= 16 NT rows reads w once and does
+// little else, so the weight stream bounds it.  A workgroup owns 16 output
+// channels and its W wavefronts share the contraction: wavefront v takes stages
+// v, v + W, ... of 128 terms.  A stage's 16 x 256 bytes come in the wide pattern
+// (4 rows x 256 contiguous bytes per load, non-temporal: read once), D stages in
+// flight in registers, go through the wavefront's own LDS tile (16-byte chunks
+// XOR-swizzled by row; LDS operations of one wavefront execute in order, so no
+// barrier) and come back in the v_mfma_f32_16x16x32_bf16 layout.  The rows of x
+// (L2-resident) are read directly.  At the end the wavefronts' accumulators meet
+// in LDS and are summed in wavefront order, 8 channels of a row to a lane.
+#include "device_common.hpp"
+#include "launch.hpp"
+#include "linear_epilogue.hpp"
+#include "lds_stream.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kStage = 128;                     // terms per stage
+constexpr int kTileBytes = 16 * kStage * 2;     // one wavefront's LDS tile
+
+template <int ACT, int NT, int CG, int W, int D>
+__global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t* __restrict__ x,
+                                                                  const uint16_t* __restrict__ w, int M, int N, int K,
+                                                                  const Epilogue ep) {
+  static_assert(NT * 16 * 16 * 4 <= kTileBytes, "the accumulators fit the tile");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[W][CG * kTileBytes];
+  const int c0 = xcd_remap(blockIdx.x, gridDim.x) * (16 * CG);  // a contiguous eighth of the channels per XCD
+  if (c0 >= N) return;                                          // the whole workgroup
+  const int lane = threadIdx.x & 63, v = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  uint8_t* tile = lds[v];
+  // stage loads: lane (lrow, lch) takes chunk lch of rows lrow, lrow + 4, ...; channels past N repeat the last
+  const int lrow = lane >> 4, lch = lane & 15;
+  const int stages = (K + kStage - 1) / kStage;
+  // descriptors bounded to the channels and rows there are: what lies past them
+  // loads as zero; a chunk past the end of a row is sent past the descriptor
+  const __amdgpu_buffer_rsrc_t dw =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(w + (int64_t)c0 * K), 0, min(16 * CG, N - c0) * K * 2, kRawBufferFlags);
+  const __amdgpu_buffer_rsrc_t dx = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(x), 0, M * K * 2, kRawBufferFlags);
+  const int woff = lrow * K * 2 + lch * 16, xoff = r * K * 2 + g * 16;
+  constexpr int kPast = (int)0x80000000u, kStream = 2;             // kStream: non-temporal, read once
+
+  u32x4_t wv[D][CG * 4], xv[D][NT * 4];
+  auto fetch = [&](u32x4_t (&wd)[CG * 4], u32x4_t (&xd)[NT * 4], int st) __attribute__((always_inline)) {
+    const int k0 = st * kStage;
+    const int wpast = k0 + lch * 8 < K ? 0 : kPast;
+#pragma unroll
+    for (int i = 0; i < CG * 4; ++i)
+      wd[i] = __builtin_amdgcn_raw_buffer_load_b128(dw, (woff + i * 4 * K * 2) | wpast, k0 * 2, kStream);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int xpast = k0 + j * 32 + g * 8 < K ? 0 : kPast;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        xd[n * 4 + j] = __builtin_amdgcn_raw_buffer_load_b128(dx, (xoff + n * 16 * K * 2 + j * 64) | xpast, k0 * 2, 0);
+    }
+  };
+  f32x4_t acc[CG][NT];
+#pragma unroll
+  for (int c = 0; c < CG; ++c)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[c][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto consume = [&](const u32x4_t (&wd)[CG * 4], const u32x4_t (&xd)[NT * 4]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < CG * 4; ++i) {
+      const int row = i * 4 + lrow;
+      *reinterpret_cast<u32x4_t*>(tile + row * (kStage * 2) + ((lch ^ (row & 15)) << 4)) = wd[i];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < CG; ++c) {
+        const uint4 a = *reinterpret_cast<const uint4*>(tile + (c * 16 + r) * (kStage * 2) + (((4 * j + g) ^ r) << 4));
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          acc[c][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), __builtin_bit_cast(bf16x8_t, xd[n * 4 + j]), acc[c][n], 0, 0, 0);
+      }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(wv[d], xv[d], v + d * W);      // past the end: zeros, nothing read
+  for (int st = v; st < stages; st += D * W) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      consume(wv[d], xv[d]);
+      fetch(wv[d], xv[d], st + (d + D) * W);
+    }
+  }
+  // lane (r, g): row n 16 + r, channels 16 c + 4 g .. + 3
+#pragma unroll
+  for (int c = 0; c < CG; ++c)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<float4*>(tile + c * kTileBytes + ((n * 16 + r) * 16 + 4 * g) * 4) =
+          make_float4(acc[c][n][0], acc[c][n][1], acc[c][n][2], acc[c][n][3]);
+  __syncthreads();
+  for (int o = threadIdx.x; o < M * 2 * CG; o += W * kWave) {
+    const int t = o / (2 * CG), q = o % (2 * CG), c = c0 + q * 8;
+    if (c >= N) continue;
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      float p[8];
+      load8f(reinterpret_cast<const float*>(lds[i] + (q >> 1) * kTileBytes) + t * 16 + (q & 1) * 8, p);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += p[k];
+    }
+    ep.store8<ACT>(t, c, N, sum);
+  }
+}
+
+template <int ACT, int NT>
+hipError_t launch_act(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
+                      hipStream_t st) {
+  const int cus = device_cu_count();
+  auto run = [&](auto kernel, int cg, int waves) {
+    const int groups = (l.N + 16 * cg - 1) / (16 * cg);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((groups + 7) / 8 * 8)), dim3(waves * kWave), 0, st, x, w, l.M, l.N, l.K, ep);
+    return hipGetLastError();
+  };
+  const int groups = (l.N + 15) / 16;
+  if (groups >= 3 * cus) return run(linear_decode_kernel<ACT, NT, 2, 8, 1>, 2, 8);
+  if (groups >= cus / 2) return run(linear_decode_kernel<ACT, NT, 1, 8, 2>, 1, 8);
+  return run(linear_decode_kernel<ACT, NT, 1, 16, 2>, 1, 16);
+}
+
+template <int ACT>
+hipError_t launch_rows(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
+                       hipStream_t st) {
+  if (l.M <= 16) return launch_act<ACT, 1>(l, x, w, ep, st);
+  return launch_act<ACT, 2>(l, x, w, ep, st);
+}
+
+}  // namespace
+
+hipError_t launch_linear_decode(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
+                                hipStream_t st) {
+  switch (l.act) {
+    case MOE_ACT_RELU: return launch_rows<MOE_ACT_RELU>(l, x, w, ep, st);
+    case MOE_ACT_SILU: return launch_rows<MOE_ACT_SILU>(l, x, w, ep, st);
+    case MOE_ACT_GELU: return launch_rows<MOE_ACT_GELU>(l, x, w, ep, st);
+    case MOE_ACT_GELU_TANH: return launch_rows<MOE_ACT_GELU_TANH>(l, x, w, ep, st);
+    default: return launch_rows<MOE_ACT_NONE>(l, x, w, ep, st);
+  }
+}
+
+}  // namespace moe

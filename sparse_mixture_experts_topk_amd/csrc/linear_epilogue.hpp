@@ -92,4 +92,10 @@ struct Epilogue {
   }
 };
 
+// Weight streaming for up to kLinearDecodeRows rows.
+constexpr int kLinearDecodeRows = 32;
+int device_cu_count();
+hipError_t launch_linear_decode(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
+                                hipStream_t st);
+
 }  // namespace moe
