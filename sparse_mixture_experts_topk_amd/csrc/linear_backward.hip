@@ -1,0 +1,126 @@
+// Gradients of the dense product.
+//
+//   dpre = dy act'(pre),  dx = dpre w,  dw = dpre^T x,  dbias = sum_m dpre
+//
+// Both products are tiles (linear_tiles.hpp) with operands as they lie in
+// memory: dx contracts over w's slow index, dw over that of dpre and of x.
+#include "device_common.hpp"
+#include "launch.hpp"
+#include "linear_plan.hpp"
+
+namespace moe {
+namespace {
+
+// ---- gradient at the pre-activation ----
+
+constexpr int kPrepCols = 256;      // columns per workgroup, 8 to a lane
+constexpr int kPrepRows = 256;      // rows per workgroup: one row of column sums comes of them
+
+// dpre = dy act'(pre) in bf16 (unless NULL), and the column sums of its fp32
+// values over the workgroup's rows into part[chunk][N] (unless NULL).
+// HBM-bound: reads dy and pre, writes dpre, once each.
+template <bool F32, bool ACT>
+__global__ __launch_bounds__(256) void dpre_kernel(const void* __restrict__ dy, const uint16_t* __restrict__ pre,
+                                                   int act, int M, int N, int col_blocks,
+                                                   uint16_t* __restrict__ dpre, float* __restrict__ part) {
+  __shared__ float sums[8][kPrepCols];
+  const int chunk = blockIdx.x / col_blocks, cb = blockIdx.x % col_blocks;
+  const int cl = (threadIdx.x & 31) * 8, rl = threadIdx.x >> 5;
+  const int c = cb * kPrepCols + cl;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int r_end = min(M, (chunk + 1) * kPrepRows);
+  if (c < N) {
+    for (int r = chunk * kPrepRows + rl; r < r_end; r += 8) {
+      const int64_t at = (int64_t)r * N + c;
+      float v[8];
+      if constexpr (F32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(dy) + at);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      } else {
+        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(dy) + at), v);
+      }
+      if constexpr (ACT) {
+        float p[8];
+        unpack8(*reinterpret_cast<const uint4*>(pre + at), p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= act_grad(p[i], act);
+      }
+      if (dpre != nullptr) *reinterpret_cast<uint4*>(dpre + at) = pack8(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += v[i];
+    }
+  }
+  if (part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[rl][cl + i] = acc[i];
+  __syncthreads();
+  const int col = cb * kPrepCols + threadIdx.x;
+  if (col < N) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += sums[i][threadIdx.x];
+    part[(int64_t)chunk * N + col] = s;
+  }
+}
+
+// dbias[c] = the sum of part[.][c], in chunk order.
+__global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ part, int chunks, int N,
+                                                    float* __restrict__ dbias) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= N) return;
+  float s = 0.f;
+  for (int i = 0; i < chunks; ++i) s += part[(int64_t)i * N + c];
+  dbias[c] = s;
+}
+
+int prep_chunks(const moe_linear_t& l) { return (l.M + kPrepRows - 1) / kPrepRows; }
+// dpre has bf16 values of its own unless dy already is what the products read.
+bool dpre_copied(const moe_linear_t& l) { return l.act != MOE_ACT_NONE || l.y_dtype == MOE_F32; }
+
+size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+size_t dpre_bytes(const moe_linear_t& l) { return dpre_copied(l) ? round256((size_t)l.M * l.N * 2) : 0; }
+
+size_t part_bytes(const moe_linear_t& l) { return round256((size_t)prep_chunks(l) * l.N * 4); }
+
+}  // namespace
+
+size_t linear_backward_workspace_bytes(const moe_linear_t& l) {
+  if (l.M == 0) return 0;
+  return dpre_bytes(l) + part_bytes(l) +
+         std::max(product_workspace(l.M, l.K, l.N), product_workspace(l.N, l.K, l.M));
+}
+
+hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const uint16_t* pre, const uint16_t* x,
+                                  const uint16_t* w, uint16_t* dx, uint16_t* dw, float* dbias, void* workspace,
+                                  hipStream_t st) {
+  uint16_t* copy = dpre_copied(l) && (dx != nullptr || dw != nullptr) ? static_cast<uint16_t*>(workspace) : nullptr;
+  float* part = dbias != nullptr ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dpre_bytes(l)) : nullptr;
+  hipError_t e = hipSuccess;
+  if (copy != nullptr || part != nullptr) {
+    const int cbs = (l.N + kPrepCols - 1) / kPrepCols;
+    const dim3 grid((unsigned)((int64_t)cbs * prep_chunks(l)));
+    const bool f32 = l.y_dtype == MOE_F32, act = l.act != MOE_ACT_NONE;
+    auto run = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, dy, pre, l.act, l.M, l.N, cbs, copy, part);
+      return hipGetLastError();
+    };
+    e = f32 ? (act ? run(dpre_kernel<true, true>) : run(dpre_kernel<true, false>))
+            : (act ? run(dpre_kernel<false, true>) : run(dpre_kernel<false, false>));
+  }
+  if (e == hipSuccess && dbias != nullptr) {
+    hipLaunchKernelGGL(dbias_kernel, dim3((l.N + 255) / 256), dim3(256), 0, st, part, prep_chunks(l), l.N, dbias);
+    e = hipGetLastError();
+  }
+  const uint16_t* d = copy != nullptr ? copy : static_cast<const uint16_t*>(dy);
+  void* partials = static_cast<uint8_t*>(workspace) + dpre_bytes(l) + part_bytes(l);
+  if (e == hipSuccess && dx != nullptr)
+    e = launch_product<false, true, MOE_ACT_NONE>(d, l.N, w, l.K, l.M, l.K, l.N, partials,
+                                                  Epilogue{nullptr, nullptr, dx, nullptr, false}, st);
+  if (e == hipSuccess && dw != nullptr)
+    e = launch_product<true, true, MOE_ACT_NONE>(d, l.N, x, l.K, l.N, l.K, l.M, partials,
+                                                 Epilogue{nullptr, nullptr, dw, nullptr, false}, st);
+  return e;
+}
+
+}  // namespace moe

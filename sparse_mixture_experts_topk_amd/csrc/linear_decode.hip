@@ -21,12 +21,12 @@ namespace {
 constexpr int kStage = 128;                     // terms per stage
 constexpr int kTileBytes = 16 * kStage * 2;     // one wavefront's LDS tile
 
-template <int ACT, int NT, int CG, int W, int D>
+template <int ACT, int NT, int CG, int W, int D, bool XLDS>
 __global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t* __restrict__ x,
                                                                   const uint16_t* __restrict__ w, int M, int N, int K,
                                                                   const Epilogue ep) {
   static_assert(NT * 16 * 16 * 4 <= kTileBytes, "the accumulators fit the tile");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[W][CG * kTileBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[W][(CG + (XLDS ? NT : 0)) * kTileBytes];
   const int c0 = xcd_remap(blockIdx.x, gridDim.x) * (16 * CG);  // a contiguous eighth of the channels per XCD
   if (c0 >= N) return;                                          // the whole workgroup
   const int lane = threadIdx.x & 63, v = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -50,12 +50,18 @@ __global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t
 #pragma unroll
     for (int i = 0; i < CG * 4; ++i)
       wd[i] = __builtin_amdgcn_raw_buffer_load_b128(dw, (woff + i * 4 * K * 2) | wpast, k0 * 2, kStream);
+    if constexpr (XLDS) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int xpast = k0 + j * 32 + g * 8 < K ? 0 : kPast;
+      for (int i = 0; i < NT * 4; ++i)
+        xd[i] = __builtin_amdgcn_raw_buffer_load_b128(dx, (woff + i * 4 * K * 2) | wpast, k0 * 2, 0);
+    } else {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        xd[n * 4 + j] = __builtin_amdgcn_raw_buffer_load_b128(dx, (xoff + n * 16 * K * 2 + j * 64) | xpast, k0 * 2, 0);
+      for (int j = 0; j < 4; ++j) {
+        const int xpast = k0 + j * 32 + g * 8 < K ? 0 : kPast;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          xd[n * 4 + j] = __builtin_amdgcn_raw_buffer_load_b128(dx, (xoff + n * 16 * K * 2 + j * 64) | xpast, k0 * 2, 0);
+      }
     }
   };
   f32x4_t acc[CG][NT];
@@ -69,15 +75,31 @@ __global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t
       const int row = i * 4 + lrow;
       *reinterpret_cast<u32x4_t*>(tile + row * (kStage * 2) + ((lch ^ (row & 15)) << 4)) = wd[i];
     }
+    if constexpr (XLDS) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int i = 0; i < NT * 4; ++i) {
+        const int row = i * 4 + lrow;
+        *reinterpret_cast<u32x4_t*>(tile + CG * kTileBytes + row * (kStage * 2) + ((lch ^ (row & 15)) << 4)) = xd[i];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint4 xs[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if constexpr (XLDS)
+          xs[n] = *reinterpret_cast<const uint4*>(tile + CG * kTileBytes + (n * 16 + r) * (kStage * 2) + (((4 * j + g) ^ r) << 4));
+        else
+          xs[n] = __builtin_bit_cast(uint4, xd[n * 4 + j]);
+      }
 #pragma unroll
       for (int c = 0; c < CG; ++c) {
         const uint4 a = *reinterpret_cast<const uint4*>(tile + (c * 16 + r) * (kStage * 2) + (((4 * j + g) ^ r) << 4));
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          acc[c][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), __builtin_bit_cast(bf16x8_t, xd[n * 4 + j]), acc[c][n], 0, 0, 0);
+          acc[c][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(xs[n]), acc[c][n], 0, 0, 0);
       }
+    }
   };
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(wv[d], xv[d], v + d * W);      // past the end: zeros, nothing read
@@ -121,9 +143,14 @@ hipError_t launch_act(const moe_linear_t& l, const uint16_t* x, const uint16_t* 
     return hipGetLastError();
   };
   const int groups = (l.N + 15) / 16;
-  if (groups >= 3 * cus) return run(linear_decode_kernel<ACT, NT, 2, 8, 1>, 2, 8);
-  if (groups >= cus / 2) return run(linear_decode_kernel<ACT, NT, 1, 8, 2>, 1, 8);
-  return run(linear_decode_kernel<ACT, NT, 1, 16, 2>, 1, 16);
+  if (groups >= 3 * cus) {
+    if constexpr (NT == 1) {
+      if (l.M <= 4) return run(linear_decode_kernel<ACT, NT, 2, 8, 1, false>, 2, 8);
+    }
+    return run(linear_decode_kernel<ACT, NT, 2, 4, 1, true>, 2, 4);
+  }
+  if (groups >= cus / 2) return run(linear_decode_kernel<ACT, NT, 1, 8, 1, true>, 1, 8);
+  return run(linear_decode_kernel<ACT, NT, 1, NT == 1 ? 16 : 8, 2, true>, 1, NT == 1 ? 16 : 8);
 }
 
 template <int ACT>

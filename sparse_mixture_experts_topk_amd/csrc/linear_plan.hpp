@@ -1,0 +1,92 @@
+// Host side of the tiled dense product: the choice of tile and schedule.
+#pragma once
+#include <algorithm>
+
+#include "linear_tiles.hpp"
+
+namespace moe {
+
+// Tile shapes (columns x rows), all 8 wavefronts.  kSlice: us per slice of 64
+// terms once the stream runs, kTile: us to store a tile, measured on MI355X
+// (8192 x 14336 x 4096 for the 256 x 256 tile: 1370 TFLOP/s; 2048 x 4096 x 4096
+// for 256 x 128: 1120; 1024 x 4096 x 4096 for 128 x 128: 940; 509 x 4096 x 2048
+// for 128 x 64: 560).  A smaller tile reads more bytes per product but leaves
+// fewer CUs idle and needs less splitting.
+struct Tile256x256 { static constexpr int NS = 2, WR = 4, WC = 2, WA = 4, WB = 8; static constexpr double kSlice = 1.48, kTile = 4.0; };
+struct Tile256x128 { static constexpr int NS = 3, WR = 4, WC = 2, WA = 4, WB = 4; static constexpr double kSlice = 0.86, kTile = 2.0; };
+struct Tile128x128 { static constexpr int NS = 4, WR = 4, WC = 2, WA = 2, WB = 4; static constexpr double kSlice = 0.50, kTile = 1.0; };
+struct Tile128x64 { static constexpr int NS = 6, WR = 4, WC = 2, WA = 2, WB = 2; static constexpr double kSlice = 0.345, kTile = 0.5; };
+template <class C> using GeomOf = ProductGeom<C::NS, C::WR, C::WC, C::WA, C::WB>;
+
+// Splitting a tail costs a second launch, and its partial tiles are written and
+// read once: 509 x 4096 x 2048 split in two with 128 x 128 tiles, 17 MB: 8 us
+// longer than its slices; with 256 x 256 tiles, 67 MB: 25 us.
+constexpr double kJoinFixed = 4.0, kJoinPerByte = 0.32e-6;
+constexpr int kMinSlices = 4;        // of a split run
+
+struct ProductPlan {
+  double cost = 1e30;                // us, without what all candidates share
+  int row_tiles = 0, col_tiles = 0, KT = 0, grid = 0;
+  bool split = false;
+  size_t workspace = 0;
+
+  template <class C>
+  static ProductPlan of(int rows, int cols, int len) {
+    using G = GeomOf<C>;
+    ProductPlan best;
+    const int64_t cus = std::min<int64_t>(device_cu_count(), kMaxPersistentGroups) / 8 * 8;
+    for (int split = 0; split < 2; ++split) {
+      ProductPlan p;
+      p.row_tiles = (rows + G::TB - 1) / G::TB;
+      p.col_tiles = (cols + G::TA - 1) / G::TA;
+      p.KT = (len + G::BK - 1) / G::BK;
+      p.split = split != 0;
+      const int64_t tiles = (int64_t)p.row_tiles * p.col_tiles;
+      const int64_t most = p.split ? tiles * p.KT / kMinSlices / 8 * 8 : (tiles + 7) / 8 * 8;
+      p.grid = (int)std::max<int64_t>(8, std::min<int64_t>(cus, most));
+      const TileShare s = TileShare::of((int)tiles, 0, p.grid / 8, p.KT, p.split);      // the largest share
+      const double parts = p.split ? 8.0 * (p.grid / 8 + s.tail) * G::PARTIAL * 4 : 0;
+      p.cost = ((double)s.R * p.KT + (p.split ? s.P : s.tail > 0 ? p.KT : 0)) * C::kSlice +
+               (s.R + (s.tail > 0 ? 1 : 0)) * C::kTile + (p.split ? kJoinFixed + kJoinPerByte * parts : 0);
+      p.workspace = p.split ? (size_t)p.grid * 2 * G::PARTIAL * 4 : 0;
+      if (p.cost < best.cost) best = p;
+    }
+    return best;
+  }
+};
+
+// Calls run(tile shape, plan) with the cheapest of the four.
+template <class F>
+auto with_plan(int rows, int cols, int len, F&& run) {
+  const ProductPlan a = ProductPlan::of<Tile256x256>(rows, cols, len), b = ProductPlan::of<Tile256x128>(rows, cols, len),
+                    c = ProductPlan::of<Tile128x128>(rows, cols, len), d = ProductPlan::of<Tile128x64>(rows, cols, len);
+  const double least = std::min(std::min(a.cost, b.cost), std::min(c.cost, d.cost));
+  if (a.cost == least) return run(Tile256x256{}, a);
+  if (b.cost == least) return run(Tile256x128{}, b);
+  if (c.cost == least) return run(Tile128x128{}, c);
+  return run(Tile128x64{}, d);
+}
+
+inline size_t product_workspace(int rows, int cols, int len) {
+  return with_plan(rows, cols, len, [](auto, const ProductPlan& p) { return p.workspace; });
+}
+
+template <bool PSLOW, bool QSLOW, int ACT>
+hipError_t launch_product(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, int rows, int cols,
+                          int len, void* partials, const Epilogue& ep, hipStream_t st) {
+  return with_plan(rows, cols, len, [&](auto tile, const ProductPlan& p) {
+    using C = decltype(tile);
+    using G = GeomOf<C>;
+    const ProductArgs a{P, Q, ldp, ldq, rows, cols, len, p.row_tiles, p.col_tiles, p.split,
+                        static_cast<float*>(partials), ep};
+    hipLaunchKernelGGL((linear_product_kernel<PSLOW, QSLOW, ACT, C::NS, C::WR, C::WC, C::WA, C::WB>),
+                       dim3((unsigned)p.grid), dim3(G::THREADS), 0, st, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !p.split) return e;
+    hipLaunchKernelGGL((linear_join_kernel<ACT, G::TA, G::TB>), dim3((unsigned)(p.grid * (G::TB / kJoinRows<G::TA>))),
+                       dim3(256), 0, st, a, p.grid / 8, p.KT);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace moe

@@ -18,7 +18,8 @@
 //           each gets one column).  Chunk c of row t sits at c ^ slow_key(t):
 //           the 4 rows of a read go to different 64-byte quarters of the 256
 //           bytes that the banks cover, rows t and t + 8 to different halves
-//           of one, so no two of the lanes served together share a bank.
+//           of one (64-wide tiles: to the same effect), so no two of the lanes
+//           served together share a bank.
 // Neither has bank conflicts (SQ_LDS_BANK_CONFLICT 0).  Buffer descriptors are
 // bounded to the operand's valid part and a chunk past the end of a [r][t] row
 // is sent past it: such loads write zeros to LDS, on both operands, so a NaN
@@ -27,8 +28,8 @@
 // The kernel is persistent (one workgroup per CU): workgroup b takes tiles of
 // XCD b % 8's contiguous share of the tile list, and the slices of all its
 // tiles form one stream through the ring, so the next tile's first slices load
-// while this one's results are stored.  The last, partial round of tiles is cut
-// along the contraction over all workgroups (TileSplit): their fp32 partial
+// while this one's results are stored.  The last, partial round of tiles may be
+// cut along the contraction over all workgroups (TileShare): their fp32 partial
 // tiles are summed in order by a second kernel, which applies the epilogue.
 #pragma once
 #include "device_common.hpp"
@@ -39,12 +40,33 @@
 
 namespace moe {
 
+// The tile list in 8 contiguous shares, one per XCD; the `slots` workgroups of
+// an XCD take its full rounds of tiles, then the last `tail` < slots tiles either
+// whole (the other workgroups idle) or, split, cut along the contraction into
+// near-equal runs of P slices, one per workgroup, each covering parts of at most
+// two tiles.  Which of the two is the plan's choice.
+struct TileShare {
+  int begin, R, tail, P;
+  __host__ __device__ static TileShare of(int total, int xcd, int slots, int KT, bool split) {
+    TileShare t;
+    const int per_xcd = (total + 7) >> 3;
+    t.begin = xcd * per_xcd;
+    const int end = t.begin + per_xcd < total ? t.begin + per_xcd : total;
+    const int len = end > t.begin ? end - t.begin : 0;
+    t.R = len / slots;
+    t.tail = len - t.R * slots;
+    t.P = split ? (t.tail * KT + slots - 1) / slots : 0;
+    return t;
+  }
+};
+
 struct ProductArgs {
   const uint16_t* P;
   const uint16_t* Q;
   int64_t ldp, ldq;         // elements
   int rows, cols, len;
   int row_tiles, col_tiles;
+  bool split;
   float* partials;
   Epilogue ep;
 };
@@ -77,7 +99,12 @@ struct ProductGeom {
 };
 
 __device__ __forceinline__ int fast_key(int row) { return (row >> 1) & 7; }
-__device__ __forceinline__ int slow_key(int t) { return ((t & 3) << 2) | (((t >> 3) & 1) << 1); }
+template <int TX>
+__device__ __forceinline__ int slow_key(int t) {
+  static_assert(TX >= 64 && TX % 64 == 0, "rows of at least 8 chunks");
+  if constexpr (TX == 64) return (((t >> 1) & 1) << 1) | (((t >> 3) & 1) << 2);   // 128-byte rows: t's parity picks the half
+  else return ((t & 3) << 2) | (((t >> 3) & 1) << 1);
+}
 
 // Which chunk of the operand this lane fetches in the wavefront's load j of a
 // slice, and its byte offset in memory.  Load j covers LDS rows (NW j + wave)
@@ -91,7 +118,7 @@ struct LoadMap {
   static_assert(64 % CPR == 0 && (NW * RPI * PERIOD) % 16 == 0, "whole swizzle periods");
   __device__ static __forceinline__ int chunk(int wave, int lane, int j) {
     const int row = (NW * j + wave) * RPI + lane / CPR;
-    return (lane % CPR) ^ (SLOW ? slow_key(row) : fast_key(row));
+    return (lane % CPR) ^ (SLOW ? slow_key<TX>(row) : fast_key(row));
   }
   __device__ static __forceinline__ int offset(int wave, int lane, int j, int rowbytes) {
     return (wave * RPI + lane / CPR) * rowbytes + chunk(wave, lane, j) * 16;   // + j * step
@@ -116,7 +143,7 @@ __device__ __forceinline__ bf16x8_t read_fragment(const uint8_t* stage, int row0
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = t0 + 4 * j;
-      const uint8_t* p = stage + t * (TX * 2) + (((x >> 3) ^ slow_key(t)) << 4) + (x & 4) * 2;
+      const uint8_t* p = stage + t * (TX * 2) + (((x >> 3) ^ slow_key<TX>(t)) << 4) + (x & 4) * 2;
       v[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
     }
     return __builtin_bit_cast(bf16x8_t, s16x8_t{v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w});
@@ -149,8 +176,8 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const P
   const int wr = wave / WC, wc = wave % WC;
   const int KT = (a.len + BK - 1) / BK;
   const int slots = gridDim.x >> 3, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-  const TileSplit sp = TileSplit::of(a.row_tiles * a.col_tiles, xcd, slots, KT);
-  const int n_whole = sp.R + (sp.whole_tail && slot < sp.tail ? 1 : 0);
+  const TileShare sp = TileShare::of(a.row_tiles * a.col_tiles, xcd, slots, KT, a.split);
+  const int n_whole = sp.R + (!a.split && slot < sp.tail ? 1 : 0);
   const int run0 = slot * sp.P, run1 = min(run0 + sp.P, sp.tail * KT);
   const int n_runs = run0 < run1 ? (run1 - 1) / KT - run0 / KT + 1 : 0;
   const int n_items = n_whole + n_runs;
@@ -162,10 +189,10 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const P
     Item it{0, 0, 0, KT, -1};
     int t;
     if (i < n_whole) {
-      t = sp.share_begin + slot + i * slots;
+      t = sp.begin + slot + i * slots;
     } else {
       const int j = run0 / KT + (i - n_whole);
-      t = sp.share_begin + sp.R * slots + j;
+      t = sp.begin + sp.R * slots + j;
       it.kb = max(run0 - j * KT, 0);
       it.ke = min(run1 - j * KT, KT);
       it.part = xcd * 2 * slots + slot + j;
@@ -341,30 +368,34 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const P
 }
 
 // Sums the partial tiles of the split tail tiles in contraction order and applies
-// the epilogue.  One workgroup per (XCD, tail tile, 32 rows of it).
+// the epilogue.  One workgroup per (XCD, tail tile, kJoinRows rows of it), 8
+// columns of a row to a lane; four partials are in flight at a time.
+template <int TA> constexpr int kJoinRows = 256 * 8 / TA;
+
 template <int ACT, int TA, int TB>
 __global__ __launch_bounds__(256) void linear_join_kernel(const ProductArgs a, int slots, int KT) {
-  constexpr int RG = TB / 32;
+  constexpr int RG = TB / kJoinRows<TA>;
   const int rg = blockIdx.x % RG, xcd = (blockIdx.x / RG) & 7, j = blockIdx.x / RG >> 3;
-  const TileSplit sp = TileSplit::of(a.row_tiles * a.col_tiles, xcd, slots, KT);
-  if (sp.whole_tail || j >= sp.tail) return;
+  const TileShare sp = TileShare::of(a.row_tiles * a.col_tiles, xcd, slots, KT, true);
+  if (j >= sp.tail) return;
   int rt, ct;
-  tile_at(sp.share_begin + sp.R * slots + j, a.row_tiles, a.col_tiles, rt, ct);
+  tile_at(sp.begin + sp.R * slots + j, a.row_tiles, a.col_tiles, rt, ct);
   const int s_lo = j * KT / sp.P, s_hi = min(((j + 1) * KT - 1) / sp.P, slots - 1);
-  const float* base = a.partials + (int64_t)(xcd * 2 * slots + j) * (TA * TB);
-  for (int i = threadIdx.x; i < 32 * TA / 8; i += 256) {
-    const int rl = rg * 32 + i / (TA / 8), cl = i % (TA / 8) * 8;
-    const int r = rt * TB + rl, c = ct * TA + cl;
-    if (r >= a.rows || c >= a.cols) continue;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int s = s_lo; s <= s_hi; ++s) {
-      float p[8];
-      load8f(base + (int64_t)s * (TA * TB) + rl * TA + cl, p);
+  const int rl = rg * kJoinRows<TA> + threadIdx.x / (TA / 8), cl = threadIdx.x % (TA / 8) * 8;
+  const int r = rt * TB + rl, c = ct * TA + cl;
+  if (r >= a.rows || c >= a.cols) return;
+  const float* base = a.partials + (int64_t)(xcd * 2 * slots + j) * (TA * TB) + rl * TA + cl;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s = s_lo; s <= s_hi; s += 4) {
+    float p[4][8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += p[k];
-    }
-    a.ep.template store8<ACT>(r, c, a.cols, v);
+    for (int q = 0; q < 4; ++q) load8f(base + (int64_t)min(s + q, s_hi) * (TA * TB), p[q]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += s + q <= s_hi ? p[q][k] : 0.0f;
   }
+  a.ep.template store8<ACT>(r, c, a.cols, v);
 }
 
 }  // namespace moe

@@ -25,12 +25,11 @@ struct TileSplit {
   int share_begin, R, tail, P;
   bool whole_tail;
 
-  __host__ __device__ static TileSplit of(int total, int xcd, int slots, int KT) {
+  __device__ static TileSplit of(int total, int xcd, int slots, int KT) {
     TileSplit t;
     const int per_xcd = (total + 7) >> 3;
     t.share_begin = xcd * per_xcd;
-    const int end = t.share_begin + per_xcd < total ? t.share_begin + per_xcd : total;
-    const int len = end > t.share_begin ? end - t.share_begin : 0;
+    const int len = max(0, min(t.share_begin + per_xcd, total) - t.share_begin);
     t.R = len / slots;
     t.tail = len - t.R * slots;
     t.whole_tail = t.tail > 0 && 8 * (slots - t.tail) < slots * (t.R + 1);
