@@ -60,6 +60,14 @@ __device__ __forceinline__ void store8f(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// 16 bytes to memory; STREAM: non-temporal, so that a large output does not push
+// the operands out of L2.
+template <bool STREAM>
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), static_cast<u32x4_t*>(p));
+  else *static_cast<uint4*>(p) = v;
+}
+
 // y = act(acc + bias) + residual, 8 channels of one row at a time (channel
 // counts are multiples of 8, so a group of 8 is in or out as a whole).
 struct Epilogue {
@@ -67,9 +75,9 @@ struct Epilogue {
   const void* residual;
   void* y;
   uint16_t* pre;
-  bool f32;      // y and residual
+  int f32;       // y and residual
 
-  template <int ACT>
+  template <int ACT, bool STREAM = false>
   __device__ __forceinline__ void store8(int r, int c, int cols, float (&v)[8]) const {
     const int64_t at = (int64_t)r * cols + c;
     float u[8];
@@ -78,7 +86,7 @@ struct Epilogue {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += u[i];
     }
-    if (pre != nullptr) *reinterpret_cast<uint4*>(pre + at) = pack8(v);
+    if (pre != nullptr) store16<STREAM>(pre + at, pack8(v));
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = act_value<ACT>(v[i]);
     if (residual != nullptr) {
@@ -87,8 +95,13 @@ struct Epilogue {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += u[i];
     }
-    if (f32) store8f(static_cast<float*>(y) + at, v);
-    else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) = pack8(v);
+    if (f32) {
+      float* o = static_cast<float*>(y) + at;
+      store16<STREAM>(o, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+      store16<STREAM>(o + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+    } else {
+      store16<STREAM>(static_cast<uint16_t*>(y) + at, pack8(v));
+    }
   }
 };
 

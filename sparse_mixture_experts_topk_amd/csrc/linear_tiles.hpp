@@ -96,6 +96,9 @@ struct ProductGeom {
   static_assert(NS >= 2 && NS * STAGE <= 160 * 1024, "LDS");
   static_assert(WA % 2 == 0, "the epilogue joins pairs of blocks");
   static constexpr int64_t PARTIAL = (int64_t)TA * TB;      // floats of a partial tile
+  // The largest tile's outputs are large: stored past L2 (8192 x 14336 x 4096 with
+  // pre kept 825 -> 735 us, the rows' pieces stored in order included).
+  static constexpr bool STREAM = TA * TB >= 256 * 256;
 };
 
 __device__ __forceinline__ int fast_key(int row) { return (row >> 1) & 7; }
@@ -130,25 +133,35 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
-// Fragment of 16 operand rows x 32 terms for v_mfma_f32_16x16x32_bf16: lane
-// (i, g) holds row i, terms 8 g .. 8 g + 7.
-template <bool SLOW, int TX>
-__device__ __forceinline__ bf16x8_t read_fragment(const uint8_t* stage, int row0, int s, int lane) {
-  const int i = lane & 15, g = lane >> 4;
-  if constexpr (!SLOW) {
-    return as_bf16x8(*reinterpret_cast<const uint4*>(stage + (row0 + i) * 128 + (((4 * s + g) ^ fast_key(i)) << 4)));
-  } else {
-    const int t0 = 32 * s + 8 * g + (i >> 2), x = row0 + 4 * (i & 3);   // this lane's part of the 4 x 16 block
-    s16x4_t v[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int t = t0 + 4 * j;
-      const uint8_t* p = stage + t * (TX * 2) + (((x >> 3) ^ slow_key<TX>(t)) << 4) + (x & 4) * 2;
-      v[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+// Fragments of 16 operand rows x 32 terms for v_mfma_f32_16x16x32_bf16: lane
+// (i, g) holds row i, terms 8 g .. 8 g + 7.  `lane_base` is this lane's byte
+// offset in a stage for block 0 of the wavefront (first row row0, a multiple
+// of the N blocks' rows), terms 0 .. 31; `read` adds block n and the half s.  In
+// the [t][r] layout a block moves chunk bits that the swizzle also moves, so it
+// enters by exclusive or (rows of the tile are a power of two of bytes).
+template <bool SLOW, int TX, int N>
+struct Fragments {
+  static_assert((N & (N - 1)) == 0 && (!SLOW || (TX & (TX - 1)) == 0), "blocks and rows by bits");
+  __device__ static __forceinline__ int lane_base(int row0, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    if constexpr (!SLOW) {
+      return (row0 + i) * 128 + ((g ^ fast_key(i)) << 4);
+    } else {
+      const int t = 8 * g + (i >> 2), x = row0 + 4 * (i & 3);          // this lane's part of the 4 x 16 block
+      return t * (TX * 2) + (((x >> 3) ^ slow_key<TX>(t)) << 4) + (x & 4) * 2;
     }
-    return __builtin_bit_cast(bf16x8_t, s16x8_t{v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w});
   }
-}
+  __device__ static __forceinline__ bf16x8_t read(const uint8_t* stage, int base, int n, int s) {
+    if constexpr (!SLOW) {
+      return as_bf16x8(*reinterpret_cast<const uint4*>(stage + (base ^ (s << 6)) + n * 16 * 128));
+    } else {
+      const uint8_t* p = stage + (base ^ (n << 5)) + s * 32 * (TX * 2);
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * (TX * 2)));
+      return __builtin_bit_cast(bf16x8_t, s16x8_t{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+    }
+  }
+};
 
 // Blocks x and x + 1 (16 columns each) of a row, 4 columns to a lane group of
 // 16, become 8 consecutive columns per lane: group g of the result holds
@@ -276,11 +289,14 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const P
   // ---- fragments and products ----
   f32x4_t acc[WA][WB];
   bf16x8_t fa[2][WA], fb[WB];
+  using FA = Fragments<QSLOW, G::TA, WA>;
+  using FB = Fragments<PSLOW, G::TB, WB>;
+  const int abase = FA::lane_base(wr * WA * 16, lane), bbase = FB::lane_base(wc * WB * 16, lane);
   auto read_a = [&](int g, int s, int i) __attribute__((always_inline)) {
-    return read_fragment<QSLOW, G::TA>(smem + (g % NS) * G::STAGE, (wr * WA + i) * 16, s, lane);
+    return FA::read(smem + (g % NS) * G::STAGE, abase, i, s);
   };
   auto read_b = [&](int g, int s, int i) __attribute__((always_inline)) {
-    return read_fragment<PSLOW, G::TB>(smem + (g % NS) * G::STAGE + G::A_BYTES, (wc * WB + i) * 16, s, lane);
+    return FB::read(smem + (g % NS) * G::STAGE + G::A_BYTES, bbase, i, s);
   };
   // One half slice: the WA x WB products of the held fragments, B outermost.  The
   // next half's fragments (gn, sn) are read meanwhile: A into the other buffer
@@ -309,20 +325,23 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const P
 
   auto epilogue = [&](const Item& it) __attribute__((always_inline)) {
     int i = lane & 15, g = lane >> 4;
-    asm volatile("" : "+v"(i), "+v"(g));              // offsets formed here, not kept through the product loop
     float* part = it.part >= 0 ? a.partials + (int64_t)it.part * G::PARTIAL : nullptr;
+    Epilogue ep = a.ep;
 #pragma unroll
-    for (int x = 0; x < WA; x += 2) {
+    for (int o = 0; o < WA * WB / 2; ++o) {
+      const int x = o % (WA / 2) * 2, y = o / (WA / 2);          // a row's 64-byte pieces one after the other
+      // Addresses are formed here and the choices made anew for every piece: kept in
+      // registers, or followed through one copy of the epilogue per combination,
+      // they would cost the product loop registers (spills: 0.7 -> 2.8 ms).
+      asm volatile("" : "+v"(i), "+v"(g), "+s"(part), "+s"(ep.bias), "+s"(ep.residual), "+s"(ep.pre), "+s"(ep.f32));
       const int cl = (wr * WA + x) * 16 + 8 * g, c = it.c0 + cl;
-#pragma unroll
-      for (int y = 0; y < WB; ++y) {
-        const int rl = (wc * WB + y) * 16 + i, r = it.r0 + rl;
-        float v[8];
-        join_blocks(acc[x][y], acc[x + 1][y], v);
-        if (part != nullptr) store8f(part + rl * G::TA + cl, v);
-        else if (r < a.rows && c < a.cols) a.ep.template store8<ACT>(r, c, a.cols, v);
-        acc[x][y] = acc[x + 1][y] = f32x4_t{};        // the next item starts from zero
-      }
+      const int rl = (wc * WB + y) * 16 + i, r = it.r0 + rl;
+      float v[8];
+      join_blocks(acc[x][y], acc[x + 1][y], v);
+      if (part != nullptr) store8f(part + rl * G::TA + cl, v);
+      else if (r < a.rows && c < a.cols) ep.template store8<ACT, G::STREAM>(r, c, a.cols, v);
+      acc[x][y] = acc[x + 1][y] = f32x4_t{};          // the next item starts from zero
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -344,13 +363,14 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const P
   for (int x = 0; x < WA; ++x)
 #pragma unroll
     for (int y = 0; y < WB; ++y) acc[x][y] = f32x4_t{};
-#pragma unroll
-  for (int x = 0; x < WA; ++x) fa[0][x] = read_a(0, 0, x);
-#pragma unroll
-  for (int y = 0; y < WB; ++y) fb[y] = read_b(0, 0, y);
   int g = 0;
   for (int ci = 0; ci < n_items; ++ci) {
     const Item it = item(ci);
+    // (read again after the last item's read ahead: no fragment lives through the epilogue)
+#pragma unroll
+    for (int x = 0; x < WA; ++x) fa[0][x] = read_a(g, 0, x);
+#pragma unroll
+    for (int y = 0; y < WB; ++y) fb[y] = read_b(g, 0, y);
     for (int kt = it.kb; kt < it.ke; ++kt, ++g) {
       __builtin_amdgcn_sched_barrier(0);
       half(0, g, 1, false, 0);
@@ -358,7 +378,6 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const P
       wait_lgkmcnt0();
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
-      // (slice g + 1 may be the next item's first, or after the last item one that is never used)
       half(1, g + 1, 0, true, g + NS);
       advance();
     }
