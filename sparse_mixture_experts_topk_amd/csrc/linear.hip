@@ -17,7 +17,7 @@
 namespace moe {
 
 size_t linear_workspace_bytes(const moe_linear_t& l) { 
-  return l.M <= kLinearDecodeRows ? 0 : product_workspace(l.M, l.N, l.K);
+  return l.M <= kLinearDecodeRows ? 0 : product_workspace(l.M, l.N, l.K, 0);
 }
 
 hipError_t launch_linear(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const float* bias,

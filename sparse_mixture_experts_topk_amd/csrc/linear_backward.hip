@@ -14,23 +14,30 @@ namespace {
 // ---- gradient at the pre-activation ----
 
 constexpr int kPrepCols = 256;      // columns per workgroup, 8 to a lane
-constexpr int kPrepRows = 256;      // rows per workgroup: one row of column sums comes of them
+// Rows per workgroup (one row of column sums comes of them): 256, fewer while that
+// leaves under four workgroups per CU (4099 x 256: 18 -> 5 us), 16 at least.
+int prep_rows(const moe_linear_t& l) {
+  const int64_t col_blocks = (l.N + kPrepCols - 1) / kPrepCols;
+  int rows = 256;
+  while (rows > 16 && col_blocks * ((l.M + rows - 1) / rows) < 4 * device_cu_count()) rows /= 2;
+  return rows;
+}
 
 // dpre = dy act'(pre) in bf16 (unless NULL), and the column sums of its fp32
 // values over the workgroup's rows into part[chunk][N] (unless NULL).
 // HBM-bound: reads dy and pre, writes dpre, once each.
 template <bool F32, bool ACT>
 __global__ __launch_bounds__(256) void dpre_kernel(const void* __restrict__ dy, const uint16_t* __restrict__ pre,
-                                                   int act, int M, int N, int col_blocks,
+                                                   int act, int M, int N, int col_blocks, int rows,
                                                    uint16_t* __restrict__ dpre, float* __restrict__ part) {
   __shared__ float sums[8][kPrepCols];
   const int chunk = blockIdx.x / col_blocks, cb = blockIdx.x % col_blocks;
   const int cl = (threadIdx.x & 31) * 8, rl = threadIdx.x >> 5;
   const int c = cb * kPrepCols + cl;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const int r_end = min(M, (chunk + 1) * kPrepRows);
+  const int r_end = min(M, (chunk + 1) * rows);
   if (c < N) {
-    for (int r = chunk * kPrepRows + rl; r < r_end; r += 8) {
+    for (int r = chunk * rows + rl; r < r_end; r += 8) {
       const int64_t at = (int64_t)r * N + c;
       float v[8];
       if constexpr (F32) {
@@ -64,17 +71,28 @@ __global__ __launch_bounds__(256) void dpre_kernel(const void* __restrict__ dy, 
   }
 }
 
-// dbias[c] = the sum of part[.][c], in chunk order.
+// dbias[c] = the sum of part[.][c]: 16 lanes to a column, each over every 16th
+// chunk, then joined in lane order.
 __global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ part, int chunks, int N,
                                                     float* __restrict__ dbias) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= N) return;
+  __shared__ float sums[16][16];
+  const int cl = threadIdx.x & 15, k = threadIdx.x >> 4, c = blockIdx.x * 16 + cl;
   float s = 0.f;
-  for (int i = 0; i < chunks; ++i) s += part[(int64_t)i * N + c];
-  dbias[c] = s;
+  if (c < N) {
+#pragma unroll 4
+    for (int i = k; i < chunks; i += 16) s += part[(int64_t)i * N + c];
+  }
+  sums[k][cl] = s;
+  __syncthreads();
+  if (threadIdx.x < 16 && c < N) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += sums[i][cl];
+    dbias[c] = t;
+  }
 }
 
-int prep_chunks(const moe_linear_t& l) { return (l.M + kPrepRows - 1) / kPrepRows; }
+int prep_chunks(const moe_linear_t& l) { return (l.M + prep_rows(l) - 1) / prep_rows(l); }
 // dpre has bf16 values of its own unless dy already is what the products read.
 bool dpre_copied(const moe_linear_t& l) { return l.act != MOE_ACT_NONE || l.y_dtype == MOE_F32; }
 
@@ -88,7 +106,7 @@ size_t part_bytes(const moe_linear_t& l) { return round256((size_t)prep_chunks(l
 size_t linear_backward_workspace_bytes(const moe_linear_t& l) {
   if (l.M == 0) return 0;
   return dpre_bytes(l) + part_bytes(l) +
-         std::max(product_workspace(l.M, l.K, l.N), product_workspace(l.N, l.K, l.M));
+         std::max(product_workspace(l.M, l.K, l.N, 1), product_workspace(l.N, l.K, l.M, 2));
 }
 
 hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const uint16_t* pre, const uint16_t* x,
@@ -102,14 +120,14 @@ hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const u
     const dim3 grid((unsigned)((int64_t)cbs * prep_chunks(l)));
     const bool f32 = l.y_dtype == MOE_F32, act = l.act != MOE_ACT_NONE;
     auto run = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, dy, pre, l.act, l.M, l.N, cbs, copy, part);
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, dy, pre, l.act, l.M, l.N, cbs, prep_rows(l), copy, part);
       return hipGetLastError();
     };
     e = f32 ? (act ? run(dpre_kernel<true, true>) : run(dpre_kernel<true, false>))
             : (act ? run(dpre_kernel<false, true>) : run(dpre_kernel<false, false>));
   }
   if (e == hipSuccess && dbias != nullptr) {
-    hipLaunchKernelGGL(dbias_kernel, dim3((l.N + 255) / 256), dim3(256), 0, st, part, prep_chunks(l), l.N, dbias);
+    hipLaunchKernelGGL(dbias_kernel, dim3((l.N + 15) / 16), dim3(256), 0, st, part, prep_chunks(l), l.N, dbias);
     e = hipGetLastError();
   }
   const uint16_t* d = copy != nullptr ? copy : static_cast<const uint16_t*>(dy);

@@ -6,16 +6,17 @@
 
 namespace moe {
 
-// Tile shapes (columns x rows), all 8 wavefronts.  kSlice: us per slice of 64
-// terms once the stream runs, kTile: us to store a tile, measured on MI355X
-// (8192 x 14336 x 4096 for the 256 x 256 tile: 1370 TFLOP/s; 2048 x 4096 x 4096
-// for 256 x 128: 1120; 1024 x 4096 x 4096 for 128 x 128: 940; 509 x 4096 x 2048
-// for 128 x 64: 560).  A smaller tile reads more bytes per product but leaves
-// fewer CUs idle and needs less splitting.
-struct Tile256x256 { static constexpr int NS = 2, WR = 4, WC = 2, WA = 4, WB = 8; static constexpr double kSlice = 1.48, kTile = 4.0; };
-struct Tile256x128 { static constexpr int NS = 3, WR = 4, WC = 2, WA = 4, WB = 4; static constexpr double kSlice = 0.86, kTile = 2.0; };
-struct Tile128x128 { static constexpr int NS = 4, WR = 4, WC = 2, WA = 2, WB = 4; static constexpr double kSlice = 0.50, kTile = 1.0; };
-struct Tile128x64 { static constexpr int NS = 6, WR = 4, WC = 2, WA = 2, WB = 2; static constexpr double kSlice = 0.345, kTile = 0.5; };
+// Tile shapes (columns x rows), all 8 wavefronts.  A smaller tile reads more
+// bytes per product but leaves fewer CUs idle and needs less splitting.
+// kSlice: us per slice of 64 terms once the stream runs, by how many operands are
+// stored [t][r] (0 forward, 1 dx, 2 dw: the transposing reads take LDS twice as
+// long per byte, which binds the smaller tiles); kTile: us a tile costs beyond
+// its slices.  Measured on MI355X: 4096^3 gives the slices (256 x 256: 1362 / 1322
+// / 1241 TFLOP/s, 128 x 64: 723 / 488 / 406), 4099 x 4096 x 256 the tiles.
+struct Tile256x256 { static constexpr int NS = 2, WR = 4, WC = 2, WA = 4, WB = 8; static constexpr double kSlice[3] = {1.45, 1.50, 1.61}, kTile = 4.5; };
+struct Tile256x128 { static constexpr int NS = 3, WR = 4, WC = 2, WA = 4, WB = 4; static constexpr double kSlice[3] = {0.86, 0.93, 1.02}, kTile = 2.7; };
+struct Tile128x128 { static constexpr int NS = 4, WR = 4, WC = 2, WA = 2, WB = 4; static constexpr double kSlice[3] = {0.51, 0.66, 0.76}, kTile = 1.6; };
+struct Tile128x64 { static constexpr int NS = 6, WR = 4, WC = 2, WA = 2, WB = 2; static constexpr double kSlice[3] = {0.355, 0.535, 0.645}, kTile = 1.2; };
 template <class C> using GeomOf = ProductGeom<C::NS, C::WR, C::WC, C::WA, C::WB>;
 
 // Splitting a tail costs a second launch, and its partial tiles are written and
@@ -31,7 +32,7 @@ struct ProductPlan {
   size_t workspace = 0;
 
   template <class C>
-  static ProductPlan of(int rows, int cols, int len) {
+  static ProductPlan of(int rows, int cols, int len, int slow) {
     using G = GeomOf<C>;
     ProductPlan best;
     const int64_t cus = std::min<int64_t>(device_cu_count(), kMaxPersistentGroups) / 8 * 8;
@@ -46,7 +47,7 @@ struct ProductPlan {
       p.grid = (int)std::max<int64_t>(8, std::min<int64_t>(cus, most));
       const TileShare s = TileShare::of((int)tiles, 0, p.grid / 8, p.KT, p.split);      // the largest share
       const double parts = p.split ? 8.0 * (p.grid / 8 + s.tail) * G::PARTIAL * 4 : 0;
-      p.cost = ((double)s.R * p.KT + (p.split ? s.P : s.tail > 0 ? p.KT : 0)) * C::kSlice +
+      p.cost = ((double)s.R * p.KT + (p.split ? s.P : s.tail > 0 ? p.KT : 0)) * C::kSlice[slow] +
                (s.R + (s.tail > 0 ? 1 : 0)) * C::kTile + (p.split ? kJoinFixed + kJoinPerByte * parts : 0);
       p.workspace = p.split ? (size_t)p.grid * 2 * G::PARTIAL * 4 : 0;
       if (p.cost < best.cost) best = p;
@@ -57,9 +58,9 @@ struct ProductPlan {
 
 // Calls run(tile shape, plan) with the cheapest of the four.
 template <class F>
-auto with_plan(int rows, int cols, int len, F&& run) {
-  const ProductPlan a = ProductPlan::of<Tile256x256>(rows, cols, len), b = ProductPlan::of<Tile256x128>(rows, cols, len),
-                    c = ProductPlan::of<Tile128x128>(rows, cols, len), d = ProductPlan::of<Tile128x64>(rows, cols, len);
+auto with_plan(int rows, int cols, int len, int slow, F&& run) {
+  const ProductPlan a = ProductPlan::of<Tile256x256>(rows, cols, len, slow), b = ProductPlan::of<Tile256x128>(rows, cols, len, slow),
+                    c = ProductPlan::of<Tile128x128>(rows, cols, len, slow), d = ProductPlan::of<Tile128x64>(rows, cols, len, slow);
   const double least = std::min(std::min(a.cost, b.cost), std::min(c.cost, d.cost));
   if (a.cost == least) return run(Tile256x256{}, a);
   if (b.cost == least) return run(Tile256x128{}, b);
@@ -67,14 +68,14 @@ auto with_plan(int rows, int cols, int len, F&& run) {
   return run(Tile128x64{}, d);
 }
 
-inline size_t product_workspace(int rows, int cols, int len) {
-  return with_plan(rows, cols, len, [](auto, const ProductPlan& p) { return p.workspace; });
+inline size_t product_workspace(int rows, int cols, int len, int slow) {
+  return with_plan(rows, cols, len, slow, [](auto, const ProductPlan& p) { return p.workspace; });
 }
 
 template <bool PSLOW, bool QSLOW, int ACT>
 hipError_t launch_product(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, int rows, int cols,
                           int len, void* partials, const Epilogue& ep, hipStream_t st) {
-  return with_plan(rows, cols, len, [&](auto tile, const ProductPlan& p) {
+  return with_plan(rows, cols, len, (PSLOW ? 1 : 0) + (QSLOW ? 1 : 0), [&](auto tile, const ProductPlan& p) {
     using C = decltype(tile);
     using G = GeomOf<C>;
     const ProductArgs a{P, Q, ldp, ldq, rows, cols, len, p.row_tiles, p.col_tiles, p.split,
