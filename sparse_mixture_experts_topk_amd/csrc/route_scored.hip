@@ -62,20 +62,24 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
   return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+// Reductions over the wavefront by DPP: row shifts within 16 lanes, then the two
+// row broadcasts, leave the result in lane 63, read back as a uniform value.
 template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, false);
+__device__ __forceinline__ uint32_t dpp_or(uint32_t none, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROW_MASK, 0xF, false);
 }
-// Largest key of the wavefront, uniform.  DPP row shifts within 16 lanes, then
-// the two row broadcasts, leave it in lane 63.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max(v, dpp_or_zero<0x111, 0xF>(v));
-  v = max(v, dpp_or_zero<0x112, 0xF>(v));
-  v = max(v, dpp_or_zero<0x114, 0xF>(v));
-  v = max(v, dpp_or_zero<0x118, 0xF>(v));
-  v = max(v, dpp_or_zero<0x142, 0xA>(v));
-  v = max(v, dpp_or_zero<0x143, 0xC>(v));
+template <class Op>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t none, Op op) {
+  v = op(v, dpp_or<0x111, 0xF>(none, v));
+  v = op(v, dpp_or<0x112, 0xF>(none, v));
+  v = op(v, dpp_or<0x114, 0xF>(none, v));
+  v = op(v, dpp_or<0x118, 0xF>(none, v));
+  v = op(v, dpp_or<0x142, 0xA>(none, v));
+  v = op(v, dpp_or<0x143, 0xC>(none, v));
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
 #pragma unroll
@@ -85,36 +89,99 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
   }
   return v;
 }
-template <class R>
-__device__ __forceinline__ R wave_sum(R v) {
+__device__ __forceinline__ float wave_sum(float v) {
+  return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
   return v;
 }
-template <class R>
-__device__ __forceinline__ R wave_max_value(R v) {
+__device__ __forceinline__ float wave_max_value(float v) {
+  return __uint_as_float(wave_reduce(__float_as_uint(v), 0xff800000u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {      // lane uniform
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+// Sum and maximum over the 8 lanes that hold the chosen experts (equal in all 8).
+__device__ __forceinline__ float xor_lane(float v, int step) {       // partner within 8: 1, 2 by quad, 7 - i for 4
+  const int b = (int)__float_as_uint(v);
+  int o;
+  if (step == 0) o = __builtin_amdgcn_mov_dpp(b, 0xB1, 0xF, 0xF, false);
+  else if (step == 1) o = __builtin_amdgcn_mov_dpp(b, 0x4E, 0xF, 0xF, false);
+  else o = __builtin_amdgcn_mov_dpp(b, 0x141, 0xF, 0xF, false);
+  return __uint_as_float((uint32_t)o);
+}
+__device__ __forceinline__ float sum8(float v) {
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const R o = __shfl_xor(v, m);
-    v = o > v ? o : v;
-  }
+  for (int i = 0; i < 3; ++i) v += xor_lane(v, i);
+  return v;
+}
+__device__ __forceinline__ float max8(float v) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) v = fmaxf(v, xor_lane(v, i));
   return v;
 }
 
-__device__ __forceinline__ float exp_r(float v) { return expf(v); }
+// e^v from the hardware's exp2 (1 ulp): the product with log2(e) is carried in two
+// parts, so that the argument's rounding does not grow with |v|; a few ulp in all.
+// -inf gives 0.
+__device__ __forceinline__ float exp_r(float v) {
+  const float hi = 1.44269502f, lo = 1.92596299e-8f;          // log2(e)
+  const float t = v * hi;
+  const float r = fmaf(v, lo, fmaf(v, hi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return v > -200.0f ? fmaf(e, r * 0.693147182f, e) : 0.0f;
+}
 __device__ __forceinline__ double exp_r(double v) { return exp(v); }
+__device__ __forceinline__ float rcp_r(float v) { return __builtin_amdgcn_rcpf(v); }     // 1 ulp
+__device__ __forceinline__ double rcp_r(double v) { return 1.0 / v; }
 
-// sigmoid(l) without overflow: e^min(l,0) / (1 + e^-|l|)
+// sigmoid(l) and 1 - sigmoid(l) without overflow or cancellation, from e^-|l|
+template <class R>
+__device__ __forceinline__ void sigmoids(R l, R& s, R& below) {
+  const R e = exp_r(l < 0 ? l : -l), r = rcp_r(R(1) + e);
+  s = l < 0 ? e * r : r;
+  below = l < 0 ? r : e * r;
+}
 template <class R>
 __device__ __forceinline__ R sigmoid(R l) {
-  const R e = exp_r(l < 0 ? l : -l);
-  return (l < 0 ? e : R(1)) / (R(1) + e);
+  R s, below;
+  sigmoids(l, s, below);
+  return s;
+}
+
+// The renormalised weight of each of the 8 lanes' chosen logits: e^l (softmax) or
+// sigmoid(l) over their sum, every term taken relative to the largest e^l, so that
+// it holds where all scores underflow; 0 where every chosen logit is -inf.
+__device__ __forceinline__ float chosen_weight(float lj, bool mine, bool softmax) {
+  float m = fmaxf(max8(lj), -3.402823466e38f);
+  float w;
+  if (softmax) {
+    w = exp_r(lj - m);
+  } else {
+    m = fminf(m, 0.0f);
+    w = exp_r(fminf(lj, 0.0f) - m) * rcp_r(1.0f + exp_r(-fabsf(lj)));
+  }
+  if (!mine) w = 0.0f;
+  const float sum = sum8(w);
+  return sum > 0.0f ? w / sum : 0.0f;
 }
 
 struct RouteArgs {
   int T, E, k;
-  int n_groups, group_size, lanes_per_group, topk_groups, group_top;
-  bool softmax, renormalize;
+  int n_groups, group_size, lanes_per_group, group_shift, topk_groups, group_top;
+  bool softmax, renormalize, vector;
   float scale;
   const float* logits;
   const float* bias;
@@ -124,23 +191,36 @@ struct RouteArgs {
   int32_t* next_ids;
 };
 
-// Scores of the lane's experts (0 at positions past the group), in R.
+// Scores of the lane's experts (0 at positions past the group), in R; returns a
+// bound of the largest score of the token.
 template <class R, int PER>
-__device__ __forceinline__ void lane_scores(const RouteArgs& a, const float (&l)[PER], const bool (&in)[PER],
-                                            float lmax, R (&s)[PER]) {
+__device__ __forceinline__ R lane_scores(const RouteArgs& a, const float (&l)[PER], const bool (&in)[PER],
+                                         float lmax, R (&s)[PER]) {
+  if (!a.softmax) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p) s[p] = in[p] ? sigmoid<R>((R)l[p]) : R(0);
+    return R(1);
+  }
   R z = 0;
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
-    if (a.softmax) s[p] = in[p] ? exp_r((R)l[p] - (R)lmax) : R(0);
-    else s[p] = in[p] ? sigmoid<R>((R)l[p]) : R(0);
+    s[p] = in[p] ? exp_r((R)l[p] - (R)lmax) : R(0);
     z += s[p];
   }
-  if (a.softmax) {
-    z = wave_sum(z);
-    const R inv = z > 0 ? R(1) / z : R(0);       // every logit -inf: no score
+  z = wave_sum(z);
+  const R inv = z > 0 ? R(1) / z : R(0);           // every logit -inf: no score
 #pragma unroll
-    for (int p = 0; p < PER; ++p) s[p] *= inv;
-  }
+  for (int p = 0; p < PER; ++p) s[p] *= inv;
+  return inv;
+}
+
+// Merges the two largest values of each half of a part: (g1, g2) with the partner's.
+template <class R>
+__device__ __forceinline__ void merge_top2(R& g1, R& g2, R o1, R o2) {
+  const R lo = o1 > g1 ? g1 : o1;
+  g1 = o1 > g1 ? o1 : g1;
+  const R hi2 = o2 > g2 ? o2 : g2;
+  g2 = lo > hi2 ? lo : hi2;
 }
 
 // The `rounds` best experts of the open groups into lanes 0 .. rounds - 1 of
@@ -152,19 +232,11 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
                                        R (&s)[PER], int& chosen) {
   using Key = std::conditional_t<sizeof(R) == 4, uint32_t, uint64_t>;
   constexpr bool CHECK = sizeof(R) == 4;
-  const int lig = lane & (a.lanes_per_group - 1), grp = lane / a.lanes_per_group;
-  if (need_scores) lane_scores<R, PER>(a, l, in, lmax, s);
+  const int lig = lane & (a.lanes_per_group - 1), grp = lane >> a.group_shift;
   const bool by_logit = a.bias == nullptr;
   bool near = false;
   float score_tol = 0;
-  if constexpr (CHECK) {
-    if (need_scores && (!by_logit || a.n_groups > 1)) {
-      float m = 0;
-#pragma unroll
-      for (int p = 0; p < PER; ++p) m = fmaxf(m, (float)s[p]);
-      score_tol = kScoreErr * __uint_as_float(wave_max(__float_as_uint(m)));   // s >= 0: ordered as integers
-    }
-  }
+  if (need_scores) score_tol = kScoreErr * (float)lane_scores<R, PER>(a, l, in, lmax, s);
   bool open = grp < a.n_groups;
   if (a.n_groups > 1) {
     // the group's score: its two largest values merged over the part's lanes
@@ -181,39 +253,55 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
       g2 = v > g1 ? g1 : (v > g2 ? v : g2);
       g1 = v > g1 ? v : g1;
     }
-    for (int m = 1; m < a.lanes_per_group; m <<= 1) {
-      const R o1 = __shfl_xor(g1, m), o2 = __shfl_xor(g2, m);
-      const R lo = o1 > g1 ? g1 : o1;
-      g1 = o1 > g1 ? o1 : g1;
-      const R hi2 = o2 > g2 ? o2 : g2;
-      g2 = lo > hi2 ? lo : hi2;
+    if constexpr (CHECK) {
+      // partners 1, 2 by quad; within 8 the mirror, whose quads already agree
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (a.lanes_per_group > (1 << i)) merge_top2(g1, g2, xor_lane(g1, i), xor_lane(g2, i));
+      for (int m = 8; m < a.lanes_per_group; m <<= 1) merge_top2(g1, g2, __shfl_xor(g1, m), __shfl_xor(g2, m));
+    } else {
+      for (int m = 1; m < a.lanes_per_group; m <<= 1) merge_top2(g1, g2, __shfl_xor(g1, m), __shfl_xor(g2, m));
     }
     const R gs = a.group_top == 1 ? g1 : g1 + g2;
+    const bool exact = a.group_top == 1 && by_logit;
+    const float tol = 2 * score_tol + 2 * kSumErr * fabsf((float)gs);
     int rank = 0;
     for (int o = 0; o < a.n_groups; ++o) {
-      const R os = __shfl(gs, o * a.lanes_per_group);
+      const R os = lane_value(gs, o << a.group_shift);
       rank += (os > gs || (os == gs && o < grp)) ? 1 : 0;
-      if constexpr (CHECK) {
-        if (!(a.group_top == 1 && by_logit) && open && o != grp)
-          near |= !(fabsf(os - gs) > 2 * score_tol + 2 * kSumErr * fabsf(gs));
-      }
+      if constexpr (CHECK) near |= !exact && o != grp && !(fabsf(os - gs) > tol);
     }
+    near &= open;
     open = open && rank < a.topk_groups;
   }
-  Key key[PER], best = 0;
-  int bp = 0;
+  // the lane's keys in descending order (equal ones by index), each with its position
+  Key key[PER];
+  int pos[PER];
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     key[p] = !(open && in[p]) ? Key(0) : by_logit ? ordered((R)l[p]) : ordered(s[p] + (R)b[p]);
-    if (key[p] > best) { best = key[p]; bp = p; }
+    pos[p] = p;
   }
+#pragma unroll
+  for (int i = 1; i < PER; ++i)
+#pragma unroll
+    for (int j = i; j > 0; --j) {
+      const bool up = key[j] > key[j - 1];
+      const Key k0 = key[j - 1];
+      const int p0 = pos[j - 1];
+      key[j - 1] = up ? key[j] : k0;
+      pos[j - 1] = up ? pos[j] : p0;
+      key[j] = up ? k0 : key[j];
+      pos[j] = up ? p0 : pos[j];
+    }
+  const int first = grp * a.group_size + lig * PER;
   chosen = -1;
   float prev = 0;
   for (int r = 0; r < rounds; ++r) {
-    const Key top = wave_max(best);
+    const Key top = wave_max(key[0]);
     if (top == 0) break;                                   // uniform: no candidate left
-    const int owner = __builtin_amdgcn_readfirstlane((int)__builtin_ctzll(__ballot(best == top)));
-    const int e = __builtin_amdgcn_readlane(grp * a.group_size + lig * PER + bp, owner);
+    const int owner = (int)__builtin_ctzll(__ballot(key[0] == top));       // the lowest index of equals
+    const int e = __builtin_amdgcn_readlane(first + pos[0], owner);
     if constexpr (CHECK) {
       if (!by_logit) {
         const float v = from_ordered(top);
@@ -222,17 +310,35 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
       }
     }
     chosen = lane == r ? e : chosen;
-    if (lane == owner) {
-      best = 0;
-      const int taken = bp;
+    if (lane == owner) {                                   // its next one moves up
 #pragma unroll
-      for (int p = 0; p < PER; ++p) {
-        if (p == taken) key[p] = 0;
-        if (key[p] > best) { best = key[p]; bp = p; }
+      for (int p = 0; p + 1 < PER; ++p) {
+        key[p] = key[p + 1];
+        pos[p] = pos[p + 1];
       }
+      key[PER - 1] = 0;
     }
   }
   return CHECK && __ballot(near) != 0;
+}
+
+// The lane's PER consecutive values; vector: whole groups of 4 at 16-byte aligned places.
+template <int PER>
+__device__ __forceinline__ void load_lane(const float* p, const bool (&in)[PER], bool vector, float (&v)[PER]) {
+  if constexpr (PER % 4 == 0) {
+    if (vector) {
+#pragma unroll
+      for (int q = 0; q < PER; q += 4)
+        if (in[q]) {
+          const float4 f = *reinterpret_cast<const float4*>(p + q);
+          v[q] = f.x; v[q + 1] = f.y; v[q + 2] = f.z; v[q + 3] = f.w;
+        }
+      return;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < PER; ++q)
+    if (in[q]) v[q] = p[q];
 }
 
 // HBM-bound in principle (4 E bytes per token in, 8 k out); in practice the
@@ -242,7 +348,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= a.T) return;
-  const int lig = lane & (a.lanes_per_group - 1), grp = lane / a.lanes_per_group;
+  const int lig = lane & (a.lanes_per_group - 1), grp = lane >> a.group_shift;
   const int first = grp * a.group_size + lig * PER;          // the lane's first expert
   const float* row = a.logits + (int64_t)t * a.E;
   float l[PER], b[PER];
@@ -250,9 +356,11 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     in[p] = grp < a.n_groups && lig * PER + p < a.group_size;
-    l[p] = in[p] ? row[first + p] : -INFINITY;
-    b[p] = in[p] && a.bias != nullptr ? a.bias[first + p] : 0.0f;
+    l[p] = -INFINITY;
+    b[p] = 0.0f;
   }
+  load_lane<PER>(row + first, in, a.vector, l);
+  if (a.bias != nullptr) load_lane<PER>(a.bias + first, in, a.vector, b);
   // the softmax of all experts is not needed where the weights are
   // renormalised over the chosen ones and nothing else looks at scores
   const bool need_scores = a.bias != nullptr || (a.n_groups > 1 && a.group_top > 1) || a.scores != nullptr ||
@@ -280,28 +388,14 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
   const float lj = mine ? row[chosen] : -INFINITY;
   float w;
   if (a.renormalize) {
-    float m = lj;
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-    m = fmaxf(m, -3.402823466e38f);
-    if (a.softmax) {
-      w = expf(lj - m);
-    } else {
-      m = fminf(m, 0.0f);
-      w = expf(fminf(lj, 0.0f) - m) / (1.0f + expf(-fabsf(lj)));
-    }
-    if (!mine) w = 0.0f;
-    float sum = w;
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor(sum, d);
-    w = sum > 0.0f ? w / sum : 0.0f;
+    w = chosen_weight(lj, mine, a.softmax);
   } else if (a.softmax) {
     // the token's softmax, its denominator from the lanes' experts again
     float z = 0;
 #pragma unroll
-    for (int p = 0; p < PER; ++p) z += in[p] ? expf(l[p] - lmax) : 0.0f;
+    for (int p = 0; p < PER; ++p) z += in[p] ? exp_r(l[p] - lmax) : 0.0f;
     z = wave_sum(z);
-    w = z > 0.0f ? expf(lj - lmax) / z : 0.0f;
+    w = z > 0.0f ? exp_r(lj - lmax) / z : 0.0f;
   } else {
     w = sigmoid(lj);
   }
@@ -315,7 +409,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
 
 struct RouteBackArgs {
   int T, E, k;
-  bool softmax, renormalize;
+  bool softmax, renormalize, vector;
   float scale;
   const float* logits;
   const int32_t* ids;
@@ -338,17 +432,23 @@ struct RouteBackArgs {
 // HBM-bound: reads 4 E bytes (8 E with D) and writes 4 E per token.
 template <int PER>
 __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_kernel(const RouteBackArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(16))) float at_chosen[kRouteWaves][kWave * PER];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x * kRouteWaves + wave;
   if (t >= a.T) return;
   const int64_t base = (int64_t)t * a.E;
   float l[PER], d[PER];
+  bool in[PER];
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
-    const int e = lane * PER + p;
-    l[p] = e < a.E ? a.logits[base + e] : -INFINITY;
-    d[p] = e < a.E && a.dscores != nullptr ? a.dscores[base + e] : 0.0f;
+    in[p] = lane * PER + p < a.E;
+    l[p] = -INFINITY;
+    d[p] = 0.0f;
   }
+  // renormalised softmax weights do not see the other experts' logits
+  const bool need = !(a.softmax && a.renormalize) || a.dscores != nullptr;
+  if (need) load_lane<PER>(a.logits + base + lane * PER, in, a.vector, l);
+  if (a.dscores != nullptr) load_lane<PER>(a.dscores + base + lane * PER, in, a.vector, d);
   // lanes j < k: the j-th chosen expert (an id outside the row adds nothing)
   int id = lane < a.k ? a.ids[(int64_t)t * a.k + lane] : -1;
   if (id >= a.E) id = -1;
@@ -356,40 +456,24 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_ker
   float q = a.scale * g;
   if (a.renormalize) {
     const float lj = id >= 0 ? a.logits[base + id] : -INFINITY;
-    float m = lj;
-#pragma unroll
-    for (int x = 1; x < 8; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-    m = fmaxf(m, -3.402823466e38f);
-    float w;
-    if (a.softmax) {
-      w = expf(lj - m);
-    } else {
-      m = fminf(m, 0.0f);
-      w = expf(fminf(lj, 0.0f) - m) / (1.0f + expf(-fabsf(lj)));
-    }
-    if (id < 0) w = 0.0f;
-    float sum = w;
-#pragma unroll
-    for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor(sum, x);
-    w = sum > 0.0f ? w / sum : 0.0f;
+    const float w = chosen_weight(lj, id >= 0, a.softmax);
     float c = 0.0f;
 #pragma unroll
     for (int x = 1; x < 8; ++x) c += __shfl_xor(w, x) * (g - __shfl_xor(g, x));
     q = a.scale * w * c;
   }
-  float sel[PER];
+  // q to the lanes that hold the chosen experts, through the wavefront's own LDS
+  // row (LDS operations of one wavefront execute in order)
+  float* row = at_chosen[wave];
 #pragma unroll
-  for (int p = 0; p < PER; ++p) sel[p] = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int ej = __builtin_amdgcn_readlane(id, j);
-    const float qj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(q), j));
+  for (int p = 0; p < PER; ++p) row[lane * PER + p] = 0.0f;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (id >= 0) row[id] = q;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  float sel[PER], out[PER];
 #pragma unroll
-    for (int p = 0; p < PER; ++p)
-      if (lane * PER + p == ej) sel[p] += qj;
-  }
-  float out[PER];
+  for (int p = 0; p < PER; ++p) sel[p] = row[lane * PER + p];
   if (a.softmax) {
-    const bool need = !a.renormalize || a.dscores != nullptr;
     if (need) {
       float lmax = -INFINITY;
 #pragma unroll
@@ -398,7 +482,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_ker
       float s[PER], z = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int p = 0; p < PER; ++p) {
-        s[p] = expf(l[p] - lmax);
+        s[p] = exp_r(l[p] - lmax);
         z += s[p];
         if (!a.renormalize) d[p] += sel[p];
         dot += d[p] * s[p];
@@ -416,16 +500,21 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_ker
   } else {
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-      const float below = sigmoid(-l[p]);                      // 1 - s
-      const float s = sigmoid(l[p]);
+      float s, below;                                          // below: 1 - s
+      sigmoids(l[p], s, below);
       out[p] = a.renormalize ? sel[p] * below + d[p] * s * below : (d[p] + sel[p]) * s * below;
     }
   }
-#pragma unroll
-  for (int p = 0; p < PER; ++p) {
-    const int e = lane * PER + p;
-    if (e < a.E) a.dlogits[base + e] = out[p];
+  float* o = a.dlogits + base + lane * PER;
+  if constexpr (PER % 4 == 0) {
+    if (a.vector) {
+      if (in[0]) *reinterpret_cast<float4*>(o) = make_float4(out[0], out[1], out[2], out[3]);
+      return;
+    }
   }
+#pragma unroll
+  for (int p = 0; p < PER; ++p)
+    if (in[p]) o[p] = out[p];
 }
 
 }  // namespace
@@ -439,7 +528,9 @@ hipError_t launch_route_scored(const moe_shape_t& s, const moe_router_t& r, cons
   int parts = 1;
   while (parts < r.n_groups) parts *= 2;
   a.lanes_per_group = kWave / parts;
-  // every group open: groups decide nothing
+  a.group_shift = 6;
+  while ((1 << a.group_shift) > a.lanes_per_group) --a.group_shift;
+  a.vector = a.group_size % 4 == 0;
   a.topk_groups = r.topk_groups;
   a.group_top = r.group_top;
   a.softmax = r.score == MOE_SCORE_SOFTMAX;
@@ -458,8 +549,8 @@ hipError_t launch_route_scored(const moe_shape_t& s, const moe_router_t& r, cons
 hipError_t launch_route_scored_backward(const moe_shape_t& s, const moe_router_t& r, const float* logits,
                                         const int32_t* ids, const float* dweights, const float* dscores,
                                         float* dlogits, hipStream_t st) {
-  RouteBackArgs a{s.T, s.n_experts, s.top_k, r.score == MOE_SCORE_SOFTMAX, r.renormalize != 0, r.scale,
-                  logits, ids, dweights, dscores, dlogits};
+  RouteBackArgs a{s.T, s.n_experts, s.top_k, r.score == MOE_SCORE_SOFTMAX, r.renormalize != 0, s.n_experts % 4 == 0,
+                  r.scale, logits, ids, dweights, dscores, dlogits};
   const dim3 grid((unsigned)((s.T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
   if (a.E <= 64) hipLaunchKernelGGL(route_scored_backward_kernel<1>, grid, block, 0, st, a);
   else if (a.E <= 128) hipLaunchKernelGGL(route_scored_backward_kernel<2>, grid, block, 0, st, a);
