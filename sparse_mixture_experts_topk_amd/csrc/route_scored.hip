@@ -27,11 +27,11 @@
 // balance bias the order of c is that of the logits and the keys are the
 // logits themselves.  Otherwise the wavefront works in fp32 and looks at
 // every gap that decided something (between consecutive chosen experts, the
-// last chosen and the first left out, any two groups): one within the fp32
-// error of the two values (kScoreErr of the largest score, kSumErr of the
-// choice) sends the token through the same steps in fp64, where scores of
-// distinct fp32 logits are distinct until they saturate.  With 256 experts
-// and N(0,1) logits about one token in 500 goes that way.
+// last chosen and the first left out, the last open group and the first closed):
+// one within the fp32 error of the two values (k...Err) sends the token through
+// the same steps in fp64, where scores of distinct fp32 logits are distinct until
+// they saturate.  With 256 experts and N(0,1) logits about one token in 500 goes
+// that way.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -41,10 +41,12 @@ namespace moe {
 namespace {
 
 constexpr int kRouteWaves = 4;     // tokens per workgroup
-// fp32 softmax or sigmoid: under 1e-6 of the largest score (expf and the sum
-// over at most 256 terms); a difference of two has twice that.  c = s + b and
-// the sum of two choices round once more, 2^-24 of the value each.
-constexpr float kScoreErr = 4e-6f;
+// Errors of a difference of two fp32 scores: softmax under 1.2e-6 of the largest
+// score for each (exp, the sum over at most 256 terms, one division), sigmoid
+// under 2.5e-7.  c = s + b and the sum of two choices round once more, 2^-24 of
+// the value each.
+constexpr float kSoftmaxErr = 4e-6f;
+constexpr float kSigmoidErr = 1e-6f;
 constexpr float kSumErr = 5e-7f;
 
 // Order-preserving map to unsigned integers; 0 is kept for "no candidate".
@@ -181,7 +183,7 @@ __device__ __forceinline__ float chosen_weight(float lj, bool mine, bool softmax
 struct RouteArgs {
   int T, E, k;
   int n_groups, group_size, lanes_per_group, group_shift, topk_groups, group_top;
-  bool softmax, renormalize, vector;
+  bool renormalize, vector;
   float scale;
   const float* logits;
   const float* bias;
@@ -193,18 +195,18 @@ struct RouteArgs {
 
 // Scores of the lane's experts (0 at positions past the group), in R; returns a
 // bound of the largest score of the token.
-template <class R, int PER>
-__device__ __forceinline__ R lane_scores(const RouteArgs& a, const float (&l)[PER], const bool (&in)[PER],
-                                         float lmax, R (&s)[PER]) {
-  if (!a.softmax) {
+template <class R, int PER, bool SOFTMAX>
+__device__ __forceinline__ R lane_scores(const float (&l)[PER], const bool (&in)[PER], float lmax, R (&s)[PER]) {
+  if constexpr (!SOFTMAX) {
 #pragma unroll
-    for (int p = 0; p < PER; ++p) s[p] = in[p] ? sigmoid<R>((R)l[p]) : R(0);
+    for (int p = 0; p < PER; ++p) s[p] = sigmoid<R>((R)l[p]);       // past the group: l = -inf
     return R(1);
   }
   R z = 0;
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
-    s[p] = in[p] ? exp_r((R)l[p] - (R)lmax) : R(0);
+    const R e = exp_r((R)l[p] - (R)lmax);
+    s[p] = in[p] ? e : R(0);
     z += s[p];
   }
   z = wave_sum(z);
@@ -223,33 +225,30 @@ __device__ __forceinline__ void merge_top2(R& g1, R& g2, R o1, R o2) {
   g2 = lo > hi2 ? lo : hi2;
 }
 
-// The `rounds` best experts of the open groups into lanes 0 .. rounds - 1 of
+// The `rounds` <= 16 best experts of the open groups into lanes 0 .. rounds - 1 of
 // `chosen` (-1: no candidate left).  Returns whether fp32 could have decided
 // any step wrongly (always false in fp64).
-template <class R, int PER>
+template <class R, int PER, bool SOFTMAX, bool BIAS, bool GROUPED>
 __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER], const bool (&in)[PER],
                                        const float (&b)[PER], float lmax, bool need_scores, int lane, int rounds,
                                        R (&s)[PER], int& chosen) {
   using Key = std::conditional_t<sizeof(R) == 4, uint32_t, uint64_t>;
   constexpr bool CHECK = sizeof(R) == 4;
   const int lig = lane & (a.lanes_per_group - 1), grp = lane >> a.group_shift;
-  const bool by_logit = a.bias == nullptr;
   bool near = false;
   float score_tol = 0;
-  if (need_scores) score_tol = kScoreErr * (float)lane_scores<R, PER>(a, l, in, lmax, s);
+  if (BIAS || need_scores)
+    score_tol = (SOFTMAX ? kSoftmaxErr : kSigmoidErr) * (float)lane_scores<R, PER, SOFTMAX>(l, in, lmax, s);
   bool open = grp < a.n_groups;
-  if (a.n_groups > 1) {
+  if constexpr (GROUPED) {
     // the group's score: its two largest values merged over the part's lanes
     const R none = -(R)INFINITY;
+    const bool by_logit = !BIAS && a.group_top == 1;
     R g1 = none, g2 = none;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-      R v = none;
-      if (in[p]) {
-        if (a.group_top == 1 && by_logit) v = (R)l[p];
-        else v = s[p] + (by_logit ? R(0) : (R)b[p]);
-        if (v != v) v = none;
-      }
+      R v = by_logit ? (R)l[p] : BIAS ? s[p] + (R)b[p] : s[p];
+      v = in[p] && v == v ? v : none;
       g2 = v > g1 ? g1 : (v > g2 ? v : g2);
       g1 = v > g1 ? v : g1;
     }
@@ -263,23 +262,28 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
       for (int m = 1; m < a.lanes_per_group; m <<= 1) merge_top2(g1, g2, __shfl_xor(g1, m), __shfl_xor(g2, m));
     }
     const R gs = a.group_top == 1 ? g1 : g1 + g2;
-    const bool exact = a.group_top == 1 && by_logit;
-    const float tol = 2 * score_tol + 2 * kSumErr * fabsf((float)gs);
     int rank = 0;
     for (int o = 0; o < a.n_groups; ++o) {
       const R os = lane_value(gs, o << a.group_shift);
       rank += (os > gs || (os == gs && o < grp)) ? 1 : 0;
-      if constexpr (CHECK) near |= !exact && o != grp && !(fabsf(os - gs) > tol);
     }
-    near &= open;
+    const bool group = open;
     open = open && rank < a.topk_groups;
+    if constexpr (CHECK) {
+      if (!by_logit) {
+        const float kept = -wave_max_value(open ? -(float)gs : -INFINITY);
+        const float shut = wave_max_value(group && !open ? (float)gs : -INFINITY);
+        near = !(kept - shut > 2 * score_tol + 2 * kSumErr * fmaxf(fabsf(kept), fabsf(shut)));
+      }
+    }
   }
   // the lane's keys in descending order (equal ones by index), each with its position
   Key key[PER];
   int pos[PER];
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
-    key[p] = !(open && in[p]) ? Key(0) : by_logit ? ordered((R)l[p]) : ordered(s[p] + (R)b[p]);
+    const Key k = ordered(BIAS ? s[p] + (R)b[p] : (R)l[p]);
+    key[p] = open && in[p] ? k : Key(0);
     pos[p] = p;
   }
 #pragma unroll
@@ -295,21 +299,17 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
       pos[j] = up ? p0 : pos[j];
     }
   const int first = grp * a.group_size + lig * PER;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) pos[p] += first;
   chosen = -1;
-  float prev = 0;
+  Key value = 0;                                             // lane r: the r-th chosen key
   for (int r = 0; r < rounds; ++r) {
     const Key top = wave_max(key[0]);
     if (top == 0) break;                                   // uniform: no candidate left
     const int owner = (int)__builtin_ctzll(__ballot(key[0] == top));       // the lowest index of equals
-    const int e = __builtin_amdgcn_readlane(first + pos[0], owner);
-    if constexpr (CHECK) {
-      if (!by_logit) {
-        const float v = from_ordered(top);
-        if (r > 0) near |= !(prev - v > score_tol + kSumErr * fmaxf(fabsf(prev), fabsf(v)));
-        prev = v;
-      }
-    }
+    const int e = __builtin_amdgcn_readlane(pos[0], owner);
     chosen = lane == r ? e : chosen;
+    if constexpr (CHECK && BIAS) value = lane == r ? top : value;
     if (lane == owner) {                                   // its next one moves up
 #pragma unroll
       for (int p = 0; p + 1 < PER; ++p) {
@@ -318,6 +318,12 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
       }
       key[PER - 1] = 0;
     }
+  }
+  if constexpr (CHECK && BIAS) {
+    const Key after = (Key)__builtin_amdgcn_mov_dpp((int)value, 0x101, 0xF, 0xF, false);     // lane r + 1's
+    const float v = from_ordered(value), n = from_ordered(after);
+    if (lane + 1 < rounds && after != 0)
+      near |= !(v - n > score_tol + kSumErr * fmaxf(fabsf(v), fabsf(n)));
   }
   return CHECK && __ballot(near) != 0;
 }
@@ -343,7 +349,7 @@ __device__ __forceinline__ void load_lane(const float* p, const bool (&in)[PER],
 
 // HBM-bound in principle (4 E bytes per token in, 8 k out); in practice the
 // k + 1 selection rounds of each wavefront bound it.
-template <int PER>
+template <int PER, bool SOFTMAX, bool BIAS, bool GROUPED>
 __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const RouteArgs a) {
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -360,13 +366,12 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
     b[p] = 0.0f;
   }
   load_lane<PER>(row + first, in, a.vector, l);
-  if (a.bias != nullptr) load_lane<PER>(a.bias + first, in, a.vector, b);
+  if constexpr (BIAS) load_lane<PER>(a.bias + first, in, a.vector, b);
   // the softmax of all experts is not needed where the weights are
   // renormalised over the chosen ones and nothing else looks at scores
-  const bool need_scores = a.bias != nullptr || (a.n_groups > 1 && a.group_top > 1) || a.scores != nullptr ||
-                           (a.softmax && !a.renormalize);
+  const bool need_scores = BIAS || (GROUPED && a.group_top > 1) || a.scores != nullptr || (SOFTMAX && !a.renormalize);
   float lmax = -INFINITY;
-  if (a.softmax && need_scores) {
+  if (SOFTMAX && need_scores) {
 #pragma unroll
     for (int p = 0; p < PER; ++p) lmax = fmaxf(lmax, l[p]);
     lmax = fmaxf(wave_max_value(lmax), -3.402823466e38f);    // all -inf: every term e^-inf
@@ -374,9 +379,9 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
   const int want = a.k + (a.next_ids != nullptr ? 2 : 0);
   float s[PER];
   int chosen;
-  if (choose<float, PER>(a, l, in, b, lmax, need_scores, lane, want + 1, s, chosen)) {
+  if (choose<float, PER, SOFTMAX, BIAS, GROUPED>(a, l, in, b, lmax, need_scores, lane, BIAS ? want + 1 : want, s, chosen)) {
     double s64[PER];
-    choose<double, PER>(a, l, in, b, lmax, need_scores, lane, want, s64, chosen);
+    choose<double, PER, SOFTMAX, BIAS, GROUPED>(a, l, in, b, lmax, need_scores, lane, want, s64, chosen);
   }
   if (a.scores != nullptr) {
 #pragma unroll
@@ -388,8 +393,8 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
   const float lj = mine ? row[chosen] : -INFINITY;
   float w;
   if (a.renormalize) {
-    w = chosen_weight(lj, mine, a.softmax);
-  } else if (a.softmax) {
+    w = chosen_weight(lj, mine, SOFTMAX);
+  } else if (SOFTMAX) {
     // the token's softmax, its denominator from the lanes' experts again
     float z = 0;
 #pragma unroll
@@ -533,17 +538,30 @@ hipError_t launch_route_scored(const moe_shape_t& s, const moe_router_t& r, cons
   a.vector = a.group_size % 4 == 0;
   a.topk_groups = r.topk_groups;
   a.group_top = r.group_top;
-  a.softmax = r.score == MOE_SCORE_SOFTMAX;
   a.renormalize = r.renormalize != 0;
   a.scale = r.scale;
   a.logits = logits; a.bias = bias; a.ids = ids; a.weights = weights; a.scores = scores; a.next_ids = next_ids;
   const int per = (a.group_size + a.lanes_per_group - 1) / a.lanes_per_group;
   const dim3 grid((unsigned)((s.T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
-  if (per <= 1) hipLaunchKernelGGL(route_scored_kernel<1>, grid, block, 0, st, a);
-  else if (per <= 2) hipLaunchKernelGGL(route_scored_kernel<2>, grid, block, 0, st, a);
-  else if (per <= 4) hipLaunchKernelGGL(route_scored_kernel<4>, grid, block, 0, st, a);
-  else hipLaunchKernelGGL(route_scored_kernel<8>, grid, block, 0, st, a);
-  return hipGetLastError();
+  // groups that are all open decide nothing, but keep the lanes' layout
+  const bool softmax = r.score == MOE_SCORE_SOFTMAX, biased = bias != nullptr, grouped = r.topk_groups < r.n_groups;
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, st, a);
+    return hipGetLastError();
+  };
+  auto by_per = [&](auto sm, auto bi, auto gr) {
+    constexpr bool S = decltype(sm)::value, B = decltype(bi)::value, G = decltype(gr)::value;
+    if (per <= 1) return run(route_scored_kernel<1, S, B, G>);
+    if (per <= 2) return run(route_scored_kernel<2, S, B, G>);
+    if (per <= 4) return run(route_scored_kernel<4, S, B, G>);
+    return run(route_scored_kernel<8, S, B, G>);
+  };
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  if (softmax && biased) return grouped ? by_per(yes, yes, yes) : by_per(yes, yes, no);
+  if (softmax) return grouped ? by_per(yes, no, yes) : by_per(yes, no, no);
+  if (biased) return grouped ? by_per(no, yes, yes) : by_per(no, yes, no);
+  return grouped ? by_per(no, no, yes) : by_per(no, no, no);
 }
 
 hipError_t launch_route_scored_backward(const moe_shape_t& s, const moe_router_t& r, const float* logits,
