@@ -356,7 +356,7 @@ typedef struct {
  * make of them, so it depends on nothing but the row.
  * Logits may be -inf (a masked expert: score 0; a row of nothing else gets zero
  * weights) and balance_bias -inf (never chosen while another candidate is left);
- * NaN ranks below -inf.  The ids of a row are distinct and in [0, E) whatever
+ * NaN ranks as -inf.  The ids of a row are distinct and in [0, E) whatever
  * the contents.
  * Errors: MOE_ERR_INVALID_ARG for a router value outside its range, n_groups
  * that does not divide n_experts, group_top above the group's size, or fewer

@@ -20,7 +20,7 @@
 // position within the lane, orders experts by index, so "the lowest lane that
 // holds the maximum" settles ties.  Keys are the choices mapped to ordered
 // unsigned integers (0: not a candidate), which also orders -inf (an expert
-// that is only chosen when nothing else is left) and NaN (below -inf), so k
+// that is only chosen when nothing else is left; NaN counts as one), so k
 // distinct experts always come out.
 //
 // The choice must not depend on how fp32 rounds the scores.  Without a
@@ -49,20 +49,25 @@ constexpr float kSoftmaxErr = 4e-6f;
 constexpr float kSigmoidErr = 1e-6f;
 constexpr float kSumErr = 5e-7f;
 
-// Order-preserving map to unsigned integers; 0 is kept for "no candidate".
+// Order-preserving map of a value that is no NaN to unsigned integers; 0 is kept
+// for "no candidate".
 __device__ __forceinline__ uint32_t ordered(float v) {
-  if (v != v) return 1u;
   const uint32_t b = __float_as_uint(v + 0.0f);          // -0 -> +0
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint64_t ordered(double v) {
-  if (v != v) return 1ull;
   const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
   return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 __device__ __forceinline__ float from_ordered(uint32_t u) {
   return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
 }
+__device__ __forceinline__ double from_ordered(uint64_t u) {
+  return __longlong_as_double((long long)(u ^ ((u >> 63) ? 0x8000000000000000ull : ~0ull)));
+}
+// NaN becomes -inf (the maximum of a number and NaN is the number).
+__device__ __forceinline__ float no_nan(float v) { return fmaxf(v, -INFINITY); }
+__device__ __forceinline__ double no_nan(double v) { return fmax(v, -(double)INFINITY); }
 
 // Reductions over the wavefront by DPP: row shifts within 16 lanes, then the two
 // row broadcasts, leave the result in lane 63, read back as a uniform value.
@@ -101,29 +106,27 @@ __device__ __forceinline__ double wave_sum(double v) {
   for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
   return v;
 }
-__device__ __forceinline__ float wave_max_value(float v) {
-  return __uint_as_float(wave_reduce(__float_as_uint(v), 0xff800000u, [](uint32_t a, uint32_t b) {
-    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-  }));
+// (as ordered integers: one instruction a step, where fp32 maxima quiet their operands first)
+__device__ __forceinline__ float wave_max_value(float v) { return from_ordered(wave_max(ordered(no_nan(v)))); }
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {      // lane uniform
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
-__device__ __forceinline__ float lane_value(float v, int lane) {      // lane uniform
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
+  const uint32_t lo = lane_value((uint32_t)v, lane), hi = lane_value((uint32_t)(v >> 32), lane);
+  return ((uint64_t)hi << 32) | lo;
 }
-__device__ __forceinline__ double lane_value(double v, int lane) {
-  const uint64_t b = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
-  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+// A reduction's partner in step 0, 1, 2 over 8 lanes: lane ^ 1, lane ^ 2 (by quad),
+// then the mirror within 8, whose quads already agree; step 3: the mirror within 16.
+__device__ __forceinline__ uint32_t partner(uint32_t v, int step) {
+  if (step == 0) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);
+  if (step == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false);
+  if (step == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false);
+}
+__device__ __forceinline__ float xor_lane(float v, int step) {
+  return __uint_as_float(partner(__float_as_uint(v), step));
 }
 // Sum and maximum over the 8 lanes that hold the chosen experts (equal in all 8).
-__device__ __forceinline__ float xor_lane(float v, int step) {       // partner within 8: 1, 2 by quad, 7 - i for 4
-  const int b = (int)__float_as_uint(v);
-  int o;
-  if (step == 0) o = __builtin_amdgcn_mov_dpp(b, 0xB1, 0xF, 0xF, false);
-  else if (step == 1) o = __builtin_amdgcn_mov_dpp(b, 0x4E, 0xF, 0xF, false);
-  else o = __builtin_amdgcn_mov_dpp(b, 0x141, 0xF, 0xF, false);
-  return __uint_as_float((uint32_t)o);
-}
 __device__ __forceinline__ float sum8(float v) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) v += xor_lane(v, i);
@@ -137,13 +140,14 @@ __device__ __forceinline__ float max8(float v) {
 
 // e^v from the hardware's exp2 (1 ulp): the product with log2(e) is carried in two
 // parts, so that the argument's rounding does not grow with |v|; a few ulp in all.
-// -inf gives 0.
+// v <= 0; -inf and whatever underflows give 0, NaN too.
 __device__ __forceinline__ float exp_r(float v) {
+  v = fmaxf(v, -200.0f);
   const float hi = 1.44269502f, lo = 1.92596299e-8f;          // log2(e)
   const float t = v * hi;
   const float r = fmaf(v, lo, fmaf(v, hi, -t));
   const float e = __builtin_amdgcn_exp2f(t);
-  return v > -200.0f ? fmaf(e, r * 0.693147182f, e) : 0.0f;
+  return fmaf(e, r * 0.693147182f, e);
 }
 __device__ __forceinline__ double exp_r(double v) { return exp(v); }
 __device__ __forceinline__ float rcp_r(float v) { return __builtin_amdgcn_rcpf(v); }     // 1 ulp
@@ -216,15 +220,6 @@ __device__ __forceinline__ R lane_scores(const float (&l)[PER], const bool (&in)
   return inv;
 }
 
-// Merges the two largest values of each half of a part: (g1, g2) with the partner's.
-template <class R>
-__device__ __forceinline__ void merge_top2(R& g1, R& g2, R o1, R o2) {
-  const R lo = o1 > g1 ? g1 : o1;
-  g1 = o1 > g1 ? o1 : g1;
-  const R hi2 = o2 > g2 ? o2 : g2;
-  g2 = lo > hi2 ? lo : hi2;
-}
-
 // The `rounds` <= 16 best experts of the open groups into lanes 0 .. rounds - 1 of
 // `chosen` (-1: no candidate left).  Returns whether fp32 could have decided
 // any step wrongly (always false in fp64).
@@ -237,53 +232,18 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
   const int lig = lane & (a.lanes_per_group - 1), grp = lane >> a.group_shift;
   bool near = false;
   float score_tol = 0;
-  if (BIAS || need_scores)
-    score_tol = (SOFTMAX ? kSoftmaxErr : kSigmoidErr) * (float)lane_scores<R, PER, SOFTMAX>(l, in, lmax, s);
-  bool open = grp < a.n_groups;
-  if constexpr (GROUPED) {
-    // the group's score: its two largest values merged over the part's lanes
-    const R none = -(R)INFINITY;
-    const bool by_logit = !BIAS && a.group_top == 1;
-    R g1 = none, g2 = none;
-#pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      R v = by_logit ? (R)l[p] : BIAS ? s[p] + (R)b[p] : s[p];
-      v = in[p] && v == v ? v : none;
-      g2 = v > g1 ? g1 : (v > g2 ? v : g2);
-      g1 = v > g1 ? v : g1;
-    }
-    if constexpr (CHECK) {
-      // partners 1, 2 by quad; within 8 the mirror, whose quads already agree
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (a.lanes_per_group > (1 << i)) merge_top2(g1, g2, xor_lane(g1, i), xor_lane(g2, i));
-      for (int m = 8; m < a.lanes_per_group; m <<= 1) merge_top2(g1, g2, __shfl_xor(g1, m), __shfl_xor(g2, m));
-    } else {
-      for (int m = 1; m < a.lanes_per_group; m <<= 1) merge_top2(g1, g2, __shfl_xor(g1, m), __shfl_xor(g2, m));
-    }
-    const R gs = a.group_top == 1 ? g1 : g1 + g2;
-    int rank = 0;
-    for (int o = 0; o < a.n_groups; ++o) {
-      const R os = lane_value(gs, o << a.group_shift);
-      rank += (os > gs || (os == gs && o < grp)) ? 1 : 0;
-    }
-    const bool group = open;
-    open = open && rank < a.topk_groups;
-    if constexpr (CHECK) {
-      if (!by_logit) {
-        const float kept = -wave_max_value(open ? -(float)gs : -INFINITY);
-        const float shut = wave_max_value(group && !open ? (float)gs : -INFINITY);
-        near = !(kept - shut > 2 * score_tol + 2 * kSumErr * fmaxf(fabsf(kept), fabsf(shut)));
-      }
-    }
+  R smax = 0;
+  if (BIAS || need_scores) {
+    smax = lane_scores<R, PER, SOFTMAX>(l, in, lmax, s);
+    score_tol = (SOFTMAX ? kSoftmaxErr : kSigmoidErr) * (float)smax;
   }
   // the lane's keys in descending order (equal ones by index), each with its position
   Key key[PER];
   int pos[PER];
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
-    const Key k = ordered(BIAS ? s[p] + (R)b[p] : (R)l[p]);
-    key[p] = open && in[p] ? k : Key(0);
+    const Key k = ordered(no_nan(BIAS ? s[p] + (R)b[p] : (R)l[p]));
+    key[p] = in[p] ? k : Key(0);
     pos[p] = p;
   }
 #pragma unroll
@@ -298,6 +258,49 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
       key[j] = up ? k0 : key[j];
       pos[j] = up ? p0 : pos[j];
     }
+  if constexpr (GROUPED) {
+    // the group's two largest choices, merged over the part's lanes
+    Key h1 = key[0], h2 = PER > 1 ? key[PER > 1 ? 1 : 0] : Key(0);
+    auto merge = [&](Key o1, Key o2) __attribute__((always_inline)) {
+      const Key lo = min(h1, o1), hi = max(h2, o2);
+      h1 = max(h1, o1);
+      h2 = max(lo, hi);
+    };
+    if constexpr (CHECK) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (a.lanes_per_group > (1 << i)) merge(partner(h1, i), partner(h2, i));
+      if (a.lanes_per_group > 16) merge((Key)__shfl_xor((int)h1, 16), (Key)__shfl_xor((int)h2, 16));
+    } else {
+      for (int m = 1; m < a.lanes_per_group; m <<= 1)
+        merge((Key)__shfl_xor((long long)h1, m), (Key)__shfl_xor((long long)h2, m));
+    }
+    // the group's score; without a bias the two logits' scores, unless one logit orders the groups
+    const bool by_logit = !BIAS && a.group_top == 1;
+    auto value = [&](Key h) __attribute__((always_inline)) -> R {
+      const R v = from_ordered(h);
+      if (BIAS || by_logit) return v;
+      if constexpr (SOFTMAX) return no_nan(exp_r(v - (R)lmax) * smax);
+      else return sigmoid<R>(v);
+    };
+    const R gs = h1 == 0 ? -(R)INFINITY : a.group_top == 1 ? value(h1) : value(h1) + value(h2);
+    const Key gk = ordered(no_nan(gs));
+    const bool group = grp < a.n_groups;
+    int rank = 0;
+    for (int o = 0; o < a.n_groups; ++o) {
+      const Key ok = lane_value(gk, o << a.group_shift);
+      rank += ok > gk || (ok == gk && o < grp) ? 1 : 0;
+    }
+    const bool open = group && rank < a.topk_groups;
+    if (!open) key[0] = 0;                                   // never the owner: the others need not go
+    if constexpr (CHECK) {
+      if (!by_logit) {
+        const float kept = from_ordered(~wave_max(open ? ~gk : 0u));
+        const float shut = from_ordered(wave_max(group && !open ? gk : 0u));
+        near = !(kept - shut > 2 * score_tol + 2 * kSumErr * fmaxf(fabsf(kept), fabsf(shut)));
+      }
+    }
+  }
   const int first = grp * a.group_size + lig * PER;
 #pragma unroll
   for (int p = 0; p < PER; ++p) pos[p] += first;
