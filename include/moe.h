@@ -336,7 +336,8 @@ typedef struct {
   float scale;          /* weights are multiplied by this (finite) */
 } moe_router_t;
 
-/* Scored top-k selection.  Uses T, n_experts, top_k of the shape.
+/* Scored top-k selection.  Uses T, n_experts, top_k of the shape (which is
+ * validated as a whole).
  * Pages: "How Mixtral 8x7B uses mixture of experts", the simplified forward pass
  * (softmax over all experts, top-k, renormalise); "Mixtral 8x7B" interview page,
  * section on how MoE design changed since Mixtral.
@@ -367,8 +368,8 @@ moe_status_t moe_route_scored(const moe_shape_t* shape, const moe_router_t* rout
                               float* scores, int32_t* next_ids, void* stream);
 
 /* Gradient of moe_route_scored at the logits (the choice itself has none).
- *   logits, topk_ids  as given to / written by moe_route_scored (the ids of a
- *                row distinct; one outside [0, E) adds nothing)
+ *   logits, topk_ids  as given to / written by moe_route_scored (an id outside
+ *                [0, E) adds nothing; an expert named twice gets both gradients)
  *   dweights     [T, k] fp32: gradient at topk_weights
  *   dscores      [T, E] fp32 or NULL: gradient that arrives at the scores from
  *                elsewhere (a balance loss)

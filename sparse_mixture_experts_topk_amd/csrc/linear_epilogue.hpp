@@ -15,7 +15,7 @@ constexpr float kGeluB = 0.044715f;
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float p) {
-  if constexpr (ACT == MOE_ACT_RELU) return fmaxf(p, 0.0f);
+  if constexpr (ACT == MOE_ACT_RELU) return p < 0.0f ? 0.0f : p;          // NaN stays NaN
   else if constexpr (ACT == MOE_ACT_SILU) return p * fast_sigmoid(p);
   else if constexpr (ACT == MOE_ACT_GELU) return 0.5f * p * erfcf(p * -0.7071067811865476f);   // erfc: exact in the left tail
   else if constexpr (ACT == MOE_ACT_GELU_TANH) return p * fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));
@@ -30,10 +30,10 @@ __device__ __forceinline__ float act_grad(float p, int act) {
       return s * (1.0f + p * (1.0f - s));
     }
     case MOE_ACT_GELU:
-      p = fminf(fmaxf(p, -32.0f), 32.0f);   // 0 or 1 exactly from there on; p * p stays finite
+      p = p < -32.0f ? -32.0f : p > 32.0f ? 32.0f : p;   // 0 or 1 exactly from there on; p * p stays finite
       return 0.5f * erfcf(p * -0.7071067811865476f) + p * fast_exp(-0.5f * p * p) * 0.3989422804014327f;
     case MOE_ACT_GELU_TANH: {
-      p = fminf(fmaxf(p, -32.0f), 32.0f);
+      p = p < -32.0f ? -32.0f : p > 32.0f ? 32.0f : p;
       const float s = fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));
       return s + p * s * (1.0f - s) * kGeluA * (1.0f + 3.0f * kGeluB * p * p);
     }

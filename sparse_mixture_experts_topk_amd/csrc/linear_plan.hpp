@@ -32,10 +32,9 @@ struct ProductPlan {
   size_t workspace = 0;
 
   template <class C>
-  static ProductPlan of(int rows, int cols, int len, int slow) {
+  static ProductPlan of(int rows, int cols, int len, int slow, int64_t cus) {
     using G = GeomOf<C>;
     ProductPlan best;
-    const int64_t cus = std::min<int64_t>(device_cu_count(), kMaxPersistentGroups) / 8 * 8;
     for (int split = 0; split < 2; ++split) {
       ProductPlan p;
       p.row_tiles = (rows + G::TB - 1) / G::TB;
@@ -59,8 +58,11 @@ struct ProductPlan {
 // Calls run(tile shape, plan) with the cheapest of the four.
 template <class F>
 auto with_plan(int rows, int cols, int len, int slow, F&& run) {
-  const ProductPlan a = ProductPlan::of<Tile256x256>(rows, cols, len, slow), b = ProductPlan::of<Tile256x128>(rows, cols, len, slow),
-                    c = ProductPlan::of<Tile128x128>(rows, cols, len, slow), d = ProductPlan::of<Tile128x64>(rows, cols, len, slow);
+  const int64_t cus = std::min<int64_t>(device_cu_count(), kMaxPersistentGroups) / 8 * 8;
+  const ProductPlan a = ProductPlan::of<Tile256x256>(rows, cols, len, slow, cus);
+  const ProductPlan b = ProductPlan::of<Tile256x128>(rows, cols, len, slow, cus);
+  const ProductPlan c = ProductPlan::of<Tile128x128>(rows, cols, len, slow, cus);
+  const ProductPlan d = ProductPlan::of<Tile128x64>(rows, cols, len, slow, cus);
   const double least = std::min(std::min(a.cost, b.cost), std::min(c.cost, d.cost));
   if (a.cost == least) return run(Tile256x256{}, a);
   if (b.cost == least) return run(Tile256x128{}, b);

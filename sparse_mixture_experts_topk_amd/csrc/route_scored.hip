@@ -476,7 +476,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_ker
 #pragma unroll
   for (int p = 0; p < PER; ++p) row[lane * PER + p] = 0.0f;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  if (id >= 0) row[id] = q;
+  if (id >= 0) atomicAdd(&row[id], q);       // (an expert named twice gets both)
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   float sel[PER], out[PER];
 #pragma unroll

@@ -285,6 +285,28 @@ def test_route_backward_ignores_ids_outside_the_row():
     close(out.np(), want, 64 * F32 * 4, "dlogits")
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_backward_of_an_expert_named_twice(kind, renorm):
+    x, dw = normal(gen(25), 5, 16), normal(gen(26), 5, 4)
+    ids = x.topk(4, 1).indices.to(torch.int32)
+    ids[:, 3] = ids[:, 1]
+    out = Out(5, 16)
+    moe.moe_route_scored_backward(moe.make_shape(5, 64, 64, 16, 4), moe.make_router(kind, renormalize=renorm),
+                                  cuda(x), cuda(ids), cuda(dw), None, out.t)
+    torch.cuda.synchronize()
+    # sum_j dw_j w_j with the expert's score counted twice, by differences in fp64
+    def loss(z):
+        s = np.take_along_axis(ref.scores(z, kind), ids.numpy().astype(np.int64), 1)
+        return float((f64(dw) * (s / s.sum(1, keepdims=True) if renorm else s)).sum())
+    h, z = 1e-6, f64(x)
+    for t, e in np.ndindex(5, 16):
+        p, m = z.copy(), z.copy()
+        p[t, e] += h
+        m[t, e] -= h
+        assert abs((loss(p) - loss(m)) / (2 * h) - out.np()[t, e]) < 1e-6
+
+
 # ---- combine ----
 
 def rows_of(T, E, k, S, drop, seed):
@@ -434,6 +456,20 @@ def test_linear_infinite_operand_stays_in_its_row():
         torch.cuda.synchronize()
         keep = [i for i in range(N) if i != 3]
         assert torch.equal(a.t[:, keep], b.t[:, keep]) and torch.isnan(a.t[:, 3]).all()
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+def test_linear_keeps_nan(act):
+    """A NaN operand shows in its row, whatever the activation."""
+    for M in (3, 200):
+        x, w = torch.ones(M, 64, dtype=torch.bfloat16), torch.ones(72, 64, dtype=torch.bfloat16)
+        x[2, 5] = float("nan")
+        lin = moe.make_linear(M, 72, 64, act=act)
+        y, p = Out(M, 72, dtype=torch.bfloat16), Out(M, 72, dtype=torch.bfloat16)
+        moe.moe_linear(lin, cuda(x), cuda(w), None, None, y.t, p.t, runner._bytes(moe.moe_linear_workspace_bytes(lin), DEV))
+        torch.cuda.synchronize()
+        for o in (y.t, p.t):
+            assert torch.isnan(o[2]).all() and torch.isfinite(o[:2]).all() and torch.isfinite(o[3:]).all()
 
 
 def linear_backward_case(M, N, K, act="none", out="bf16", seed=0, outputs=(True, True, True), std=1.0):
