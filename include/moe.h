@@ -423,8 +423,8 @@ typedef struct {
   int32_t M;        /* rows (tokens), 0..2^24 */
   int32_t N;        /* output channels: a multiple of 8, at most 2^18 */
   int32_t K;        /* input channels: a multiple of 8, at most 2^18 */
-  int32_t dtype;    /* x, w, pre, dx, dw: MOE_BF16 (MOE_F32: MOE_ERR_UNSUPPORTED) */
-  int32_t y_dtype;  /* y, residual, dy: MOE_BF16 or MOE_F32 */
+  int32_t dtype;    /* x, w, pre, dx, dw: MOE_BF16 or MOE_F32 */
+  int32_t y_dtype;  /* y, residual, dy: MOE_BF16 or MOE_F32 (MOE_F32 with MOE_F32 operands) */
   int32_t act;      /* moe_act_t */
 } moe_linear_t;
 

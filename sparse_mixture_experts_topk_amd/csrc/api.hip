@@ -201,7 +201,9 @@ moe_status_t validate_linear(const moe_linear_t* l) {
   if (l->dtype < MOE_F32 || l->dtype > MOE_MXFP4 || l->y_dtype < MOE_F32 || l->y_dtype > MOE_MXFP4)
     return MOE_ERR_INVALID_ARG;
   if (l->act < MOE_ACT_NONE || l->act > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
-  if (l->dtype != MOE_BF16 || (l->y_dtype != MOE_BF16 && l->y_dtype != MOE_F32)) return MOE_ERR_UNSUPPORTED;
+  const bool combo = (l->dtype == MOE_BF16 && (l->y_dtype == MOE_BF16 || l->y_dtype == MOE_F32)) ||
+                     (l->dtype == MOE_F32 && l->y_dtype == MOE_F32);
+  if (!combo) return MOE_ERR_UNSUPPORTED;
   if (l->N % 8 != 0 || l->K % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if (l->N > moe::kMaxLinearWidth || l->K > moe::kMaxLinearWidth) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -570,8 +572,7 @@ moe_status_t moe_linear(const moe_linear_t* l, const void* x, const void* w, con
   const size_t need = moe::linear_workspace_bytes(*l);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
     return MOE_ERR_WORKSPACE;
-  return from_hip(moe::launch_linear(*l, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), bias,
-                                     residual, y, static_cast<uint16_t*>(pre), need > 0 ? workspace : nullptr,
+  return from_hip(moe::launch_linear(*l, x, w, bias, residual, y, pre, need > 0 ? workspace : nullptr,
                                      static_cast<hipStream_t>(stream)));
 }
 
@@ -585,7 +586,7 @@ moe_status_t moe_linear_backward(const moe_linear_t* l, const void* dy, const vo
   if (l->M == 0) {   // the sums over no rows
     if ((v = check_ptrs({}, {dw, dbias})) != MOE_OK) return v;
     hipError_t e = hipSuccess;
-    if (dw != nullptr) e = launch_fill_u8(static_cast<uint8_t*>(dw), (int64_t)l->N * l->K * 2, 0, st);
+    if (dw != nullptr) e = launch_fill_u8(static_cast<uint8_t*>(dw), (int64_t)l->N * l->K * act_bytes(l->dtype), 0, st);
     if (e == hipSuccess && dbias != nullptr)
       e = launch_fill_u8(reinterpret_cast<uint8_t*>(dbias), (int64_t)l->N * 4, 0, st);
     return from_hip(e);
@@ -597,10 +598,7 @@ moe_status_t moe_linear_backward(const moe_linear_t* l, const void* dy, const vo
   const size_t need = moe::linear_backward_workspace_bytes(*l);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
     return MOE_ERR_WORKSPACE;
-  return from_hip(moe::launch_linear_backward(*l, dy, static_cast<const uint16_t*>(pre),
-                                              static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w),
-                                              static_cast<uint16_t*>(dx), static_cast<uint16_t*>(dw), dbias,
-                                              need > 0 ? workspace : nullptr, st));
+  return from_hip(moe::launch_linear_backward(*l, dy, pre, x, w, dx, dw, dbias, need > 0 ? workspace : nullptr, st));
 }
 
 moe_status_t moe_forward_noalloc(const moe_shape_t* s, const void* x, const void* w_gate,

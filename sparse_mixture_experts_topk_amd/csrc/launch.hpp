@@ -163,11 +163,10 @@ hipError_t launch_combine_backward(const moe_shape_t& s, const void* dy, const f
 constexpr int kMaxLinearWidth = 1 << 18;
 size_t linear_workspace_bytes(const moe_linear_t& l);
 size_t linear_backward_workspace_bytes(const moe_linear_t& l);
-hipError_t launch_linear(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const float* bias,
-                         const void* residual, void* y, uint16_t* pre, void* workspace, hipStream_t st);
-hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const uint16_t* pre, const uint16_t* x,
-                                  const uint16_t* w, uint16_t* dx, uint16_t* dw, float* dbias, void* workspace,
-                                  hipStream_t st);
+hipError_t launch_linear(const moe_linear_t& l, const void* x, const void* w, const float* bias,
+                         const void* residual, void* y, void* pre, void* workspace, hipStream_t st);
+hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const void* pre, const void* x,
+                                  const void* w, void* dx, void* dw, float* dbias, void* workspace, hipStream_t st);
 
 // Largest number of rows any routed expert can receive: each token picks an expert at most once.
 inline int64_t max_rows_per_routed_expert(const moe_shape_t& s) {

@@ -105,6 +105,14 @@ struct Epilogue {
   }
 };
 
+// fp32 operands (linear_f32.hip).
+size_t linear_workspace_bytes_f32(const moe_linear_t& l);
+size_t linear_backward_product_bytes_f32(const moe_linear_t& l);
+hipError_t launch_linear_f32(const moe_linear_t& l, const float* x, const float* w, const float* bias,
+                             const float* residual, float* y, float* pre, void* workspace, hipStream_t st);
+hipError_t launch_linear_products_f32(const moe_linear_t& l, const float* dpre, const float* x, const float* w,
+                                      float* dx, float* dw, void* partials, hipStream_t st);
+
 // Weight streaming for up to kLinearDecodeRows rows.
 constexpr int kLinearDecodeRows = 32;
 int device_cu_count();

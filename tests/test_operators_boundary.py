@@ -91,7 +91,7 @@ def test_combine_backward_refusals():
 @pytest.mark.parametrize("kw,want", [
     (dict(), 0), (dict(M=0), 0), (dict(M=-1), INVALID), (dict(M=(1 << 24) + 1), INVALID), (dict(N=0), INVALID),
     (dict(K=0), INVALID), (dict(N=12), UNSUPPORTED), (dict(K=100), UNSUPPORTED), (dict(N=(1 << 18) + 8), UNSUPPORTED),
-    (dict(K=(1 << 18) + 8), UNSUPPORTED), (dict(dtype="f32"), UNSUPPORTED), (dict(dtype="fp8_e4m3"), UNSUPPORTED),
+    (dict(K=(1 << 18) + 8), UNSUPPORTED), (dict(dtype="f32"), UNSUPPORTED), (dict(dtype="f32", y_dtype="f32"), 0), (dict(dtype="fp8_e4m3"), UNSUPPORTED),
     (dict(dtype=9), INVALID), (dict(y_dtype="mxfp4"), UNSUPPORTED), (dict(y_dtype=-1), INVALID),
     (dict(act=5), INVALID), (dict(act=-1), INVALID),
 ])

@@ -366,31 +366,35 @@ def test_combine_backward(T, d, k, S, act, drop):
 
 # ---- dense product ----
 
-def linear_case(M, N, K, act="none", out="bf16", bias=True, residual=False, pre=False, seed=0, std=1.0):
-    say(f"linear M={M} N={N} K={K} {act} {out} bias={bias} residual={residual} pre={pre}")
+def linear_case(M, N, K, act="none", out="bf16", bias=True, residual=False, pre=False, seed=0, std=1.0,
+                dtype="bf16"):
+    say(f"linear {dtype} M={M} N={N} K={K} {act} {out} bias={bias} residual={residual} pre={pre}")
     g = gen(seed + M + N + K)
     odt = torch.bfloat16 if out == "bf16" else torch.float32
-    x = normal(g, M, K, std=std, dtype=torch.bfloat16)
-    w = normal(g, N, K, std=K ** -0.5, dtype=torch.bfloat16)
+    idt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = normal(g, M, K, std=std, dtype=idt)
+    w = normal(g, N, K, std=K ** -0.5, dtype=idt)
     b = normal(g, N) if bias else None
     r = normal(g, M, N, dtype=odt) if residual else None
-    lin = moe.make_linear(M, N, K, y_dtype=out, act=act)
+    lin = moe.make_linear(M, N, K, dtype=dtype, y_dtype=out, act=act)
     n = moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR)
     ws = Out(n, dtype=torch.uint8, fill=77) if n else None
     if ws:
         ws.t.fill_(0xFF)                                     # NaN patterns: no content is counted on
-    y, p = Out(M, N, dtype=odt), Out(M, N, dtype=torch.bfloat16) if pre else None
+    y, p = Out(M, N, dtype=odt), Out(M, N, dtype=idt) if pre else None
     moe.moe_linear(lin, cuda(x), cuda(w), cuda(b), cuda(r), y.t, p.t if p else None, ws.t if ws else None)
     torch.cuda.synchronize()
     wy, wp = ref.linear(f64(x), f64(w), f64(b), f64(r), act)
-    dot = (K + 4) * 2.0 ** -23 * (np.abs(f64(x)) @ np.abs(f64(w)).T + (np.abs(f64(b)) if bias else 0))
+    # bf16 products are exact in fp32; fp32 ones round too
+    per = 2.0 ** -23 if dtype == "bf16" else 2.0 ** -22
+    dot = (K + 4) * per * (np.abs(f64(x)) @ np.abs(f64(w)).T + (np.abs(f64(b)) if bias else 0))
     step = BF16 if out == "bf16" else 2 * F32
     tol = 1.13 * dot + (2.0 ** -19 * (1 + np.abs(wp)) if act not in ("none", "relu") else 0) + step * np.abs(wy)
     if residual:
         tol = tol + 2 * F32 * np.abs(f64(r))
     close(y.np(), wy, tol * (1 + BF16), "y")
     if p:
-        close(p.np(), wp, (dot + BF16 * np.abs(wp)) * (1 + BF16), "pre")
+        close(p.np(), wp, (dot + (BF16 if dtype == "bf16" else F32) * np.abs(wp)) * (1 + BF16), "pre")
     if ws:
         ws.np()                                              # nothing past the workspace
     return y.t.clone()
@@ -408,6 +412,7 @@ def test_linear(dims):
     linear_case(M, N, K, "none", "f32", bias=False)
     linear_case(M, N, K, "silu", "bf16", bias=True, pre=True)
     linear_case(M, N, K, "gelu_tanh", "bf16", bias=True, residual=True)
+    linear_case(M, N, K, "silu", "f32", bias=True, residual=True, pre=True, dtype="f32")
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
@@ -416,6 +421,8 @@ def test_linear(dims):
 def test_linear_activations(act, out, dims):
     linear_case(*dims, act, out, bias=True, residual=True, pre=True, std=3.0)
     linear_case(*dims, act, out, bias=False, residual=False, pre=False, std=0.1)
+    if out == "f32":
+        linear_case(*dims, act, out, bias=True, residual=True, pre=True, std=3.0, dtype="f32")
 
 
 @pytest.mark.parametrize("dims", [(3, 256, 512), (300, 264, 520)])
@@ -437,13 +444,14 @@ def test_linear_residual_in_place(dims, out):
 
 def test_linear_infinite_operand_stays_in_its_row():
     """Rows and channels next to each other share loads, never values."""
-    for M, N, K in ((5, 72, 136), (70, 136, 264), (300, 264, 200)):
-        say(f"infinite row M={M} N={N} K={K}")
+    for M, N, K, dt in ((5, 72, 136, "bf16"), (70, 136, 264, "bf16"), (300, 264, 200, "bf16"), (70, 136, 264, "f32")):
+        say(f"infinite row {dt} M={M} N={N} K={K}")
         g = gen(41)
-        x, w = normal(g, M, K, dtype=torch.bfloat16), normal(g, N, K, std=0.1, dtype=torch.bfloat16)
+        tdt = torch.bfloat16 if dt == "bf16" else torch.float32
+        x, w = normal(g, M, K, dtype=tdt), normal(g, N, K, std=0.1, dtype=tdt)
         clean = x.clone()
         x[1] = float("inf")
-        lin = moe.make_linear(M, N, K, y_dtype="f32")
+        lin = moe.make_linear(M, N, K, dtype=dt, y_dtype="f32")
         ws = runner._bytes(moe.moe_linear_workspace_bytes(lin), DEV)
         a, b = Out(M, N), Out(M, N)
         moe.moe_linear(lin, cuda(x), cuda(w), None, None, a.t, None, ws)
@@ -472,19 +480,22 @@ def test_linear_keeps_nan(act):
             assert torch.isnan(o[2]).all() and torch.isfinite(o[:2]).all() and torch.isfinite(o[3:]).all()
 
 
-def linear_backward_case(M, N, K, act="none", out="bf16", seed=0, outputs=(True, True, True), std=1.0):
-    say(f"linear backward M={M} N={N} K={K} {act} {out} outputs={outputs}")
+def linear_backward_case(M, N, K, act="none", out="bf16", seed=0, outputs=(True, True, True), std=1.0,
+                         dtype="bf16"):
+    say(f"linear backward {dtype} M={M} N={N} K={K} {act} {out} outputs={outputs}")
     g = gen(seed + M + N + K)
     odt = torch.bfloat16 if out == "bf16" else torch.float32
-    dy, x = normal(g, M, N, dtype=odt), normal(g, M, K, dtype=torch.bfloat16)
-    w = normal(g, N, K, dtype=torch.bfloat16)
-    pre = normal(g, M, N, std=std, dtype=torch.bfloat16) if act != "none" else None
-    lin = moe.make_linear(M, N, K, y_dtype=out, act=act)
+    idt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    step, per = (BF16, 2.0 ** -23) if dtype == "bf16" else (F32, 2.0 ** -22)
+    dy, x = normal(g, M, N, dtype=odt), normal(g, M, K, dtype=idt)
+    w = normal(g, N, K, dtype=idt)
+    pre = normal(g, M, N, std=std, dtype=idt) if act != "none" else None
+    lin = moe.make_linear(M, N, K, dtype=dtype, y_dtype=out, act=act)
     n = moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR_BACKWARD)
     ws = Out(n, dtype=torch.uint8, fill=77) if n else None
     if ws:
         ws.t.fill_(0xFF)
-    dx, dw, db = Out(M, K, dtype=torch.bfloat16), Out(N, K, dtype=torch.bfloat16), Out(N)
+    dx, dw, db = Out(M, K, dtype=idt), Out(N, K, dtype=idt), Out(N)
     moe.moe_linear_backward(lin, cuda(dy), cuda(pre), cuda(x) if outputs[1] else None,
                             cuda(w) if outputs[0] else None, dx.t if outputs[0] else None,
                             dw.t if outputs[1] else None, db.t if outputs[2] else None, ws.t if ws else None)
@@ -492,21 +503,21 @@ def linear_backward_case(M, N, K, act="none", out="bf16", seed=0, outputs=(True,
     wdx, wdw, wdb, d = ref.linear_backward(f64(dy), f64(pre), f64(x), f64(w), act)
     # the derivative's error, and the rounding of dpre to the products' operand type
     slope = np.abs(f64(dy)) * 2.0 ** -19 * (1 + np.abs(f64(pre))) if act not in ("none", "relu") else 0.0 * d
-    copied = act != "none" or out == "f32"
-    e = slope + (BF16 * np.abs(d) if copied else 0)
+    copied = act != "none" or out != dtype
+    e = slope + (step * np.abs(d) if copied else 0)
     a = np.abs(d) + e
     got = dx.np()
     if outputs[0]:
         aw = np.abs(f64(w))
-        tol = e @ aw + (N + 4) * 2.0 ** -23 * (a @ aw)
-        close(got, wdx, tol * (1 + BF16) + BF16 * np.abs(wdx), "dx")
+        tol = e @ aw + (N + 4) * per * (a @ aw)
+        close(got, wdx, tol * (1 + BF16) + step * np.abs(wdx), "dx")
     else:
         assert (got == -7.0).all()
     got = dw.np()
     if outputs[1]:
         ax = np.abs(f64(x))
-        tol = e.T @ ax + (M + 4) * 2.0 ** -23 * (a.T @ ax)
-        close(got, wdw, tol * (1 + BF16) + BF16 * np.abs(wdw), "dw")
+        tol = e.T @ ax + (M + 4) * per * (a.T @ ax)
+        close(got, wdw, tol * (1 + BF16) + step * np.abs(wdw), "dw")
     else:
         assert (got == -7.0).all()
     got = db.np()
@@ -525,6 +536,7 @@ def test_linear_backward(dims):
     linear_backward_case(M, N, K, "none", "f32")
     linear_backward_case(M, N, K, "silu", "bf16")
     linear_backward_case(M, N, K, "none", "bf16")
+    linear_backward_case(M, N, K, "gelu", "f32", dtype="f32")
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
@@ -533,6 +545,8 @@ def test_linear_backward_activations(act, out):
     linear_backward_case(37, 136, 72, act, out, std=3.0)
     for outputs in ((True, False, False), (False, True, False), (False, False, True), (True, False, True)):
         linear_backward_case(37, 136, 72, act, out, outputs=outputs)
+        if out == "f32":
+            linear_backward_case(37, 136, 72, act, out, outputs=outputs, dtype="f32")
 
 
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
@@ -635,7 +649,7 @@ def layer(T=96, E=32, k=4, shared=1, **kw):
 
 
 LAYERS = [dict(), dict(T=16, E=8, k=2, shared=0), dict(T=1, E=8, k=2, shared=0), dict(T=700, E=8, k=2, shared=0),
-          dict(capacity=9), dict(T=200, E=8, k=2, shared=0, capacity=30, overflow="next_best")]
+          dict(T=50, E=8, k=2, shared=0, act_dtype="f32", w_dtype="f32"), dict(capacity=9), dict(T=200, E=8, k=2, shared=0, capacity=30, overflow="next_best")]
 ROUTER = dict(score="sigmoid", n_groups=4, topk_groups=2, group_top=2, renormalize=True, scale=2.5)
 
 
@@ -660,7 +674,7 @@ def test_scored_layer_and_its_gate_gradient(kw):
     ids, w, s, nxt = ref.route_scored(logits, f64(balance), k, *args)
     assert np.array_equal(f64(st["topk_ids"]), ids) and np.array_equal(f64(st["next_ids"]), nxt)
     wl = f64(inp.x) @ f64(inp.w_gate).T + f64(inp.router_bias)
-    close(logits, wl, 260 * 2.0 ** -23 * (np.abs(f64(inp.x)) @ np.abs(f64(inp.w_gate)).T + 2), "logits")
+    close(logits, wl, 260 * 2.0 ** -22 * (np.abs(f64(inp.x)) @ np.abs(f64(inp.w_gate)).T + 2), "logits")
     # y from the experts' rows
     rows, y_perm, s2r = st["slot_to_row"].cpu().numpy(), f64(st["y_perm"]), st["slot_to_row"].cpu().numpy()
     want = np.zeros((T, cfg.d_model))
@@ -674,7 +688,8 @@ def test_scored_layer_and_its_gate_gradient(kw):
             want[t] += y_perm[rows[T * k + t]]
     close(f64(st["y"]), want, BF16 * np.abs(want) + 128 * F32 * (size + np.abs(want)), "y")
     # and the gradient of <dy, y> + <D, scores> back to x and the router's weights
-    dy, D = normal(gen(72), T, cfg.d_model, dtype=torch.bfloat16), normal(gen(73), T, E, std=0.1)
+    dy = normal(gen(72), T, cfg.d_model, dtype=torch.bfloat16 if cfg.act_dtype == "bf16" else torch.float32)
+    D = normal(gen(73), T, E, std=0.1)
     g = runner.gate_backward(di, st, router, cuda(dy), cuda(D))
     torch.cuda.synchronize()
     want_rows, want_dw = ref.combine_backward(f64(dy), y_perm, s2r, w, k, S)
