@@ -30,7 +30,7 @@
 // last chosen and the first left out, the last open group and the first closed):
 // one within the fp32 error of the two values (k...Err) sends the token through
 // the same steps in fp64, where scores of distinct fp32 logits are distinct until
-// they saturate.  With 256 experts and N(0,1) logits about one token in 500 goes
+// they saturate.  With 256 experts and N(0,1) logits about one token in 1500 goes
 // that way.
 #include <type_traits>
 
@@ -41,13 +41,14 @@ namespace moe {
 namespace {
 
 constexpr int kRouteWaves = 4;     // tokens per workgroup
-// Errors of a difference of two fp32 scores: softmax under 1.2e-6 of the largest
-// score for each (exp, the sum over at most 256 terms, one division), sigmoid
-// under 2.5e-7.  c = s + b and the sum of two choices round once more, 2^-24 of
-// the value each.
-constexpr float kSoftmaxErr = 4e-6f;
-constexpr float kSigmoidErr = 1e-6f;
-constexpr float kSumErr = 5e-7f;
+// Errors of a difference of two fp32 scores.  Sigmoid: 2.2e-7 each (exp and the
+// reciprocal to 1 ulp, three roundings).  Softmax, of the largest score: the
+// denominator's 8.5e-7 (a sum of depth 10 of exps), which both share, and 2e-7
+// each.  c = s + b and the sum of two choices round once more, 2^-24 of the
+// value each.  A group's score has two scores' errors.
+constexpr float kSoftmaxErr = 1.5e-6f;
+constexpr float kSigmoidErr = 5e-7f;
+constexpr float kSumErr = 1.25e-7f;
 
 // Order-preserving map of a value that is no NaN to unsigned integers; 0 is kept
 // for "no candidate".
@@ -88,13 +89,10 @@ __device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t none, Op op
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const uint64_t o = (uint64_t)__shfl_xor((long long)v, m);
-    v = o > v ? o : v;
-  }
-  return v;
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {       // the upper halves, then the lower ones of their largest
+  const uint32_t hi = wave_max((uint32_t)(v >> 32));
+  const uint32_t lo = wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((uint64_t)hi << 32) | lo;
 }
 __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {

@@ -144,6 +144,30 @@ def test_route_is_decided_by_the_scores_not_their_rounding(kind):
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (8, 4, 2), (16, 5, 1)])
+@pytest.mark.parametrize("spread", [1.0, 0.01, 8.0])
+def test_route_choices_of_many_tokens_are_those_of_fp64(kind, groups, spread):
+    """A quarter of a million choices: near ties turn up by themselves, more so with crowded scores."""
+    T, E, k = 32768, 128, 8
+    n, kept, top = groups
+    say(f"many tokens {kind} groups={groups} spread={spread}")
+    g = torch.Generator(device=DEV).manual_seed(17)
+    x = torch.randn(T, E, device=DEV, generator=g) * spread
+    b = torch.randn(E, device=DEV, generator=g) * (0.05 if kind == "sigmoid" else 0.5 / E) * min(spread, 1.0)
+    ids, w = Out(T, k, dtype=torch.int32, fill=-77), Out(T, k)
+    moe.moe_route_scored(moe.make_shape(T, 64, 64, E, k), moe.make_router(kind, n, kept, top), x, b, ids.t, w.t)
+    z = x.double()
+    c = (torch.sigmoid(z) if kind == "sigmoid" else torch.softmax(z, 1)) + b.double()
+    if n > 1:
+        of_group = c.view(T, n, E // n).sort(dim=2, descending=True).values[:, :, :top].sum(2)
+        best = of_group.sort(dim=1, descending=True, stable=True).indices[:, :kept]
+        mask = torch.zeros(T, n, dtype=torch.bool, device=DEV).scatter_(1, best, True)
+        c = torch.where(mask.repeat_interleave(E // n, 1), c, -float("inf"))
+    want = c.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.t.long(), want)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_route_masked_logits_and_biases(kind, renorm):
     T, E, k = 12, 32, 4
