@@ -16,7 +16,10 @@ namespace {
 
 constexpr int kPrepCols = 256;      // columns per workgroup, 8 to a lane
 // Rows per workgroup (one row of column sums comes of them): 256, fewer while that
-// leaves under four workgroups per CU (4099 x 256: 18 -> 5 us), 16 at least.
+// leaves under four workgroups per CU (4099 x 256: 18 -> 5 us), 16 at least.  Where one
+// workgroup has all rows, its sums are dbias and the second kernel falls away (16 x
+// 256 x 4096, whole pass: 15.3 -> 9.0 us; taken up to 64 rows instead, 64 x 4096 x
+// 4096 took 41 us for 36).
 int prep_rows(const moe_linear_t& l) {
   const int64_t col_blocks = (l.N + kPrepCols - 1) / kPrepCols;
   int rows = 256;
@@ -107,15 +110,17 @@ size_t part_bytes(const moe_linear_t& l) { return round256((size_t)prep_chunks(l
 size_t linear_backward_workspace_bytes(const moe_linear_t& l) {
   if (l.M == 0) return 0;
   if (l.dtype == MOE_F32) return dpre_bytes(l) + part_bytes(l) + linear_backward_product_bytes_f32(l);
-  return dpre_bytes(l) + part_bytes(l) +
-         std::max(product_workspace(l.M, l.K, l.N, 1), product_workspace(l.N, l.K, l.M, 2));
+  return dpre_bytes(l) + part_bytes(l) + gradient_workspace(l.M, l.N, l.K);
 }
 
 hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const void* pre, const void* x,
                                   const void* w, void* dx, void* dw, float* dbias, void* workspace,
                                   hipStream_t st) {
   void* copy = dpre_copied(l) && (dx != nullptr || dw != nullptr) ? workspace : nullptr;
-  float* part = dbias != nullptr ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dpre_bytes(l)) : nullptr;
+  const bool one_chunk = prep_chunks(l) == 1;
+  float* part = dbias == nullptr ? nullptr
+                : one_chunk      ? dbias
+                                 : reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dpre_bytes(l));
   hipError_t e = hipSuccess;
   if (copy != nullptr || part != nullptr) {
     const int rows = prep_rows(l), cbs = (l.N + kPrepCols - 1) / kPrepCols;
@@ -129,7 +134,7 @@ hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const v
     else if (f32) e = act ? run(dpre_kernel<true, true, false>) : run(dpre_kernel<true, false, false>);
     else e = act ? run(dpre_kernel<false, true, false>) : run(dpre_kernel<false, false, false>);
   }
-  if (e == hipSuccess && dbias != nullptr) {
+  if (e == hipSuccess && dbias != nullptr && !one_chunk) {
     hipLaunchKernelGGL(dbias_kernel, dim3((l.N + 15) / 16), dim3(256), 0, st, part, prep_chunks(l), l.N, dbias);
     e = hipGetLastError();
   }
@@ -140,14 +145,9 @@ hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const v
     return launch_linear_products_f32(l, static_cast<const float*>(d), static_cast<const float*>(x),
                                       static_cast<const float*>(w), static_cast<float*>(dx), static_cast<float*>(dw),
                                       partials, st);
-  const uint16_t* d16 = static_cast<const uint16_t*>(d);
-  if (dx != nullptr)
-    e = launch_product<false, true, MOE_ACT_NONE>(d16, l.N, static_cast<const uint16_t*>(w), l.K, l.M, l.K, l.N, partials,
-                                                  Epilogue{nullptr, nullptr, dx, nullptr, false}, st);
-  if (e == hipSuccess && dw != nullptr)
-    e = launch_product<true, true, MOE_ACT_NONE>(d16, l.N, static_cast<const uint16_t*>(x), l.K, l.N, l.K, l.M, partials,
-                                                 Epilogue{nullptr, nullptr, dw, nullptr, false}, st);
-  return e;
+  return launch_gradients(static_cast<const uint16_t*>(d), static_cast<const uint16_t*>(x),
+                          static_cast<const uint16_t*>(w), static_cast<uint16_t*>(dx), static_cast<uint16_t*>(dw), l.M,
+                          l.N, l.K, partials, st);
 }
 
 }  // namespace moe

@@ -30,7 +30,8 @@
 // tiles form one stream through the ring, so the next tile's first slices load
 // while this one's results are stored.  The last, partial round of tiles may be
 // cut along the contraction over all workgroups (TileShare): their fp32 partial
-// tiles are summed in order by a second kernel, which applies the epilogue.
+// tiles are summed in order by a second kernel, which applies the epilogue.  The
+// two products of a backward pass share one launch of each.
 #pragma once
 #include "device_common.hpp"
 #include "launch.hpp"
@@ -177,18 +178,18 @@ __device__ __forceinline__ void join_blocks(f32x4_t a, f32x4_t b, float (&v)[8])
   }
 }
 
+// Workgroup `block` of the `blocks` (a multiple of 8) that share the product.
 template <bool PSLOW, bool QSLOW, int ACT, int NS, int WR, int WC, int WA, int WB>
-__global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const ProductArgs a) {
+__device__ __forceinline__ void product_workgroup(const ProductArgs& a, uint8_t* smem, int block, int blocks) {
   using G = ProductGeom<NS, WR, WC, WA, WB>;
   using MA = LoadMap<QSLOW, G::TA, G::NW>;
   using MB = LoadMap<PSLOW, G::TB, G::NW>;
   constexpr int BK = G::BK;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * G::STAGE];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WC, wc = wave % WC;
   const int KT = (a.len + BK - 1) / BK;
-  const int slots = gridDim.x >> 3, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  const int slots = blocks >> 3, xcd = block & 7, slot = block >> 3;
   const TileShare sp = TileShare::of(a.row_tiles * a.col_tiles, xcd, slots, KT, a.split);
   const int n_whole = sp.R + (!a.split && slot < sp.tail ? 1 : 0);
   const int run0 = slot * sp.P, run1 = min(run0 + sp.P, sp.tail * KT);
@@ -386,15 +387,33 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const P
   wait_vmcnt<0>();   // the zero loads past the end land before the workgroup's LDS is released
 }
 
+template <bool PSLOW, bool QSLOW, int ACT, int NS, int WR, int WC, int WA, int WB>
+__global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
+  product_workgroup<PSLOW, QSLOW, ACT, NS, WR, WC, WA, WB>(a, smem, blockIdx.x, gridDim.x);
+}
+
+// dx on the first dx_blocks workgroups, dw on the others: one launch, and dw's
+// workgroups fill the CUs that dx's last round of tiles leaves idle.
+template <int NS, int WR, int WC, int WA, int WB>
+__global__ __launch_bounds__(64 * WR * WC, 1) void linear_gradients_kernel(const ProductArgs dx, const ProductArgs dw,
+                                                                           int dx_blocks) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
+  const int b = blockIdx.x;
+  if (b < dx_blocks) product_workgroup<false, true, MOE_ACT_NONE, NS, WR, WC, WA, WB>(dx, smem, b, dx_blocks);
+  else product_workgroup<true, true, MOE_ACT_NONE, NS, WR, WC, WA, WB>(dw, smem, b - dx_blocks, gridDim.x - dx_blocks);
+}
+
 // Sums the partial tiles of the split tail tiles in contraction order and applies
 // the epilogue.  One workgroup per (XCD, tail tile, kJoinRows rows of it), 8
 // columns of a row to a lane; four partials are in flight at a time.
 template <int TA> constexpr int kJoinRows = 256 * 8 / TA;
 
 template <int ACT, int TA, int TB>
-__global__ __launch_bounds__(256) void linear_join_kernel(const ProductArgs a, int slots, int KT) {
+__device__ __forceinline__ void join_workgroup(const ProductArgs& a, int slots, int block) {
   constexpr int RG = TB / kJoinRows<TA>;
-  const int rg = blockIdx.x % RG, xcd = (blockIdx.x / RG) & 7, j = blockIdx.x / RG >> 3;
+  const int KT = (a.len + 63) / 64;
+  const int rg = block % RG, xcd = (block / RG) & 7, j = block / RG >> 3;
   const TileShare sp = TileShare::of(a.row_tiles * a.col_tiles, xcd, slots, KT, true);
   if (j >= sp.tail) return;
   int rt, ct;
@@ -415,6 +434,20 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const ProductArgs a, i
       for (int k = 0; k < 8; ++k) v[k] += s + q <= s_hi ? p[q][k] : 0.0f;
   }
   a.ep.template store8<ACT>(r, c, a.cols, v);
+}
+
+template <int ACT, int TA, int TB>
+__global__ __launch_bounds__(256) void linear_join_kernel(const ProductArgs a, int slots) {
+  join_workgroup<ACT, TA, TB>(a, slots, blockIdx.x);
+}
+
+// The joins of two products of one tile shape, a's on the first a_blocks workgroups.
+template <int TA, int TB>
+__global__ __launch_bounds__(256) void linear_join2_kernel(const ProductArgs a, const ProductArgs b, int a_slots,
+                                                           int b_slots, int a_blocks) {
+  const int i = blockIdx.x;
+  if (i < a_blocks) join_workgroup<MOE_ACT_NONE, TA, TB>(a, a_slots, i);
+  else join_workgroup<MOE_ACT_NONE, TA, TB>(b, b_slots, i - a_blocks);
 }
 
 }  // namespace moe
