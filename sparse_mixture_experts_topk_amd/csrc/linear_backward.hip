@@ -5,6 +5,8 @@
 // Both products are tiles (linear_tiles.hpp; fp32 operands: linear_f32.hip) with
 // operands as they lie in memory: dx contracts over w's slow index, dw over that
 // of dpre and of x.
+#include <algorithm>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "linear_plan.hpp"
@@ -75,27 +77,6 @@ __global__ __launch_bounds__(256) void dpre_kernel(const void* __restrict__ dy, 
   }
 }
 
-// dbias[c] = the sum of part[.][c]: 16 lanes to a column, each over every 16th
-// chunk, then joined in lane order.
-__global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ part, int chunks, int N,
-                                                    float* __restrict__ dbias) {
-  __shared__ float sums[16][16];
-  const int cl = threadIdx.x & 15, k = threadIdx.x >> 4, c = blockIdx.x * 16 + cl;
-  float s = 0.f;
-  if (c < N) {
-#pragma unroll 4
-    for (int i = k; i < chunks; i += 16) s += part[(int64_t)i * N + c];
-  }
-  sums[k][cl] = s;
-  __syncthreads();
-  if (threadIdx.x < 16 && c < N) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t += sums[i][cl];
-    dbias[c] = t;
-  }
-}
-
 int prep_chunks(const moe_linear_t& l) { return (l.M + prep_rows(l) - 1) / prep_rows(l); }
 // dpre has values of its own unless dy already is what the products read.
 bool dpre_copied(const moe_linear_t& l) { return l.act != MOE_ACT_NONE || l.y_dtype != l.dtype; }
@@ -104,6 +85,147 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 size_t dpre_bytes(const moe_linear_t& l) { return dpre_copied(l) ? round256((size_t)l.M * l.N * (l.dtype == MOE_F32 ? 4 : 2)) : 0; }
 
 size_t part_bytes(const moe_linear_t& l) { return round256((size_t)prep_chunks(l) * l.N * 4); }
+
+// ---- dbias, dx, dw ----
+
+// Column sums of part[chunks][N]: out[c] = the sum of part[.][c], 16 lanes to a
+// column, each over every 16th chunk, then joined in lane order.
+struct ColumnSums {
+  const float* part;
+  float* out;                // NULL: none wanted
+  int chunks, N;
+};
+template <int THREADS>
+__device__ __forceinline__ void column_sums_workgroup(const ColumnSums& a, float (&sums)[THREADS], int block) {
+  constexpr int COLS = THREADS / 16;
+  const int cl = threadIdx.x % COLS, k = threadIdx.x / COLS, c = block * COLS + cl;
+  float s = 0.f;
+  if (c < a.N) {
+#pragma unroll 4
+    for (int i = k; i < a.chunks; i += 16) s += a.part[(int64_t)i * a.N + c];
+  }
+  sums[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x < COLS && c < a.N) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += sums[i * COLS + cl];
+    a.out[c] = v;
+  }
+}
+
+__global__ __launch_bounds__(256) void dbias_kernel(const ColumnSums a) {
+  __shared__ float sums[256];
+  column_sums_workgroup<256>(a, sums, blockIdx.x);
+}
+hipError_t launch_dbias(const ColumnSums& a, hipStream_t st) {
+  if (a.out == nullptr) return hipSuccess;
+  hipLaunchKernelGGL(dbias_kernel, dim3((a.N + 15) / 16), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+// dbias on the first bias_blocks (a multiple of 8) workgroups, dx on the next
+// dx_blocks, dw on the others: one launch, and dw's workgroups fill the CUs that
+// dx's last round of tiles leaves idle.
+template <int NS, int WR, int WC, int WA, int WB>
+__global__ __launch_bounds__(64 * WR * WC, 1) void linear_gradients_kernel(const ProductArgs dx, const ProductArgs dw,
+                                                                           const ColumnSums dbias, int bias_blocks,
+                                                                           int dx_blocks) {
+  constexpr int THREADS = 64 * WR * WC;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
+  static_assert(THREADS * 4 <= sizeof(smem), "the column sums fit");
+  if ((int)blockIdx.x < bias_blocks) {
+    column_sums_workgroup<THREADS>(dbias, *reinterpret_cast<float (*)[THREADS]>(smem), blockIdx.x);
+    return;
+  }
+  const int b = blockIdx.x - bias_blocks;
+  if (b < dx_blocks) product_workgroup<false, true, MOE_ACT_NONE, NS, WR, WC, WA, WB>(dx, smem, b, dx_blocks);
+  else
+    product_workgroup<true, true, MOE_ACT_NONE, NS, WR, WC, WA, WB>(dw, smem, b - dx_blocks,
+                                                                    gridDim.x - bias_blocks - dx_blocks);
+}
+
+// The joins of two products of one tile shape, a's on the first a_blocks workgroups.
+template <int TA, int TB>
+__global__ __launch_bounds__(256) void linear_join2_kernel(const ProductArgs a, const ProductArgs b, int a_slots,
+                                                           int b_slots, int a_blocks) {
+  const int i = blockIdx.x;
+  if (i < a_blocks) join_workgroup<MOE_ACT_NONE, TA, TB>(a, a_slots, i);
+  else join_workgroup<MOE_ACT_NONE, TA, TB>(b, b_slots, i - a_blocks);
+}
+
+// Both products of a backward pass in one launch, with one tile shape: dw's
+// workgroups fill the CUs that dx's last round leaves, and a launch is saved.
+// Worth kOneLaunch us against each product in its best shape and dbias alone
+// (MI355X, 64 x 512 x 512: 12.1 us against 18.3, 300 x 1024 x 2048: 19.0 against
+// 26.7, 4099 x 256 x 4096, by the plan 1.9 us above: 55.2 against 59.8; not 509 x
+// 4096 x 2048, 3.4 above: 47.7 against 45.8, nor 1024 x 4096 x 4096, 15 above: 100
+// against 92.5).
+constexpr double kOneLaunch = 2.5;
+struct GradientPlan {
+  ProductPlan dx, dw;
+  bool one = false;                  // launch; otherwise each product has its own plan
+};
+template <class F>
+auto with_gradient_plan(int M, int N, int K, F&& run) {
+  const int64_t cus = std::min<int64_t>(device_cu_count(), kMaxPersistentGroups) / 8 * 8;
+  const double apart = with_plan(M, K, N, 1, [](auto, const ProductPlan& p) { return p.cost; }) +
+                       with_plan(N, K, M, 2, [](auto, const ProductPlan& p) { return p.cost; });
+  auto pair = [&](auto tile) {
+    using C = decltype(tile);
+    GradientPlan p{ProductPlan::of<C>(M, K, N, 1, cus), ProductPlan::of<C>(N, K, M, 2, cus)};
+    p.one = p.dx.cost + p.dw.cost <= apart + kOneLaunch;
+    return p;
+  };
+  const GradientPlan a = pair(Tile256x256{}), b = pair(Tile256x128{}), c = pair(Tile128x128{}), d = pair(Tile128x64{});
+  auto cost = [](const GradientPlan& p) { return p.dx.cost + p.dw.cost; };
+  const double least = std::min(std::min(cost(a), cost(b)), std::min(cost(c), cost(d)));
+  if (cost(a) == least) return run(Tile256x256{}, a);
+  if (cost(b) == least) return run(Tile256x128{}, b);
+  if (cost(c) == least) return run(Tile128x128{}, c);
+  return run(Tile128x64{}, d);
+}
+
+// Partial tiles of a backward pass: both products', or those of one at a time.
+size_t gradient_workspace(int M, int N, int K) {
+  const size_t each = std::max(product_workspace(M, K, N, 1), product_workspace(N, K, M, 2));
+  return with_gradient_plan(M, N, K, [&](auto, const GradientPlan& p) {
+    return p.one ? std::max(each, p.dx.workspace + p.dw.workspace) : each;
+  });
+}
+
+// dx = dpre w, dw = dpre^T x and dbias; any of them may be NULL.
+hipError_t launch_gradients(const uint16_t* dpre, const uint16_t* x, const uint16_t* w, uint16_t* dx, uint16_t* dw,
+                            const ColumnSums& dbias, int M, int N, int K, void* partials, hipStream_t st) {
+  const Epilogue to_dx{nullptr, nullptr, dx, nullptr, false}, to_dw{nullptr, nullptr, dw, nullptr, false};
+  return with_gradient_plan(M, N, K, [&](auto tile, const GradientPlan& p) {
+    using C = decltype(tile);
+    using G = GeomOf<C>;
+    hipError_t e = hipSuccess;
+    if (!p.one || dx == nullptr || dw == nullptr) {
+      e = launch_dbias(dbias, st);
+      if (e == hipSuccess && dx != nullptr)
+        e = launch_product<false, true, MOE_ACT_NONE>(dpre, N, w, K, M, K, N, partials, to_dx, st);
+      if (e == hipSuccess && dw != nullptr)
+        e = launch_product<true, true, MOE_ACT_NONE>(dpre, N, x, K, N, K, M, partials, to_dw, st);
+      return e;
+    }
+    const ProductArgs a{dpre, w, N, K, M, K, N, p.dx.row_tiles, p.dx.col_tiles, p.dx.split,
+                        static_cast<float*>(partials), to_dx};
+    const ProductArgs b{dpre, x, N, K, N, K, M, p.dw.row_tiles, p.dw.col_tiles, p.dw.split,
+                        reinterpret_cast<float*>(static_cast<uint8_t*>(partials) + p.dx.workspace), to_dw};
+    const int cols = G::THREADS / 16, bias_blocks = dbias.out != nullptr ? (N + 8 * cols - 1) / (8 * cols) * 8 : 0;
+    hipLaunchKernelGGL((linear_gradients_kernel<C::NS, C::WR, C::WC, C::WA, C::WB>),
+                       dim3((unsigned)(bias_blocks + p.dx.grid + p.dw.grid)), dim3(G::THREADS), 0, st, a, b, dbias,
+                       bias_blocks, p.dx.grid);
+    e = hipGetLastError();
+    if (e != hipSuccess || !(p.dx.split || p.dw.split)) return e;
+    const int ja = p.dx.split ? (int)join_blocks_of<C>(p.dx) : 0, jb = p.dw.split ? (int)join_blocks_of<C>(p.dw) : 0;
+    hipLaunchKernelGGL((linear_join2_kernel<G::TA, G::TB>), dim3((unsigned)(ja + jb)), dim3(256), 0, st, a, b,
+                       p.dx.grid / 8, p.dw.grid / 8, ja);
+    return hipGetLastError();
+  });
+}
 
 }  // namespace
 
@@ -134,20 +256,20 @@ hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const v
     else if (f32) e = act ? run(dpre_kernel<true, true, false>) : run(dpre_kernel<true, false, false>);
     else e = act ? run(dpre_kernel<false, true, false>) : run(dpre_kernel<false, false, false>);
   }
-  if (e == hipSuccess && dbias != nullptr && !one_chunk) {
-    hipLaunchKernelGGL(dbias_kernel, dim3((l.N + 15) / 16), dim3(256), 0, st, part, prep_chunks(l), l.N, dbias);
-    e = hipGetLastError();
-  }
   if (e != hipSuccess) return e;
   const void* d = copy != nullptr ? copy : dy;
   void* partials = static_cast<uint8_t*>(workspace) + dpre_bytes(l) + part_bytes(l);
-  if (l.dtype == MOE_F32)
+  const ColumnSums sums{part, one_chunk ? nullptr : dbias, prep_chunks(l), l.N};
+  if (l.dtype == MOE_F32) {
+    e = launch_dbias(sums, st);
+    if (e != hipSuccess) return e;
     return launch_linear_products_f32(l, static_cast<const float*>(d), static_cast<const float*>(x),
                                       static_cast<const float*>(w), static_cast<float*>(dx), static_cast<float*>(dw),
                                       partials, st);
+  }
   return launch_gradients(static_cast<const uint16_t*>(d), static_cast<const uint16_t*>(x),
-                          static_cast<const uint16_t*>(w), static_cast<uint16_t*>(dx), static_cast<uint16_t*>(dw), l.M,
-                          l.N, l.K, partials, st);
+                          static_cast<const uint16_t*>(w), static_cast<uint16_t*>(dx), static_cast<uint16_t*>(dw), sums,
+                          l.M, l.N, l.K, partials, st);
 }
 
 }  // namespace moe

@@ -98,72 +98,4 @@ hipError_t launch_product(const uint16_t* P, int64_t ldp, const uint16_t* Q, int
   });
 }
 
-// Both products of a backward pass in one launch, with one tile shape: dw's
-// workgroups fill the CUs that dx's last round leaves, and a launch is saved.
-// Worth kOneLaunch us against each product in its best shape (MI355X, 64 x 512 x
-// 512: 13.9 us against 18.3, 300 x 1024 x 2048: 21.1 against 26.7, 4099 x 256 x
-// 4096, 1.9 us above: 57.7 against 59.8; 509 x 4096 x 2048, 3.4 above: 47.7
-// against 45.8, 1024 x 4096 x 4096, 15 above: 100 against 92.5).
-constexpr double kOneLaunch = 2.5;
-struct GradientPlan {
-  ProductPlan dx, dw;
-  bool one = false;                  // launch; otherwise each product has its own plan
-};
-template <class F>
-auto with_gradient_plan(int M, int N, int K, F&& run) {
-  const int64_t cus = std::min<int64_t>(device_cu_count(), kMaxPersistentGroups) / 8 * 8;
-  const double apart = with_plan(M, K, N, 1, [](auto, const ProductPlan& p) { return p.cost; }) +
-                       with_plan(N, K, M, 2, [](auto, const ProductPlan& p) { return p.cost; });
-  auto pair = [&](auto tile) {
-    using C = decltype(tile);
-    GradientPlan p{ProductPlan::of<C>(M, K, N, 1, cus), ProductPlan::of<C>(N, K, M, 2, cus)};
-    p.one = p.dx.cost + p.dw.cost <= apart + kOneLaunch;
-    return p;
-  };
-  const GradientPlan a = pair(Tile256x256{}), b = pair(Tile256x128{}), c = pair(Tile128x128{}), d = pair(Tile128x64{});
-  auto cost = [](const GradientPlan& p) { return p.dx.cost + p.dw.cost; };
-  const double least = std::min(std::min(cost(a), cost(b)), std::min(cost(c), cost(d)));
-  if (cost(a) == least) return run(Tile256x256{}, a);
-  if (cost(b) == least) return run(Tile256x128{}, b);
-  if (cost(c) == least) return run(Tile128x128{}, c);
-  return run(Tile128x64{}, d);
-}
-
-// Partial tiles of a backward pass: both products', or those of one at a time.
-inline size_t gradient_workspace(int M, int N, int K) {
-  const size_t each = std::max(product_workspace(M, K, N, 1), product_workspace(N, K, M, 2));
-  return with_gradient_plan(M, N, K, [&](auto, const GradientPlan& p) {
-    return p.one ? std::max(each, p.dx.workspace + p.dw.workspace) : each;
-  });
-}
-
-// dx = dpre w and dw = dpre^T x; either may be NULL.
-inline hipError_t launch_gradients(const uint16_t* dpre, const uint16_t* x, const uint16_t* w, uint16_t* dx, uint16_t* dw,
-                                   int M, int N, int K, void* partials, hipStream_t st) {
-  const Epilogue to_dx{nullptr, nullptr, dx, nullptr, false}, to_dw{nullptr, nullptr, dw, nullptr, false};
-  return with_gradient_plan(M, N, K, [&](auto tile, const GradientPlan& p) {
-    using C = decltype(tile);
-    using G = GeomOf<C>;
-    hipError_t e = hipSuccess;
-    if (!p.one || dx == nullptr || dw == nullptr) {
-      if (dx != nullptr) e = launch_product<false, true, MOE_ACT_NONE>(dpre, N, w, K, M, K, N, partials, to_dx, st);
-      if (e == hipSuccess && dw != nullptr)
-        e = launch_product<true, true, MOE_ACT_NONE>(dpre, N, x, K, N, K, M, partials, to_dw, st);
-      return e;
-    }
-    const ProductArgs a{dpre, w, N, K, M, K, N, p.dx.row_tiles, p.dx.col_tiles, p.dx.split,
-                        static_cast<float*>(partials), to_dx};
-    const ProductArgs b{dpre, x, N, K, N, K, M, p.dw.row_tiles, p.dw.col_tiles, p.dw.split,
-                        reinterpret_cast<float*>(static_cast<uint8_t*>(partials) + p.dx.workspace), to_dw};
-    hipLaunchKernelGGL((linear_gradients_kernel<C::NS, C::WR, C::WC, C::WA, C::WB>),
-                       dim3((unsigned)(p.dx.grid + p.dw.grid)), dim3(G::THREADS), 0, st, a, b, p.dx.grid);
-    e = hipGetLastError();
-    if (e != hipSuccess || !(p.dx.split || p.dw.split)) return e;
-    const int ja = p.dx.split ? (int)join_blocks_of<C>(p.dx) : 0, jb = p.dw.split ? (int)join_blocks_of<C>(p.dw) : 0;
-    hipLaunchKernelGGL((linear_join2_kernel<G::TA, G::TB>), dim3((unsigned)(ja + jb)), dim3(256), 0, st, a, b,
-                       p.dx.grid / 8, p.dw.grid / 8, ja);
-    return hipGetLastError();
-  });
-}
-
 }  // namespace moe

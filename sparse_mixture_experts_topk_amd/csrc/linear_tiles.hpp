@@ -393,17 +393,6 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void linear_product_kernel(const P
   product_workgroup<PSLOW, QSLOW, ACT, NS, WR, WC, WA, WB>(a, smem, blockIdx.x, gridDim.x);
 }
 
-// dx on the first dx_blocks workgroups, dw on the others: one launch, and dw's
-// workgroups fill the CUs that dx's last round of tiles leaves idle.
-template <int NS, int WR, int WC, int WA, int WB>
-__global__ __launch_bounds__(64 * WR * WC, 1) void linear_gradients_kernel(const ProductArgs dx, const ProductArgs dw,
-                                                                           int dx_blocks) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
-  const int b = blockIdx.x;
-  if (b < dx_blocks) product_workgroup<false, true, MOE_ACT_NONE, NS, WR, WC, WA, WB>(dx, smem, b, dx_blocks);
-  else product_workgroup<true, true, MOE_ACT_NONE, NS, WR, WC, WA, WB>(dw, smem, b - dx_blocks, gridDim.x - dx_blocks);
-}
-
 // Sums the partial tiles of the split tail tiles in contraction order and applies
 // the epilogue.  One workgroup per (XCD, tail tile, kJoinRows rows of it), 8
 // columns of a row to a lane; four partials are in flight at a time.
@@ -439,15 +428,6 @@ __device__ __forceinline__ void join_workgroup(const ProductArgs& a, int slots, 
 template <int ACT, int TA, int TB>
 __global__ __launch_bounds__(256) void linear_join_kernel(const ProductArgs a, int slots) {
   join_workgroup<ACT, TA, TB>(a, slots, blockIdx.x);
-}
-
-// The joins of two products of one tile shape, a's on the first a_blocks workgroups.
-template <int TA, int TB>
-__global__ __launch_bounds__(256) void linear_join2_kernel(const ProductArgs a, const ProductArgs b, int a_slots,
-                                                           int b_slots, int a_blocks) {
-  const int i = blockIdx.x;
-  if (i < a_blocks) join_workgroup<MOE_ACT_NONE, TA, TB>(a, a_slots, i);
-  else join_workgroup<MOE_ACT_NONE, TA, TB>(b, b_slots, i - a_blocks);
 }
 
 }  // namespace moe
