@@ -8,8 +8,11 @@
 // flight in registers, go through the wavefront's own LDS tile (16-byte chunks
 // XOR-swizzled by row; LDS operations of one wavefront execute in order, so no
 // barrier) and come back in the v_mfma_f32_16x16x32_bf16 layout.  The rows of x
-// (L2-resident) are read directly.  At the end the wavefronts' accumulators meet
-// in LDS and are summed in wavefront order, 8 channels of a row to a lane.
+// (L2-resident) go the same way: read in the layout of the products instead, 16
+// rows of 64 bytes a load, 32 rows took 31 us for 26 (MI355X, 14336 x 4096).  At
+// the end the wavefronts' accumulators meet in LDS and are summed in wavefront
+// order, 8 channels of a row to a lane.  Bound by the weight stream: 1 row, 14336
+// x 4096: 21.2 us, 5.5 TB/s; few channels by latency (16 rows, 256 x 4096: 6.8 us).
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "linear_epilogue.hpp"
@@ -21,12 +24,12 @@ namespace {
 constexpr int kStage = 128;                     // terms per stage
 constexpr int kTileBytes = 16 * kStage * 2;     // one wavefront's LDS tile
 
-template <int ACT, int NT, int CG, int W, int D, bool XLDS>
+template <int ACT, int NT, int CG, int W, int D>
 __global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t* __restrict__ x,
                                                                   const uint16_t* __restrict__ w, int M, int N, int K,
                                                                   const Epilogue ep) {
   static_assert(NT * 16 * 16 * 4 <= kTileBytes, "the accumulators fit the tile");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[W][(CG + (XLDS ? NT : 0)) * kTileBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[W][(CG + NT) * kTileBytes];
   const int c0 = xcd_remap(blockIdx.x, gridDim.x) * (16 * CG);  // a contiguous eighth of the channels per XCD
   if (c0 >= N) return;                                          // the whole workgroup
   const int lane = threadIdx.x & 63, v = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -40,7 +43,7 @@ __global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t
   const __amdgpu_buffer_rsrc_t dw =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(w + (int64_t)c0 * K), 0, min(16 * CG, N - c0) * K * 2, kRawBufferFlags);
   const __amdgpu_buffer_rsrc_t dx = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(x), 0, M * K * 2, kRawBufferFlags);
-  const int woff = lrow * K * 2 + lch * 16, xoff = r * K * 2 + g * 16;
+  const int off = lrow * K * 2 + lch * 16;
   constexpr int kPast = (int)0x80000000u, kStream = 2;             // kStream: non-temporal, read once
 
   u32x4_t wv[D][CG * 4], xv[D][NT * 4];
@@ -49,20 +52,10 @@ __global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t
     const int wpast = k0 + lch * 8 < K ? 0 : kPast;
 #pragma unroll
     for (int i = 0; i < CG * 4; ++i)
-      wd[i] = __builtin_amdgcn_raw_buffer_load_b128(dw, (woff + i * 4 * K * 2) | wpast, k0 * 2, kStream);
-    if constexpr (XLDS) {
+      wd[i] = __builtin_amdgcn_raw_buffer_load_b128(dw, (off + i * 4 * K * 2) | wpast, k0 * 2, kStream);
 #pragma unroll
-      for (int i = 0; i < NT * 4; ++i)
-        xd[i] = __builtin_amdgcn_raw_buffer_load_b128(dx, (woff + i * 4 * K * 2) | wpast, k0 * 2, 0);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int xpast = k0 + j * 32 + g * 8 < K ? 0 : kPast;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          xd[n * 4 + j] = __builtin_amdgcn_raw_buffer_load_b128(dx, (xoff + n * 16 * K * 2 + j * 64) | xpast, k0 * 2, 0);
-      }
-    }
+    for (int i = 0; i < NT * 4; ++i)
+      xd[i] = __builtin_amdgcn_raw_buffer_load_b128(dx, (off + i * 4 * K * 2) | wpast, k0 * 2, 0);
   };
   f32x4_t acc[CG][NT];
 #pragma unroll
@@ -75,23 +68,17 @@ __global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t
       const int row = i * 4 + lrow;
       *reinterpret_cast<u32x4_t*>(tile + row * (kStage * 2) + ((lch ^ (row & 15)) << 4)) = wd[i];
     }
-    if constexpr (XLDS) {
 #pragma unroll
-      for (int i = 0; i < NT * 4; ++i) {
-        const int row = i * 4 + lrow;
-        *reinterpret_cast<u32x4_t*>(tile + CG * kTileBytes + row * (kStage * 2) + ((lch ^ (row & 15)) << 4)) = xd[i];
-      }
+    for (int i = 0; i < NT * 4; ++i) {
+      const int row = i * 4 + lrow;
+      *reinterpret_cast<u32x4_t*>(tile + CG * kTileBytes + row * (kStage * 2) + ((lch ^ (row & 15)) << 4)) = xd[i];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint4 xs[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if constexpr (XLDS)
-          xs[n] = *reinterpret_cast<const uint4*>(tile + CG * kTileBytes + (n * 16 + r) * (kStage * 2) + (((4 * j + g) ^ r) << 4));
-        else
-          xs[n] = __builtin_bit_cast(uint4, xd[n * 4 + j]);
-      }
+      for (int n = 0; n < NT; ++n)
+        xs[n] = *reinterpret_cast<const uint4*>(tile + CG * kTileBytes + (n * 16 + r) * (kStage * 2) + (((4 * j + g) ^ r) << 4));
 #pragma unroll
       for (int c = 0; c < CG; ++c) {
         const uint4 a = *reinterpret_cast<const uint4*>(tile + (c * 16 + r) * (kStage * 2) + (((4 * j + g) ^ r) << 4));
@@ -133,24 +120,25 @@ __global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t
   }
 }
 
+// One block of 16 channels and 8 wavefronts per workgroup, one stage in flight
+// each.  Two blocks of rows leave LDS for one such workgroup per CU: where there
+// are more channels than one round of them takes, 4 wavefronts on two blocks of
+// channels, two workgroups per CU, share each read of x twice.  MI355X, us, wide
+// against narrow: 32 rows of 4096 terms, N 4096 13.3 / 11.6, N 6144 14.3 / 18.7, N
+// 14336 25.8 / 35.3; with 16 rows N 12288 21.8 / 19.3, N 14336 23.1 / 24.0.  16
+// wavefronts or two stages in flight gain nothing (16 rows, N 4096: 10.2, 9.6 / 9.2).
 template <int ACT, int NT>
 hipError_t launch_act(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
                       hipStream_t st) {
-  const int cus = device_cu_count();
   auto run = [&](auto kernel, int cg, int waves) {
     const int groups = (l.N + 16 * cg - 1) / (16 * cg);
     hipLaunchKernelGGL(kernel, dim3((unsigned)((groups + 7) / 8 * 8)), dim3(waves * kWave), 0, st, x, w, l.M, l.N, l.K, ep);
     return hipGetLastError();
   };
-  const int groups = (l.N + 15) / 16;
-  if (groups >= 3 * cus) {
-    if constexpr (NT == 1) {
-      if (l.M <= 4) return run(linear_decode_kernel<ACT, NT, 2, 8, 1, false>, 2, 8);
-    }
-    return run(linear_decode_kernel<ACT, NT, 2, 4, 1, true>, 2, 4);
+  if constexpr (NT == 2) {
+    if ((l.N + 15) / 16 > device_cu_count()) return run(linear_decode_kernel<ACT, NT, 2, 4, 2>, 2, 4);
   }
-  if (groups >= cus / 2) return run(linear_decode_kernel<ACT, NT, 1, 8, 1, true>, 1, 8);
-  return run(linear_decode_kernel<ACT, NT, 1, NT == 1 ? 16 : 8, 2, true>, 1, NT == 1 ? 16 : 8);
+  return run(linear_decode_kernel<ACT, NT, 1, 8, 1>, 1, 8);
 }
 
 template <int ACT>

@@ -113,7 +113,9 @@ hipError_t launch_linear_f32(const moe_linear_t& l, const float* x, const float*
 hipError_t launch_linear_products_f32(const moe_linear_t& l, const float* dpre, const float* x, const float* w,
                                       float* dx, float* dw, void* partials, hipStream_t st);
 
-// Weight streaming for up to kLinearDecodeRows rows.
+// Weight streaming for up to kLinearDecodeRows rows (MI355X, us, 32 rows streamed
+// against 33 in tiles: 4096 x 4096 11.1 / 15.6, 14336 x 4096 26.0 / 30.8; 64 rows
+// streamed four blocks at a time 34.7 against 31.2).
 constexpr int kLinearDecodeRows = 32;
 int device_cu_count();
 hipError_t launch_linear_decode(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
