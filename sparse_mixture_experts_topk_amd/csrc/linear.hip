@@ -6,8 +6,9 @@
 //
 //   y = act(x w^T + bias) + residual
 //
-// bf16: up to kLinearDecodeRows rows stream the weights (linear_decode.hip); more
-// run as tiles (linear_tiles.hpp).  fp32: linear_f32.hip.
+// bf16: up to kLinearDecodeRows rows stream the weights (linear_decode.hip); more,
+// or few channels of a long contraction, run as tiles (linear_tiles.hpp).  fp32:
+// linear_f32.hip.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -16,9 +17,23 @@
 
 namespace moe {
 
+// Streaming keeps a block of 16 channels on one CU, which takes in 45-65 KB per us: its
+// weights and, again for each block, the rows of x.  Where the blocks leave CUs
+// idle and that is longer than the tiles' runs and their join (kTilesStart us more
+// than a stream to get going), tiles it is.  MI355X, us, stream / tiles: 31 x 368 x
+// 9120 19.6 / 14.1, 32 x 2048 x 14336 27.5 / 19.8, 16 x 208 x 12472 20.2 / 13.5; 16
+// x 1024 x 8192 10.9 / 15.1, 16 x 4096 x 14336 24.8 / 28.9.
+constexpr double kCuBytesPerUs = 55e3, kTilesStart = 3;
+static bool streams(const moe_linear_t& l) {
+  if (l.M > kLinearDecodeRows) return false;
+  if ((l.N + 15) / 16 > device_cu_count()) return true;
+  const double stream = 2.0 * l.K * (16 + l.M) / kCuBytesPerUs;
+  return with_plan(l.M, l.N, l.K, 0, [&](auto, const ProductPlan& p) { return stream <= p.cost + kTilesStart; });
+}
+
 size_t linear_workspace_bytes(const moe_linear_t& l) {
   if (l.dtype == MOE_F32) return linear_workspace_bytes_f32(l);
-  return l.M <= kLinearDecodeRows ? 0 : product_workspace(l.M, l.N, l.K, 0);
+  return streams(l) ? 0 : product_workspace(l.M, l.N, l.K, 0);
 }
 
 hipError_t launch_linear(const moe_linear_t& l, const void* x_, const void* w_, const float* bias,
@@ -29,7 +44,7 @@ hipError_t launch_linear(const moe_linear_t& l, const void* x_, const void* w_, 
                              workspace, st);
   const uint16_t *x = static_cast<const uint16_t*>(x_), *w = static_cast<const uint16_t*>(w_);
   const Epilogue ep{bias, residual, y, static_cast<uint16_t*>(pre), l.y_dtype == MOE_F32};
-  if (l.M <= kLinearDecodeRows) return launch_linear_decode(l, x, w, ep, st);
+  if (streams(l)) return launch_linear_decode(l, x, w, ep, st);
   auto run = [&](auto act) {
     return launch_product<false, false, decltype(act)::value>(x, l.K, w, l.K, l.M, l.N, l.K, workspace, ep, st);
   };

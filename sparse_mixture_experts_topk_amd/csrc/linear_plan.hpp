@@ -23,7 +23,9 @@ template <class C> using GeomOf = ProductGeom<C::NS, C::WR, C::WC, C::WA, C::WB>
 // read once: 509 x 4096 x 2048 split in two with 128 x 128 tiles, 17 MB: 8 us
 // longer than its slices; with 256 x 256 tiles, 67 MB: 25 us.
 constexpr double kJoinFixed = 4.0, kJoinPerByte = 0.32e-6;
-constexpr int kMinSlices = 4;        // of a split run
+// Slices of a split run, at least (8 against 4, us: 33 x 256 x 4096 10.2 / 11.7, 1 x
+// 8176 x 408 backward 19.5 / 22.7).
+constexpr int kMinSlices = 8;
 
 struct ProductPlan {
   double cost = 1e30;                // us, without what all candidates share
@@ -42,7 +44,7 @@ struct ProductPlan {
       p.KT = (len + G::BK - 1) / G::BK;
       p.split = split != 0;
       const int64_t tiles = (int64_t)p.row_tiles * p.col_tiles;
-      const int64_t most = p.split ? tiles * p.KT / kMinSlices / 8 * 8 : (tiles + 7) / 8 * 8;
+      const int64_t per_xcd = (tiles + 7) / 8, most = 8 * (p.split ? per_xcd * p.KT / kMinSlices : per_xcd);
       p.grid = (int)std::max<int64_t>(8, std::min<int64_t>(cus, most));
       const TileShare s = TileShare::of((int)tiles, 0, p.grid / 8, p.KT, p.split);      // the largest share
       const double parts = p.split ? 8.0 * (p.grid / 8 + s.tail) * G::PARTIAL * 4 : 0;

@@ -563,6 +563,51 @@ def test_linear_backward(dims):
     linear_backward_case(M, N, K, "gelu", "f32", dtype="f32")
 
 
+# each tile shape, with either, both or none of the products cut along its contraction
+# and joined; one launch for all gradients, then (the last two) a launch for each
+@pytest.mark.parametrize("dims", [(64, 256, 256), (1024, 256, 256), (64, 1024, 256), (1500, 2048, 256),
+                                  (700, 256, 3000), (1500, 256, 2048), (200, 3000, 1024), (2048, 2048, 512),
+                                  (700, 1024, 8192), (4096, 512, 2048), (200, 8192, 3000), (4096, 4096, 512),
+                                  (1500, 2048, 8192), (509, 4096, 2048), (64, 1024, 8192)])
+def test_linear_backward_together_and_alone(dims):
+    """All gradients of one call, and each of a call of its own, against 64-bit products on the device."""
+    M, N, K = dims
+    say(f"linear backward together M={M} N={N} K={K}")
+    g = gen(sum(dims))
+    dy, x, w = (cuda(normal(g, *s, dtype=torch.bfloat16)) for s in ((M, N), (M, K), (N, K)))
+    lin = moe.make_linear(M, N, K)
+    n = moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR_BACKWARD)
+    d64, x64, w64 = dy.double(), x.double(), w.double()
+    wants = [(d64 @ w64, d64.abs() @ w64.abs()), (d64.t().contiguous() @ x64, d64.t().abs().contiguous() @ x64.abs()),
+             (d64.sum(0), d64.abs().sum(0))]
+    tols = [(N + 4) * 2.0 ** -23 * (1 + BF16) * wants[0][1] + BF16 * wants[0][0].abs(),
+            (M + 4) * 2.0 ** -23 * (1 + BF16) * wants[1][1] + BF16 * wants[1][0].abs(), (M + 4) * F32 * wants[2][1]]
+    for outputs in ((True, True, True), (True, True, False), (True, False, True), (False, True, False)):
+        ws = Out(n, dtype=torch.uint8, fill=77) if n else None
+        if ws:
+            ws.t.fill_(0xFF)
+        outs = [Out(M, K, dtype=torch.bfloat16), Out(N, K, dtype=torch.bfloat16), Out(N)]
+        moe.moe_linear_backward(lin, dy, None, x, w, *(o.t if on else None for o, on in zip(outs, outputs)),
+                                ws.t if ws else None)
+        torch.cuda.synchronize()
+        for o, on, (want, _), tol, name in zip(outs, outputs, wants, tols, ("dx", "dw", "dbias")):
+            got = o.np()
+            if on:
+                close(got, want.cpu().numpy(), tol.cpu().numpy(), name)
+            else:
+                assert (got == -7.0).all()
+        if ws:
+            ws.np()
+
+
+# few rows: two blocks of channels to a workgroup, and long contractions of few channels cut into runs
+@pytest.mark.parametrize("dims", [(17, 4104, 136), (32, 6144, 520), (16, 208, 12472), (31, 368, 9120), (9, 40, 16384),
+                                  (32, 4096, 392)])
+def test_linear_of_few_rows(dims):
+    linear_case(*dims, "none", "f32", bias=False)
+    linear_case(*dims, "silu", "bf16", bias=True, residual=True, pre=True)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_linear_backward_activations(act, out):
