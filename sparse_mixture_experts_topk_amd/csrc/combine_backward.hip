@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
+constexpr int kMaxTokens = 1 << 23;      // per launch
 
 // K slots and S (0 or 1) shared rows.  A dropped slot reads row 0 (present
 // whenever T > 0) and is selected away, so that all loads of a step are in
@@ -26,10 +27,10 @@ constexpr int kWaves = kThreads / kWave;
 template <bool BF16, int K, int S>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const void* __restrict__ dy, const float* __restrict__ y_perm, const int32_t* __restrict__ slot_to_row,
-    const float* __restrict__ gw, int d, int T, void* __restrict__ dy_perm, float* __restrict__ dweights) {
+    const float* __restrict__ gw, int d, int T, int first, void* __restrict__ dy_perm, float* __restrict__ dweights) {
   constexpr int N = K + S;
   __shared__ double part[kWaves][K];
-  const int t = blockIdx.x;
+  const int t = first + blockIdx.x;
   int rows[N];
   float g[N];
 #pragma unroll
@@ -111,13 +112,19 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
 template <int K, int S>
 hipError_t launch_ks(const moe_shape_t& s, const void* dy, const float* y_perm, const int32_t* slot_to_row,
                      const float* weights, void* dy_perm, float* dweights, hipStream_t st) {
-  if (s.act_dtype == MOE_BF16)
-    hipLaunchKernelGGL((combine_backward_kernel<true, K, S>), dim3(s.T), dim3(kThreads), 0, st, dy, y_perm,
-                       slot_to_row, weights, s.d_model, s.T, dy_perm, dweights);
-  else
-    hipLaunchKernelGGL((combine_backward_kernel<false, K, S>), dim3(s.T), dim3(kThreads), 0, st, dy, y_perm,
-                       slot_to_row, weights, s.d_model, s.T, dy_perm, dweights);
-  return hipGetLastError();
+  // a grid has fewer than 2^32 threads: 2^24 tokens take two launches
+  for (int first = 0; first < s.T; first += kMaxTokens) {
+    const dim3 grid((unsigned)(s.T - first < kMaxTokens ? s.T - first : kMaxTokens));
+    if (s.act_dtype == MOE_BF16)
+      hipLaunchKernelGGL((combine_backward_kernel<true, K, S>), grid, dim3(kThreads), 0, st, dy, y_perm,
+                         slot_to_row, weights, s.d_model, s.T, first, dy_perm, dweights);
+    else
+      hipLaunchKernelGGL((combine_backward_kernel<false, K, S>), grid, dim3(kThreads), 0, st, dy, y_perm,
+                         slot_to_row, weights, s.d_model, s.T, first, dy_perm, dweights);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int S>

@@ -73,6 +73,7 @@ class ForwardBuffers:
     drop_mask: torch.Tensor
     logits: torch.Tensor
     workspace: torch.Tensor
+    routing: Optional[dict] = None        # scored_routing's buffers: as long-lived as the others
 
 
 def alloc_forward(cfg, device="cuda", with_outputs=True) -> ForwardBuffers:
@@ -97,7 +98,8 @@ def _bytes(n: int, device) -> Optional[torch.Tensor]:
 def scored_routing(di: DeviceInputs, router, balance_bias=None, stream=None, out: Optional[dict] = None,
                    scores: bool = False) -> dict:
     """logits = x . w_gate^T (+ router_bias) in fp32, then moe_route_scored: the buffers of both
-    (``out`` holds ones to use: logits, topk_ids, topk_weights, next_ids, scores, linear_ws)."""
+    (``out`` holds ones to use: logits, topk_ids, topk_weights, next_ids, scores, linear_ws).
+    n_experts must be a multiple of 8, like every width of moe_linear."""
     cfg, dev = di.cfg, di.x.device
     T, E, k = cfg.T, cfg.n_experts, cfg.top_k
     lin = make_linear(T, E, cfg.d_model, dtype=cfg.act_dtype, y_dtype="f32")
@@ -144,8 +146,9 @@ def forward(di: DeviceInputs, buf: Optional[ForwardBuffers] = None, stream=None,
     if buf is None:
         buf = alloc_forward(cfg, di.x.device)
     if router is not None:
-        r = scored_routing(di, router, balance_bias, stream,
-                           {"topk_ids": buf.topk_ids, "topk_weights": buf.topk_weights, "logits": buf.logits})
+        if buf.routing is None:
+            buf.routing = {"topk_ids": buf.topk_ids, "topk_weights": buf.topk_weights, "logits": buf.logits}
+        r = scored_routing(di, router, balance_bias, stream, buf.routing)
         moe_forward_routed(shape_of(cfg), di.x, r["topk_ids"], r["topk_weights"], r["next_ids"], di.w1, di.w3,
                            di.w2, di.w1_scale, di.w3_scale, di.w2_scale, buf.y, buf.expert_counts,
                            buf.drop_mask, buf.workspace, stream)

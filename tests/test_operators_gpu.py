@@ -859,3 +859,101 @@ def test_scored_layer_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip((buf.y, r["topk_ids"], r["topk_weights"], dl), want)), i
+
+
+# ---- sizes whose offsets pass 32 bits ----
+
+def device_normal(seed, *shape, std=1.0, dtype=torch.bfloat16):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.empty(*shape, device=DEV, dtype=dtype).normal_(0, std, generator=g)
+
+
+def test_combine_backward_of_the_most_tokens():
+    T, d = 1 << 24, 64
+    say(f"combine backward T={T} d={d}")
+    dy, w = device_normal(1, T, d), device_normal(2, T, 1, dtype=torch.float32)
+    y = device_normal(3, T, d, dtype=torch.float32)
+    rows = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV)       # last token first
+    dyp, dw = torch.empty(T, d, dtype=torch.bfloat16, device=DEV), torch.empty(T, 1, device=DEV)
+    moe.moe_combine_backward(moe.make_shape(T, d, 64, 16, 1), dy, y, rows, w, dyp, dw)
+    torch.cuda.synchronize()
+    for at in (0, (1 << 23) - 50, T - 100):
+        tok = slice(at, at + 100)
+        r = rows[tok].long()
+        want = w[tok].double() * dy[tok].double()
+        close(f64(dyp[r]), f64(want), f64((BF16 + 2 * F32) * want.abs()), "dy_perm")
+        prod = dy[tok].double() * y[r].double()
+        want = prod.sum(1, keepdim=True)
+        close(f64(dw[tok]), f64(want), f64(F32 * want.abs() + d * 2.0 ** -52 * prod.abs().sum(1, keepdim=True)), "dw")
+
+
+def test_route_of_more_than_2_31_logits():
+    T, E, k = (1 << 23) + 3, 256, 8
+    say(f"route T={T} E={E}")
+    l, b = device_normal(4, T, E, dtype=torch.float32), device_normal(5, E, std=0.1, dtype=torch.float32)
+    router = moe.make_router("sigmoid", 8, 4, 2, scale=2.5)
+
+    def route(rows):
+        n = rows.shape[0]
+        shape = moe.make_shape(n, 64, 64, E, k)
+        ids, w = torch.empty(n, k, dtype=torch.int32, device=DEV), torch.empty(n, k, device=DEV)
+        moe.moe_route_scored(shape, router, rows, b, ids, w)
+        dl = torch.empty(n, E, device=DEV)
+        moe.moe_route_scored_backward(shape, router, rows, ids, w, None, dl)
+        return ids, w, dl
+
+    whole = route(l)
+    for at in (0, (1 << 23) - 20):                                          # rows do not depend on the batch
+        for got, want in zip(whole, route(l[at:at + 23].contiguous())):
+            assert torch.equal(got[at:at + 23], want)
+
+
+@pytest.mark.parametrize("N,K", [(8, 1032), (1032, 8)])
+def test_linear_of_more_than_2_31_elements(N, K):
+    M = (1 << 21) + 37
+    say(f"linear M={M} N={N} K={K}")
+    x, w = device_normal(6, M, K), device_normal(7, N, K, std=K ** -0.5)
+    dy, pre = device_normal(8, M, N), torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    y = torch.empty_like(pre)
+    lin = moe.make_linear(M, N, K, act="relu")
+    moe.moe_linear(lin, x, w, None, None, y, pre, runner._bytes(moe.moe_linear_workspace_bytes(lin), DEV))
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(N, device=DEV)
+    ws = runner._bytes(moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR_BACKWARD), DEV)
+    moe.moe_linear_backward(lin, dy, pre, x, w, dx, dw, db, ws)
+    torch.cuda.synchronize()
+    w64, aw = w.double(), w.double().abs()
+    wt, awt = w64.t().contiguous(), aw.t().contiguous()
+    wdw, adw, wdb, adb = (torch.zeros(s, device=DEV, dtype=torch.float64) for s in ((N, K), (N, K), (N,), (N,)))
+    step = 1 << 15
+    for at in range(0, M, step):
+        rows = slice(at, min(at + step, M))
+        x64, d64 = x[rows].double(), dy[rows].double() * (pre[rows].double() > 0)
+        wdw += d64.t().contiguous() @ x64
+        adw += d64.t().abs().contiguous() @ x64.abs()
+        wdb += d64.sum(0)
+        adb += d64.abs().sum(0)
+        if at in (0, M // step * step):
+            want = x64 @ wt
+            close(f64(pre[rows]), f64(want), f64((K + 4) * 2.0 ** -23 * (1 + BF16) * (x64.abs() @ awt) + BF16 * want.abs()), "pre")
+            want = d64 @ w64
+            close(f64(dx[rows]), f64(want), f64((N + 4) * 2.0 ** -23 * (1 + BF16) * (d64.abs() @ aw) + BF16 * want.abs()), "dx")
+    close(f64(dw), f64(wdw), f64((M + 4) * 2.0 ** -23 * (1 + BF16) * adw + BF16 * wdw.abs()), "dw")
+    close(f64(db), f64(wdb), f64((M + 4) * F32 * adb), "dbias")
+
+
+def test_scored_layer_on_a_stream_of_its_own():
+    """Temporaries of a call outlive it: memory taken and written afterwards on the current stream is not theirs."""
+    cfg, inp, balance = layer(T=500, E=64, k=6)
+    say("scored layer on a stream of its own")
+    di = runner.DeviceInputs.from_host(inp)
+    router, b = moe.make_router(**ROUTER), cuda(balance)
+    want = runner.forward(di, router=router, balance_bias=b)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = runner.forward(di, stream=side, router=router, balance_bias=b)
+    junk = [torch.full((n,), -1, dtype=torch.int32, device=DEV) for n in (cfg.T * 2, 1 << 18, 1 << 20, 1 << 22)]
+    torch.cuda.synchronize()
+    assert all(bool((j == -1).all()) for j in junk)
+    assert torch.equal(got.y, want.y) and torch.equal(got.topk_ids, want.topk_ids)
