@@ -13,11 +13,35 @@ __device__ __forceinline__ float fast_sigmoid(float v) { return __builtin_amdgcn
 constexpr float kGeluA = 1.5957691216057308f;    // 2 sqrt(2 / pi): 0.5 (1 + tanh(u)) = sigmoid(2 u)
 constexpr float kGeluB = 0.044715f;
 
+// Phi(-|p|) of the normal distribution and e = exp(-p^2 / 2): the product of e and
+// a polynomial in 1 / (1 + 0.2121 |p|) fitted to Phi(-u) e^(u^2/2) over 0 <= u <=
+// 13.6 (relative error 2e-8; in fp32 5e-7, and up to 8e-6 from the rounding of p^2
+// where the value is below 1e-30).  The library's erfc took 96 us for 60 in the
+// gradient of 6061 x 8064 values.
+__device__ __forceinline__ float normal_tail(float p, float& e) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.2121f, fabsf(p), 1.0f));
+  float q = -0.0648413971f;
+  q = fmaf(q, t, 0.243251517f);
+  q = fmaf(q, t, -0.256910831f);
+  q = fmaf(q, t, 0.274553031f);
+  q = fmaf(q, t, -0.0476802252f);
+  q = fmaf(q, t, 0.107557312f);
+  q = fmaf(q, t, 0.0741440579f);
+  q = fmaf(q, t, 0.0853452384f);
+  q = fmaf(q, t, 0.0845813006f);
+  e = __builtin_amdgcn_exp2f(p * p * -0.7213475204f);
+  return q * t * e;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float p) {
   if constexpr (ACT == MOE_ACT_RELU) return p < 0.0f ? 0.0f : p;          // NaN stays NaN
   else if constexpr (ACT == MOE_ACT_SILU) return p * fast_sigmoid(p);
-  else if constexpr (ACT == MOE_ACT_GELU) return 0.5f * p * erfcf(p * -0.7071067811865476f);   // erfc: exact in the left tail
+  else if constexpr (ACT == MOE_ACT_GELU) {
+    float e;
+    const float q = normal_tail(p, e);
+    return p * (p < 0.0f ? q : 1.0f - q);
+  }
   else if constexpr (ACT == MOE_ACT_GELU_TANH) return p * fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));
   else return p;
 }
@@ -29,9 +53,12 @@ __device__ __forceinline__ float act_grad(float p, int act) {
       const float s = fast_sigmoid(p);
       return s * (1.0f + p * (1.0f - s));
     }
-    case MOE_ACT_GELU:
+    case MOE_ACT_GELU: {
       p = p < -32.0f ? -32.0f : p > 32.0f ? 32.0f : p;   // 0 or 1 exactly from there on; p * p stays finite
-      return 0.5f * erfcf(p * -0.7071067811865476f) + p * fast_exp(-0.5f * p * p) * 0.3989422804014327f;
+      float e;
+      const float q = normal_tail(p, e);
+      return fmaf(p * e, 0.3989422804014327f, p < 0.0f ? q : 1.0f - q);
+    }
     case MOE_ACT_GELU_TANH: {
       p = p < -32.0f ? -32.0f : p > 32.0f ? 32.0f : p;
       const float s = fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));

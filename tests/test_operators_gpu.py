@@ -6,6 +6,7 @@ A dot product of n terms on the matrix cores, whose adder may truncate, is held 
 (n + 4) 2^-23 sum |a b|; each activation and its derivative to 2^-19 (1 + |p|) (a few roundings,
 the hardware's exp2 and reciprocal, and the rounding of an argument up to 1.6 |p| (1 + |p|^2 / 22)
 whose slope dies out as that grows)."""
+import math
 import sys
 
 import numpy as np
@@ -634,6 +635,29 @@ def test_linear_of_large_pre_activations_is_finite(act):
     want = np.zeros((M, K))
     want[4:] = 1.0
     close(dx.np(), want, 2.0 ** -40, "dx")
+
+
+def test_gelu_and_its_slope_over_the_whole_range():
+    """fp32 operands and the identity as weights: value and slope of p itself, both tails included."""
+    p = torch.linspace(-13.5, 13.5, 4096 * 8).view(4096, 8)
+    lin = moe.make_linear(4096, 8, 8, dtype="f32", y_dtype="f32", act="gelu")
+    eye, dy = cuda(torch.eye(8)), torch.ones(4096, 8, device=DEV)
+    y, dx = Out(4096, 8), Out(4096, 8)
+    moe.moe_linear(lin, cuda(p), eye, None, None, y.t, None, runner._bytes(moe.moe_linear_workspace_bytes(lin), DEV))
+    moe.moe_linear_backward(lin, dy, cuda(p), None, eye, dx.t, None, None,
+                            runner._bytes(moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR_BACKWARD), DEV))
+    torch.cuda.synchronize()
+    v = f64(p)
+    tail = np.array([0.5 * math.erfc(abs(t) / math.sqrt(2)) for t in v.ravel()]).reshape(v.shape)
+    cdf = np.where(v < 0, tail, 1 - tail)
+    phi = np.exp(-0.5 * v * v) / math.sqrt(2 * math.pi)
+    # the polynomial in fp32 5e-7, doubled for a reciprocal to 1 ulp; exp2 and two products a step each, and
+    # the rounding of p^2 (1.5 steps of it enter the exponent); what is denormal may be 0
+    e_phi = phi * (4 + 1.5 * v * v) * F32
+    e_tail = tail * (1e-6 + (4 + 1.5 * v * v) * F32)
+    close(y.np(), v * cdf, np.abs(v) * (e_tail + F32 * cdf) + F32 * np.abs(v * cdf) + 2.0 ** -120, "gelu")
+    close(dx.np(), cdf + v * phi, e_tail + F32 * cdf + np.abs(v) * (e_phi + 2 * F32 * phi) + 2 * F32 * (cdf + np.abs(v) * phi) + 2.0 ** -120,
+          "slope")
 
 
 def test_linear_backward_of_no_rows_is_zero():
