@@ -173,11 +173,12 @@ def _ptr(fn: str, name: str, t, dtype, numel: int, dev: Optional[int]):
     `numel` elements, contiguous, on device `dev` (a raw address passes unchecked)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
+    try:
+        if (t.get_device() == dev and (t.dtype is dtype or dtype is None) and t.numel() >= numel
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
         return int(t)
-    if (t.get_device() == dev and (t.dtype is dtype or dtype is None) and t.numel() >= numel
-            and t.is_contiguous()):
-        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{fn}: {name} must live in device memory")
     if dtype is not None and t.dtype is not dtype:
@@ -192,8 +193,10 @@ def _ptr(fn: str, name: str, t, dtype, numel: int, dev: Optional[int]):
 def _device(*tensors) -> Optional[int]:
     """Index of the device of the first device tensor (None: raw addresses only)."""
     for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            return t.get_device()
+        if isinstance(t, torch.Tensor):
+            d = t.get_device()
+            if d >= 0:
+                return d
     return None
 
 
@@ -206,8 +209,10 @@ def _workspace(fn: str, t, dev):
     return _ptr(fn, "workspace", t, None, 0, dev), t.numel() * t.element_size()
 
 
-# The current stream's handle without building a Stream object (1.1 us less per call).
+# The current stream's handle without building a Stream object (1.1 us less per call), and the
+# current device without looking whether there is one (0.2 us less): a call with device tensors has.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run(fn: str, dev: Optional[int], stream, *args):
@@ -215,7 +220,7 @@ def _run(fn: str, dev: Optional[int], stream, *args):
     f = getattr(_lib.load(), fn)
     if dev is None:
         _check(fn, f(*args, _stream(stream)))
-    elif dev == torch.cuda.current_device():
+    elif dev == _current_device():
         if stream is not None or _raw_stream is None:
             _check(fn, f(*args, _stream(stream)))
         else:
