@@ -9,6 +9,7 @@
 // bf16: up to kLinearDecodeRows rows stream the weights (linear_decode.hip); more,
 // or few channels of a long contraction, run as tiles (linear_tiles.hpp).  fp32:
 // linear_f32.hip.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -17,17 +18,19 @@
 
 namespace moe {
 
-// Streaming keeps a block of 16 channels on one CU, which takes in 45-65 KB per us: its
+// Streaming keeps a block of channels on one CU, which takes in 45-65 KB per us: its
 // weights and, again for each block, the rows of x.  Where the blocks leave CUs
 // idle and that is longer than the tiles' runs and their join (kTilesStart us more
-// than a stream to get going), tiles it is.  MI355X, us, stream / tiles: 31 x 368 x
-// 9120 19.6 / 14.1, 32 x 2048 x 14336 27.5 / 19.8, 16 x 208 x 12472 20.2 / 13.5; 16
-// x 1024 x 8192 10.9 / 15.1, 16 x 4096 x 14336 24.8 / 28.9.
+// than a stream to get going), tiles it is.  MI355X, us, stream / tiles: 32 x 2048 x
+// 14336 27.5 / 19.8, 16 x 2048 x 14336 22.1 / 19.9; 32 x 4096 x 4096 11.1 / 15.6, 16 x
+// 4096 x 14336 24.8 / 28.9, 31 x 368 x 9120 9.8 / 13.2.
 constexpr double kCuBytesPerUs = 55e3, kTilesStart = 3;
 static bool streams(const moe_linear_t& l) {
   if (l.M > kLinearDecodeRows) return false;
   if ((l.N + 15) / 16 > device_cu_count()) return true;
-  const double stream = 2.0 * l.K * (16 + l.M) / kCuBytesPerUs;
+  const DecodeBlock b = DecodeBlock::of(l);
+  const double stream = 2.0 * l.K * (b.channels + std::min(b.rows, l.M)) / kCuBytesPerUs;
+  if (stream <= kTilesStart) return true;            // whatever the tiles take (planning them costs the host time)
   return with_plan(l.M, l.N, l.K, 0, [&](auto, const ProductPlan& p) { return stream <= p.cost + kTilesStart; });
 }
 

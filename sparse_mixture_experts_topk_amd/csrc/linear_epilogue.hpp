@@ -144,6 +144,27 @@ hipError_t launch_linear_products_f32(const moe_linear_t& l, const float* dpre, 
 // against 33 in tiles: 4096 x 4096 11.1 / 15.6, 14336 x 4096 26.0 / 30.8; 64 rows
 // streamed four blocks at a time 34.7 against 31.2).
 constexpr int kLinearDecodeRows = 32;
+// The part of the output that one workgroup of the stream has.  16 channels of all
+// rows, read by 8 wavefronts, one stage in flight each.  Two blocks of 16 rows leave
+// LDS for one such workgroup per CU: where there are more channels than one round
+// of them takes, 4 wavefronts on 32 channels, two workgroups per CU, share each read
+// of x twice.  MI355X, us, wide against narrow: 32 rows of 4096 terms, N 4096 13.3 /
+// 11.6, N 6144 14.3 / 18.7, N 14336 25.8 / 35.3; with 16 rows N 12288 21.8 / 19.3, N
+// 14336 23.1 / 24.0.  16 wavefronts or two stages in flight gain nothing (16 rows, N
+// 4096: 10.2, 9.6 / 9.2).  Few channels are bound by what one CU takes in (its part
+// of w and of x): 8 channels of 8 or 4 rows, two stages in flight, where the CUs hold
+// that many blocks (16 rows of 4096 terms, N 256: 4.3 / 6.8, N 1024: 5.1 / 7.1; of
+// 512 terms, N 512: 3.3 / 3.0).
+struct DecodeBlock {
+  int rows, channels;
+  static DecodeBlock of(const moe_linear_t& l) {
+    const int cus = device_cu_count(), eights = (l.N + 7) / 8;
+    if (eights * ((l.M + 3) / 4) <= cus) return {4, 8};
+    if (eights * ((l.M + 7) / 8) <= cus) return {8, 8};
+    if (l.M <= 16) return {16, 16};
+    return {32, (l.N + 15) / 16 > cus ? 32 : 16};
+  }
+};
 int device_cu_count();
 hipError_t launch_linear_decode(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
                                 hipStream_t st);

@@ -603,7 +603,8 @@ def test_linear_backward_together_and_alone(dims):
 
 # few rows: two blocks of channels to a workgroup, and long contractions of few channels cut into runs
 @pytest.mark.parametrize("dims", [(17, 4104, 136), (32, 6144, 520), (16, 208, 12472), (31, 368, 9120), (9, 40, 16384),
-                                  (32, 4096, 392)])
+                                  (32, 4096, 392), (20, 1032, 14336), (5, 2048, 136), (7, 1032, 1000),
+                                  (29, 504, 264), (32, 8, 72)])
 def test_linear_of_few_rows(dims):
     linear_case(*dims, "none", "f32", bias=False)
     linear_case(*dims, "silu", "bf16", bias=True, residual=True, pre=True)
