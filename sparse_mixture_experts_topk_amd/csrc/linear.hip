@@ -25,18 +25,33 @@ namespace moe {
 // 14336 27.5 / 19.8, 16 x 2048 x 14336 22.1 / 19.9; 32 x 4096 x 4096 11.1 / 15.6, 16 x
 // 4096 x 14336 24.8 / 28.9, 31 x 368 x 9120 9.8 / 13.2.
 constexpr double kCuBytesPerUs = 55e3, kTilesStart = 3;
-static bool streams(const moe_linear_t& l) {
-  if (l.M > kLinearDecodeRows) return false;
-  if ((l.N + 15) / 16 > device_cu_count()) return true;
-  const DecodeBlock b = DecodeBlock::of(l);
-  const double stream = 2.0 * l.K * (b.channels + std::min(b.rows, l.M)) / kCuBytesPerUs;
-  if (stream <= kTilesStart) return true;            // whatever the tiles take (planning them costs the host time)
-  return with_plan(l.M, l.N, l.K, 0, [&](auto, const ProductPlan& p) { return stream <= p.cost + kTilesStart; });
-}
+namespace {
+struct LinearPlan {
+  bool stream = true;
+  DecodeBlock block{};
+  ProductPlans tiles{};
+
+  static LinearPlan of(const moe_linear_t& l) {
+    LinearPlan p;
+    const int cus = device_cu_count();
+    double stream = 0;
+    if (l.M <= kLinearDecodeRows) {
+      p.block = DecodeBlock::of(l, cus);
+      if ((l.N + 15) / 16 > cus) return p;
+      stream = 2.0 * l.K * (p.block.channels + std::min(p.block.rows, l.M)) / kCuBytesPerUs;
+      if (stream <= kTilesStart) return p;           // whatever the tiles take (planning them costs the host time)
+    }
+    p.tiles = ProductPlans::of(l.M, l.N, l.K, 0, plan_cus(cus));
+    p.stream = l.M <= kLinearDecodeRows && stream <= p.tiles.least().cost + kTilesStart;
+    return p;
+  }
+};
+}  // namespace
 
 size_t linear_workspace_bytes(const moe_linear_t& l) {
   if (l.dtype == MOE_F32) return linear_workspace_bytes_f32(l);
-  return streams(l) ? 0 : product_workspace(l.M, l.N, l.K, 0);
+  const LinearPlan p = LinearPlan::of(l);
+  return p.stream ? 0 : p.tiles.least().workspace;
 }
 
 hipError_t launch_linear(const moe_linear_t& l, const void* x_, const void* w_, const float* bias,
@@ -47,9 +62,10 @@ hipError_t launch_linear(const moe_linear_t& l, const void* x_, const void* w_, 
                              workspace, st);
   const uint16_t *x = static_cast<const uint16_t*>(x_), *w = static_cast<const uint16_t*>(w_);
   const Epilogue ep{bias, residual, y, static_cast<uint16_t*>(pre), l.y_dtype == MOE_F32};
-  if (streams(l)) return launch_linear_decode(l, x, w, ep, st);
+  const LinearPlan p = LinearPlan::of(l);
+  if (p.stream) return launch_linear_decode(l, p.block, x, w, ep, st);
   auto run = [&](auto act) {
-    return launch_product<false, false, decltype(act)::value>(x, l.K, w, l.K, l.M, l.N, l.K, workspace, ep, st);
+    return launch_product<false, false, decltype(act)::value>(x, l.K, w, l.K, l.M, l.N, l.K, p.tiles, workspace, ep, st);
   };
   switch (l.act) {
     case MOE_ACT_RELU: return run(std::integral_constant<int, MOE_ACT_RELU>{});

@@ -24,8 +24,9 @@ constexpr int kPrepCols = 256;      // columns per workgroup, 8 to a lane
 // 4096 took 41 us for 36).
 int prep_rows(const moe_linear_t& l) {
   const int64_t col_blocks = (l.N + kPrepCols - 1) / kPrepCols;
+  const int64_t workgroups = 4 * device_cu_count();
   int rows = 256;
-  while (rows > 16 && col_blocks * ((l.M + rows - 1) / rows) < 4 * device_cu_count()) rows /= 2;
+  while (rows > 16 && col_blocks * ((l.M + rows - 1) / rows) < workgroups) rows /= 2;
   return rows;
 }
 
@@ -77,14 +78,13 @@ __global__ __launch_bounds__(256) void dpre_kernel(const void* __restrict__ dy, 
   }
 }
 
-int prep_chunks(const moe_linear_t& l) { return (l.M + prep_rows(l) - 1) / prep_rows(l); }
 // dpre has values of its own unless dy already is what the products read.
 bool dpre_copied(const moe_linear_t& l) { return l.act != MOE_ACT_NONE || l.y_dtype != l.dtype; }
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 size_t dpre_bytes(const moe_linear_t& l) { return dpre_copied(l) ? round256((size_t)l.M * l.N * (l.dtype == MOE_F32 ? 4 : 2)) : 0; }
 
-size_t part_bytes(const moe_linear_t& l) { return round256((size_t)prep_chunks(l) * l.N * 4); }
+size_t part_bytes(const moe_linear_t& l, int rows) { return round256((size_t)((l.M + rows - 1) / rows) * l.N * 4); }
 
 // ---- dbias, dx, dw ----
 
@@ -163,66 +163,55 @@ __global__ __launch_bounds__(256) void linear_join2_kernel(const ProductArgs a, 
 // against 92.5).
 constexpr double kOneLaunch = 2.5;
 struct GradientPlan {
-  ProductPlan dx, dw;
-  bool one = false;                  // launch; otherwise each product has its own plan
-};
-template <class F>
-auto with_gradient_plan(int M, int N, int K, F&& run) {
-  const int64_t cus = std::min<int64_t>(device_cu_count(), kMaxPersistentGroups) / 8 * 8;
-  const double apart = with_plan(M, K, N, 1, [](auto, const ProductPlan& p) { return p.cost; }) +
-                       with_plan(N, K, M, 2, [](auto, const ProductPlan& p) { return p.cost; });
-  auto pair = [&](auto tile) {
-    using C = decltype(tile);
-    GradientPlan p{ProductPlan::of<C>(M, K, N, 1, cus), ProductPlan::of<C>(N, K, M, 2, cus)};
-    p.one = p.dx.cost + p.dw.cost <= apart + kOneLaunch;
-    return p;
-  };
-  const GradientPlan a = pair(Tile256x256{}), b = pair(Tile256x128{}), c = pair(Tile128x128{}), d = pair(Tile128x64{});
-  auto cost = [](const GradientPlan& p) { return p.dx.cost + p.dw.cost; };
-  const double least = std::min(std::min(cost(a), cost(b)), std::min(cost(c), cost(d)));
-  if (cost(a) == least) return run(Tile256x256{}, a);
-  if (cost(b) == least) return run(Tile256x128{}, b);
-  if (cost(c) == least) return run(Tile128x128{}, c);
-  return run(Tile128x64{}, d);
-}
+  ProductPlans dx, dw;
+  int tile = 0;                      // the shape for both
+  bool one;                          // launch; otherwise each product has its own shape
 
-// Partial tiles of a backward pass: both products', or those of one at a time.
-size_t gradient_workspace(int M, int N, int K) {
-  const size_t each = std::max(product_workspace(M, K, N, 1), product_workspace(N, K, M, 2));
-  return with_gradient_plan(M, N, K, [&](auto, const GradientPlan& p) {
-    return p.one ? std::max(each, p.dx.workspace + p.dw.workspace) : each;
-  });
-}
+  static GradientPlan of(int M, int N, int K) {
+    const int64_t cus = plan_cus(device_cu_count());
+    GradientPlan g{ProductPlans::of(M, K, N, 1, cus), ProductPlans::of(N, K, M, 2, cus)};
+    for (int i = 1; i < 4; ++i)
+      if (g.cost(i) < g.cost(g.tile)) g.tile = i;
+    g.one = g.cost(g.tile) <= g.dx.least().cost + g.dw.least().cost + kOneLaunch;
+    return g;
+  }
+  double cost(int i) const { return dx.p[i].cost + dw.p[i].cost; }
+  // partial tiles: both products', or those of one at a time
+  size_t workspace() const {
+    const size_t each = std::max(dx.least().workspace, dw.least().workspace);
+    return one ? std::max(each, dx.p[tile].workspace + dw.p[tile].workspace) : each;
+  }
+};
 
 // dx = dpre w, dw = dpre^T x and dbias; any of them may be NULL.
 hipError_t launch_gradients(const uint16_t* dpre, const uint16_t* x, const uint16_t* w, uint16_t* dx, uint16_t* dw,
                             const ColumnSums& dbias, int M, int N, int K, void* partials, hipStream_t st) {
   const Epilogue to_dx{nullptr, nullptr, dx, nullptr, false}, to_dw{nullptr, nullptr, dw, nullptr, false};
-  return with_gradient_plan(M, N, K, [&](auto tile, const GradientPlan& p) {
+  const GradientPlan plan = GradientPlan::of(M, N, K);
+  if (!plan.one || dx == nullptr || dw == nullptr) {
+    hipError_t e = launch_dbias(dbias, st);
+    if (e == hipSuccess && dx != nullptr)
+      e = launch_product<false, true, MOE_ACT_NONE>(dpre, N, w, K, M, K, N, plan.dx, partials, to_dx, st);
+    if (e == hipSuccess && dw != nullptr)
+      e = launch_product<true, true, MOE_ACT_NONE>(dpre, N, x, K, N, K, M, plan.dw, partials, to_dw, st);
+    return e;
+  }
+  return with_tile(plan.tile, [&](auto tile) {
     using C = decltype(tile);
     using G = GeomOf<C>;
-    hipError_t e = hipSuccess;
-    if (!p.one || dx == nullptr || dw == nullptr) {
-      e = launch_dbias(dbias, st);
-      if (e == hipSuccess && dx != nullptr)
-        e = launch_product<false, true, MOE_ACT_NONE>(dpre, N, w, K, M, K, N, partials, to_dx, st);
-      if (e == hipSuccess && dw != nullptr)
-        e = launch_product<true, true, MOE_ACT_NONE>(dpre, N, x, K, N, K, M, partials, to_dw, st);
-      return e;
-    }
-    const ProductArgs a{dpre, w, N, K, M, K, N, p.dx.row_tiles, p.dx.col_tiles, p.dx.split,
-                        static_cast<float*>(partials), to_dx};
-    const ProductArgs b{dpre, x, N, K, N, K, M, p.dw.row_tiles, p.dw.col_tiles, p.dw.split,
-                        reinterpret_cast<float*>(static_cast<uint8_t*>(partials) + p.dx.workspace), to_dw};
+    const ProductPlan &px = plan.dx.p[plan.tile], &pw = plan.dw.p[plan.tile];
+    const ProductArgs a{dpre, w, N, K, M, K, N, px.row_tiles, px.col_tiles, px.split, static_cast<float*>(partials), to_dx};
+    const ProductArgs b{dpre, x, N, K, N, K, M, pw.row_tiles, pw.col_tiles, pw.split,
+                        reinterpret_cast<float*>(static_cast<uint8_t*>(partials) + px.workspace), to_dw};
     const int cols = G::THREADS / 16, bias_blocks = dbias.out != nullptr ? (N + 8 * cols - 1) / (8 * cols) * 8 : 0;
     hipLaunchKernelGGL((linear_gradients_kernel<C::NS, C::WR, C::WC, C::WA, C::WB>),
-                       dim3((unsigned)(bias_blocks + p.dx.grid + p.dw.grid)), dim3(G::THREADS), 0, st, a, b, dbias,
-                       bias_blocks, p.dx.grid);
-    e = hipGetLastError();
-    if (e != hipSuccess || !(p.dx.split || p.dw.split)) return e;
-    const int ja = p.dx.split ? (int)join_blocks_of<C>(p.dx) : 0, jb = p.dw.split ? (int)join_blocks_of<C>(p.dw) : 0;
+                       dim3((unsigned)(bias_blocks + px.grid + pw.grid)), dim3(G::THREADS), 0, st, a, b, dbias,
+                       bias_blocks, px.grid);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !(px.split || pw.split)) return e;
+    const int ja = px.split ? (int)join_blocks_of<C>(px) : 0, jb = pw.split ? (int)join_blocks_of<C>(pw) : 0;
     hipLaunchKernelGGL((linear_join2_kernel<G::TA, G::TB>), dim3((unsigned)(ja + jb)), dim3(256), 0, st, a, b,
-                       p.dx.grid / 8, p.dw.grid / 8, ja);
+                       px.grid / 8, pw.grid / 8, ja);
     return hipGetLastError();
   });
 }
@@ -231,22 +220,24 @@ hipError_t launch_gradients(const uint16_t* dpre, const uint16_t* x, const uint1
 
 size_t linear_backward_workspace_bytes(const moe_linear_t& l) {
   if (l.M == 0) return 0;
-  if (l.dtype == MOE_F32) return dpre_bytes(l) + part_bytes(l) + linear_backward_product_bytes_f32(l);
-  return dpre_bytes(l) + part_bytes(l) + gradient_workspace(l.M, l.N, l.K);
+  const size_t prep = dpre_bytes(l) + part_bytes(l, prep_rows(l));
+  if (l.dtype == MOE_F32) return prep + linear_backward_product_bytes_f32(l);
+  return prep + GradientPlan::of(l.M, l.N, l.K).workspace();
 }
 
 hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const void* pre, const void* x,
                                   const void* w, void* dx, void* dw, float* dbias, void* workspace,
                                   hipStream_t st) {
   void* copy = dpre_copied(l) && (dx != nullptr || dw != nullptr) ? workspace : nullptr;
-  const bool one_chunk = prep_chunks(l) == 1;
+  const int rows = prep_rows(l), chunks = (l.M + rows - 1) / rows;
+  const bool one_chunk = chunks == 1;
   float* part = dbias == nullptr ? nullptr
                 : one_chunk      ? dbias
                                  : reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dpre_bytes(l));
   hipError_t e = hipSuccess;
   if (copy != nullptr || part != nullptr) {
-    const int rows = prep_rows(l), cbs = (l.N + kPrepCols - 1) / kPrepCols;
-    const dim3 grid((unsigned)((int64_t)cbs * ((l.M + rows - 1) / rows)));
+    const int cbs = (l.N + kPrepCols - 1) / kPrepCols;
+    const dim3 grid((unsigned)((int64_t)cbs * chunks));
     const bool f32 = l.y_dtype == MOE_F32, act = l.act != MOE_ACT_NONE;
     auto run = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, dy, pre, l.act, l.M, l.N, cbs, rows, copy, part);
@@ -258,8 +249,8 @@ hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const v
   }
   if (e != hipSuccess) return e;
   const void* d = copy != nullptr ? copy : dy;
-  void* partials = static_cast<uint8_t*>(workspace) + dpre_bytes(l) + part_bytes(l);
-  const ColumnSums sums{part, one_chunk ? nullptr : dbias, prep_chunks(l), l.N};
+  void* partials = static_cast<uint8_t*>(workspace) + dpre_bytes(l) + part_bytes(l, rows);
+  const ColumnSums sums{part, one_chunk ? nullptr : dbias, chunks, l.N};
   if (l.dtype == MOE_F32) {
     e = launch_dbias(sums, st);
     if (e != hipSuccess) return e;

@@ -132,14 +132,13 @@ __global__ __launch_bounds__(W * kWave) void linear_decode_kernel(const uint16_t
 }
 
 template <int ACT>
-hipError_t launch_act(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
-                      hipStream_t st) {
+hipError_t launch_act(const moe_linear_t& l, const DecodeBlock& b, const uint16_t* x, const uint16_t* w,
+                      const Epilogue& ep, hipStream_t st) {
   auto run = [&](auto kernel, int rw, int ch, int waves) {
     const int rb = (l.M + rw - 1) / rw, blocks = (l.N + ch - 1) / ch * rb;
     hipLaunchKernelGGL(kernel, dim3((unsigned)((blocks + 7) / 8 * 8)), dim3(waves * kWave), 0, st, x, w, l.M, l.N, l.K, rb, ep);
     return hipGetLastError();
   };
-  const DecodeBlock b = DecodeBlock::of(l);
   if (b.rows == 4) return run(linear_decode_kernel<ACT, 4, 8, 8, 2>, 4, 8, 8);
   if (b.rows == 8) return run(linear_decode_kernel<ACT, 8, 8, 8, 2>, 8, 8, 8);
   if (b.rows == 16) return run(linear_decode_kernel<ACT, 16, 16, 8, 1>, 16, 16, 8);
@@ -149,14 +148,14 @@ hipError_t launch_act(const moe_linear_t& l, const uint16_t* x, const uint16_t* 
 
 }  // namespace
 
-hipError_t launch_linear_decode(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
-                                hipStream_t st) {
+hipError_t launch_linear_decode(const moe_linear_t& l, const DecodeBlock& block, const uint16_t* x, const uint16_t* w,
+                                const Epilogue& ep, hipStream_t st) {
   switch (l.act) {
-    case MOE_ACT_RELU: return launch_act<MOE_ACT_RELU>(l, x, w, ep, st);
-    case MOE_ACT_SILU: return launch_act<MOE_ACT_SILU>(l, x, w, ep, st);
-    case MOE_ACT_GELU: return launch_act<MOE_ACT_GELU>(l, x, w, ep, st);
-    case MOE_ACT_GELU_TANH: return launch_act<MOE_ACT_GELU_TANH>(l, x, w, ep, st);
-    default: return launch_act<MOE_ACT_NONE>(l, x, w, ep, st);
+    case MOE_ACT_RELU: return launch_act<MOE_ACT_RELU>(l, block, x, w, ep, st);
+    case MOE_ACT_SILU: return launch_act<MOE_ACT_SILU>(l, block, x, w, ep, st);
+    case MOE_ACT_GELU: return launch_act<MOE_ACT_GELU>(l, block, x, w, ep, st);
+    case MOE_ACT_GELU_TANH: return launch_act<MOE_ACT_GELU_TANH>(l, block, x, w, ep, st);
+    default: return launch_act<MOE_ACT_NONE>(l, block, x, w, ep, st);
   }
 }
 

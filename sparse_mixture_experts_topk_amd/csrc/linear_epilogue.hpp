@@ -157,16 +157,15 @@ constexpr int kLinearDecodeRows = 32;
 // 512 terms, N 512: 3.3 / 3.0).
 struct DecodeBlock {
   int rows, channels;
-  static DecodeBlock of(const moe_linear_t& l) {
-    const int cus = device_cu_count(), eights = (l.N + 7) / 8;
+  static DecodeBlock of(const moe_linear_t& l, int cus) {
+    const int eights = (l.N + 7) / 8;
     if (eights * ((l.M + 3) / 4) <= cus) return {4, 8};
     if (eights * ((l.M + 7) / 8) <= cus) return {8, 8};
     if (l.M <= 16) return {16, 16};
     return {32, (l.N + 15) / 16 > cus ? 32 : 16};
   }
 };
-int device_cu_count();
-hipError_t launch_linear_decode(const moe_linear_t& l, const uint16_t* x, const uint16_t* w, const Epilogue& ep,
-                                hipStream_t st);
+hipError_t launch_linear_decode(const moe_linear_t& l, const DecodeBlock& block, const uint16_t* x, const uint16_t* w,
+                                const Epilogue& ep, hipStream_t st);
 
 }  // namespace moe

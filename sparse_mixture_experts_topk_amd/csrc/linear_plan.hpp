@@ -57,23 +57,31 @@ struct ProductPlan {
   }
 };
 
-// Calls run(tile shape, plan) with the cheapest of the four.
-template <class F>
-auto with_plan(int rows, int cols, int len, int slow, F&& run) {
-  const int64_t cus = std::min<int64_t>(device_cu_count(), kMaxPersistentGroups) / 8 * 8;
-  const ProductPlan a = ProductPlan::of<Tile256x256>(rows, cols, len, slow, cus);
-  const ProductPlan b = ProductPlan::of<Tile256x128>(rows, cols, len, slow, cus);
-  const ProductPlan c = ProductPlan::of<Tile128x128>(rows, cols, len, slow, cus);
-  const ProductPlan d = ProductPlan::of<Tile128x64>(rows, cols, len, slow, cus);
-  const double least = std::min(std::min(a.cost, b.cost), std::min(c.cost, d.cost));
-  if (a.cost == least) return run(Tile256x256{}, a);
-  if (b.cost == least) return run(Tile256x128{}, b);
-  if (c.cost == least) return run(Tile128x128{}, c);
-  return run(Tile128x64{}, d);
-}
+// A product's plan in each of the four shapes, and the cheapest.
+struct ProductPlans {
+  ProductPlan p[4];
+  int best = 0;
 
-inline size_t product_workspace(int rows, int cols, int len, int slow) {
-  return with_plan(rows, cols, len, slow, [](auto, const ProductPlan& p) { return p.workspace; });
+  static ProductPlans of(int rows, int cols, int len, int slow, int64_t cus) {
+    ProductPlans s{{ProductPlan::of<Tile256x256>(rows, cols, len, slow, cus),
+                    ProductPlan::of<Tile256x128>(rows, cols, len, slow, cus),
+                    ProductPlan::of<Tile128x128>(rows, cols, len, slow, cus),
+                    ProductPlan::of<Tile128x64>(rows, cols, len, slow, cus)}};
+    for (int i = 1; i < 4; ++i)
+      if (s.p[i].cost < s.p[s.best].cost) s.best = i;
+    return s;
+  }
+  const ProductPlan& least() const { return p[best]; }
+};
+inline int64_t plan_cus(int cus) { return std::min<int64_t>(cus, kMaxPersistentGroups) / 8 * 8; }
+
+// Calls run(tile shape) with shape i of the four.
+template <class F>
+auto with_tile(int i, F&& run) {
+  if (i == 0) return run(Tile256x256{});
+  if (i == 1) return run(Tile256x128{});
+  if (i == 2) return run(Tile128x128{});
+  return run(Tile128x64{});
 }
 
 // Workgroups of a join: every tail tile there may be (fewer than the slots of an XCD), all its rows.
@@ -84,8 +92,9 @@ unsigned join_blocks_of(const ProductPlan& p) {
 
 template <bool PSLOW, bool QSLOW, int ACT>
 hipError_t launch_product(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, int rows, int cols,
-                          int len, void* partials, const Epilogue& ep, hipStream_t st) {
-  return with_plan(rows, cols, len, (PSLOW ? 1 : 0) + (QSLOW ? 1 : 0), [&](auto tile, const ProductPlan& p) {
+                          int len, const ProductPlans& plans, void* partials, const Epilogue& ep, hipStream_t st) {
+  const ProductPlan& p = plans.least();
+  return with_tile(plans.best, [&](auto tile) {
     using C = decltype(tile);
     using G = GeomOf<C>;
     const ProductArgs a{P, Q, ldp, ldq, rows, cols, len, p.row_tiles, p.col_tiles, p.split,
