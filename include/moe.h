@@ -452,8 +452,9 @@ moe_status_t moe_linear(const moe_linear_t* linear, const void* x, const void* w
  *            unless act is MOE_ACT_NONE (then ignored); the residual's gradient
  *            is dy itself
  * dpre is rounded to dtype for the two products (their matrix-core operand), which
- * accumulate in fp32.  relu'(0) = 0.  Outputs overlap no input and are fully
- * written, with M = 0 too (dw and dbias are then zero). */
+ * accumulate in fp32, in an order that depends on the sizes and on which outputs are
+ * asked for, and on nothing else.  relu'(0) = 0.  Outputs overlap no input and are
+ * fully written, with M = 0 too (dw and dbias are then zero). */
 moe_status_t moe_linear_backward(const moe_linear_t* linear, const void* dy, const void* pre,
                                  const void* x, const void* w, void* dx, void* dw, float* dbias,
                                  void* workspace, size_t workspace_bytes, void* stream);
