@@ -20,8 +20,10 @@
 // position within the lane, orders experts by index, so "the lowest lane that
 // holds the maximum" settles ties.  Keys are the choices mapped to ordered
 // unsigned integers (0: not a candidate), which also orders -inf (an expert
-// that is only chosen when nothing else is left; NaN counts as one), so k
-// distinct experts always come out.
+// that is only chosen when nothing else is left; a NaN choice counts as one), so
+// k distinct experts always come out.  A NaN logit is read as -inf (usable), so
+// that its rank, score, weight and gradient are those of a masked expert, in
+// fp32 as in fp64.
 //
 // The choice must not depend on how fp32 rounds the scores.  Without a
 // balance bias the order of c is that of the logits and the keys are the
@@ -69,6 +71,8 @@ __device__ __forceinline__ double from_ordered(uint64_t u) {
 // NaN becomes -inf (the maximum of a number and NaN is the number).
 __device__ __forceinline__ float no_nan(float v) { return fmaxf(v, -INFINITY); }
 __device__ __forceinline__ double no_nan(double v) { return fmax(v, -(double)INFINITY); }
+// A logit as the router takes it.
+__device__ __forceinline__ float usable(float v) { return no_nan(v); }
 
 // Reductions over the wavefront by DPP: row shifts within 16 lanes, then the two
 // row broadcasts, leave the result in lane 63, read back as a uniform value.
@@ -105,7 +109,7 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 // (as ordered integers: one instruction a step, where fp32 maxima quiet their operands first)
-__device__ __forceinline__ float wave_max_value(float v) { return from_ordered(wave_max(ordered(no_nan(v)))); }
+__device__ __forceinline__ float wave_max_value(float v) { return from_ordered(wave_max(ordered(v))); }      // no NaN
 __device__ __forceinline__ uint32_t lane_read(uint32_t v, int lane) { return (uint32_t)__shfl((int)v, lane); }
 __device__ __forceinline__ uint64_t lane_read(uint64_t v, int lane) { return (uint64_t)__shfl((long long)v, lane); }
 // A reduction's partner in step 0, 1, 2 over 8 lanes: lane ^ 1, lane ^ 2 (by quad),
@@ -235,7 +239,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
   int pos[PER];
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
-    const Key k = ordered(no_nan(BIAS ? s[p] + (R)b[p] : (R)l[p]));
+    const Key k = ordered(BIAS ? no_nan(s[p] + (R)b[p]) : (R)l[p]);
     key[p] = in[p] ? k : Key(0);
     pos[p] = p;
   }
@@ -328,7 +332,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
   return CHECK && __ballot(near) != 0;
 }
 
-// The lane's PER consecutive values; vector: whole groups of 4 at 16-byte aligned places.
+// The lane's PER consecutive values (those of in[]); vector: whole groups of 4 at 16-byte aligned places.
 template <int PER>
 __device__ __forceinline__ void load_lane(const float* p, const bool (&in)[PER], bool vector, float (&v)[PER]) {
   if constexpr (PER % 4 == 0) {
@@ -345,6 +349,12 @@ __device__ __forceinline__ void load_lane(const float* p, const bool (&in)[PER],
 #pragma unroll
   for (int q = 0; q < PER; ++q)
     if (in[q]) v[q] = p[q];
+}
+template <int PER>
+__device__ __forceinline__ void load_logits(const float* p, const bool (&in)[PER], bool vector, float (&l)[PER]) {
+  load_lane<PER>(p, in, vector, l);
+#pragma unroll
+  for (int q = 0; q < PER; ++q) l[q] = usable(l[q]);
 }
 
 // Bound by instruction issue: 480 vector instructions per token, 20 of them in each
@@ -366,7 +376,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
     l[p] = -INFINITY;
     b[p] = 0.0f;
   }
-  load_lane<PER>(row + first, in, a.vector, l);
+  load_logits<PER>(row + first, in, a.vector, l);
   if constexpr (BIAS) load_lane<PER>(a.bias + first, in, a.vector, b);
   // the softmax of all experts is not needed where the weights are
   // renormalised over the chosen ones and nothing else looks at scores
@@ -391,7 +401,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
   }
   // weights: lane j < k holds the j-th chosen expert
   const bool mine = lane < a.k;
-  const float lj = mine ? row[chosen] : -INFINITY;
+  const float lj = mine ? usable(row[chosen]) : -INFINITY;
   float w;
   if (a.renormalize) {
     w = chosen_weight(lj, mine, SOFTMAX);
@@ -454,7 +464,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_ker
   }
   // renormalised softmax weights do not see the other experts' logits
   const bool need = !(a.softmax && a.renormalize) || a.dscores != nullptr;
-  if (need) load_lane<PER>(a.logits + base + lane * PER, in, a.vector, l);
+  if (need) load_logits<PER>(a.logits + base + lane * PER, in, a.vector, l);
   if (a.dscores != nullptr) load_lane<PER>(a.dscores + base + lane * PER, in, a.vector, d);
   // lanes j < k: the j-th chosen expert (an id outside the row adds nothing)
   int id = lane < a.k ? a.ids[(int64_t)t * a.k + lane] : -1;
@@ -462,7 +472,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_ker
   const float g = id >= 0 ? a.dweights[(int64_t)t * a.k + lane] : 0.0f;
   float q = a.scale * g;
   if (a.renormalize) {
-    const float lj = id >= 0 ? a.logits[base + id] : -INFINITY;
+    const float lj = id >= 0 ? usable(a.logits[base + id]) : -INFINITY;
     const float w = chosen_weight(lj, id >= 0, a.softmax);
     float c = 0.0f;
 #pragma unroll

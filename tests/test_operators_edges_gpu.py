@@ -1,0 +1,70 @@
+"""GPU checks of the scored router and the dense product at their edges: NaN and infinite logits, groups
+whose choices cancel, expert counts that are no multiple of 8, activations of fp32 operands over their
+whole range, every tile shape of the forward product.
+
+Tolerances count half steps (see test_operators_gpu); what a test needs beyond that is derived in it."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_mixture_experts_topk_amd as moe
+import test_operators_gpu as base
+from oracle import operators as ref
+from sparse_mixture_experts_topk_amd import runner
+from test_operators_gpu import BF16, DEV, F32, Out, close, cuda, f64, gen, normal, say
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- logits that are no numbers ----
+
+def unclean_logits(T, E, values):
+    """Rows with every third, one, all but two and all logits replaced by each of `values` in turn."""
+    x = normal(gen(101), T, E)
+    for i, v in enumerate(values):
+        x[4 * i, ::3] = v
+        x[4 * i + 1, 5 + i] = v
+        x[4 * i + 2, 2:] = v
+        x[4 * i + 3] = v
+    return x
+
+
+def check_as(x, counts_as, k, kind, groups, bias, renorm):
+    """Ids, weights, scores and both gradients of x are those of `counts_as` (fp64 reference)."""
+    T, E = x.shape
+    say(f"unclean {kind} groups={groups} bias={None if bias is None else float(bias.abs().max())} renorm={renorm}")
+    n, kept, top = groups
+    s, r = moe.make_shape(T, 64, 64, E, k), moe.make_router(kind, n, kept, top, renorm, 1.5)
+    ids, w, sc = Out(T, k, dtype=torch.int32, fill=-77), Out(T, k), Out(T, E)
+    nx = Out(T, 2, dtype=torch.int32, fill=-77)
+    moe.moe_route_scored(s, r, cuda(x), cuda(bias), ids.t, w.t, sc.t, nx.t)
+    g, D, dl = normal(gen(102), T, k), normal(gen(103), T, E), Out(T, E)
+    moe.moe_route_scored_backward(s, r, cuda(x), ids.t, cuda(g), cuda(D), dl.t)
+    torch.cuda.synchronize()
+    want = ref.route_scored(f64(counts_as), f64(bias), k, kind, n, kept, top, renorm, 1.5)
+    assert np.array_equal(ids.np(), want[0]), "ids"
+    assert np.array_equal(nx.np(), want[3]), "next ids"
+    # logits of N(0, 1), span below 10: exp's argument up to that many half steps, some ten roundings, the sum
+    tol = 2 * F32 * (10 + 24)
+    close(w.np(), want[1], tol * want[1] + 1e-37, "weights")
+    close(sc.np(), want[2], tol * want[2] + 1e-37, "scores")
+    wdl = ref.route_scored_backward(f64(counts_as), want[0], f64(g), f64(D), kind, renorm, 1.5)
+    size = 1.5 * np.abs(f64(g)).max(1, keepdims=True) * (2 if renorm else 1) + np.abs(f64(D)).max(1, keepdims=True)
+    close(dl.np(), wdl, 2 * tol * size, "dlogits")
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (8, 4, 2), (8, 3, 1)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_nan_logit_counts_as_minus_infinity(kind, groups, renorm):
+    T, E, k = 8, 40, 8
+    x = unclean_logits(T, E, [float("nan")])
+    x[4] = x[0]
+    x[4, 1] = -float("inf")                                  # beside a masked one: equal, the lower index first
+    as_masked = torch.where(torch.isnan(x), -float("inf"), x)
+    favoured = torch.zeros(E)
+    favoured[5], favoured[6] = 0.75, 0.25                    # 5 and 6: NaN in some of the rows
+    for bias in (None, torch.zeros(E), normal(gen(104), E, std=0.05), favoured):
+        check_as(x, as_masked, k, kind, groups, bias, renorm)
