@@ -46,11 +46,14 @@ constexpr int kRouteWaves = 4;     // tokens per workgroup
 // Errors of a difference of two fp32 scores.  Sigmoid: 2.2e-7 each (exp and the
 // reciprocal to 1 ulp, three roundings).  Softmax, of the largest score: the
 // denominator's 8.5e-7 (a sum of depth 10 of exps), which both share, and 2e-7
-// each.  c = s + b and the sum of two choices round once more, 2^-24 of the
-// value each.  A group's score has two scores' errors.
+// each.  c = s + b rounds once more, 2^-24 of its value.  A group's score has two
+// scores' errors, its choices' roundings and that of their sum, 2^-24 (|c1| + |c2| +
+// |c1 + c2|): of the choices' own sizes, which two of opposite sign do not show in
+// their sum.  kGroupErr (|c1| + |c2|) holds these and the rounding of the score's end.
 constexpr float kSoftmaxErr = 1.5e-6f;
 constexpr float kSigmoidErr = 5e-7f;
 constexpr float kSumErr = 1.25e-7f;
+constexpr float kGroupErr = 1.9e-7f;
 
 // Order-preserving map of a value that is no NaN to unsigned integers; 0 is kept
 // for "no candidate".
@@ -280,7 +283,12 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
       if constexpr (SOFTMAX) return no_nan(exp_r(v - (R)lmax) * smax);
       else return sigmoid<R>(v);
     };
-    const R gs = h1 == 0 ? -(R)INFINITY : a.group_top == 1 ? value(h1) : value(h1) + value(h2);
+    R gs = -(R)INFINITY, sizes = 0;                          // sizes: |c1| + |c2|
+    if (h1 != 0) {
+      const R c1 = value(h1), c2 = a.group_top == 1 ? R(0) : value(h2);
+      gs = c1 + c2;
+      sizes = fabs(c1) + fabs(c2);
+    }
     const Key gk = ordered(no_nan(gs));
     const bool group = grp < a.n_groups;
     // groups ahead of the lane's own: lane i of a part looks at group i, i + lanes, ...
@@ -294,10 +302,12 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[PER]
     const bool open = group && rank < a.topk_groups;
     if (!open) key[0] = 0;                                   // never the owner: the others need not go
     if constexpr (CHECK) {
+      // every open group, at the lower end of its error, above every closed one at its upper end
       if (!by_logit) {
-        const float kept = from_ordered(~wave_max(open ? ~gk : 0u));
-        const float shut = from_ordered(wave_max(group && !open ? gk : 0u));
-        near = !(kept - shut > 2 * score_tol + 2 * kSumErr * fmaxf(fabsf(kept), fabsf(shut)));
+        const float err = kGroupErr * (float)sizes;
+        const float kept = from_ordered(~wave_max(open ? ~ordered(no_nan(gs - err)) : 0u));
+        const float shut = from_ordered(wave_max(group && !open ? ordered(no_nan(gs + err)) : 0u));
+        near = !(kept - shut > 2 * score_tol);
       }
     }
   }

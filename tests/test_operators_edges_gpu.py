@@ -68,3 +68,27 @@ def test_route_nan_logit_counts_as_minus_infinity(kind, groups, renorm):
     favoured[5], favoured[6] = 0.75, 0.25                    # 5 and 6: NaN in some of the rows
     for bias in (None, torch.zeros(E), normal(gen(104), E, std=0.05), favoured):
         check_as(x, as_masked, k, kind, groups, bias, renorm)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("spread", [1e-4, 0.01, 1.0])
+@pytest.mark.parametrize("size", [(33.0,), (0.5, 33.0, 1000.0)])
+def test_route_groups_whose_choices_cancel_are_ordered_as_in_fp64(kind, spread, size):
+    """Groups of two experts with biases +B and -B: each choice is rounded by B, their sum is far below it."""
+    T, E, k, n, kept = 32768, 64, 8, 32, 12
+    say(f"cancelling groups {kind} spread={spread} biases={size}")
+    g = torch.Generator(device=DEV).manual_seed(18)
+    x = torch.randn(T, E, device=DEV, generator=g) * spread
+    b = torch.tensor([size[i % len(size)] for i in range(n)], device=DEV)
+    b = torch.stack((b, -b), 1).flatten().contiguous()
+    ids, w = Out(T, k, dtype=torch.int32, fill=-77), Out(T, k)
+    moe.moe_route_scored(moe.make_shape(T, 64, 64, E, k), moe.make_router(kind, n, kept, 2), x, b, ids.t, w.t)
+    z = x.double()
+    c = (torch.sigmoid(z) if kind == "sigmoid" else torch.softmax(z, 1)) + b.double()
+    of_group = c.view(T, n, 2).sum(2)
+    best = of_group.sort(dim=1, descending=True, stable=True).indices[:, :kept]
+    mask = torch.zeros(T, n, dtype=torch.bool, device=DEV).scatter_(1, best, True)
+    c = torch.where(mask.repeat_interleave(2, 1), c, -float("inf"))
+    want = c.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    off = (ids.t.long() != want).any(1)
+    assert not off.any(), f"{int(off.sum())} of {T} tokens"
