@@ -358,8 +358,8 @@ typedef struct {
  * Logits may be -inf (a masked expert: score 0, so c = balance_bias; a row of
  * nothing else gets zero weights) and balance_bias -inf (never chosen while
  * another candidate is left).  A NaN logit counts as -inf, in rank, score, weight
- * and gradient; a NaN balance_bias ranks as -inf.  The ids of a row are distinct
- * and in [0, E) whatever the contents.
+ * and gradient; +inf counts as the largest finite value; a NaN balance_bias ranks as
+ * -inf.  The ids of a row are distinct and in [0, E) whatever the contents.
  * Errors: MOE_ERR_INVALID_ARG for a router value outside its range, n_groups
  * that does not divide n_experts, group_top above the group's size, or fewer
  * than top_k experts in topk_groups groups; MOE_ERR_UNSUPPORTED above 64 groups.

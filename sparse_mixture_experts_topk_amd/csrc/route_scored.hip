@@ -23,7 +23,7 @@
 // that is only chosen when nothing else is left; a NaN choice counts as one), so
 // k distinct experts always come out.  A NaN logit is read as -inf (usable), so
 // that its rank, score, weight and gradient are those of a masked expert, in
-// fp32 as in fp64.
+// fp32 as in fp64; +inf is read as the largest number.
 //
 // The choice must not depend on how fp32 rounds the scores.  Without a
 // balance bias the order of c is that of the logits and the keys are the
@@ -54,6 +54,7 @@ constexpr float kSoftmaxErr = 1.5e-6f;
 constexpr float kSigmoidErr = 5e-7f;
 constexpr float kSumErr = 1.25e-7f;
 constexpr float kGroupErr = 1.9e-7f;
+constexpr float kLargest = 3.402823466e38f;
 
 // Order-preserving map of a value that is no NaN to unsigned integers; 0 is kept
 // for "no candidate".
@@ -74,8 +75,9 @@ __device__ __forceinline__ double from_ordered(uint64_t u) {
 // NaN becomes -inf (the maximum of a number and NaN is the number).
 __device__ __forceinline__ float no_nan(float v) { return fmaxf(v, -INFINITY); }
 __device__ __forceinline__ double no_nan(double v) { return fmax(v, -(double)INFINITY); }
-// A logit as the router takes it.
-__device__ __forceinline__ float usable(float v) { return no_nan(v); }
+// A logit as the router takes it: NaN as -inf, +inf as the largest number (differences
+// of logits are then numbers or -inf).
+__device__ __forceinline__ float usable(float v) { return fminf(no_nan(v), kLargest); }
 
 // Reductions over the wavefront by DPP: row shifts within 16 lanes, then the two
 // row broadcasts, leave the result in lane 63, read back as a uniform value.
@@ -171,7 +173,7 @@ __device__ __forceinline__ R sigmoid(R l) {
 // sigmoid(l) over their sum, every term taken relative to the largest e^l, so that
 // it holds where all scores underflow; 0 where every chosen logit is -inf.
 __device__ __forceinline__ float chosen_weight(float lj, bool mine, bool softmax) {
-  float m = fmaxf(max8(lj), -3.402823466e38f);
+  float m = fmaxf(max8(lj), -kLargest);
   float w;
   if (softmax) {
     w = exp_r(lj - m);
@@ -395,7 +397,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const
   if (SOFTMAX && need_scores) {
 #pragma unroll
     for (int p = 0; p < PER; ++p) lmax = fmaxf(lmax, l[p]);
-    lmax = fmaxf(wave_max_value(lmax), -3.402823466e38f);    // all -inf: every term e^-inf
+    lmax = fmaxf(wave_max_value(lmax), -kLargest);    // all -inf: every term e^-inf
   }
   const int want = a.k + (a.next_ids != nullptr ? 2 : 0);
   float s[PER];
@@ -505,7 +507,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_ker
       float lmax = -INFINITY;
 #pragma unroll
       for (int p = 0; p < PER; ++p) lmax = fmaxf(lmax, l[p]);
-      lmax = fmaxf(wave_max_value(lmax), -3.402823466e38f);
+      lmax = fmaxf(wave_max_value(lmax), -kLargest);
       float s[PER], z = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int p = 0; p < PER; ++p) {

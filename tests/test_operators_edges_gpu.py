@@ -92,3 +92,17 @@ def test_route_groups_whose_choices_cancel_are_ordered_as_in_fp64(kind, spread, 
     want = c.sort(dim=1, descending=True, stable=True).indices[:, :k]
     off = (ids.t.long() != want).any(1)
     assert not off.any(), f"{int(off.sum())} of {T} tokens"
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (8, 4, 2), (8, 3, 1)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_infinite_logit_counts_as_the_largest_number(kind, groups, renorm):
+    T, E, k = 12, 40, 8
+    x = unclean_logits(T, E, [float("inf")])
+    x[4] = x[0]
+    x[4, 1], x[4, 2] = -float("inf"), float("nan")
+    x[5, 3] = torch.finfo(torch.float32).max
+    counts_as = torch.nan_to_num(x, nan=-float("inf"), posinf=torch.finfo(torch.float32).max, neginf=-float("inf"))
+    for bias in (None, torch.zeros(E), normal(gen(104), E, std=0.05)):
+        check_as(x, counts_as, k, kind, groups, bias, renorm)
