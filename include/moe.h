@@ -390,7 +390,7 @@ moe_status_t moe_route_scored_backward(const moe_shape_t* shape, const moe_route
  *                no slot points to are left as they were
  *   dweights     [T, k] fp32 out, or NULL: <dy[t], y_perm[row]>, summed in fp64; 0
  *                for a dropped slot
- * At least one output must be given.  No workspace. */
+ * At least one output must be given where T > 0.  No workspace. */
 moe_status_t moe_combine_backward(const moe_shape_t* shape, const void* dy, const float* y_perm,
                                   const int32_t* slot_to_row, const float* topk_weights, void* dy_perm,
                                   float* dweights, void* stream);
@@ -455,7 +455,8 @@ moe_status_t moe_linear(const moe_linear_t* linear, const void* x, const void* w
  * dpre is rounded to dtype for the two products (their matrix-core operand), which
  * accumulate in fp32, in an order that depends on the sizes and on which outputs are
  * asked for, and on nothing else.  relu'(0) = 0.  Outputs overlap no input and are
- * fully written, with M = 0 too (dw and dbias are then zero). */
+ * fully written, with M = 0 too (dw and dbias are then zero).  At least one output
+ * must be given where M > 0. */
 moe_status_t moe_linear_backward(const moe_linear_t* linear, const void* dy, const void* pre,
                                  const void* x, const void* w, void* dx, void* dw, float* dbias,
                                  void* workspace, size_t workspace_bytes, void* stream);

@@ -544,8 +544,8 @@ moe_status_t moe_combine_backward(const moe_shape_t* s, const void* dy, const fl
                                   float* dweights, void* stream) {
   moe_status_t v = validate_shape(s);
   if (v != MOE_OK) return v;
-  if (dy_perm == nullptr && dweights == nullptr) return MOE_ERR_INVALID_ARG;
   if (s->T == 0) return MOE_OK;
+  if (dy_perm == nullptr && dweights == nullptr) return MOE_ERR_INVALID_ARG;
   if ((v = check_ptrs({dy, slot_to_row, topk_weights}, {y_perm, dy_perm, dweights})) != MOE_OK) return v;
   if (dweights != nullptr && y_perm == nullptr) return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_combine_backward(*s, dy, y_perm, slot_to_row, topk_weights, dy_perm, dweights,
@@ -581,9 +581,8 @@ moe_status_t moe_linear_backward(const moe_linear_t* l, const void* dy, const vo
                                  void* workspace, size_t workspace_bytes, void* stream) {
   moe_status_t v = validate_linear(l);
   if (v != MOE_OK) return v;
-  if (dx == nullptr && dw == nullptr && dbias == nullptr) return MOE_ERR_INVALID_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (l->M == 0) {   // the sums over no rows
+  if (l->M == 0) {   // the sums over no rows; dx has no element (and may have no address)
     if ((v = check_ptrs({}, {dw, dbias})) != MOE_OK) return v;
     hipError_t e = hipSuccess;
     if (dw != nullptr) e = launch_fill_u8(static_cast<uint8_t*>(dw), (int64_t)l->N * l->K * act_bytes(l->dtype), 0, st);
@@ -591,6 +590,7 @@ moe_status_t moe_linear_backward(const moe_linear_t* l, const void* dy, const vo
       e = launch_fill_u8(reinterpret_cast<uint8_t*>(dbias), (int64_t)l->N * 4, 0, st);
     return from_hip(e);
   }
+  if (dx == nullptr && dw == nullptr && dbias == nullptr) return MOE_ERR_INVALID_ARG;
   if ((v = check_ptrs({dy}, {pre, x, w, dx, dw, dbias})) != MOE_OK) return v;
   if ((dx != nullptr && w == nullptr) || (dw != nullptr && x == nullptr) ||
       (l->act != MOE_ACT_NONE && pre == nullptr))

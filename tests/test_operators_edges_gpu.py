@@ -106,3 +106,17 @@ def test_route_infinite_logit_counts_as_the_largest_number(kind, groups, renorm)
     counts_as = torch.nan_to_num(x, nan=-float("inf"), posinf=torch.finfo(torch.float32).max, neginf=-float("inf"))
     for bias in (None, torch.zeros(E), normal(gen(104), E, std=0.05)):
         check_as(x, counts_as, k, kind, groups, bias, renorm)
+
+
+# ---- nothing to do ----
+
+def test_gradients_of_no_rows_through_the_binding():
+    """Outputs of no elements, alone: nothing is written and nothing is refused."""
+    say("no rows")
+    e = torch.empty(0, 64, device=DEV, dtype=torch.bfloat16)
+    w = torch.zeros(72, 64, device=DEV, dtype=torch.bfloat16)
+    moe.moe_linear_backward(moe.make_linear(0, 72, 64), e, None, e, w, e, None, None)
+    f, i = torch.empty(0, 2, device=DEV), torch.empty(0, device=DEV, dtype=torch.int32)
+    moe.moe_combine_backward(moe.make_shape(0, 64, 64, 8, 2), e, f, i, f, e, None)
+    moe.moe_combine_backward(moe.make_shape(0, 64, 64, 8, 2), e, f, i, f, None, f)
+    torch.cuda.synchronize()
