@@ -336,8 +336,8 @@ typedef struct {
   float scale;          /* weights are multiplied by this (finite) */
 } moe_router_t;
 
-/* Scored top-k selection.  Uses T, n_experts, top_k of the shape (which is
- * validated as a whole).
+/* Scored top-k selection.  Uses T, n_experts (to 256, whatever the types) and top_k
+ * of the shape; its other fields are not looked at.
  * Pages: "How Mixtral 8x7B uses mixture of experts", the simplified forward pass
  * (softmax over all experts, top-k, renormalise); "Mixtral 8x7B" interview page,
  * section on how MoE design changed since Mixtral.

@@ -178,11 +178,13 @@ ForwardLayout forward_layout(const moe_shape_t& s) {
   return L;
 }
 
-// Shape limits that T, n_experts and top_k alone decide, and the router's own.
+// Limits of T, n_experts and top_k, which are all that routing from given logits
+// has of the shape, and the router's own.
 moe_status_t validate_router(const moe_shape_t* s, const moe_router_t* r) {
-  moe_status_t v = validate_shape(s);
-  if (v != MOE_OK) return v;
-  if (r == nullptr) return MOE_ERR_INVALID_ARG;
+  if (s == nullptr || r == nullptr) return MOE_ERR_INVALID_ARG;
+  if (s->T < 0 || s->T > (1 << 24)) return MOE_ERR_INVALID_ARG;
+  if (s->top_k < 1 || s->n_experts < 2 || s->top_k > s->n_experts) return MOE_ERR_INVALID_ARG;
+  if (s->top_k > moe::kMaxTopK || s->n_experts > moe::kMaxExperts) return MOE_ERR_UNSUPPORTED;
   if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
   if (r->n_groups < 1 || r->n_groups > s->n_experts || s->n_experts % r->n_groups != 0) return MOE_ERR_INVALID_ARG;
   const int group_size = s->n_experts / r->n_groups;

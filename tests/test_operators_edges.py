@@ -28,3 +28,23 @@ def test_no_rows_with_outputs_of_no_elements():
     assert status("moe_linear_backward", moe.make_linear(1, 64, 128), A, A, A, A, None, None, None, A, 1 << 40, None) == INVALID
     # and what is given still has to be aligned
     assert status("moe_linear_backward", moe.make_linear(0, 64, 128), *[None] * 5, A + 4, None, None, 0, None) == INVALID
+
+
+def test_routing_looks_at_tokens_experts_and_k_alone():
+    """Routing from given logits has no use for the layer's widths and types, nor for the limits they bring."""
+    r = moe.make_router("sigmoid", 8, 4, 2)
+    forward = lambda s: status("moe_route_scored", s, r, *[None] * 6, None)              # noqa: E731
+    backward = lambda s: status("moe_route_scored_backward", s, r, *[None] * 5, None)    # noqa: E731
+    for call in (forward, backward):
+        # more experts than the fp32 router takes, more rows than MXFP4 experts do, widths of no kernel
+        for kw in (dict(act_dtype="f32", w_dtype="f32"), dict(w_dtype="mxfp4"), dict(w_dtype="fp8_e4m3"),
+                   dict(d_model=100, d_ff=0), dict(overflow="next_best", capacity=4, top_k=6)):
+            s = moe.make_shape(0, **{**dict(d_model=320, d_ff=64, n_experts=256, top_k=8), **kw})
+            assert call(s) == 0, kw
+            s.T = 1
+            assert call(s) == INVALID, kw                   # missing pointers
+        for kw, want in ((dict(T=-1), INVALID), (dict(T=(1 << 24) + 1), INVALID), (dict(top_k=0), INVALID),
+                         (dict(n_experts=1), INVALID), (dict(n_experts=8, top_k=9), INVALID),
+                         (dict(top_k=9), UNSUPPORTED), (dict(n_experts=264), UNSUPPORTED)):
+            s = moe.make_shape(**{**dict(T=0, d_model=256, d_ff=256, n_experts=256, top_k=8), **kw})
+            assert call(s) == want, kw

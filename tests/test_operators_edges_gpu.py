@@ -120,3 +120,18 @@ def test_gradients_of_no_rows_through_the_binding():
     moe.moe_combine_backward(moe.make_shape(0, 64, 64, 8, 2), e, f, i, f, e, None)
     moe.moe_combine_backward(moe.make_shape(0, 64, 64, 8, 2), e, f, i, f, None, f)
     torch.cuda.synchronize()
+
+
+def test_route_looks_at_tokens_experts_and_k_alone():
+    x, b = cuda(normal(gen(106), 50, 256)), cuda(normal(gen(107), 256, std=0.05))
+    say("route with shapes of other types and widths")
+    r, outs = moe.make_router("sigmoid", 8, 4, 2), []
+    for kw in (dict(), dict(act_dtype="f32", w_dtype="f32"), dict(w_dtype="mxfp4", capacity=3), dict(d_model=100)):
+        s = moe.make_shape(50, **{**dict(d_model=64, d_ff=64, n_experts=256, top_k=8), **kw})
+        ids, w, dl = Out(50, 8, dtype=torch.int32, fill=-77), Out(50, 8), Out(50, 256)
+        moe.moe_route_scored(s, r, x, b, ids.t, w.t)
+        moe.moe_route_scored_backward(s, r, x, ids.t, w.t, None, dl.t)
+        torch.cuda.synchronize()
+        outs.append((ids.np(), w.np(), dl.np()))
+    for o in outs[1:]:
+        assert all(np.array_equal(g, want) for g, want in zip(o, outs[0]))
