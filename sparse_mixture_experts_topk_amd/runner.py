@@ -10,6 +10,7 @@ pass back to x and the router's weights (the experts' weights held fixed).
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Optional
 
@@ -95,23 +96,36 @@ def _bytes(n: int, device) -> Optional[torch.Tensor]:
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
+def _on(stream, device):
+    """The context in which torch's own operations go to ``stream`` (None: where they go anyway)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
+                             else torch.cuda.ExternalStream(int(stream), device=device))
+
+
 def scored_routing(di: DeviceInputs, router, balance_bias=None, stream=None, out: Optional[dict] = None,
                    scores: bool = False) -> dict:
     """logits = x . w_gate^T (+ router_bias) in fp32, then moe_route_scored: the buffers of both
     (``out`` holds ones to use: logits, topk_ids, topk_weights, next_ids, scores, linear_ws).
-    n_experts must be a multiple of 8, like every width of moe_linear."""
+    moe_linear has widths of multiples of 8: the logits of other expert counts are those that
+    moe_route_topk writes, and its choice is written over."""
     cfg, dev = di.cfg, di.x.device
     T, E, k = cfg.T, cfg.n_experts, cfg.top_k
-    lin = make_linear(T, E, cfg.d_model, dtype=cfg.act_dtype, y_dtype="f32")
     o = {} if out is None else out
     for name, shape, dtype in (("topk_ids", (T, k), torch.int32), ("topk_weights", (T, k), torch.float32),
                                ("logits", (T, E), torch.float32), ("next_ids", (T, 2), torch.int32),
                                ("scores", (T, E) if scores else None, torch.float32)):
         if o.get(name) is None:
             o[name] = None if shape is None else torch.empty(*shape, dtype=dtype, device=dev)
-    if o.get("linear_ws") is None:
-        o["linear_ws"] = _bytes(moe_linear_workspace_bytes(lin, MOE_CALL_LINEAR), dev)
-    moe_linear(lin, di.x, di.w_gate, di.router_bias, None, o["logits"], None, o["linear_ws"], stream)
+    if E % 8 == 0:
+        lin = make_linear(T, E, cfg.d_model, dtype=cfg.act_dtype, y_dtype="f32")
+        if o.get("linear_ws") is None:
+            o["linear_ws"] = _bytes(moe_linear_workspace_bytes(lin, MOE_CALL_LINEAR), dev)
+        moe_linear(lin, di.x, di.w_gate, di.router_bias, None, o["logits"], None, o["linear_ws"], stream)
+    else:
+        moe_route_topk(shape_of(cfg), di.x, di.w_gate, di.router_bias, o["topk_ids"], o["topk_weights"], o["logits"],
+                       None, None, stream)
     moe_route_scored(shape_of(cfg), router, o["logits"], balance_bias, o["topk_ids"], o["topk_weights"],
                      o["scores"], o["next_ids"], stream)
     return o
@@ -119,24 +133,34 @@ def scored_routing(di: DeviceInputs, router, balance_bias=None, stream=None, out
 
 def gate_backward(di: DeviceInputs, st: dict, router, dy: torch.Tensor, dscores=None, stream=None) -> dict:
     """Gradients of the gate from the gradient ``dy`` at y: ``st`` is the result of ``staged`` with
-    the same router.  dy_perm is the gradient at the experts' rows; dx and dw_gate, dbias are those
-    of the router's product alone (the path through the gate weights)."""
+    the same router.  dy_perm is the gradient at the experts' rows, for the caller's own backward pass
+    of the experts (the library has none); dx and dw_gate, dbias are those of the router's product
+    alone (the path through the gate weights)."""
     cfg, dev = di.cfg, di.x.device
     T, d, E, k = cfg.T, cfg.d_model, cfg.n_experts, cfg.top_k
-    shape = shape_of(cfg)
-    o = {"dy_perm": torch.empty(T * (k + cfg.n_shared), d, dtype=_act_dtype(cfg), device=dev),
+    W = (E + 7) // 8 * 8          # moe_linear_backward has widths of multiples of 8: zero rows behind the experts'
+    act, shape = _act_dtype(cfg), shape_of(cfg)
+    dw = torch.empty(W, d, dtype=act, device=dev)
+    db = torch.empty(W, device=dev) if di.router_bias is not None else None
+    o = {"dy_perm": torch.empty(T * (k + cfg.n_shared), d, dtype=act, device=dev),
          "dweights": torch.empty(T, k, device=dev), "dlogits": torch.empty(T, E, device=dev),
-         "dx": torch.empty(T, d, dtype=_act_dtype(cfg), device=dev),
-         "dw_gate": torch.empty(E, d, dtype=_act_dtype(cfg), device=dev),
-         "dbias": torch.empty(E, device=dev) if di.router_bias is not None else None}
+         "dx": torch.empty(T, d, dtype=act, device=dev), "dw_gate": dw[:E],
+         "dbias": None if db is None else db[:E]}
     moe_combine_backward(shape, dy, st["y_perm"], st["slot_to_row"], st["topk_weights"], o["dy_perm"],
                          o["dweights"], stream)
     moe_route_scored_backward(shape, router, st["logits"], st["topk_ids"], o["dweights"], dscores,
                               o["dlogits"], stream)
-    lin = make_linear(T, E, d, dtype=cfg.act_dtype, y_dtype="f32")
+    dlogits, w_gate = o["dlogits"], di.w_gate
+    if W != E:
+        o["padded"] = dlogits, w_gate = torch.empty(T, W, device=dev), torch.empty(W, d, dtype=act, device=dev)
+        with _on(stream, dev):
+            dlogits[:, :E].copy_(o["dlogits"])
+            dlogits[:, E:].zero_()
+            w_gate[:E].copy_(di.w_gate)
+            w_gate[E:].zero_()
+    lin = make_linear(T, W, d, dtype=cfg.act_dtype, y_dtype="f32")
     o["ws"] = _bytes(moe_linear_workspace_bytes(lin, MOE_CALL_LINEAR_BACKWARD), dev)
-    moe_linear_backward(lin, o["dlogits"], None, di.x, di.w_gate, o["dx"], o["dw_gate"], o["dbias"], o["ws"],
-                        stream)
+    moe_linear_backward(lin, dlogits, None, di.x, w_gate, o["dx"], dw, db, o["ws"], stream)
     return o
 
 

@@ -135,3 +135,27 @@ def test_route_looks_at_tokens_experts_and_k_alone():
         outs.append((ids.np(), w.np(), dl.np()))
     for o in outs[1:]:
         assert all(np.array_equal(g, want) for g, want in zip(o, outs[0]))
+
+
+@pytest.mark.parametrize("kw", [dict(E=60), dict(T=5, E=12, k=3, shared=0), dict(T=33, E=100, k=6),
+                                dict(T=50, E=12, k=2, shared=0, act_dtype="f32", w_dtype="f32")])
+def test_scored_layer_of_expert_counts_that_are_no_multiple_of_8(kw):
+    base.test_scored_layer_and_its_gate_gradient(kw)
+
+
+def test_gate_gradient_of_12_experts_on_a_stream_of_its_own():
+    cfg, inp, balance = base.layer(T=700, E=12, k=3)
+    say("gate gradient of 12 experts on another stream")
+    di = runner.DeviceInputs.from_host(inp)
+    router, dy = moe.make_router(**base.ROUTER), cuda(normal(gen(105), 700, cfg.d_model, dtype=torch.bfloat16))
+    st = runner.staged(di, router=router, balance_bias=cuda(balance))
+    want = runner.gate_backward(di, st, router, dy)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    for stream in (side, side.cuda_stream):
+        got = runner.gate_backward(di, st, router, dy, stream=stream)
+        side.synchronize()
+        for name in ("dx", "dw_gate", "dbias", "dlogits"):
+            assert torch.equal(got[name], want[name]), name
