@@ -1,11 +1,13 @@
 """CPU checks of the operators' calls at their edges: no tokens, shapes that only routing looks at, what the
 documents show."""
+import ast
 import ctypes
-
-import pytest
+import inspect
+import pathlib
+import re
 
 import sparse_mixture_experts_topk_amd as moe
-from sparse_mixture_experts_topk_amd import _lib
+from sparse_mixture_experts_topk_amd import _lib, runner
 
 A = 0x10000                 # an aligned address that no refused call reads
 INVALID, UNSUPPORTED = 1, 2
@@ -48,3 +50,22 @@ def test_routing_looks_at_tokens_experts_and_k_alone():
                          (dict(top_k=9), UNSUPPORTED), (dict(n_experts=264), UNSUPPORTED)):
             s = moe.make_shape(**{**dict(T=0, d_model=256, d_ff=256, n_experts=256, top_k=8), **kw})
             assert call(s) == want, kw
+
+
+def test_calls_in_the_readme_fit_their_signatures():
+    """Names that the README's Python gives to arguments are those of the parameters, in their order."""
+    root = pathlib.Path(__file__).resolve().parent.parent
+    blocks = re.findall(r"```python\n(.*?)```", (root / "README.md").read_text(), re.S)
+    calls = 0
+    for node in (n for b in blocks for n in ast.walk(ast.parse(b)) if isinstance(n, ast.Call)):
+        f = node.func
+        owner = {"moe": moe, "runner": runner}.get(getattr(getattr(f, "value", None), "id", None))
+        if owner is None:
+            continue
+        calls += 1
+        sig = inspect.signature(getattr(owner, f.attr))
+        bound = sig.bind(*node.args, **{k.arg: k.value for k in node.keywords})
+        for name, value in bound.arguments.items():
+            if isinstance(value, ast.Name) and value.id in sig.parameters:
+                assert value.id == name, f"{f.attr}: {value.id} in the place of {name}"
+    assert calls >= 8

@@ -4,6 +4,8 @@ whole range, every tile shape of the forward product.
 
 Tolerances count half steps (see test_operators_gpu); what a test needs beyond that is derived in it."""
 import math
+import pathlib
+import re
 
 import numpy as np
 import pytest
@@ -12,7 +14,7 @@ import torch
 import sparse_mixture_experts_topk_amd as moe
 import test_operators_gpu as base
 from oracle import operators as ref
-from sparse_mixture_experts_topk_amd import runner
+from sparse_mixture_experts_topk_amd import runner, synthetic
 from test_operators_gpu import BF16, DEV, F32, Out, close, cuda, f64, gen, normal, say
 
 pytestmark = pytest.mark.gpu
@@ -159,3 +161,17 @@ def test_gate_gradient_of_12_experts_on_a_stream_of_its_own():
         side.synchronize()
         for name in ("dx", "dw_gate", "dbias", "dlogits"):
             assert torch.equal(got[name], want[name]), name
+
+
+def test_readme_example_of_the_scored_layer_runs():
+    readme = pathlib.Path(__file__).resolve().parent.parent / "README.md"
+    if not readme.exists():
+        pytest.skip("a copy of the tree without its documents")
+    code = [b for b in re.findall(r"```python\n(.*?)```", readme.read_text(), re.S) if "make_router" in b]
+    say("the README's example")
+    names = {"torch": torch, "moe": moe, "runner": runner, "synthetic": synthetic}
+    exec(compile(code[0], "README.md", "exec"), names)
+    torch.cuda.synchronize()
+    assert len(code) == 1 and torch.equal(names["out"].y, names["st"]["y"])
+    assert all(bool(torch.isfinite(names["grads"][n]).all()) for n in ("dx", "dw_gate", "dlogits"))
+    assert bool(torch.isfinite(names["y"]).all())
