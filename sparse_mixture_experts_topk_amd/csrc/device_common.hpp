@@ -44,6 +44,35 @@ __device__ __forceinline__ int block_exponent(float amax) {
   return man == 0 ? ex - 127 : ex - 126;
 }
 
+// e^v from the hardware's exp2 (1 ulp): the product with log2(e) is carried in two
+// parts, so that the argument's rounding does not grow with |v|; a few ulp in all.
+// v <= 0; -inf and whatever underflows give 0, NaN too.
+__device__ __forceinline__ float exp_r(float v) {
+  v = fmaxf(v, -200.0f);
+  const float hi = 1.44269502f, lo = 1.92596299e-8f;          // log2(e)
+  const float t = v * hi;
+  const float r = fmaf(v, lo, fmaf(v, hi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, r * 0.693147182f, e);
+}
+__device__ __forceinline__ double exp_r(double v) { return exp(v); }
+__device__ __forceinline__ float rcp_r(float v) { return __builtin_amdgcn_rcpf(v); }     // 1 ulp
+__device__ __forceinline__ double rcp_r(double v) { return 1.0 / v; }
+
+// sigmoid(l) and 1 - sigmoid(l) without overflow or cancellation, from e^-|l|
+template <class R>
+__device__ __forceinline__ void sigmoids(R l, R& s, R& below) {
+  const R e = exp_r(l < 0 ? l : -l), r = rcp_r(R(1) + e);
+  s = l < 0 ? e * r : r;
+  below = l < 0 ? r : e * r;
+}
+template <class R>
+__device__ __forceinline__ R sigmoid(R l) {
+  R s, below;
+  sigmoids(l, s, below);
+  return s;
+}
+
 __device__ __forceinline__ float silu_f32(float g) { return g / (1.0f + expf(-g)); }
 
 __device__ __forceinline__ bf16x8_t as_bf16x8(uint4 v) { return __builtin_bit_cast(bf16x8_t, v); }

@@ -55,7 +55,7 @@ __global__ __launch_bounds__(256) void dpre_kernel(const void* __restrict__ dy, 
         if constexpr (OP32) load8f(static_cast<const float*>(pre) + at, p);
         else unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pre) + at), p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= act_grad(p[i], act);
+        for (int i = 0; i < 8; ++i) v[i] *= act_grad<OP32>(p[i], act);
       }
       if (dpre != nullptr) {
         if constexpr (OP32) store8f(static_cast<float*>(dpre) + at, v);

@@ -5,8 +5,12 @@
 
 namespace moe {
 
-// exp by the hardware's exp2: about 1 ulp in fp32 plus the rounding of the
-// scaled argument, far below the bf16 rounding that follows.
+// Activations and their slopes.  F32 (fp32 operands): the argument of each exponential
+// is carried in two parts, so that no error grows with |p| (silu and gelu (tanh) 8 half
+// steps of the value, gelu 16, in either tail, where plain products lose 2 |p|, 2.5 p^2 / 2
+// and 8 |2 u| more).  Otherwise it is rounded as it comes: that is a change of p by a few
+// half steps, which is what the sum of products behind p is off by itself; here too the
+// error is relative to the value.
 __device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.4426950408889634f); }
 __device__ __forceinline__ float fast_sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-v)); }
 
@@ -15,9 +19,10 @@ constexpr float kGeluB = 0.044715f;
 
 // Phi(-|p|) of the normal distribution and e = exp(-p^2 / 2): the product of e and
 // a polynomial in 1 / (1 + 0.2121 |p|) fitted to Phi(-u) e^(u^2/2) over 0 <= u <=
-// 13.6 (relative error 2e-8; in fp32 5e-7, and up to 8e-6 from the rounding of p^2
-// where the value is below 1e-30).  The library's erfc took 96 us for 60 in the
+// 13.6 (these coefficients: relative error 4.4e-8; evaluated in fp32, with a
+// reciprocal to 1 ulp, 6.4e-7).  The library's erfc took 96 us for 60 in the
 // gradient of 6061 x 8064 values.
+template <bool F32>
 __device__ __forceinline__ float normal_tail(float p, float& e) {
   const float t = __builtin_amdgcn_rcpf(fmaf(0.2121f, fabsf(p), 1.0f));
   float q = -0.0648413971f;
@@ -29,40 +34,85 @@ __device__ __forceinline__ float normal_tail(float p, float& e) {
   q = fmaf(q, t, 0.0741440579f);
   q = fmaf(q, t, 0.0853452384f);
   q = fmaf(q, t, 0.0845813006f);
-  e = __builtin_amdgcn_exp2f(p * p * -0.7213475204f);
+  if constexpr (F32) {
+    const float hi = -0.72134751f, lo = -9.62981495e-9f;        // -log2(e) / 2
+    const float u = fminf(fabsf(p), 32.0f), sq = u * u;         // 0 from there on
+    const float x = sq * hi;
+    const float r = fmaf(fmaf(u, u, -sq), hi, fmaf(sq, lo, fmaf(sq, hi, -x)));
+    e = __builtin_amdgcn_exp2f(x);
+    e = fmaf(e, r * 0.693147182f, e);
+  } else {
+    e = __builtin_amdgcn_exp2f(p * p * -0.7213475204f);
+  }
   return q * t * e;
 }
 
-template <int ACT>
+// sigmoid(2 u) and 1 - sigmoid(2 u), u = sqrt(2 / pi) (p + 0.044715 p^3), from 2^-|2 u
+// log2(e)| with that exponent in two parts; |p| <= 32 (0 and 1 exactly from there on).
+__device__ __forceinline__ void tanh_sigmoids(float p, float& s, float& below) {
+  constexpr double kA = 2.302208198144325;                      // 2 sqrt(2 / pi) log2(e)
+  constexpr float a = (float)kA, a_lo = (float)(kA - (double)a), b_lo = (float)(0.044715 - (double)kGeluB);
+  const float sq = p * p, sq_lo = fmaf(p, p, -sq);
+  const float g = fmaf(kGeluB, sq, 1.0f);                       // (1 - g is exact: g >= 1 is a multiple of its own step)
+  const float g_lo = fmaf(kGeluB, sq, 1.0f - g) + fmaf(kGeluB, sq_lo, b_lo * sq);
+  const float v = p * g, v_lo = fmaf(p, g_lo, fmaf(p, g, -v));
+  const float x = v * a, r = fmaf(v_lo, a, fmaf(v, a_lo, fmaf(v, a, -x)));
+  float e = __builtin_amdgcn_exp2f(-fabsf(x));
+  e = fmaf(e, (x < 0.0f ? r : -r) * 0.693147182f, e);
+  const float n = __builtin_amdgcn_rcpf(1.0f + e);
+  s = x < 0.0f ? e * n : n;
+  below = x < 0.0f ? n : e * n;
+}
+__device__ __forceinline__ float to_32(float p) { return p < -32.0f ? -32.0f : p > 32.0f ? 32.0f : p; }   // NaN stays
+
+template <int ACT, bool F32 = false>
 __device__ __forceinline__ float act_value(float p) {
   if constexpr (ACT == MOE_ACT_RELU) return p < 0.0f ? 0.0f : p;          // NaN stays NaN
-  else if constexpr (ACT == MOE_ACT_SILU) return p * fast_sigmoid(p);
+  else if constexpr (ACT == MOE_ACT_SILU) return p * (F32 ? sigmoid(p) : fast_sigmoid(p));
   else if constexpr (ACT == MOE_ACT_GELU) {
     float e;
-    const float q = normal_tail(p, e);
+    const float q = normal_tail<F32>(p, e);
     return p * (p < 0.0f ? q : 1.0f - q);
   }
-  else if constexpr (ACT == MOE_ACT_GELU_TANH) return p * fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));
+  else if constexpr (ACT == MOE_ACT_GELU_TANH) {
+    if constexpr (!F32) return p * fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));
+    float s, below;
+    tanh_sigmoids(to_32(p), s, below);
+    return p * s;
+  }
   else return p;
 }
 
+template <bool F32>
 __device__ __forceinline__ float act_grad(float p, int act) {
   switch (act) {
     case MOE_ACT_RELU: return p > 0.0f ? 1.0f : 0.0f;
     case MOE_ACT_SILU: {
-      const float s = fast_sigmoid(p);
-      return s * (1.0f + p * (1.0f - s));
+      float s, below;
+      if constexpr (F32) {
+        sigmoids(p, s, below);
+      } else {
+        s = fast_sigmoid(p);
+        below = 1.0f - s;
+      }
+      return s * (1.0f + p * below);
     }
     case MOE_ACT_GELU: {
-      p = p < -32.0f ? -32.0f : p > 32.0f ? 32.0f : p;   // 0 or 1 exactly from there on; p * p stays finite
+      p = to_32(p);                                      // 0 or 1 exactly from there on; p * p stays finite
       float e;
-      const float q = normal_tail(p, e);
+      const float q = normal_tail<F32>(p, e);
       return fmaf(p * e, 0.3989422804014327f, p < 0.0f ? q : 1.0f - q);
     }
     case MOE_ACT_GELU_TANH: {
-      p = p < -32.0f ? -32.0f : p > 32.0f ? 32.0f : p;
-      const float s = fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));
-      return s + p * s * (1.0f - s) * kGeluA * (1.0f + 3.0f * kGeluB * p * p);
+      p = to_32(p);
+      float s, below;
+      if constexpr (F32) {
+        tanh_sigmoids(p, s, below);
+      } else {
+        s = fast_sigmoid(kGeluA * (p + kGeluB * p * p * p));
+        below = 1.0f - s;
+      }
+      return s + p * s * below * kGeluA * (1.0f + 3.0f * kGeluB * p * p);
     }
     default: return 1.0f;
   }

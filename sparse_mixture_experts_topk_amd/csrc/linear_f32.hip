@@ -41,7 +41,8 @@ struct EpilogueF32 {
       v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
     }
     if (pre != nullptr) *reinterpret_cast<float4*>(pre + at) = v;
-    v = make_float4(act_value<ACT>(v.x), act_value<ACT>(v.y), act_value<ACT>(v.z), act_value<ACT>(v.w));
+    v = make_float4(act_value<ACT, true>(v.x), act_value<ACT, true>(v.y), act_value<ACT, true>(v.z),
+                    act_value<ACT, true>(v.w));
     if (residual != nullptr) {
       const float4 q = *reinterpret_cast<const float4*>(residual + at);
       v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;

@@ -1,10 +1,13 @@
 """CPU checks of the operators' calls at their edges: no tokens, shapes that only routing looks at, what the
-documents show."""
+documents show, the constants of the sources."""
 import ast
 import ctypes
 import inspect
+import math
 import pathlib
 import re
+
+import numpy as np
 
 import sparse_mixture_experts_topk_amd as moe
 from sparse_mixture_experts_topk_amd import _lib, runner
@@ -69,3 +72,21 @@ def test_calls_in_the_readme_fit_their_signatures():
             if isinstance(value, ast.Name) and value.id in sig.parameters:
                 assert value.id == name, f"{f.attr}: {value.id} in the place of {name}"
     assert calls >= 8
+
+
+def test_gelu_tail_polynomial_is_as_near_as_its_comment_says():
+    """The coefficients of the source against erfc, in 64 bits over the stated range."""
+    root = pathlib.Path(moe.__file__).resolve().parent
+    src = (root / "csrc" / "linear_epilogue.hpp").read_text()
+    q0 = re.search(r"float q = ([-0-9.]+)f;", src)
+    coeffs = [float(q0.group(1))] + [float(v) for v in re.findall(r"q = fmaf\(q, t, ([-0-9.]+)f\);", src)]
+    scale = np.float64(np.float32(re.search(r"fmaf\(([0-9.]+)f, fabsf\(p\), 1\.0f\)", src).group(1)))
+    bound = float(re.search(r"these coefficients: relative error ([-0-9.e]+);", src).group(1))
+    assert len(coeffs) == 9
+    u = np.linspace(0.0, 13.6, 20001)
+    want = np.array([0.5 * math.erfc(v / math.sqrt(2)) * math.exp(0.5 * v * v) for v in u])
+    t, q = 1.0 / (scale * u + 1.0), 0.0
+    for c in coeffs:
+        q = q * t + np.float64(np.float32(c))
+    err = np.abs(q * t / want - 1.0).max()
+    assert 0.9 * bound < err < bound, err

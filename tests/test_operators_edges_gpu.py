@@ -175,3 +175,80 @@ def test_readme_example_of_the_scored_layer_runs():
     assert len(code) == 1 and torch.equal(names["out"].y, names["st"]["y"])
     assert all(bool(torch.isfinite(names["grads"][n]).all()) for n in ("dx", "dw_gate", "dlogits"))
     assert bool(torch.isfinite(names["y"]).all())
+
+
+def fp32_activation(act, span, out_dtype="f32", dtype="f32"):
+    """(p, act(p), act'(p)) of 32768 values over +-span, the identity as weights: pre-activations are exact."""
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    p = torch.linspace(-span, span, 4096 * 8).to(dt).view(4096, 8)
+    lin = moe.make_linear(4096, 8, 8, dtype=dtype, y_dtype=out_dtype, act=act)
+    eye = cuda(torch.eye(8, dtype=dt))
+    y = Out(4096, 8)
+    moe.moe_linear(lin, cuda(p), eye, None, None, y.t, None, runner._bytes(moe.moe_linear_workspace_bytes(lin), DEV))
+    if dtype != "f32":
+        torch.cuda.synchronize()
+        return f64(p), y.np(), None
+    dx, dy = Out(4096, 8), torch.ones(4096, 8, device=DEV)
+    moe.moe_linear_backward(lin, dy, cuda(p), None, eye, dx.t, None, None,
+                            runner._bytes(moe.moe_linear_workspace_bytes(lin, moe.MOE_CALL_LINEAR_BACKWARD), DEV))
+    torch.cuda.synchronize()
+    return f64(p), y.np(), dx.np()
+
+
+def sigmoid_pair(z):
+    """sigmoid(z), 1 - sigmoid(z) in fp64."""
+    e = np.exp(-np.abs(z))
+    return np.where(z < 0, e, 1.0) / (1.0 + e), np.where(z < 0, 1.0, e) / (1.0 + e)
+
+
+# sigmoid from e^-|z|: e to 3 half steps (exp2 to 1 ulp, one rounding), 1 + e one more, the reciprocal to 1 ulp,
+# one product: 3 / (1 + e) + 1 + 2 + 1 <= 7 relative, 1 - sigmoid likewise
+SIGMOID = 7 * F32
+
+
+def test_silu_of_fp32_operands_over_the_whole_range():
+    p, y, dx = fp32_activation("silu", 86.0)
+    s, below = sigmoid_pair(p)
+    close(y, p * s, 1.05 * (SIGMOID + F32) * np.abs(p * s) + 2.0 ** -120, "silu")
+    slope = s * (1 + p * below)
+    # s, the rounding of 1 + p below, the product; below inside the bracket
+    close(dx, slope, 1.05 * ((SIGMOID + 2 * F32) * np.abs(slope) + SIGMOID * s * np.abs(p) * below) + 2.0 ** -120, "slope")
+
+
+def test_gelu_tanh_of_fp32_operands_over_the_whole_range():
+    p, y, dx = fp32_activation("gelu_tanh", 10.0)
+    a, b = 2 * math.sqrt(2 / math.pi), 0.044715
+    s, below = sigmoid_pair(a * (p + b * p ** 3))
+    close(y, p * s, 1.05 * (SIGMOID + F32) * np.abs(p * s) + 2.0 ** -120, "gelu_tanh")
+    inner = np.abs(p) * s * below * a * (1 + 3 * b * p * p)
+    # both factors, four products, a and 3 b p^2 with two roundings and a constant's: 7 + 7 + 4 + 1 + 4
+    tol = 23 * F32 * inner + SIGMOID * s + F32 * np.abs(s + np.sign(p) * inner)
+    close(dx, s + np.sign(p) * inner, 1.05 * tol + 2.0 ** -120, "slope")
+
+
+def test_gelu_of_fp32_operands_over_the_whole_range():
+    p, y, dx = fp32_activation("gelu", 13.0)
+    tail = np.array([0.5 * math.erfc(abs(t) / math.sqrt(2)) for t in p.ravel()]).reshape(p.shape)
+    cdf, phi = np.where(p < 0, tail, 1 - tail), np.exp(-0.5 * p * p) / math.sqrt(2 * math.pi)
+    # the tail's polynomial with a reciprocal to 1 ulp 6.4e-7, e^(-p^2/2) 3 half steps, their product one
+    e_tail = (6.4e-7 + 4 * F32) * tail
+    e_cdf = e_tail + np.where(p < 0, 0.0, F32 * cdf)
+    close(y, p * cdf, 1.05 * (np.abs(p) * e_cdf + F32 * np.abs(p) * cdf) + 2.0 ** -120, "gelu")
+    slope = cdf + p * phi
+    close(dx, slope, 1.05 * (e_cdf + 4.5 * F32 * np.abs(p) * phi + F32 * np.abs(slope)) + 2.0 ** -120, "slope")
+
+
+@pytest.mark.parametrize("act,span", [("silu", 86.0), ("gelu", 13.0), ("gelu_tanh", 10.0)])
+def test_activation_tails_of_bf16_operands(act, span):
+    """fp32 outputs of bf16 operands: exact to a few half steps of the value and of exp's argument."""
+    p, y, _ = fp32_activation(act, span, dtype="bf16")
+    want = ref.activation(p, act)[0]
+    if act == "gelu":                                        # (1 + erf cancels in the reference)
+        want = p * np.array([0.5 * math.erfc(-t / math.sqrt(2)) for t in p.ravel()]).reshape(p.shape)
+    if act == "gelu_tanh":                                   # (1 + tanh too)
+        z = 2 * math.sqrt(2 / math.pi) * (p + 0.044715 * p ** 3)
+        want = p * sigmoid_pair(z)[0]
+    # the argument's roundings: |p| by its product with log2 e; p^2 / 2 by two products; 2 u by seven of its terms
+    arg = {"silu": 1.25 * np.abs(p), "gelu": 2.5 * p * p / 2,
+           "gelu_tanh": 8 * 2 * math.sqrt(2 / math.pi) * np.abs(p + 0.044715 * p ** 3)}[act]
+    close(y, want, 1.05 * (6.4e-7 + (9 + arg) * F32) * np.abs(want) + 2.0 ** -120, act)
