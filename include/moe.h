@@ -439,8 +439,10 @@ moe_status_t moe_linear_workspace_bytes(const moe_linear_t* linear, moe_call_t c
  *   y        [M, N] y_dtype out; may be the residual's memory, else overlaps no input
  *   pre      [M, N] dtype out, or NULL: x . w^T + bias, kept for the backward pass
  * fp32 accumulation; bias, activation and residual in fp32, one rounding to
- * y_dtype (the activation sees the unrounded pre).  A row's result depends on M
- * only through which kernel runs. */
+ * y_dtype (the activation sees the unrounded pre).  The order of an element's sum
+ * depends on M, N, K, the element's row and channel and the device's number of CUs,
+ * and is the same from call to call; equal rows of x may differ in their last bits,
+ * within one call and between calls of other M. */
 moe_status_t moe_linear(const moe_linear_t* linear, const void* x, const void* w, const float* bias,
                         const void* residual, void* y, void* pre, void* workspace,
                         size_t workspace_bytes, void* stream);
@@ -453,8 +455,9 @@ moe_status_t moe_linear(const moe_linear_t* linear, const void* x, const void* w
  *            unless act is MOE_ACT_NONE (then ignored); the residual's gradient
  *            is dy itself
  * dpre is rounded to dtype for the two products (their matrix-core operand), which
- * accumulate in fp32, in an order that depends on the sizes and on which outputs are
- * asked for, and on nothing else.  relu'(0) = 0.  Outputs overlap no input and are
+ * accumulate in fp32, in an order that depends on the sizes, the element's place, the
+ * device's number of CUs and which outputs are asked for, and is the same from call
+ * to call.  relu'(0) = 0.  Outputs overlap no input and are
  * fully written, with M = 0 too (dw and dbias are then zero).  At least one output
  * must be given where M > 0. */
 moe_status_t moe_linear_backward(const moe_linear_t* linear, const void* dy, const void* pre,

@@ -252,3 +252,24 @@ def test_activation_tails_of_bf16_operands(act, span):
     arg = {"silu": 1.25 * np.abs(p), "gelu": 2.5 * p * p / 2,
            "gelu_tanh": 8 * 2 * math.sqrt(2 / math.pi) * np.abs(p + 0.044715 * p ** 3)}[act]
     close(y, want, 1.05 * (6.4e-7 + (9 + arg) * F32) * np.abs(want) + 2.0 ** -120, act)
+
+
+@pytest.mark.parametrize("dims", [(33, 4096, 4096), (64, 4096, 4096), (65, 4096, 4096), (129, 4096, 4096), (16, 256, 4096)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_repeats_bit_for_bit(dims, dtype):
+    """Whatever the workspace held before."""
+    M, N, K = dims
+    say(f"repeated {dtype} M={M} N={N} K={K}")
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, w = base.device_normal(1, M, K, dtype=dt), base.device_normal(2, N, K, std=K ** -0.5, dtype=dt)
+    lin = moe.make_linear(M, N, K, dtype=dtype, y_dtype="f32")
+    ws = runner._bytes(moe.moe_linear_workspace_bytes(lin), DEV)
+    outs = []
+    for fill in (0xFF, 0, 77):
+        if ws is not None:
+            ws.fill_(fill)
+        y = torch.empty(M, N, device=DEV)
+        moe.moe_linear(lin, x, w, None, None, y, None, ws)
+        outs.append(y)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
