@@ -273,3 +273,47 @@ def test_linear_repeats_bit_for_bit(dims, dtype):
         outs.append(y)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+# each tile shape of the forward product: taken whole in part of a round, whole over several rounds,
+# cut along the contraction and joined, with and without full rounds before
+@pytest.mark.parametrize("dims", [(40, 256, 72), (40, 256, 2056), (1900, 1032, 72), (1100, 1000, 4104), (2500, 1544, 2056),
+                                  (256, 4096, 4096), (2500, 1544, 72), (512, 14336, 4096), (700, 4096, 8200),
+                                  (384, 4096, 14336), (2049, 4096, 4104), (2049, 4096, 72), (2500, 4096, 8200),
+                                  (4097, 4096, 4104), (8192, 14336, 4096)])
+def test_linear_in_every_tile_shape(dims):
+    """Against 64-bit products on the device: bare with fp32 output, and with bias, silu, residual and pre."""
+    M, N, K = dims
+    say(f"linear tiles M={M} N={N} K={K}")
+    x, w = base.device_normal(1, M, K), base.device_normal(2, N, K, std=K ** -0.5)
+    b, r = base.device_normal(3, N, dtype=torch.float32), base.device_normal(4, M, N)
+    x64, wt64 = x.double(), w.double().t().contiguous()
+    want = x64 @ wt64
+    dot = (K + 4) * 2.0 ** -23 * (x64.abs() @ wt64.abs() + b.double().abs())
+
+    def inside(got, want, tol, what):
+        off = (got.double() - want).abs() - tol
+        assert not torch.isnan(got).any() and off.max() <= 0, f"{what}: {float(off.max())} past the tolerance"
+
+    for out in ("f32", "bf16"):
+        whole = out == "bf16"
+        lin = moe.make_linear(M, N, K, y_dtype=out, act="silu" if whole else "none")
+        n = moe.moe_linear_workspace_bytes(lin)
+        ws = Out(n, dtype=torch.uint8, fill=77) if n else None
+        if ws:
+            ws.t.fill_(0xFF)
+        y = Out(M, N, dtype=torch.bfloat16 if whole else torch.float32)
+        p = Out(M, N, dtype=torch.bfloat16)
+        moe.moe_linear(lin, x, w, b if whole else None, r if whole else None, y.t, p.t if whole else None,
+                       ws.t if ws else None)
+        torch.cuda.synchronize()
+        for o in (y, p, ws):
+            assert o is None or bool((o.flat[o.n:] == o.fill).all()), "written past the end"
+        if whole:
+            want += b.double()
+            inside(p.t, want, (dot + BF16 * want.abs()) * (1 + BF16), "pre")
+            value = want * torch.sigmoid(want) + r.double()
+            tol = 1.13 * dot + 2.0 ** -19 * (1 + want.abs()) + BF16 * value.abs() + 2 * F32 * r.double().abs()
+            inside(y.t, value, tol * (1 + BF16), "y")
+        else:
+            inside(y.t, want, dot + 2 * F32 * want.abs(), "y")
