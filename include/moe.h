@@ -454,12 +454,12 @@ moe_status_t moe_linear(const moe_linear_t* linear, const void* x, const void* w
  *   dy       [M, N] y_dtype;  pre [M, N] dtype as written by moe_linear, required
  *            unless act is MOE_ACT_NONE (then ignored); the residual's gradient
  *            is dy itself
- * dpre is rounded to dtype for the two products (their matrix-core operand), which
- * accumulate in fp32, in an order that depends on the sizes, the element's place, the
- * device's number of CUs and which outputs are asked for, and is the same from call
- * to call.  relu'(0) = 0.  Outputs overlap no input and are
- * fully written, with M = 0 too (dw and dbias are then zero).  At least one output
- * must be given where M > 0. */
+ * dpre is rounded to dtype for the two products, their matrix-core operand (an fp32 dy
+ * of bf16 operands too; MOE_F32 operands keep it whole).  They accumulate in fp32, in
+ * an order that depends on the sizes, the element's place, the device's number of CUs
+ * and which outputs are asked for, and is the same from call to call.  relu'(0) = 0.
+ * Outputs overlap no input and are fully written, with M = 0 too (dw and dbias are
+ * then zero).  At least one output must be given where M > 0. */
 moe_status_t moe_linear_backward(const moe_linear_t* linear, const void* dy, const void* pre,
                                  const void* x, const void* w, void* dx, void* dw, float* dbias,
                                  void* workspace, size_t workspace_bytes, void* stream);

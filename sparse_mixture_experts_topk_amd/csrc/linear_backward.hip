@@ -32,8 +32,13 @@ int prep_rows(const moe_linear_t& l) {
 
 // dpre = dy act'(pre) in the operands' type (unless NULL), and the column sums of
 // its fp32 values over the workgroup's rows into part[chunk][N] (unless NULL).
-// F32: dy is fp32; OP32: the operands are (pre and dpre too).  HBM-bound: reads dy
-// and pre, writes dpre, once each (8192 x 14336, bf16: 140 us, 5.0 TB/s).
+// F32: dy is fp32; OP32: the operands are (pre and dpre too).  With bf16 operands
+// dpre is rounded to bf16, for the matrix cores take both operands in one type: dx and
+// dw are then 2.34e-3 of their size from the exact ones, where their own rounding
+// alone makes 1.66e-3.  The low half of dpre as a second operand would take that away
+// and double the terms of both products (they are 1420 of 1600 us at 8192 x 14336 x
+// 4096); fp32 operands keep all of it.  HBM-bound: reads dy and pre, writes dpre, once
+// each (8192 x 14336, bf16: 140 us, 5.0 TB/s).
 template <bool F32, bool ACT, bool OP32>
 __global__ __launch_bounds__(256) void dpre_kernel(const void* __restrict__ dy, const void* __restrict__ pre,
                                                    int act, int M, int N, int col_blocks, int rows,
