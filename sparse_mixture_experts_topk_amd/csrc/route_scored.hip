@@ -340,9 +340,9 @@ __device__ __forceinline__ void load_logits(const float* p, const bool (&in)[PER
   for (int q = 0; q < PER; ++q) l[q] = usable(l[q]);
 }
 
-// Bound by instruction issue: 480 vector instructions per token, 20 of them in each
+// Bound by instruction issue: 495 vector instructions per token, 20 of them in each
 // of the k + 1 selection rounds (16384 tokens of 256 experts, sigmoid, 4 of 8
-// groups, top 8, MI355X: 16.0 us; its 17.8 MB need 3.6).
+// groups, top 8, MI355X: 15.4-16.6 us; its 17.8 MB need 3.6).
 template <int PER, bool SOFTMAX, bool BIAS, bool GROUPED>
 __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_kernel(const RouteArgs a) {
   const int lane = threadIdx.x & 63;
@@ -429,7 +429,7 @@ struct RouteBackArgs {
 // The differences g_j - g_i are taken before they are weighted: they hold
 // where the g are near each other.  1 - sigmoid(l) is sigmoid(-l).
 // HBM-bound: reads 4 E bytes (8 E with D) and writes 4 E per token (16384 x 256,
-// sigmoid, MI355X: 9.4 us, 3.7 TB/s).
+// sigmoid, MI355X: 9.7 us, 3.6 TB/s).
 template <int PER>
 __global__ __launch_bounds__(kRouteWaves * kWave) void route_scored_backward_kernel(const RouteBackArgs a) {
   __shared__ __attribute__((aligned(16))) float at_chosen[kRouteWaves][kWave * PER];
