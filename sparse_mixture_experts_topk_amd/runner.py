@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import dataclasses
+import functools
 from typing import Optional
 
 import torch
@@ -104,6 +105,19 @@ def _on(stream, device):
                              else torch.cuda.ExternalStream(int(stream), device=device))
 
 
+def _on_its_device(f):
+    """The calls of a sequence go to the device that its inputs are on, whichever is current."""
+    @functools.wraps(f)
+    def run(di, *args, **kw):
+        dev = di.x.device
+        if dev.index is None or dev.index == torch.cuda.current_device():
+            return f(di, *args, **kw)
+        with torch.cuda.device(dev):
+            return f(di, *args, **kw)
+    return run
+
+
+@_on_its_device
 def scored_routing(di: DeviceInputs, router, balance_bias=None, stream=None, out: Optional[dict] = None,
                    scores: bool = False) -> dict:
     """logits = x . w_gate^T (+ router_bias) in fp32, then moe_route_scored: the buffers of both
@@ -131,6 +145,7 @@ def scored_routing(di: DeviceInputs, router, balance_bias=None, stream=None, out
     return o
 
 
+@_on_its_device
 def gate_backward(di: DeviceInputs, st: dict, router, dy: torch.Tensor, dscores=None, stream=None) -> dict:
     """Gradients of the gate from the gradient ``dy`` at y: ``st`` is the result of ``staged`` with
     the same router.  dy_perm is the gradient at the experts' rows, for the caller's own backward pass
@@ -164,6 +179,7 @@ def gate_backward(di: DeviceInputs, st: dict, router, dy: torch.Tensor, dscores=
     return o
 
 
+@_on_its_device
 def forward(di: DeviceInputs, buf: Optional[ForwardBuffers] = None, stream=None, router=None,
             balance_bias=None) -> ForwardBuffers:
     cfg = di.cfg
@@ -183,6 +199,7 @@ def forward(di: DeviceInputs, buf: Optional[ForwardBuffers] = None, stream=None,
     return buf
 
 
+@_on_its_device
 def staged(di: DeviceInputs, stream=None, router=None, balance_bias=None) -> dict:
     """The five boundary calls in sequence (with a router: scored_routing in place of
     moe_route_topk); returns every intermediate buffer."""

@@ -6,8 +6,11 @@ import inspect
 import math
 import pathlib
 import re
+import types
 
 import numpy as np
+import pytest
+import torch
 
 import sparse_mixture_experts_topk_amd as moe
 from sparse_mixture_experts_topk_amd import _lib, runner
@@ -90,3 +93,27 @@ def test_gelu_tail_polynomial_is_as_near_as_its_comment_says():
         q = q * t + np.float64(np.float32(c))
     err = np.abs(q * t / want - 1.0).max()
     assert 0.9 * bound < err < bound, err
+
+
+@pytest.mark.parametrize("name", ["scored_routing", "gate_backward", "forward", "staged"])
+def test_sequences_run_on_their_inputs_device(name, monkeypatch):
+    """With another device current, the calls (some take the current device's stream) are made on the inputs' one."""
+    entered = []
+
+    class Entered:
+        def __init__(self, device):
+            self.device = torch.device(device)
+
+        def __enter__(self):
+            entered.append(self.device.index)
+            raise InterruptedError                     # nothing of the sequence itself runs here
+
+        def __exit__(self, *exc):
+            return False
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Entered)
+    di = types.SimpleNamespace(x=types.SimpleNamespace(device=torch.device("cuda", 1)))
+    with pytest.raises(InterruptedError):
+        getattr(runner, name)(di)
+    assert entered == [1]
