@@ -136,7 +136,9 @@ typedef struct {
 typedef enum { MOE_CALL_PERMUTE = 0, MOE_CALL_GATE_UP = 1, MOE_CALL_DOWN = 2,
                MOE_CALL_FORWARD = 3, MOE_CALL_ROUTE = 4,
                /* of moe_linear_workspace_bytes only */
-               MOE_CALL_LINEAR = 5, MOE_CALL_LINEAR_BACKWARD = 6 } moe_call_t;
+               MOE_CALL_LINEAR = 5, MOE_CALL_LINEAR_BACKWARD = 6,
+               /* of moe_ffn_workspace_bytes only */
+               MOE_CALL_FFN_GATE_UP = 7, MOE_CALL_FFN_BACKWARD = 8 } moe_call_t;
 
 /* Human-readable name of a status.  Never NULL. */
 const char* moe_status_string(moe_status_t status);
@@ -463,6 +465,101 @@ moe_status_t moe_linear(const moe_linear_t* linear, const void* x, const void* w
 moe_status_t moe_linear_backward(const moe_linear_t* linear, const void* dy, const void* pre,
                                  const void* x, const void* w, void* dx, void* dw, float* dbias,
                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- gated feed-forward block, dense or grouped by expert, and its gradients ----
+ *   g = x . w1[e]^T,  u = x . w3[e]^T,  h = act(g) * u,  y = h . w2[e]^T
+ * for the rows of group e.  Pages: "Mixtral" study notes, MixtralExpert.forward and
+ * "SwiGLU Experts".  The training form of moe_expert_gemm_gate_up (which keeps nothing
+ * and has silu only) and the gated block of a dense layer or shared expert. */
+typedef struct {
+  int32_t M;        /* rows of the row buffers, 0..2^24 */
+  int32_t d_model;  /* channels of x, y: a multiple of 8, at most 2^18 */
+  int32_t d_ff;     /* channels of g, u, h: a multiple of 8, at most 2^18 */
+  int32_t groups;   /* experts, the shared one included: 1..257 */
+  int32_t dtype;    /* every tensor: MOE_BF16 or MOE_F32 */
+  int32_t act;      /* moe_act_t */
+} moe_ffn_t;
+/* No buffer has more than 2^36 elements (M d_model, M d_ff, groups d_model d_ff;
+ * MOE_ERR_UNSUPPORTED).
+ *
+ * offsets [groups + 1] int32 (device), as expert_offsets of moe_permute: group e has the
+ * rows offsets[e] .. offsets[e + 1] - 1.  NULL with one group: all M rows.  Groups may be
+ * empty.  Rows of no group are not read, and left as they were in every output.
+ * (Offsets below 0, above M or descending are read as the nearest that are not.) */
+
+/* Bytes of device workspace moe_ffn_gate_up (MOE_CALL_FFN_GATE_UP) or moe_ffn_backward
+ * (MOE_CALL_FFN_BACKWARD) needs; 0 is possible (a NULL workspace is accepted then).  Two
+ * calls that share a workspace must not run concurrently. */
+moe_status_t moe_ffn_workspace_bytes(const moe_ffn_t* ffn, moe_call_t call, size_t* bytes);
+
+/*   x        [M, d_model];  w1, w3 [groups, d_ff, d_model]
+ *   h        [M, d_ff] out
+ *   pre1, pre3 [M, d_ff] out, both or neither NULL: g and u, kept for the backward pass
+ * fp32 accumulation; h from the unrounded g and u, one rounding.  Outputs overlap no
+ * input.  The order of an element's sum depends on M, the widths, the offsets, the element's place
+ * and the device's number of CUs, and is the same from call to call. */
+moe_status_t moe_ffn_gate_up(const moe_ffn_t* ffn, const void* x, const int32_t* offsets, const void* w1,
+                             const void* w3, void* h, void* pre1, void* pre3, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Gradients of y = h . w2[e]^T, h = moe_ffn_gate_up(x).  With dh = dy . w2[e] (fp32),
+ * dg = dh * u * act'(g), du = dh * act(g), g and u as kept:
+ *   dx       [M, d_model] out or NULL:  dg . w1[e] + du . w3[e]  (needs w1, w3)
+ *   dw1, dw3 [groups, d_ff, d_model] out, both or neither NULL:  dg^T . x, du^T . x over the
+ *            group's rows  (needs x)
+ *   dw2      [groups, d_model, d_ff] out or NULL:  dy^T . h  (needs h)
+ *   dy       [M, d_model]
+ *   pre1, pre3 [M, d_ff] as written by moe_ffn_gate_up, w2 [groups, d_model, d_ff]:
+ *            required for dx, dw1 and dw3
+ * dg and du are rounded to dtype for the products, their matrix-core operands (MOE_F32:
+ * kept whole); sums in fp32, in an order that is the same from call to call.  relu'(0) =
+ * 0.  Weight gradients are fully written, zero for a group without rows (M = 0 too).
+ * Outputs overlap no input.  At least one output must be given where M > 0. */
+moe_status_t moe_ffn_backward(const moe_ffn_t* ffn, const void* dy, const int32_t* offsets, const void* x,
+                              const void* pre1, const void* pre3, const void* h, const void* w1,
+                              const void* w3, const void* w2, void* dx, void* dw1, void* dw3, void* dw2,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of moe_permute's x_perm at x.  Uses T, d_model, top_k, n_shared and act_dtype
+ * of the (valid) shape.
+ *   dx_perm      [R, d] act dtype: gradient at x_perm
+ *   slot_to_row  [R] as written by moe_permute
+ *   addend       [T, d] act dtype or NULL: gradient that reaches x elsewhere (the router's)
+ *   dx           [T, d] act dtype out: addend[t] + the sum over kept slots of
+ *                dx_perm[slot_to_row[t*k+s]] (+ dx_perm[slot_to_row[T*k+t]] with a shared
+ *                expert), in fp32 in that order, rounded once; may be the addend's memory,
+ *                else overlaps no input
+ * No workspace. */
+moe_status_t moe_permute_backward(const moe_shape_t* shape, const void* dx_perm, const int32_t* slot_to_row,
+                                  const void* addend, void* dx, void* stream);
+
+/* ---- norm of a list of gradients, and clipping ---- */
+typedef struct {
+  void* data;       /* device; aligned to its elements (no more), NULL with n = 0 */
+  int64_t n;        /* elements, 0..2^40 */
+  int32_t dtype;    /* MOE_BF16 or MOE_F32 */
+} moe_tensor_t;
+
+/* Bytes of device workspace moe_grad_norm needs for the list. */
+moe_status_t moe_grad_norm_workspace_bytes(const moe_tensor_t* tensors, int32_t count, size_t* bytes);
+
+/*   tensors      host array of `count` (0..2^16) tensors; read before the call returns
+ *   sum_squares  [1] fp64 out: the sum of the squares of all elements, in fp64, in an
+ *                order that depends on the list's sizes and alignments alone.  (Ranks that
+ *                hold parts of a model add theirs before moe_grad_clip.)
+ *   norm         [1] fp32 out or NULL: its square root
+ * An infinite or NaN element makes both so. */
+moe_status_t moe_grad_norm(const moe_tensor_t* tensors, int32_t count, double* sum_squares, float* norm,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scales the list to a norm of at most max_norm: out = in * min(1, max_norm / sqrt(*sum_squares)),
+ * one rounding.  A sum that is not finite scales nothing: the caller sees it in the norm.
+ *   tensors, outs  host arrays of `count` tensors each; outs[i] has tensors[i]'s n and dtype
+ *                and may be its memory.  outs NULL: in place.  Nothing else may overlap an
+ *                output (MOE_ERR_INVALID_ARG).
+ *   sum_squares  [1] fp64 (device), read by the kernel;  max_norm >= 0 */
+moe_status_t moe_grad_clip(const moe_tensor_t* tensors, const moe_tensor_t* outs, int32_t count,
+                           const double* sum_squares, float max_norm, void* stream);
 
 #ifdef __cplusplus
 }

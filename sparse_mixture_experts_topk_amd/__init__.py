@@ -19,7 +19,7 @@ from ._lib import (MOE_BF16, MOE_CALL_DOWN, MOE_CALL_FORWARD, MOE_CALL_GATE_UP,
                    MOE_NOALLOC_SCRATCH_BYTES, MOE_OVERFLOW_DROP, MOE_OVERFLOW_NEXT_BEST, MoeShape,
                    MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU,
                    MOE_CALL_LINEAR, MOE_CALL_LINEAR_BACKWARD, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
-                   MoeLinear, MoeRouter)
+                   MOE_CALL_FFN_BACKWARD, MOE_CALL_FFN_GATE_UP, MoeFfn, MoeLinear, MoeRouter, MoeTensor)
 
 __all__ = ["MoEError", "MoeShape", "make_shape", "moe_status_string", "moe_version",
            "moe_workspace_bytes", "moe_route_topk", "moe_permute", "moe_expert_gemm_gate_up",
@@ -29,7 +29,10 @@ __all__ = ["MoEError", "MoeShape", "make_shape", "moe_status_string", "moe_versi
            "MOE_CALL_DOWN", "MOE_CALL_FORWARD", "MOE_CALL_ROUTE", "MOE_OVERFLOW_DROP", "MOE_OVERFLOW_NEXT_BEST",
            "MoeRouter", "MoeLinear", "make_router", "make_linear", "moe_route_scored",
            "moe_route_scored_backward", "moe_combine_backward", "moe_forward_routed", "moe_linear",
-           "moe_linear_backward", "moe_linear_workspace_bytes", "MOE_CALL_LINEAR",
+           "moe_linear_backward", "moe_linear_workspace_bytes", "MoeFfn", "make_ffn", "moe_ffn_workspace_bytes",
+           "moe_ffn_gate_up", "moe_ffn_backward", "moe_permute_backward", "MoeTensors", "make_tensors",
+           "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_grad_clip", "MOE_CALL_FFN_GATE_UP",
+           "MOE_CALL_FFN_BACKWARD", "MOE_CALL_LINEAR",
            "MOE_CALL_LINEAR_BACKWARD", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_ACT_NONE",
            "MOE_ACT_RELU", "MOE_ACT_SILU", "MOE_ACT_GELU", "MOE_ACT_GELU_TANH"]
 
@@ -317,3 +320,96 @@ def moe_forward_routed(shape, x, topk_ids, topk_weights, next_ids, w1, w3, w2, w
          _ptr(fn, "w2_scale", w2_scale, st, n_down, d), _ptr(fn, "y", y, dt, T * dm, d),
          _ptr(fn, "expert_counts_out", expert_counts_out, i32, G, d),
          _ptr(fn, "drop_mask_out", drop_mask_out, torch.uint8, T * k, d), *_workspace(fn, workspace, d))
+
+
+# ---- gated feed-forward block and its gradients, gradient norm and clipping ----
+
+def make_ffn(M: int, d_model: int, d_ff: int, groups: int = 1, dtype="bf16", act="silu") -> MoeFfn:
+    return MoeFfn(M, d_model, d_ff, groups, _DT.get(dtype, dtype), _ACT.get(act, act))
+
+
+def moe_ffn_workspace_bytes(ffn: MoeFfn, call: int = MOE_CALL_FFN_GATE_UP) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_ffn_workspace_bytes", _lib.load().moe_ffn_workspace_bytes(ctypes.byref(ffn), call, ctypes.byref(n)))
+    return n.value
+
+
+def moe_ffn_gate_up(ffn, x, offsets, w1, w3, h, pre1=None, pre3=None, workspace=None, stream=None):
+    fn = "moe_ffn_gate_up"
+    dt, d = _TORCH.get(ffn.dtype), _device(x, w1, h)
+    n_x, n_h, n_w = ffn.M * ffn.d_model, ffn.M * ffn.d_ff, ffn.groups * ffn.d_model * ffn.d_ff
+    _run(fn, d, stream, ctypes.byref(ffn), _ptr(fn, "x", x, dt, n_x, d),
+         _ptr(fn, "offsets", offsets, torch.int32, ffn.groups + 1, d), _ptr(fn, "w1", w1, dt, n_w, d),
+         _ptr(fn, "w3", w3, dt, n_w, d), _ptr(fn, "h", h, dt, n_h, d), _ptr(fn, "pre1", pre1, dt, n_h, d),
+         _ptr(fn, "pre3", pre3, dt, n_h, d), *_workspace(fn, workspace, d))
+
+
+def moe_ffn_backward(ffn, dy, offsets, x, pre1, pre3, h, w1, w3, w2, dx, dw1, dw3, dw2, workspace=None, stream=None):
+    fn = "moe_ffn_backward"
+    dt, d = _TORCH.get(ffn.dtype), _device(dy, dx, dw1, dw2)
+    n_x, n_h, n_w = ffn.M * ffn.d_model, ffn.M * ffn.d_ff, ffn.groups * ffn.d_model * ffn.d_ff
+    _run(fn, d, stream, ctypes.byref(ffn), _ptr(fn, "dy", dy, dt, n_x, d),
+         _ptr(fn, "offsets", offsets, torch.int32, ffn.groups + 1, d), _ptr(fn, "x", x, dt, n_x, d),
+         _ptr(fn, "pre1", pre1, dt, n_h, d), _ptr(fn, "pre3", pre3, dt, n_h, d), _ptr(fn, "h", h, dt, n_h, d),
+         _ptr(fn, "w1", w1, dt, n_w, d), _ptr(fn, "w3", w3, dt, n_w, d), _ptr(fn, "w2", w2, dt, n_w, d),
+         _ptr(fn, "dx", dx, dt, n_x, d), _ptr(fn, "dw1", dw1, dt, n_w, d), _ptr(fn, "dw3", dw3, dt, n_w, d),
+         _ptr(fn, "dw2", dw2, dt, n_w, d), *_workspace(fn, workspace, d))
+
+
+def moe_permute_backward(shape, dx_perm, slot_to_row, addend, dx, stream=None):
+    fn = "moe_permute_backward"
+    R = shape.T * (shape.top_k + shape.n_shared)
+    dt, dm, d = _TORCH.get(shape.act_dtype), shape.d_model, _device(dx_perm, slot_to_row, dx)
+    _run(fn, d, stream, ctypes.byref(shape), _ptr(fn, "dx_perm", dx_perm, dt, R * dm, d),
+         _ptr(fn, "slot_to_row", slot_to_row, torch.int32, R, d), _ptr(fn, "addend", addend, dt, shape.T * dm, d),
+         _ptr(fn, "dx", dx, dt, shape.T * dm, d))
+
+
+class MoeTensors:
+    """A list of tensors (fp32 or bf16, contiguous, on one device) for moe_grad_norm and moe_grad_clip, and
+    their descriptors; it keeps the tensors alive."""
+    _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.device = _device(*self.tensors)
+        self.array = (MoeTensor * max(1, len(self.tensors)))()
+        for i, t in enumerate(self.tensors):
+            code = self._CODES.get(t.dtype)
+            if code is None:
+                raise ValueError(f"make_tensors: tensor {i} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+            self.array[i] = (_ptr("make_tensors", f"tensor {i}", t, t.dtype, 0, self.device) or None, t.numel(), code)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def make_tensors(tensors) -> MoeTensors:
+    return tensors if isinstance(tensors, MoeTensors) else MoeTensors(tensors)
+
+
+def moe_grad_norm_workspace_bytes(tensors) -> int:
+    t, n = make_tensors(tensors), ctypes.c_size_t(0)
+    _check("moe_grad_norm_workspace_bytes",
+           _lib.load().moe_grad_norm_workspace_bytes(t.array, len(t), ctypes.byref(n)))
+    return n.value
+
+
+def moe_grad_norm(tensors, sum_squares, norm=None, workspace=None, stream=None):
+    fn, t = "moe_grad_norm", make_tensors(tensors)
+    d = t.device if t.device is not None else _device(sum_squares)
+    _run(fn, d, stream, t.array, len(t), _ptr(fn, "sum_squares", sum_squares, torch.float64, 1, d),
+         _ptr(fn, "norm", norm, torch.float32, 1, d), *_workspace(fn, workspace, d))
+
+
+def moe_grad_clip(tensors, outs, sum_squares, max_norm: float, stream=None):
+    """In place where ``outs`` is None."""
+    fn, t = "moe_grad_clip", make_tensors(tensors)
+    o = None if outs is None else make_tensors(outs)
+    if o is not None and len(o) != len(t):
+        raise ValueError(f"{fn}: {len(t)} tensors, {len(o)} outputs")
+    d = t.device if t.device is not None else _device(sum_squares)
+    if o is not None and o.device not in (None, d):
+        raise ValueError(f"{fn}: the outputs are on device {o.device}, the tensors on device {d}")
+    _run(fn, d, stream, t.array, None if o is None else o.array, len(t),
+         _ptr(fn, "sum_squares", sum_squares, torch.float64, 1, d), max_norm)

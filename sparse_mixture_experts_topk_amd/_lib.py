@@ -12,6 +12,7 @@ MOE_DROPLESS = -1
 MOE_OVERFLOW_DROP, MOE_OVERFLOW_NEXT_BEST = 0, 1
 MOE_CALL_PERMUTE, MOE_CALL_GATE_UP, MOE_CALL_DOWN, MOE_CALL_FORWARD, MOE_CALL_ROUTE = range(5)
 MOE_CALL_LINEAR, MOE_CALL_LINEAR_BACKWARD = 5, 6
+MOE_CALL_FFN_GATE_UP, MOE_CALL_FFN_BACKWARD = 7, 8
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -21,7 +22,9 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_workspace_bytes", "moe_route
            "moe_permute", "moe_expert_gemm_gate_up", "moe_expert_gemm_down", "moe_combine",
            "moe_forward", "moe_forward_noalloc", "moe_forward_routed", "moe_route_scored",
            "moe_route_scored_backward", "moe_combine_backward", "moe_linear_workspace_bytes",
-           "moe_linear", "moe_linear_backward")
+           "moe_linear", "moe_linear_backward", "moe_ffn_workspace_bytes", "moe_ffn_gate_up",
+           "moe_ffn_backward", "moe_permute_backward", "moe_grad_norm_workspace_bytes", "moe_grad_norm",
+           "moe_grad_clip")
 
 
 class MoeShape(ctypes.Structure):
@@ -43,12 +46,22 @@ class MoeLinear(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
+class MoeFfn(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("d_model", ctypes.c_int32), ("d_ff", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 SZ = ctypes.c_size_t
 SHAPE = ctypes.POINTER(MoeShape)
 ROUTER = ctypes.POINTER(MoeRouter)
 LINEAR = ctypes.POINTER(MoeLinear)
+FFN = ctypes.POINTER(MoeFfn)
 
 _SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [I32]),
@@ -68,6 +81,14 @@ _SIGNATURES = {
     "moe_linear_workspace_bytes": (I32, [LINEAR, I32, ctypes.POINTER(SZ)]),
     "moe_linear": (I32, [LINEAR, P, P, P, P, P, P, P, SZ, P]),
     "moe_linear_backward": (I32, [LINEAR, P, P, P, P, P, P, P, P, SZ, P]),
+    "moe_ffn_workspace_bytes": (I32, [FFN, I32, ctypes.POINTER(SZ)]),
+    "moe_ffn_gate_up": (I32, [FFN, P, P, P, P, P, P, P, P, SZ, P]),
+    "moe_ffn_backward": (I32, [FFN, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+    "moe_permute_backward": (I32, [SHAPE, P, P, P, P, P]),
+    # lists of MoeTensor: arrays of them
+    "moe_grad_norm_workspace_bytes": (I32, [P, I32, ctypes.POINTER(SZ)]),
+    "moe_grad_norm": (I32, [P, I32, P, P, P, SZ, P]),
+    "moe_grad_clip": (I32, [P, P, I32, P, ctypes.c_float, P]),
 }
 
 _lib = None

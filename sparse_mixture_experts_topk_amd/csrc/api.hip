@@ -2,10 +2,12 @@
 // Every public function validates on the host before enqueueing anything.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <new>
 
 #include "../../include/moe.h"
 #include "launch.hpp"
@@ -209,6 +211,61 @@ moe_status_t validate_linear(const moe_linear_t* l) {
   if (l->N % 8 != 0 || l->K % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if (l->N > moe::kMaxLinearWidth || l->K > moe::kMaxLinearWidth) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
+}
+
+moe_status_t validate_ffn(const moe_ffn_t* f) {
+  if (f == nullptr) return MOE_ERR_INVALID_ARG;
+  if (f->M < 0 || f->M > (1 << 24) || f->d_model <= 0 || f->d_ff <= 0 || f->groups <= 0) return MOE_ERR_INVALID_ARG;
+  if (f->dtype < MOE_F32 || f->dtype > MOE_MXFP4) return MOE_ERR_INVALID_ARG;
+  if (f->act < MOE_ACT_NONE || f->act > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+  if (f->dtype != MOE_BF16 && f->dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (f->groups > moe::kMaxExpertGroups || f->d_model % 8 != 0 || f->d_ff % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (f->d_model > moe::kMaxLinearWidth || f->d_ff > moe::kMaxLinearWidth) return MOE_ERR_UNSUPPORTED;
+  const int64_t most = (int64_t)1 << 36, d = f->d_model, ff = f->d_ff;      // elements: launch grids
+  if (f->M * d > most || f->M * ff > most || f->groups * d * ff > most) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Lists: host arrays, whose entries are looked at.
+moe_status_t validate_tensors(const moe_tensor_t* t, int32_t count) {
+  if (count < 0 || count > (1 << 16) || (count > 0 && t == nullptr)) return MOE_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < count; ++i) {
+    if (t[i].n < 0 || t[i].n > ((int64_t)1 << 40)) return MOE_ERR_INVALID_ARG;
+    if (t[i].dtype < MOE_F32 || t[i].dtype > MOE_MXFP4) return MOE_ERR_INVALID_ARG;
+    if (t[i].dtype != MOE_F32 && t[i].dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (t[i].n > 0 && (t[i].data == nullptr || reinterpret_cast<uintptr_t>(t[i].data) % act_bytes(t[i].dtype) != 0))
+      return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+struct Range {
+  uintptr_t begin, end;
+  bool out;
+};
+
+// Whether an output overlaps anything but its own input (which it then is exactly).
+moe_status_t check_overlap(const moe_tensor_t* in, const moe_tensor_t* out, int32_t count) {
+  Range* r = new (std::nothrow) Range[2 * (size_t)count + 1];
+  if (r == nullptr) return MOE_ERR_INVALID_ARG;
+  size_t n = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (in[i].n == 0) continue;
+    const uintptr_t bytes = (uintptr_t)in[i].n * act_bytes(in[i].dtype);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in[i].data), b = reinterpret_cast<uintptr_t>(out[i].data);
+    r[n++] = {b, b + bytes, true};
+    if (a != b) r[n++] = {a, a + bytes, false};
+  }
+  std::sort(r, r + n, [](const Range& x, const Range& y) { return x.begin < y.begin; });
+  uintptr_t any = 0, outs = 0;           // ends so far
+  bool bad = false;
+  for (size_t i = 0; i < n && !bad; ++i) {
+    bad = r[i].begin < (r[i].out ? any : outs);
+    any = std::max(any, r[i].end);
+    if (r[i].out) outs = std::max(outs, r[i].end);
+  }
+  delete[] r;
+  return bad ? MOE_ERR_INVALID_ARG : MOE_OK;
 }
 
 template <typename T>
@@ -601,6 +658,105 @@ moe_status_t moe_linear_backward(const moe_linear_t* l, const void* dy, const vo
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
     return MOE_ERR_WORKSPACE;
   return from_hip(moe::launch_linear_backward(*l, dy, pre, x, w, dx, dw, dbias, need > 0 ? workspace : nullptr, st));
+}
+
+moe_status_t moe_ffn_workspace_bytes(const moe_ffn_t* f, moe_call_t call, size_t* bytes) {
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  moe_status_t v = validate_ffn(f);
+  if (v != MOE_OK) return v;
+  if (call != MOE_CALL_FFN_GATE_UP && call != MOE_CALL_FFN_BACKWARD) return MOE_ERR_INVALID_ARG;
+  *bytes = f->M == 0 ? 0
+           : call == MOE_CALL_FFN_GATE_UP ? moe::ffn_gate_up_workspace_bytes(*f)
+                                          : moe::ffn_backward_workspace_bytes(*f);
+  return MOE_OK;
+}
+
+moe_status_t moe_ffn_gate_up(const moe_ffn_t* f, const void* x, const int32_t* offsets, const void* w1,
+                             const void* w3, void* h, void* pre1, void* pre3, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  moe_status_t v = validate_ffn(f);
+  if (v != MOE_OK) return v;
+  if (f->M == 0) return MOE_OK;
+  if ((v = check_ptrs({x, w1, w3, h}, {offsets, pre1, pre3})) != MOE_OK) return v;
+  if ((pre1 == nullptr) != (pre3 == nullptr) || (offsets == nullptr && f->groups > 1)) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::ffn_gate_up_workspace_bytes(*f);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
+    return MOE_ERR_WORKSPACE;
+  return from_hip(moe::launch_ffn_gate_up(*f, x, offsets, w1, w3, h, pre1, pre3, need > 0 ? workspace : nullptr,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_ffn_backward(const moe_ffn_t* f, const void* dy, const int32_t* offsets, const void* x,
+                              const void* pre1, const void* pre3, const void* h, const void* w1,
+                              const void* w3, const void* w2, void* dx, void* dw1, void* dw3, void* dw2,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  moe_status_t v = validate_ffn(f);
+  if (v != MOE_OK) return v;
+  if ((dw1 == nullptr) != (dw3 == nullptr)) return MOE_ERR_INVALID_ARG;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (f->M == 0) {   // the sums over no rows; dx has no element (and may have no address)
+    if ((v = check_ptrs({}, {dw1, dw3, dw2})) != MOE_OK) return v;
+    const int64_t bytes = (int64_t)f->groups * f->d_model * f->d_ff * act_bytes(f->dtype);
+    hipError_t e = hipSuccess;
+    for (void* p : {dw1, dw3, dw2})
+      if (e == hipSuccess && p != nullptr) e = launch_fill_u8(static_cast<uint8_t*>(p), bytes, 0, st);
+    return from_hip(e);
+  }
+  if (dx == nullptr && dw1 == nullptr && dw2 == nullptr) return MOE_ERR_INVALID_ARG;
+  if ((v = check_ptrs({dy}, {offsets, x, pre1, pre3, h, w1, w3, w2, dx, dw1, dw3, dw2})) != MOE_OK) return v;
+  if (offsets == nullptr && f->groups > 1) return MOE_ERR_INVALID_ARG;
+  if ((dx != nullptr || dw1 != nullptr) && (pre1 == nullptr || pre3 == nullptr || w2 == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if ((dx != nullptr && (w1 == nullptr || w3 == nullptr)) || (dw1 != nullptr && x == nullptr) ||
+      (dw2 != nullptr && h == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::ffn_backward_workspace_bytes(*f);
+  if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
+  return from_hip(moe::launch_ffn_backward(*f, dy, offsets, x, pre1, pre3, h, w1, w3, w2, dx, dw1, dw3, dw2,
+                                           workspace, st));
+}
+
+moe_status_t moe_permute_backward(const moe_shape_t* s, const void* dx_perm, const int32_t* slot_to_row,
+                                  const void* addend, void* dx, void* stream) {
+  moe_status_t v = validate_shape(s);
+  if (v != MOE_OK) return v;
+  if (s->T == 0) return MOE_OK;
+  if ((v = check_ptrs({dx_perm, slot_to_row, dx}, {addend})) != MOE_OK) return v;
+  return from_hip(moe::launch_permute_backward(*s, dx_perm, slot_to_row, addend, dx, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_grad_norm_workspace_bytes(const moe_tensor_t* tensors, int32_t count, size_t* bytes) {
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  moe_status_t v = validate_tensors(tensors, count);
+  if (v != MOE_OK) return v;
+  *bytes = moe::grad_norm_workspace_bytes(tensors, count);
+  return MOE_OK;
+}
+
+moe_status_t moe_grad_norm(const moe_tensor_t* tensors, int32_t count, double* sum_squares, float* norm,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  moe_status_t v = validate_tensors(tensors, count);
+  if (v != MOE_OK) return v;
+  if ((v = check_ptrs({sum_squares}, {norm})) != MOE_OK) return v;
+  const size_t need = moe::grad_norm_workspace_bytes(tensors, count);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
+    return MOE_ERR_WORKSPACE;
+  return from_hip(moe::launch_grad_norm(tensors, count, sum_squares, norm, workspace, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_grad_clip(const moe_tensor_t* tensors, const moe_tensor_t* outs, int32_t count,
+                           const double* sum_squares, float max_norm, void* stream) {
+  moe_status_t v = validate_tensors(tensors, count);
+  if (v != MOE_OK) return v;
+  if (!(max_norm >= 0)) return MOE_ERR_INVALID_ARG;
+  if (outs != nullptr) {
+    if ((v = validate_tensors(outs, count)) != MOE_OK) return v;
+    for (int32_t i = 0; i < count; ++i)
+      if (outs[i].n != tensors[i].n || outs[i].dtype != tensors[i].dtype) return MOE_ERR_INVALID_ARG;
+  }
+  if ((v = check_ptrs({sum_squares}, {})) != MOE_OK) return v;
+  if ((v = check_overlap(tensors, outs != nullptr ? outs : tensors, count)) != MOE_OK) return v;
+  return from_hip(moe::launch_grad_clip(tensors, outs, count, sum_squares, max_norm, static_cast<hipStream_t>(stream)));
 }
 
 moe_status_t moe_forward_noalloc(const moe_shape_t* s, const void* x, const void* w_gate,

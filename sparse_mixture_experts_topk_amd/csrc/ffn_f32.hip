@@ -1,0 +1,286 @@
+// Gated feed-forward block and its gradients on the fp32 matrix cores
+// (v_mfma_f32_16x16x4_f32, f32_tiles.hpp): nothing is rounded below fp32.
+//
+// The products are those of FfnKind.  A workgroup of 4 wavefronts (2 x 2) has a tile
+// of 32 B x 32 B of one group, each wavefront B x B blocks of 16 x 16.  kGateUp takes
+// 16 channels of w1 and the same 16 of w3 in turn as column blocks, so that a lane
+// holds g and u of the same elements; kDx walks dg, w1 and then du, w3.
+// Where the tiles leave CUs idle the contraction is cut into runs whose results
+// are summed in order by a second kernel, which has the same lanes and epilogue.
+#include <algorithm>
+
+#include "device_common.hpp"
+#include "f32_tiles.hpp"
+#include "ffn_groups.hpp"
+#include "launch.hpp"
+#include "linear_epilogue.hpp"
+
+namespace moe {
+namespace {
+
+template <class E>
+struct FfnArgsF32 {
+  const E *P0, *P1, *Q0, *Q1;      // P1, Q1: the second half where there are two
+  const int32_t* offsets;
+  int M, groups;
+  int rows, cols, len;             // weight rows (kDw13, kDw2), columns (channels), terms of a half (else)
+  int col_tiles, runs;
+  int64_t group_tiles;             // kDw13, kDw2: tiles per group
+  float* partials;
+  const E *g, *u;                  // kDh: pre-activations
+  E *o0, *o1, *o2;
+  int act;
+};
+
+template <class E, int KIND, int B, bool JOIN>
+__global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32<E> a) {
+  constexpr int T = 32 * B;
+  constexpr bool OVER_ROWS = ffn_over_rows(KIND), PAIR = KIND == kGateUp, TWO = KIND == kDx;
+  constexpr bool PSLOW = OVER_ROWS, QSLOW = KIND != kGateUp, F32 = sizeof(E) == 4;
+  __shared__ __attribute__((aligned(16))) float ps[2][T * kTerms];
+  __shared__ __attribute__((aligned(16))) float qs[2][T * kTerms];
+  __shared__ FfnGroups groups;
+  groups.load(a.offsets, a.groups, a.M, T);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = lane & 15, g = lane >> 4;
+  const int64_t tile = JOIN ? blockIdx.x : blockIdx.x / a.runs;
+  const int run = JOIN ? 0 : blockIdx.x % a.runs;
+
+  // the tile's group, first row and column, rows' end, and the operands there
+  int e, r0, r_end, c0, len = a.len;
+  const E *P0 = a.P0, *P1 = a.P1, *Q0 = a.Q0, *Q1 = a.Q1;
+  E *o0 = a.o0, *o1 = a.o1;
+  int64_t ldp, ldq;
+  if constexpr (OVER_ROWS) {
+    e = (int)(tile / a.group_tiles);
+    int in = (int)(tile % a.group_tiles);
+    if constexpr (KIND == kDw13) {
+      const int half = (int)(a.group_tiles / 2);
+      if (in >= half) {
+        in -= half;
+        P0 = P1;
+        o0 = o1;
+      }
+    }
+    r0 = in / a.col_tiles * T;
+    c0 = in % a.col_tiles * T;
+    r_end = a.rows;
+    ldp = a.rows;
+    ldq = a.cols;
+    const int64_t first = groups.off[e];
+    len = groups.off[e + 1] - groups.off[e];
+    P0 += first * ldp;
+    Q0 += first * ldq;
+    o0 += (int64_t)e * a.rows * a.cols;
+  } else {
+    const int t = (int)(tile / a.col_tiles);
+    if (t >= groups.pre[a.groups]) return;                   // the whole workgroup
+    int lo = 0, hi = a.groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (groups.pre[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    e = lo;
+    r0 = groups.off[e] + (t - groups.pre[e]) * T;
+    r_end = groups.off[e + 1];
+    c0 = (int)(tile % a.col_tiles) * (PAIR ? T / 2 : T);     // kGateUp: channels
+    ldp = a.len;
+    ldq = PAIR ? a.len : a.cols;
+    const int64_t w = (int64_t)e * a.cols * a.len;
+    Q0 += w;
+    if constexpr (PAIR || TWO) Q1 += w;
+  }
+
+  const int wr = (wave >> 1) * 16 * B, wc = (wave & 1) * 16 * B;
+  f32x4_t acc[B][B];
+#pragma unroll
+  for (int x = 0; x < B; ++x)
+#pragma unroll
+    for (int y = 0; y < B; ++y) acc[x][y] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto partial = [&](int64_t r, int x, int y) __attribute__((always_inline)) {
+    return a.partials + (((tile * a.runs + r) * 4 + wave) * (B * B) + x * B + y) * 256 + lane * 4;
+  };
+
+  if constexpr (!JOIN) {
+    const int half_slices = (len + kTerms - 1) / kTerms, slices = TWO ? 2 * half_slices : half_slices;
+    const int per = (slices + a.runs - 1) / a.runs, s0 = run * per, s1 = min(slices, s0 + per);
+    SliceF32<E, PSLOW, T> p;
+    SliceF32<E, QSLOW, T> q;
+    auto load = [&](int s) __attribute__((always_inline)) {
+      const bool second = TWO && s >= half_slices;
+      const int t = (second ? s - half_slices : s) * kTerms;
+      p.load(second ? P1 : P0, ldp, r0, r_end, t, len);
+      if constexpr (PAIR) q.load_pair(Q0, Q1, ldq, c0, a.cols, t, len);
+      else q.load(second ? Q1 : Q0, ldq, c0, a.cols, t, len);
+    };
+    if (s0 < s1) load(s0);
+    for (int s = s0, stage = 0; s < s1; ++s, stage ^= 1) {
+      p.store(ps[stage]);
+      q.store(qs[stage]);
+      __syncthreads();      // (the other stage's readers were past it at the last barrier)
+      if (s + 1 < s1) load(s + 1);
+      multiply_f32<B>(ps[stage], qs[stage], wr, wc, i, g, acc);
+    }
+    if (a.runs > 1) {
+#pragma unroll
+      for (int y = 0; y < B; ++y)
+#pragma unroll
+        for (int x = 0; x < B; ++x) *reinterpret_cast<f32x4_t*>(partial(run, x, y)) = acc[x][y];
+      return;
+    }
+  } else {
+#pragma unroll
+    for (int y = 0; y < B; ++y)
+#pragma unroll
+      for (int x = 0; x < B; ++x)
+#pragma unroll 4
+        for (int r = 0; r < a.runs; ++r) {
+          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(partial(r, x, y));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[x][y][k] += v[k];
+        }
+  }
+
+  // lane (i, g): row y 16 + i, columns x 16 + 4 g .. + 3
+#pragma unroll
+  for (int y = 0; y < B; ++y) {
+    const int r = r0 + wr + y * 16 + i;
+    if (r >= r_end) continue;
+    if constexpr (PAIR) {
+#pragma unroll
+      for (int x = 0; x < B; x += 2) {
+        const int c = c0 + (wc + x * 16) / 2 + 4 * g;
+        if (c >= a.cols) continue;
+        const int64_t at = (int64_t)r * a.cols + c;
+        const f32x4_t vg = acc[x][y], vu = acc[x + 1][y];
+        float h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = act_value<F32>(vg[k], a.act) * vu[k];
+        store4(a.o0 + at, make_float4(h[0], h[1], h[2], h[3]));
+        if (a.o1 != nullptr) {
+          store4(a.o1 + at, make_float4(vg[0], vg[1], vg[2], vg[3]));
+          store4(a.o2 + at, make_float4(vu[0], vu[1], vu[2], vu[3]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < B; ++x) {
+        const int c = c0 + wc + x * 16 + 4 * g;
+        if (c >= a.cols) continue;
+        const int64_t at = (int64_t)r * a.cols + c;
+        const float4 v = make_float4(acc[x][y][0], acc[x][y][1], acc[x][y][2], acc[x][y][3]);
+        if constexpr (KIND == kDh) {
+          const float4 pg = load4(a.g + at), pu = load4(a.u + at);
+          const float vg[4] = {pg.x, pg.y, pg.z, pg.w}, vu[4] = {pu.x, pu.y, pu.z, pu.w}, d[4] = {v.x, v.y, v.z, v.w};
+          float dg[4], du[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float value, slope;
+            act_both<F32>(vg[k], a.act, value, slope);
+            dg[k] = d[k] * vu[k] * slope;
+            du[k] = d[k] * value;
+          }
+          store4(a.o0 + at, make_float4(dg[0], dg[1], dg[2], dg[3]));
+          store4(a.o1 + at, make_float4(du[0], du[1], du[2], du[3]));
+        } else {
+          store4(o0 + at, v);
+        }
+      }
+    }
+  }
+}
+
+// 128 x 128 tiles where they give every CU one, 64 x 64 otherwise; the contraction in
+// as many runs as give each CU two workgroups, of 4 slices at least.
+struct FfnPlanF32 {
+  int T, col_tiles, runs;
+  int64_t tiles, group_tiles;      // tiles: all that any offsets can give
+  static FfnPlanF32 of(const moe_ffn_t& f, int kind) {
+    FfnPlanF32 p{};
+    const int64_t cus = device_cu_count();
+    const bool over_rows = ffn_over_rows(kind);
+    const int rows = kind == kDw2 ? f.d_model : f.d_ff, halves = kind == kDw13 ? 2 : 1;
+    const int cols = kind == kGateUp ? 2 * f.d_ff : kind == kDh || kind == kDw2 ? f.d_ff : f.d_model;
+    const int64_t len = over_rows ? (f.M + f.groups - 1) / f.groups
+                        : kind == kDx ? 2 * (int64_t)f.d_ff : f.d_model;
+    for (p.T = 128;; p.T = 64) {
+      p.col_tiles = (cols + p.T - 1) / p.T;
+      p.group_tiles = over_rows ? (int64_t)halves * ((rows + p.T - 1) / p.T) * p.col_tiles : 0;
+      const int64_t row_tiles = (f.M + p.T - 1) / p.T + f.groups - 1;
+      p.tiles = over_rows ? p.group_tiles * f.groups : std::min<int64_t>(row_tiles, f.M) * p.col_tiles;
+      const int64_t usual = over_rows ? p.tiles : std::max<int64_t>(p.tiles - (int64_t)(f.groups - 1) / 2 * p.col_tiles, 1);
+      p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({64, 2 * cus / usual, len / (4 * kTerms)}));
+      if (usual >= cus || p.T == 64) return p;
+    }
+  }
+  size_t workspace() const { return runs > 1 ? (size_t)tiles * runs * T * T * 4 : 0; }
+};
+
+template <class E, int KIND>
+hipError_t launch(const moe_ffn_t& f, FfnArgsF32<E> a, void* partials, hipStream_t st) {
+  const FfnPlanF32 p = FfnPlanF32::of(f, KIND);
+  a.M = f.M;
+  a.groups = f.groups;
+  a.act = f.act;
+  a.col_tiles = p.col_tiles;
+  a.runs = p.runs;
+  a.group_tiles = p.group_tiles;
+  a.partials = static_cast<float*>(partials);
+  auto run = [&](auto product, auto join) {
+    hipLaunchKernelGGL(product, dim3((unsigned)(p.tiles * p.runs)), dim3(256), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.runs == 1) return e;
+    hipLaunchKernelGGL(join, dim3((unsigned)p.tiles), dim3(256), 0, st, a);
+    return hipGetLastError();
+  };
+  if (p.T == 128) return run(ffn_f32_kernel<E, KIND, 4, false>, ffn_f32_kernel<E, KIND, 4, true>);
+  return run(ffn_f32_kernel<E, KIND, 2, false>, ffn_f32_kernel<E, KIND, 2, true>);
+}
+
+}  // namespace
+
+size_t ffn_gate_up_bytes_f32(const moe_ffn_t& f) { return FfnPlanF32::of(f, kGateUp).workspace(); }
+
+size_t ffn_backward_product_bytes_f32(const moe_ffn_t& f) {
+  size_t most = 0;
+  for (int kind : {kDh, kDx, kDw13, kDw2}) most = std::max(most, FfnPlanF32::of(f, kind).workspace());
+  return most;
+}
+
+template <class E>
+hipError_t launch_ffn_gate_up_f32(const moe_ffn_t& f, const FfnTensors<E>& t, void* workspace, hipStream_t st) {
+  FfnArgsF32<E> a{};
+  a.P0 = t.x; a.Q0 = t.w1; a.Q1 = t.w3; a.offsets = t.offsets; a.cols = f.d_ff; a.len = f.d_model;
+  a.o0 = t.h_out; a.o1 = t.g_out; a.o2 = t.u_out;
+  return launch<E, kGateUp>(f, a, workspace, st);
+}
+
+template <class E>
+hipError_t launch_ffn_backward_f32(const moe_ffn_t& f, const FfnTensors<E>& t, void* partials, hipStream_t st) {
+  hipError_t e = hipSuccess;
+  FfnArgsF32<E> a{};
+  a.offsets = t.offsets;
+  if (t.dw2 != nullptr) {
+    a.P0 = t.dy; a.Q0 = t.h; a.rows = f.d_model; a.cols = f.d_ff; a.o0 = t.dw2;
+    if ((e = launch<E, kDw2>(f, a, partials, st)) != hipSuccess) return e;
+  }
+  if (t.dx == nullptr && t.dw1 == nullptr) return e;
+  a.P0 = t.dy; a.Q0 = t.w2; a.cols = f.d_ff; a.len = f.d_model; a.g = t.g; a.u = t.u; a.o0 = t.dg; a.o1 = t.du;
+  if ((e = launch<E, kDh>(f, a, partials, st)) != hipSuccess) return e;
+  a.P0 = t.dg; a.P1 = t.du;
+  if (t.dx != nullptr) {
+    a.Q0 = t.w1; a.Q1 = t.w3; a.cols = f.d_model; a.len = f.d_ff; a.o0 = t.dx;
+    if ((e = launch<E, kDx>(f, a, partials, st)) != hipSuccess) return e;
+  }
+  if (t.dw1 == nullptr) return e;
+  a.Q0 = t.x; a.rows = f.d_ff; a.cols = f.d_model; a.o0 = t.dw1; a.o1 = t.dw3;
+  return launch<E, kDw13>(f, a, partials, st);
+}
+
+template hipError_t launch_ffn_gate_up_f32<float>(const moe_ffn_t&, const FfnTensors<float>&, void*, hipStream_t);
+template hipError_t launch_ffn_backward_f32<float>(const moe_ffn_t&, const FfnTensors<float>&, void*, hipStream_t);
+template hipError_t launch_ffn_gate_up_f32<uint16_t>(const moe_ffn_t&, const FfnTensors<uint16_t>&, void*, hipStream_t);
+template hipError_t launch_ffn_backward_f32<uint16_t>(const moe_ffn_t&, const FfnTensors<uint16_t>&, void*, hipStream_t);
+
+}  // namespace moe

@@ -168,6 +168,27 @@ hipError_t launch_linear(const moe_linear_t& l, const void* x, const void* w, co
 hipError_t launch_linear_backward(const moe_linear_t& l, const void* dy, const void* pre, const void* x,
                                   const void* w, void* dx, void* dw, float* dbias, void* workspace, hipStream_t st);
 
+// Gated feed-forward block (dense or grouped) and its gradients.
+size_t ffn_gate_up_workspace_bytes(const moe_ffn_t& f);
+size_t ffn_backward_workspace_bytes(const moe_ffn_t& f);
+hipError_t launch_ffn_gate_up(const moe_ffn_t& f, const void* x, const int32_t* offsets, const void* w1,
+                              const void* w3, void* h, void* pre1, void* pre3, void* workspace, hipStream_t st);
+hipError_t launch_ffn_backward(const moe_ffn_t& f, const void* dy, const int32_t* offsets, const void* x,
+                               const void* pre1, const void* pre3, const void* h, const void* w1, const void* w3,
+                               const void* w2, void* dx, void* dw1, void* dw3, void* dw2, void* workspace,
+                               hipStream_t st);
+
+// Gradient of the permutation.
+hipError_t launch_permute_backward(const moe_shape_t& s, const void* dx_perm, const int32_t* slot_to_row,
+                                   const void* addend, void* dx, hipStream_t st);
+
+// Norm over a list of tensors, and the list scaled to a bound.
+size_t grad_norm_workspace_bytes(const moe_tensor_t* tensors, int count);
+hipError_t launch_grad_norm(const moe_tensor_t* tensors, int count, double* sum_squares, float* norm, void* workspace,
+                            hipStream_t st);
+hipError_t launch_grad_clip(const moe_tensor_t* tensors, const moe_tensor_t* outs, int count,
+                            const double* sum_squares, float max_norm, hipStream_t st);
+
 // Largest number of rows any routed expert can receive: each token picks an expert at most once.
 inline int64_t max_rows_per_routed_expert(const moe_shape_t& s) {
   int64_t m = s.T;

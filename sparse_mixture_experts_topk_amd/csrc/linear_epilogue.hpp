@@ -118,6 +118,63 @@ __device__ __forceinline__ float act_grad(float p, int act) {
   }
 }
 
+// Both at once, from one exponential.
+template <bool F32>
+__device__ __forceinline__ void act_both(float p, int act, float& value, float& slope) {
+  switch (act) {
+    case MOE_ACT_RELU:
+      value = p < 0.0f ? 0.0f : p;
+      slope = p > 0.0f ? 1.0f : 0.0f;
+      return;
+    case MOE_ACT_SILU: {
+      float s, below;
+      if constexpr (F32) {
+        sigmoids(p, s, below);
+      } else {
+        s = fast_sigmoid(p);
+        below = 1.0f - s;
+      }
+      value = p * s;
+      slope = fmaf(value, below, s);
+      return;
+    }
+    case MOE_ACT_GELU: {
+      const float c = to_32(p);
+      float e;
+      const float q = normal_tail<F32>(c, e), cdf = p < 0.0f ? q : 1.0f - q;
+      value = p * cdf;
+      slope = fmaf(c * e, 0.3989422804014327f, cdf);
+      return;
+    }
+    case MOE_ACT_GELU_TANH: {
+      const float c = to_32(p);
+      float s, below;
+      if constexpr (F32) {
+        tanh_sigmoids(c, s, below);
+      } else {
+        s = fast_sigmoid(kGeluA * (c + kGeluB * c * c * c));
+        below = 1.0f - s;
+      }
+      value = p * s;
+      slope = fmaf(c * s * below, kGeluA * (1.0f + 3.0f * kGeluB * c * c), s);
+      return;
+    }
+    default:
+      value = p;
+      slope = 1.0f;
+  }
+}
+template <bool F32>
+__device__ __forceinline__ float act_value(float p, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return act_value<MOE_ACT_RELU, F32>(p);
+    case MOE_ACT_SILU: return act_value<MOE_ACT_SILU, F32>(p);
+    case MOE_ACT_GELU: return act_value<MOE_ACT_GELU, F32>(p);
+    case MOE_ACT_GELU_TANH: return act_value<MOE_ACT_GELU_TANH, F32>(p);
+    default: return p;
+  }
+}
+
 __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll

@@ -4,13 +4,8 @@
 //
 // All products are out[r][c] = sum_t P(r, t) Q(c, t); an operand is stored [r][t]
 // or, SLOW, [t][r].  A workgroup of 4 wavefronts (2 x 2) computes a tile of
-// 32 B x 32 B, each wavefront B x B blocks of 16 x 16.  The contraction advances
-// 16 at a time: the next slice is loaded into registers while this one is
-// multiplied from LDS.  An LDS row holds the 16 terms of one operand row; lane
-// (i, g) reads row i's terms 4 g .. 4 g + 3 at once and instruction s takes term
-// 4 g + s of both operands (any order of the terms will do, as long as it is the
-// same one).  16-byte chunk c of row r sits at c ^ ((r >> 2) & 3): the 16 rows of
-// a read phase cover all banks.  Bound by the fp32 matrix rate (157 TFLOP/s):
+// 32 B x 32 B, each wavefront B x B blocks of 16 x 16 (f32_tiles.hpp).  Bound by the
+// fp32 matrix rate (157 TFLOP/s):
 // 4096^3 1128 us, 122 TFLOP/s (library 138), its gradients 2596 us; few rows by
 // the latency of a short contraction and the join: 16 x 256 x 4096 12.1 us.
 // Where the tiles leave CUs idle the contraction is cut into equal runs whose
@@ -19,13 +14,12 @@
 #include <type_traits>
 
 #include "device_common.hpp"
+#include "f32_tiles.hpp"
 #include "launch.hpp"
 #include "linear_epilogue.hpp"
 
 namespace moe {
 namespace {
-
-constexpr int kTerms = 16;
 
 struct EpilogueF32 {
   const float* bias;
@@ -61,41 +55,6 @@ struct ArgsF32 {
   EpilogueF32 ep;
 };
 
-// This thread's parts of an operand's slice (rows x 16 terms, 16 bytes each).
-template <bool SLOW, int ROWS>
-struct SliceF32 {
-  static constexpr int N = ROWS * kTerms / 4 / 256;
-  float4 v[N];
-
-  __device__ __forceinline__ void load(const float* p, int64_t ld, int r0, int rows, int t0, int end) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int i = threadIdx.x + 256 * k;
-      const int r = r0 + (SLOW ? i % (ROWS / 4) * 4 : i / 4), t = t0 + (SLOW ? i / (ROWS / 4) : i % 4 * 4);
-      v[k] = r < rows && t < end
-                 ? *reinterpret_cast<const float4*>(SLOW ? p + (int64_t)t * ld + r : p + (int64_t)r * ld + t)
-                 : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  }
-  __device__ __forceinline__ void store(float* lds) const {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int i = threadIdx.x + 256 * k;
-      if constexpr (SLOW) {
-        const int r = i % (ROWS / 4) * 4, t = i / (ROWS / 4);       // 4 rows r .., one swizzle key
-        const int at = (((t >> 2) ^ ((r >> 2) & 3)) << 2) + (t & 3);
-        lds[(r + 0) * kTerms + at] = v[k].x;
-        lds[(r + 1) * kTerms + at] = v[k].y;
-        lds[(r + 2) * kTerms + at] = v[k].z;
-        lds[(r + 3) * kTerms + at] = v[k].w;
-      } else {
-        const int r = i / 4, c = i % 4;
-        *reinterpret_cast<float4*>(lds + r * kTerms + ((c ^ ((r >> 2) & 3)) << 2)) = v[k];
-      }
-    }
-  }
-};
-
 template <bool PSLOW, bool QSLOW, int ACT, int B>
 __global__ __launch_bounds__(256) void linear_f32_kernel(const ArgsF32 a) {
   constexpr int T = 32 * B;
@@ -112,8 +71,8 @@ __global__ __launch_bounds__(256) void linear_f32_kernel(const ArgsF32 a) {
   for (int x = 0; x < B; ++x)
 #pragma unroll
     for (int y = 0; y < B; ++y) acc[x][y] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  SliceF32<PSLOW, T> p;
-  SliceF32<QSLOW, T> q;
+  SliceF32<float, PSLOW, T> p;
+  SliceF32<float, QSLOW, T> q;
   p.load(a.P, a.ldp, r0, a.rows, t0, end);
   q.load(a.Q, a.ldq, c0, a.cols, t0, end);
   int stage = 0;
@@ -125,21 +84,7 @@ __global__ __launch_bounds__(256) void linear_f32_kernel(const ArgsF32 a) {
       p.load(a.P, a.ldp, r0, a.rows, t + kTerms, end);
       q.load(a.Q, a.ldq, c0, a.cols, t + kTerms, end);
     }
-    float4 fa[B], fb[B];
-#pragma unroll
-    for (int x = 0; x < B; ++x) {
-      const int c = wc + x * 16 + i, r = wr + x * 16 + i;
-      fa[x] = *reinterpret_cast<const float4*>(&qs[stage][c * kTerms + ((g ^ ((c >> 2) & 3)) << 2)]);
-      fb[x] = *reinterpret_cast<const float4*>(&ps[stage][r * kTerms + ((g ^ ((r >> 2) & 3)) << 2)]);
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int x = 0; x < B; ++x)
-#pragma unroll
-        for (int y = 0; y < B; ++y)
-          acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x4f32(reinterpret_cast<const float*>(&fa[x])[s],
-                                                           reinterpret_cast<const float*>(&fb[y])[s], acc[x][y], 0, 0, 0);
+    multiply_f32<B>(ps[stage], qs[stage], wr, wc, i, g, acc);
   }
   // lane (i, g): row y 16 + i, columns x 16 + 4 g .. + 3
 #pragma unroll

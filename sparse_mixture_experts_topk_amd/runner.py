@@ -7,6 +7,9 @@ Given a ``MoeRouter``, both route by ``scored_routing`` (``moe_linear`` for the
 logits, ``moe_route_scored`` for the choice) instead of the library's top-k
 softmax router, and ``gate_backward`` takes the gradient at y of such a staged
 pass back to x and the router's weights (the experts' weights held fixed).
+``layer_backward`` takes it back through the whole layer, the experts' weights
+included, from a pass that kept what it needs (``staged(..., keep=True)``), and
+``clip_gradients`` scales gradients to a bound of their norm.
 """
 from __future__ import annotations
 
@@ -17,12 +20,14 @@ from typing import Optional
 
 import torch
 
-from . import (make_linear, moe_combine, moe_combine_backward, moe_expert_gemm_down,
-               moe_expert_gemm_gate_up, moe_forward, moe_forward_routed, moe_linear,
-               moe_linear_backward, moe_linear_workspace_bytes, moe_permute, moe_route_scored,
+from . import (make_ffn, make_linear, make_router, make_tensors, moe_combine, moe_combine_backward,
+               moe_expert_gemm_down, moe_expert_gemm_gate_up, moe_ffn_backward, moe_ffn_gate_up,
+               moe_ffn_workspace_bytes, moe_forward, moe_forward_routed, moe_grad_clip, moe_grad_norm,
+               moe_grad_norm_workspace_bytes, moe_linear, moe_linear_backward,
+               moe_linear_workspace_bytes, moe_permute, moe_permute_backward, moe_route_scored,
                moe_route_scored_backward, moe_route_topk, moe_workspace_bytes, shape_of,
-               MOE_CALL_DOWN, MOE_CALL_FORWARD, MOE_CALL_LINEAR, MOE_CALL_LINEAR_BACKWARD,
-               MOE_CALL_ROUTE)
+               MOE_CALL_DOWN, MOE_CALL_FFN_BACKWARD, MOE_CALL_FFN_GATE_UP, MOE_CALL_FORWARD,
+               MOE_CALL_LINEAR, MOE_CALL_LINEAR_BACKWARD, MOE_CALL_ROUTE)
 
 
 def _dev(t: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
@@ -179,6 +184,46 @@ def gate_backward(di: DeviceInputs, st: dict, router, dy: torch.Tensor, dscores=
     return o
 
 
+def _ffn_of(cfg):
+    """The experts' block as moe_ffn_gate_up and moe_ffn_backward have it: a group per expert."""
+    if cfg.w_dtype != cfg.act_dtype:
+        raise ValueError(f"{cfg.w_dtype} experts have no backward pass: bf16 or fp32 weights do")
+    return make_ffn(cfg.T * (cfg.top_k + cfg.n_shared), cfg.d_model, cfg.d_ff, cfg.n_experts + cfg.n_shared,
+                    cfg.act_dtype, "silu")
+
+
+@_on_its_device
+def layer_backward(di: DeviceInputs, st: dict, dy: torch.Tensor, router=None, dscores=None, stream=None) -> dict:
+    """Gradients of the whole layer from the gradient ``dy`` at y: ``st`` is the result of
+    ``staged(..., keep=True)`` with the same router (None: the library's own, a softmax over the kept
+    logits).  dx, dw_gate, dbias (with a router bias), dw1, dw3, dw2, beside what gate_backward gives."""
+    cfg, dev = di.cfg, di.x.device
+    ffn = _ffn_of(cfg)
+    o = gate_backward(di, st, make_router() if router is None else router, dy, dscores, stream)
+    o["dx_perm"] = torch.empty_like(st["x_perm"])
+    for n in ("w1", "w3", "w2"):
+        o["d" + n] = torch.empty_like(getattr(di, n))
+    o["ffn_ws"] = _bytes(moe_ffn_workspace_bytes(ffn, MOE_CALL_FFN_BACKWARD), dev)
+    moe_ffn_backward(ffn, o["dy_perm"], st["expert_offsets"], st["x_perm"], st["pre1"], st["pre3"], st["h"], di.w1,
+                     di.w3, di.w2, o["dx_perm"], o["dw1"], o["dw3"], o["dw2"], o["ffn_ws"], stream)
+    moe_permute_backward(shape_of(cfg), o["dx_perm"], st["slot_to_row"], o["dx"], o["dx"], stream)
+    return o
+
+
+def clip_gradients(grads, max_norm: float, stream=None) -> torch.Tensor:
+    """Scales the tensors ``grads`` in place to a norm of at most ``max_norm`` (not where the norm is not
+    finite); returns the norm they had, [1] fp32 on the device."""
+    t = make_tensors(grads)
+    if t.device is None:
+        return torch.zeros(1)
+    with torch.cuda.device(t.device), _on(stream, t.device):
+        total, norm = torch.empty(1, dtype=torch.float64, device=t.device), torch.empty(1, device=t.device)
+        ws = _bytes(moe_grad_norm_workspace_bytes(t), t.device)
+        moe_grad_norm(t, total, norm, ws, stream)
+        moe_grad_clip(t, None, total, max_norm, stream)
+    return norm
+
+
 @_on_its_device
 def forward(di: DeviceInputs, buf: Optional[ForwardBuffers] = None, stream=None, router=None,
             balance_bias=None) -> ForwardBuffers:
@@ -200,9 +245,10 @@ def forward(di: DeviceInputs, buf: Optional[ForwardBuffers] = None, stream=None,
 
 
 @_on_its_device
-def staged(di: DeviceInputs, stream=None, router=None, balance_bias=None) -> dict:
+def staged(di: DeviceInputs, stream=None, router=None, balance_bias=None, keep: bool = False) -> dict:
     """The five boundary calls in sequence (with a router: scored_routing in place of
-    moe_route_topk); returns every intermediate buffer."""
+    moe_route_topk); returns every intermediate buffer.  ``keep``: for layer_backward, the
+    experts' pre-activations too, by moe_ffn_gate_up (bf16 or fp32 experts)."""
     cfg = di.cfg
     dev = di.x.device
     T, d, F, E, k, S = cfg.T, cfg.d_model, cfg.d_ff, cfg.n_experts, cfg.top_k, cfg.n_shared
@@ -234,8 +280,15 @@ def staged(di: DeviceInputs, stream=None, router=None, balance_bias=None) -> dic
                 o["x_perm_scale"], None, stream)
     o["h"] = torch.empty(R, F, dtype=_perm_dtype(cfg), device=dev)
     o["h_scale"] = torch.empty(R, F // 32, dtype=torch.uint8, device=dev) if fp8 else None
-    moe_expert_gemm_gate_up(shape, o["x_perm"], o["x_perm_scale"], o["expert_offsets"], di.w1,
-                            di.w3, di.w1_scale, di.w3_scale, o["h"], o["h_scale"], None, stream)
+    if keep:
+        ffn = _ffn_of(cfg)
+        o["pre1"], o["pre3"] = (torch.empty(R, F, dtype=_act_dtype(cfg), device=dev) for _ in range(2))
+        o["ffn_ws"] = _bytes(moe_ffn_workspace_bytes(ffn, MOE_CALL_FFN_GATE_UP), dev)
+        moe_ffn_gate_up(ffn, o["x_perm"], o["expert_offsets"], di.w1, di.w3, o["h"], o["pre1"], o["pre3"],
+                        o["ffn_ws"], stream)
+    else:
+        moe_expert_gemm_gate_up(shape, o["x_perm"], o["x_perm_scale"], o["expert_offsets"], di.w1,
+                                di.w3, di.w1_scale, di.w3_scale, o["h"], o["h_scale"], None, stream)
     o["y_perm"] = torch.empty(R, d, dtype=torch.float32, device=dev)
     down_ws = moe_workspace_bytes(shape, MOE_CALL_DOWN)
     o["down_ws"] = torch.empty(down_ws, dtype=torch.uint8, device=dev) if down_ws else None
