@@ -15,22 +15,15 @@ namespace moe {
 constexpr int kTerms = 16;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const uint16_t* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(uint16_t* p, float4 v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
 
-// This thread's parts of an operand's slice (rows x 16 terms, 4 each).
-template <class E, bool SLOW, int ROWS>
+// This thread's parts of an operand's slice (rows x 16 terms, 16 bytes each).
+template <bool SLOW, int ROWS>
 struct SliceF32 {
   static constexpr int N = ROWS * kTerms / 4 / 256;
   float4 v[N];
 
-  __device__ __forceinline__ void load(const E* p, int64_t ld, int r0, int rows, int t0, int end) {
+  __device__ __forceinline__ void load(const float* p, int64_t ld, int r0, int rows, int t0, int end) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int i = threadIdx.x + 256 * k;
@@ -41,7 +34,7 @@ struct SliceF32 {
     }
   }
   // Blocks of 16 rows of two operands in turn: rows r0 .. of p, the same of q.
-  __device__ __forceinline__ void load_pair(const E* p, const E* q, int64_t ld, int r0, int rows, int t0, int end) {
+  __device__ __forceinline__ void load_pair(const float* p, const float* q, int64_t ld, int r0, int rows, int t0, int end) {
     static_assert(!SLOW, "rows as they lie");
 #pragma unroll
     for (int k = 0; k < N; ++k) {

@@ -16,10 +16,12 @@ size_t pre_bytes(const moe_ffn_t& f) { return ((size_t)f.M * f.d_ff * elem(f) + 
 
 }  // namespace
 
-size_t ffn_gate_up_workspace_bytes(const moe_ffn_t& f) { return ffn_gate_up_bytes_f32(f); }
+size_t ffn_gate_up_workspace_bytes(const moe_ffn_t& f) {
+  return f.dtype == MOE_F32 ? ffn_gate_up_bytes_f32(f) : ffn_gate_up_bytes_bf16(f);
+}
 
 size_t ffn_backward_workspace_bytes(const moe_ffn_t& f) {
-  return 2 * pre_bytes(f) + ffn_backward_product_bytes_f32(f);
+  return 2 * pre_bytes(f) + (f.dtype == MOE_F32 ? ffn_backward_product_bytes_f32(f) : ffn_backward_product_bytes_bf16(f));
 }
 
 hipError_t launch_ffn_gate_up(const moe_ffn_t& f, const void* x, const int32_t* offsets, const void* w1,
@@ -34,7 +36,8 @@ hipError_t launch_ffn_gate_up(const moe_ffn_t& f, const void* x, const int32_t* 
     t.h_out = static_cast<E*>(h);
     t.g_out = static_cast<E*>(pre1);
     t.u_out = static_cast<E*>(pre3);
-    return launch_ffn_gate_up_f32<E>(f, t, workspace, st);
+    if constexpr (sizeof(E) == 4) return launch_ffn_gate_up_f32(f, t, workspace, st);
+    else return launch_ffn_gate_up_bf16(f, t, workspace, st);
   };
   return f.dtype == MOE_F32 ? run(float{}) : run(uint16_t{});
 }
@@ -62,7 +65,9 @@ hipError_t launch_ffn_backward(const moe_ffn_t& f, const void* dy, const int32_t
     t.dw2 = static_cast<E*>(dw2);
     t.dg = reinterpret_cast<E*>(ws);
     t.du = reinterpret_cast<E*>(ws + pre_bytes(f));
-    return launch_ffn_backward_f32<E>(f, t, ws + 2 * pre_bytes(f), st);
+    void* partials = ws + 2 * pre_bytes(f);
+    if constexpr (sizeof(E) == 4) return launch_ffn_backward_f32(f, t, partials, st);
+    else return launch_ffn_backward_bf16(f, t, partials, st);
   };
   return f.dtype == MOE_F32 ? run(float{}) : run(uint16_t{});
 }

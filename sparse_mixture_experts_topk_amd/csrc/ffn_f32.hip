@@ -18,29 +18,28 @@
 namespace moe {
 namespace {
 
-template <class E>
 struct FfnArgsF32 {
-  const E *P0, *P1, *Q0, *Q1;      // P1, Q1: the second half where there are two
+  const float *P0, *P1, *Q0, *Q1;      // P1, Q1: the second half where there are two
   const int32_t* offsets;
   int M, groups;
   int rows, cols, len;             // weight rows (kDw13, kDw2), columns (channels), terms of a half (else)
   int col_tiles, runs;
   int64_t group_tiles;             // kDw13, kDw2: tiles per group
   float* partials;
-  const E *g, *u;                  // kDh: pre-activations
-  E *o0, *o1, *o2;
+  const float *g, *u;              // kDh: pre-activations
+  float *o0, *o1, *o2;
   int act;
 };
 
-template <class E, int KIND, int B, bool JOIN>
-__global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32<E> a) {
+template <int KIND, int B, bool JOIN>
+__global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32 a) {
   constexpr int T = 32 * B;
   constexpr bool OVER_ROWS = ffn_over_rows(KIND), PAIR = KIND == kGateUp, TWO = KIND == kDx;
-  constexpr bool PSLOW = OVER_ROWS, QSLOW = KIND != kGateUp, F32 = sizeof(E) == 4;
+  constexpr bool PSLOW = OVER_ROWS, QSLOW = KIND != kGateUp;
   __shared__ __attribute__((aligned(16))) float ps[2][T * kTerms];
   __shared__ __attribute__((aligned(16))) float qs[2][T * kTerms];
   __shared__ FfnGroups groups;
-  groups.load(a.offsets, a.groups, a.M, T);
+  groups.load(a.offsets, a.groups, a.M, [](int rows) { return (rows + T - 1) / T; });
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
   const int64_t tile = JOIN ? blockIdx.x : blockIdx.x / a.runs;
@@ -48,8 +47,8 @@ __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32<E> a) {
 
   // the tile's group, first row and column, rows' end, and the operands there
   int e, r0, r_end, c0, len = a.len;
-  const E *P0 = a.P0, *P1 = a.P1, *Q0 = a.Q0, *Q1 = a.Q1;
-  E *o0 = a.o0, *o1 = a.o1;
+  const float *P0 = a.P0, *P1 = a.P1, *Q0 = a.Q0, *Q1 = a.Q1;
+  float *o0 = a.o0, *o1 = a.o1;
   int64_t ldp, ldq;
   if constexpr (OVER_ROWS) {
     e = (int)(tile / a.group_tiles);
@@ -67,23 +66,17 @@ __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32<E> a) {
     r_end = a.rows;
     ldp = a.rows;
     ldq = a.cols;
-    const int64_t first = groups.off[e];
-    len = groups.off[e + 1] - groups.off[e];
+    const int64_t first = groups.first(e);
+    len = groups.first(e + 1) - groups.first(e);
     P0 += first * ldp;
     Q0 += first * ldq;
     o0 += (int64_t)e * a.rows * a.cols;
   } else {
     const int t = (int)(tile / a.col_tiles);
-    if (t >= groups.pre[a.groups]) return;                   // the whole workgroup
-    int lo = 0, hi = a.groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (groups.pre[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    e = lo;
-    r0 = groups.off[e] + (t - groups.pre[e]) * T;
-    r_end = groups.off[e + 1];
+    if (t >= groups.before(a.groups)) return;                // the whole workgroup
+    e = groups.of(t, a.groups);
+    r0 = groups.first(e) + (t - groups.before(e)) * T;
+    r_end = groups.first(e + 1);
     c0 = (int)(tile % a.col_tiles) * (PAIR ? T / 2 : T);     // kGateUp: channels
     ldp = a.len;
     ldq = PAIR ? a.len : a.cols;
@@ -105,8 +98,8 @@ __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32<E> a) {
   if constexpr (!JOIN) {
     const int half_slices = (len + kTerms - 1) / kTerms, slices = TWO ? 2 * half_slices : half_slices;
     const int per = (slices + a.runs - 1) / a.runs, s0 = run * per, s1 = min(slices, s0 + per);
-    SliceF32<E, PSLOW, T> p;
-    SliceF32<E, QSLOW, T> q;
+    SliceF32<PSLOW, T> p;
+    SliceF32<QSLOW, T> q;
     auto load = [&](int s) __attribute__((always_inline)) {
       const bool second = TWO && s >= half_slices;
       const int t = (second ? s - half_slices : s) * kTerms;
@@ -156,7 +149,7 @@ __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32<E> a) {
         const f32x4_t vg = acc[x][y], vu = acc[x + 1][y];
         float h[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = act_value<F32>(vg[k], a.act) * vu[k];
+        for (int k = 0; k < 4; ++k) h[k] = act_value<true>(vg[k], a.act) * vu[k];
         store4(a.o0 + at, make_float4(h[0], h[1], h[2], h[3]));
         if (a.o1 != nullptr) {
           store4(a.o1 + at, make_float4(vg[0], vg[1], vg[2], vg[3]));
@@ -177,7 +170,7 @@ __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32<E> a) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float value, slope;
-            act_both<F32>(vg[k], a.act, value, slope);
+            act_both<true>(vg[k], a.act, value, slope);
             dg[k] = d[k] * vu[k] * slope;
             du[k] = d[k] * value;
           }
@@ -217,8 +210,8 @@ struct FfnPlanF32 {
   size_t workspace() const { return runs > 1 ? (size_t)tiles * runs * T * T * 4 : 0; }
 };
 
-template <class E, int KIND>
-hipError_t launch(const moe_ffn_t& f, FfnArgsF32<E> a, void* partials, hipStream_t st) {
+template <int KIND>
+hipError_t launch(const moe_ffn_t& f, FfnArgsF32 a, void* partials, hipStream_t st) {
   const FfnPlanF32 p = FfnPlanF32::of(f, KIND);
   a.M = f.M;
   a.groups = f.groups;
@@ -234,8 +227,8 @@ hipError_t launch(const moe_ffn_t& f, FfnArgsF32<E> a, void* partials, hipStream
     hipLaunchKernelGGL(join, dim3((unsigned)p.tiles), dim3(256), 0, st, a);
     return hipGetLastError();
   };
-  if (p.T == 128) return run(ffn_f32_kernel<E, KIND, 4, false>, ffn_f32_kernel<E, KIND, 4, true>);
-  return run(ffn_f32_kernel<E, KIND, 2, false>, ffn_f32_kernel<E, KIND, 2, true>);
+  if (p.T == 128) return run(ffn_f32_kernel<KIND, 4, false>, ffn_f32_kernel<KIND, 4, true>);
+  return run(ffn_f32_kernel<KIND, 2, false>, ffn_f32_kernel<KIND, 2, true>);
 }
 
 }  // namespace
@@ -248,39 +241,32 @@ size_t ffn_backward_product_bytes_f32(const moe_ffn_t& f) {
   return most;
 }
 
-template <class E>
-hipError_t launch_ffn_gate_up_f32(const moe_ffn_t& f, const FfnTensors<E>& t, void* workspace, hipStream_t st) {
-  FfnArgsF32<E> a{};
+hipError_t launch_ffn_gate_up_f32(const moe_ffn_t& f, const FfnTensors<float>& t, void* workspace, hipStream_t st) {
+  FfnArgsF32 a{};
   a.P0 = t.x; a.Q0 = t.w1; a.Q1 = t.w3; a.offsets = t.offsets; a.cols = f.d_ff; a.len = f.d_model;
   a.o0 = t.h_out; a.o1 = t.g_out; a.o2 = t.u_out;
-  return launch<E, kGateUp>(f, a, workspace, st);
+  return launch<kGateUp>(f, a, workspace, st);
 }
 
-template <class E>
-hipError_t launch_ffn_backward_f32(const moe_ffn_t& f, const FfnTensors<E>& t, void* partials, hipStream_t st) {
+hipError_t launch_ffn_backward_f32(const moe_ffn_t& f, const FfnTensors<float>& t, void* partials, hipStream_t st) {
   hipError_t e = hipSuccess;
-  FfnArgsF32<E> a{};
+  FfnArgsF32 a{};
   a.offsets = t.offsets;
   if (t.dw2 != nullptr) {
     a.P0 = t.dy; a.Q0 = t.h; a.rows = f.d_model; a.cols = f.d_ff; a.o0 = t.dw2;
-    if ((e = launch<E, kDw2>(f, a, partials, st)) != hipSuccess) return e;
+    if ((e = launch<kDw2>(f, a, partials, st)) != hipSuccess) return e;
   }
   if (t.dx == nullptr && t.dw1 == nullptr) return e;
   a.P0 = t.dy; a.Q0 = t.w2; a.cols = f.d_ff; a.len = f.d_model; a.g = t.g; a.u = t.u; a.o0 = t.dg; a.o1 = t.du;
-  if ((e = launch<E, kDh>(f, a, partials, st)) != hipSuccess) return e;
+  if ((e = launch<kDh>(f, a, partials, st)) != hipSuccess) return e;
   a.P0 = t.dg; a.P1 = t.du;
   if (t.dx != nullptr) {
     a.Q0 = t.w1; a.Q1 = t.w3; a.cols = f.d_model; a.len = f.d_ff; a.o0 = t.dx;
-    if ((e = launch<E, kDx>(f, a, partials, st)) != hipSuccess) return e;
+    if ((e = launch<kDx>(f, a, partials, st)) != hipSuccess) return e;
   }
   if (t.dw1 == nullptr) return e;
   a.Q0 = t.x; a.rows = f.d_ff; a.cols = f.d_model; a.o0 = t.dw1; a.o1 = t.dw3;
-  return launch<E, kDw13>(f, a, partials, st);
+  return launch<kDw13>(f, a, partials, st);
 }
-
-template hipError_t launch_ffn_gate_up_f32<float>(const moe_ffn_t&, const FfnTensors<float>&, void*, hipStream_t);
-template hipError_t launch_ffn_backward_f32<float>(const moe_ffn_t&, const FfnTensors<float>&, void*, hipStream_t);
-template hipError_t launch_ffn_gate_up_f32<uint16_t>(const moe_ffn_t&, const FfnTensors<uint16_t>&, void*, hipStream_t);
-template hipError_t launch_ffn_backward_f32<uint16_t>(const moe_ffn_t&, const FfnTensors<uint16_t>&, void*, hipStream_t);
 
 }  // namespace moe

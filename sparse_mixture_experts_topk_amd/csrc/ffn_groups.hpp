@@ -20,44 +20,58 @@ constexpr bool ffn_over_rows(int kind) { return kind == kDw13 || kind == kDw2; }
 constexpr int kMaxFfnGroups = kMaxExpertGroups;
 
 // Row offsets of the groups, in LDS: bounded to the buffers' rows and ascending,
-// whatever the array holds (NULL: one group of all rows); and the tiles of
-// `rows_per_tile` rows before each group.  By the first wavefront.
+// whatever the array holds (NULL: one group of all rows); and a running sum over the
+// groups before each of units(rows of the group).
 struct FfnGroups {
   int32_t off[kMaxFfnGroups + 1];
   int32_t pre[kMaxFfnGroups + 1];
 
-  __device__ __forceinline__ void load(const int32_t* offsets, int groups, int M, int rows_per_tile) {
+  // By the first wavefront; then a barrier.
+  template <class Units>
+  __device__ __forceinline__ void load(const int32_t* offsets, int groups, int M, Units&& units) {
     if (threadIdx.x < kWave) {
-      int carry = 0, high = 0;
+      const int lane = threadIdx.x;
+      int high = 0, carry = 0;
       for (int base = 0; base <= groups; base += kWave) {
-        const int e = base + (int)threadIdx.x;
+        const int e = base + lane;
         int o = 0;
         if (e <= groups) o = offsets != nullptr ? min(max(offsets[e], 0), M) : e == 0 ? 0 : M;
-        // running maximum, then running tile count
 #pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
+        for (int d = 1; d < kWave; d <<= 1) {                         // running maximum
           const int v = __shfl_up(o, d);
-          if ((int)threadIdx.x >= d) o = max(o, v);
+          if (lane >= d) o = max(o, v);
         }
         o = max(o, high);
-        int before = __shfl_up(o, 1);
-        if (threadIdx.x == 0) before = base == 0 ? o : high;
-        int tiles = e == 0 ? 0 : (o - before + rows_per_tile - 1) / rows_per_tile;      // of group e - 1
+        const int above = __shfl_up(o, 1), before = lane == 0 ? high : above;
+        int sum = e == 0 || e > groups ? 0 : units(o - before);       // of group e - 1
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
-          const int v = __shfl_up(tiles, d);
-          if ((int)threadIdx.x >= d) tiles += v;
+          const int v = __shfl_up(sum, d);
+          if (lane >= d) sum += v;
         }
-        tiles += carry;
+        sum += carry;
         if (e <= groups) {
           off[e] = o;
-          pre[e] = tiles;
+          pre[e] = sum;
         }
         high = __shfl(o, kWave - 1);
-        carry = __shfl(tiles, kWave - 1);
+        carry = __shfl(sum, kWave - 1);
       }
     }
     __syncthreads();
+  }
+  // (uniform values)
+  __device__ __forceinline__ int first(int e) const { return __builtin_amdgcn_readfirstlane(off[e]); }
+  __device__ __forceinline__ int before(int e) const { return __builtin_amdgcn_readfirstlane(pre[e]); }
+  // The last group with before(group) <= v: one that has units, if v is below their sum.
+  __device__ __forceinline__ int of(int v, int groups) const {
+    int lo = 0, hi = groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before(mid) <= v) lo = mid;
+      else hi = mid;
+    }
+    return lo;
   }
 };
 
@@ -71,12 +85,17 @@ struct FfnTensors {
   E *dg, *du;                          // backward: gradients at the pre-activations, in the workspace
 };
 
+// bf16 operands: each call's products (ffn_gate_up.hip, ffn_gradients.hip).
+size_t ffn_gate_up_bytes_bf16(const moe_ffn_t& f);
+size_t ffn_backward_product_bytes_bf16(const moe_ffn_t& f);
+hipError_t launch_ffn_gate_up_bf16(const moe_ffn_t& f, const FfnTensors<uint16_t>& t, void* workspace, hipStream_t st);
+hipError_t launch_ffn_dh_bf16(const moe_ffn_t& f, const FfnTensors<uint16_t>& t, void* partials, hipStream_t st);
+hipError_t launch_ffn_backward_bf16(const moe_ffn_t& f, const FfnTensors<uint16_t>& t, void* partials, hipStream_t st);
+
 // fp32 operands (ffn_f32.hip).
 size_t ffn_gate_up_bytes_f32(const moe_ffn_t& f);
 size_t ffn_backward_product_bytes_f32(const moe_ffn_t& f);
-template <class E>
-hipError_t launch_ffn_gate_up_f32(const moe_ffn_t& f, const FfnTensors<E>& t, void* workspace, hipStream_t st);
-template <class E>
-hipError_t launch_ffn_backward_f32(const moe_ffn_t& f, const FfnTensors<E>& t, void* partials, hipStream_t st);
+hipError_t launch_ffn_gate_up_f32(const moe_ffn_t& f, const FfnTensors<float>& t, void* workspace, hipStream_t st);
+hipError_t launch_ffn_backward_f32(const moe_ffn_t& f, const FfnTensors<float>& t, void* partials, hipStream_t st);
 
 }  // namespace moe

@@ -1,0 +1,453 @@
+// The products of the feed-forward block (FfnKind) as streams of bf16 matrix-core tiles
+// (tile_stream of linear_tiles.hpp) over groups of rows that only the device knows.
+//
+//   kind      rows (P)              columns (Q)                    terms
+//   kGateUp   x [r][t]              w1, w3 [r][t], 16 + 16 in turn  d_model
+//   kDh       dy [r][t]             w2 [t][r]                      d_model
+//   kDx       dg then du [r][t]     w1 then w3 [t][r]              2 d_ff
+//   kDw13     dg or du [t][r]       x [t][r]                       the group's rows
+//   kDw2      dy [t][r]             h [t][r]                       the group's rows
+//
+// Nothing is transposed in memory and dh never goes there: kDh's epilogue meets each
+// element of it with g and u and stores dg and du.  Every workgroup reads the offsets
+// and finds its own tiles: they are cut into 8 contiguous shares, one per XCD, and its
+// workgroups take full rounds of them.  The last, partial round is cut along the
+// contraction where that is shorter by the plan's costs (FfnShare), its partial tiles
+// joined in order by a second kernel; weight gradients of several groups have tiles of
+// as many slices as their group has rows, so there the shares are even by slices,
+// and no tile is cut.
+#pragma once
+#include "device_common.hpp"
+#include "ffn_groups.hpp"
+#include "linear_tiles.hpp"
+
+namespace moe {
+
+// A split's join and its partial tiles in ns, and the least slices of a run (as in the
+// dense product's plan).
+constexpr int kFfnJoinNs = 4000, kFfnJoinNsPer100KiB = 33;
+constexpr int kFfnMinSlices = 8;
+// A tile's epilogue in slices, for shares that are even by slices.
+constexpr int kFfnTileSlices = 3;
+
+struct FfnTileArgs {
+  const uint16_t *P0, *P1, *Q0, *Q1;      // P1, Q1: the second half where there are two
+  const int32_t* offsets;
+  int M, groups;
+  int rows, cols, len;                    // kDw13, kDw2: rows of the weight; columns (kGateUp: channels); terms of a half
+  int row_tiles, col_tiles;               // row_tiles: kDw13, kDw2, of a half
+  int split_ns;                           // a slice, where there is room for partial tiles; else 0
+  float* partials;
+  const uint16_t *g, *u;                  // kDh
+  uint16_t *o0, *o1, *o2;
+  int act;
+};
+
+__host__ __device__ __forceinline__ int slices_of(int terms) { return (terms + 63) / 64; }
+
+template <int KIND>
+__device__ __forceinline__ void load_groups(FfnGroups& groups, const FfnTileArgs& a, int rows_per_tile) {
+  // rows: tiles; weights: slices and the epilogue of one tile
+  if constexpr (ffn_over_rows(KIND))
+    groups.load(a.offsets, a.groups, a.M, [](int rows) { return max(slices_of(rows), 1) + kFfnTileSlices; });
+  else
+    groups.load(a.offsets, a.groups, a.M, [=](int rows) { return (rows + rows_per_tile - 1) / rows_per_tile; });
+}
+
+// The XCD's share of the tile list: tiles begin .., R full rounds of its `slots`
+// workgroups, then `tail` < slots tiles, taken whole (P = 0) or cut into runs of P slices,
+// one per workgroup, each covering parts of at most two tiles.
+struct FfnShare {
+  int begin, R, tail, P, KT;              // KT: slices of a tile; 0: not the same for all
+
+  // Of `total` tiles of KT slices (whole numbers, so that host and device agree).
+  __host__ __device__ static FfnShare even(int total, int KT, int xcd, int slots, int split_ns, int tile_floats) {
+    FfnShare s;
+    const int per_xcd = (total + 7) >> 3;
+    s.KT = KT;
+    s.begin = xcd * per_xcd;
+    const int end = s.begin + per_xcd < total ? s.begin + per_xcd : total, len = end > s.begin ? end - s.begin : 0;
+    s.R = len / slots;
+    s.tail = len - s.R * slots;
+    s.P = 0;
+    if (split_ns > 0 && s.tail > 0 && KT > kFfnMinSlices) {
+      const int even = (s.tail * KT + slots - 1) / slots, P = even > kFfnMinSlices ? even : kFfnMinSlices;
+      const int64_t parts = (int64_t)8 * (slots + s.tail) * tile_floats / 256;      // KiB
+      if ((int64_t)P * split_ns + kFfnJoinNs + parts * kFfnJoinNsPer100KiB / 100 < (int64_t)KT * split_ns) s.P = P;
+    }
+    return s;
+  }
+  template <int KIND>
+  __device__ static FfnShare of(const FfnTileArgs& a, const FfnGroups& groups, int xcd, int slots, int tile_floats) {
+    const int per_group = (KIND == kDw13 ? 2 : 1) * a.row_tiles * a.col_tiles;
+    if (!ffn_over_rows(KIND))
+      return even(groups.before(a.groups) * a.col_tiles, (KIND == kDx ? 2 : 1) * slices_of(a.len), xcd, slots, a.split_ns,
+                  tile_floats);
+    if (a.groups == 1)
+      return even(per_group, max(slices_of(groups.first(1) - groups.first(0)), 1), xcd, slots, a.split_ns, tile_floats);
+    FfnShare s;
+    s.KT = s.P = 0;
+    s.begin = bound(groups, a.groups, per_group, xcd);
+    const int len = bound(groups, a.groups, per_group, xcd + 1) - s.begin;
+    s.R = len / slots;
+    s.tail = len - s.R * slots;
+    return s;
+  }
+
+ private:
+  // First tile of XCD x's share: an eighth of all slices each, to a tile.
+  __device__ static int bound(const FfnGroups& groups, int n, int per_group, int x) {
+    if (x == 8) return n * per_group;
+    const int64_t to = (int64_t)x * per_group * groups.before(n) / 8;      // slices before it
+    const int e = groups.of((int)(to / per_group), n);
+    const int w = groups.before(e + 1) - groups.before(e);
+    const int in = (int)((to - (int64_t)per_group * groups.before(e) + w - 1) / w);
+    return e * per_group + min(in, per_group);
+  }
+};
+
+// Stores of 8 columns from c of row r.
+template <int KIND>
+__device__ __forceinline__ void gated_gradients(const FfnTileArgs& a, const float (&dh)[8], uint4 g, uint4 u, uint4& dg,
+                                                uint4& du) {
+  float vg[8], vu[8];
+  unpack8(g, vg);
+  unpack8(u, vu);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float value, slope;
+    act_both<false>(vg[k], a.act, value, slope);
+    vg[k] = dh[k] * vu[k] * slope;
+    vu[k] = dh[k] * value;
+  }
+  dg = pack8(vg);
+  du = pack8(vu);
+}
+
+// The job of workgroup `block` of `blocks` (a multiple of 8).
+template <int KIND, class G>
+struct FfnJob {
+  static constexpr bool kOverRows = ffn_over_rows(KIND), kPair = KIND == kGateUp;
+  static constexpr bool PSLOW = kOverRows, QSLOW = KIND != kGateUp;
+  // e: group; r0, r_end: rows (of the weight for its gradients); first, terms: kDw13, kDw2,
+  // the group's rows; half: kDw13, of w3
+  struct Item { int e, r0, r_end, c0, first, terms, half, kb, ke, part; };
+  const FfnTileArgs& a;
+  const FfnGroups& groups;
+  FfnShare sp;
+  int slots, xcd, slot, n_whole, run0, run1, n_items, wave, half_slices;
+  int load_e = 0, tile_e = 0;             // groups of the two cursors
+
+  __device__ __forceinline__ FfnJob(const FfnTileArgs& args, const FfnGroups& gr, int block, int blocks)
+      : a(args), groups(gr) {
+    slots = blocks >> 3;
+    xcd = block & 7;
+    slot = block >> 3;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    half_slices = slices_of(a.len);
+    sp = FfnShare::of<KIND>(a, groups, xcd, slots, G::PARTIAL);
+    n_whole = sp.R + (sp.P == 0 && slot < sp.tail ? 1 : 0);
+    run0 = slot * sp.P;
+    run1 = min(run0 + sp.P, sp.tail * sp.KT);
+    n_items = n_whole + (run0 < run1 ? (run1 - 1) / sp.KT - run0 / sp.KT + 1 : 0);
+  }
+  __device__ __forceinline__ Item item(int i, int& e) const {
+    Item it{};
+    int t;
+    it.ke = sp.KT;
+    it.part = -1;
+    if (i < n_whole) {
+      t = sp.begin + slot + i * slots;
+    } else {
+      const int j = run0 / sp.KT + (i - n_whole);
+      t = sp.begin + sp.R * slots + j;
+      it.kb = max(run0 - j * sp.KT, 0);
+      it.ke = min(run1 - j * sp.KT, sp.KT);
+      it.part = xcd * 2 * slots + slot + j;
+    }
+    int rt, ct;
+    if constexpr (kOverRows) {
+      const int per_half = a.row_tiles * a.col_tiles, per_group = (KIND == kDw13 ? 2 : 1) * per_half;
+      e = t / per_group;
+      int in = t - e * per_group;
+      if (KIND == kDw13 && in >= per_half) {
+        in -= per_half;
+        it.half = 1;
+      }
+      tile_at(in, a.row_tiles, a.col_tiles, rt, ct);
+      it.first = groups.first(e);
+      it.terms = groups.first(e + 1) - it.first;
+      if (sp.KT == 0) it.ke = max(slices_of(it.terms), 1);     // an empty group: one slice of nothing
+      it.r0 = rt * G::TB;
+      it.r_end = a.rows;
+    } else {
+      while (groups.before(e + 1) * a.col_tiles <= t) ++e;     // tiles ascend
+      const int before = groups.before(e);
+      tile_at(t - before * a.col_tiles, groups.before(e + 1) - before, a.col_tiles, rt, ct);
+      it.r0 = groups.first(e) + rt * G::TB;
+      it.r_end = groups.first(e + 1);
+    }
+    it.e = e;
+    it.c0 = ct * (kPair ? G::TA / 2 : G::TA);
+    it.e = __builtin_amdgcn_readfirstlane(it.e);
+    it.r0 = __builtin_amdgcn_readfirstlane(it.r0);
+    it.r_end = __builtin_amdgcn_readfirstlane(it.r_end);
+    it.c0 = __builtin_amdgcn_readfirstlane(it.c0);
+    it.half = __builtin_amdgcn_readfirstlane(it.half);
+    it.kb = __builtin_amdgcn_readfirstlane(it.kb);
+    it.ke = __builtin_amdgcn_readfirstlane(it.ke);
+    it.part = __builtin_amdgcn_readfirstlane(it.part);
+    return it;
+  }
+  __device__ __forceinline__ Item load_item(int i) { return item(i, load_e); }
+  __device__ __forceinline__ Item tile_item(int i) { return item(i, tile_e); }
+  __device__ __forceinline__ const void* base() const { return a.Q0; }
+  __device__ __forceinline__ int64_t ldp() const { return kOverRows ? a.rows : a.len; }
+  __device__ __forceinline__ int64_t ldq() const { return kPair ? a.len : a.cols; }
+  __device__ __forceinline__ int row_slice(int kt) const { return KIND == kDx && kt >= half_slices ? kt - half_slices : kt; }
+  __device__ __forceinline__ int row_terms() const { return a.len; }
+  __device__ __forceinline__ void descs(const Item& it, int kt, bool first, i32x4_t& dq, i32x4_t& dp) const {
+    const bool second = KIND == kDx && kt >= half_slices;
+    const int64_t t0 = (int64_t)row_slice(kt) * G::BK;
+    if constexpr (kPair) {
+      const uint16_t* q = (wave >> 1) & 1 ? a.Q1 : a.Q0;
+      if (first) dq = make_desc(q + ((int64_t)it.e * a.cols + it.c0) * a.len, min(G::TA / 2, a.cols - it.c0) * ldq() * 2);
+    } else if constexpr (kOverRows) {
+      dq = make_desc(a.Q0 + (it.first + t0) * ldq() + it.c0, ((it.terms - t0) * ldq() - it.c0) * 2);
+    } else {
+      const uint16_t* q = (second ? a.Q1 : a.Q0) + (int64_t)it.e * a.len * a.cols;
+      dq = make_desc(q + t0 * ldq() + it.c0, ((a.len - t0) * ldq() - it.c0) * 2);
+    }
+    if constexpr (kOverRows) {
+      const uint16_t* p = it.half != 0 ? a.P1 : a.P0;
+      dp = make_desc(p + (it.first + t0) * ldp() + it.r0, ((it.terms - t0) * ldp() - it.r0) * 2);
+    } else if (first || (KIND == kDx && kt == half_slices)) {
+      dp = make_desc((second ? a.P1 : a.P0) + it.r0 * ldp(), min(G::TB, it.r_end - it.r0) * ldp() * 2);
+    }
+  }
+
+  template <int WA, int WB>
+  __device__ __forceinline__ void epilogue(const Item& it, f32x4_t (&acc)[WA][WB], int wr, int wc, int lane) const {
+    int i = lane & 15, g = lane >> 4;
+    float* part = it.part >= 0 ? a.partials + (int64_t)it.part * G::PARTIAL : nullptr;
+    if (part != nullptr) {
+#pragma unroll
+      for (int o = 0; o < WA * WB; ++o) {
+        const int x = o % WA, y = o / WA;
+        asm volatile("" : "+v"(i), "+v"(g), "+s"(part));
+        *reinterpret_cast<f32x4_t*>(part + ((wc * WB + y) * 16 + i) * G::TA + (wr * WA + x) * 16 + 4 * g) = acc[x][y];
+        acc[x][y] = f32x4_t{};
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      return;
+    }
+    if constexpr (kPair) {
+      store_gate_up(it, acc, wr, wc, i, g);
+    } else if constexpr (KIND == kDh) {
+      store_gradients(it, acc, wr, wc, i, g);
+    } else {
+      uint16_t* out = it.half != 0 ? a.o1 : a.o0;
+      if constexpr (kOverRows) out += (int64_t)it.e * a.rows * a.cols;
+#pragma unroll
+      for (int o = 0; o < WA * WB / 2; ++o) {
+        const int x = o % (WA / 2) * 2, y = o / (WA / 2);
+        // (addresses are formed anew for every piece: kept, they would cost the product loop registers)
+        asm volatile("" : "+v"(i), "+v"(g), "+s"(out));
+        const int c = it.c0 + (wr * WA + x) * 16 + 8 * g, r = it.r0 + (wc * WB + y) * 16 + i;
+        float v[8];
+        join_blocks(acc[x][y], acc[x + 1][y], v);
+        if (r < it.r_end && c < a.cols) store16<G::STREAM>(out + (int64_t)r * a.cols + c, pack8(v));
+        acc[x][y] = acc[x + 1][y] = f32x4_t{};
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
+  // Blocks 2 n and 2 n + 1 of a wavefront are g and u of the same 16 channels.
+  template <int WA, int WB>
+  __device__ __forceinline__ void store_gate_up(const Item& it, f32x4_t (&acc)[WA][WB], int wr, int wc, int i, int g) const {
+    uint16_t *h = a.o0, *pg = a.o1, *pu = a.o2;
+    int act = a.act;
+    if constexpr (WA == 4) {
+#pragma unroll
+      for (int y = 0; y < WB; ++y) {
+        asm volatile("" : "+v"(i), "+v"(g), "+s"(h), "+s"(pg), "+s"(pu), "+s"(act));
+        const int c = it.c0 + wr * 32 + 8 * g, r = it.r0 + (wc * WB + y) * 16 + i;
+        float vg[8], vu[8];
+        join_blocks(acc[0][y], acc[2][y], vg);
+        join_blocks(acc[1][y], acc[3][y], vu);
+        if (r < it.r_end && c < a.cols) {
+          const int64_t at = (int64_t)r * a.cols + c;
+          if (pg != nullptr) {
+            store16<G::STREAM>(pg + at, pack8(vg));
+            store16<G::STREAM>(pu + at, pack8(vu));
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) vg[k] = act_value<false>(vg[k], act) * vu[k];
+          store16<G::STREAM>(h + at, pack8(vg));
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[x][y] = f32x4_t{};
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      static_assert(WA == 2, "one pair of blocks");
+#pragma unroll
+      for (int y = 0; y < WB; ++y) {
+        asm volatile("" : "+v"(i), "+v"(g), "+s"(h), "+s"(pg), "+s"(pu), "+s"(act));
+        const int c = it.c0 + wr * 16 + 4 * g, r = it.r0 + (wc * WB + y) * 16 + i;
+        const f32x4_t vg = acc[0][y], vu = acc[1][y];
+        if (r < it.r_end && c < a.cols) {
+          const int64_t at = (int64_t)r * a.cols + c;
+          if (pg != nullptr) {
+            *reinterpret_cast<uint2*>(pg + at) = make_uint2(pack_bf16x2(vg[0], vg[1]), pack_bf16x2(vg[2], vg[3]));
+            *reinterpret_cast<uint2*>(pu + at) = make_uint2(pack_bf16x2(vu[0], vu[1]), pack_bf16x2(vu[2], vu[3]));
+          }
+          float v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = act_value<false>(vg[k], act) * vu[k];
+          *reinterpret_cast<uint2*>(h + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+        acc[0][y] = acc[1][y] = f32x4_t{};
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
+  // dg and du: g and u of D pieces (8 channels of a row per lane) are on their way.
+  template <int WA, int WB>
+  __device__ __forceinline__ void store_gradients(const Item& it, f32x4_t (&acc)[WA][WB], int wr, int wc, int i, int g) const {
+    constexpr int N = WA * WB / 2, D = N < 4 ? N : 4;
+    const uint16_t *pg = a.g, *pu = a.u;
+    uint16_t *og = a.o0, *ou = a.o1;
+    uint4 vg[D], vu[D];
+    auto place = [&](int o, int& r, int& c) __attribute__((always_inline)) {
+      c = it.c0 + (wr * WA + o % (WA / 2) * 2) * 16 + 8 * g;
+      r = it.r0 + (wc * WB + o / (WA / 2)) * 16 + i;
+    };
+    auto fetch = [&](int o) __attribute__((always_inline)) {
+      int r, c;
+      place(o, r, c);
+      const int64_t at = (int64_t)min(r, it.r_end - 1) * a.cols + min(c, a.cols - 8);
+      vg[o % D] = load_stream16(pg + at);
+      vu[o % D] = load_stream16(pu + at);
+    };
+#pragma unroll
+    for (int o = 0; o < D; ++o) fetch(o);
+#pragma unroll
+    for (int o = 0; o < N; ++o) {
+      const int x = o % (WA / 2) * 2, y = o / (WA / 2);
+      asm volatile("" : "+v"(i), "+v"(g), "+s"(pg), "+s"(pu), "+s"(og), "+s"(ou));
+      int r, c;
+      place(o, r, c);
+      float v[8];
+      uint4 dg, du;
+      join_blocks(acc[x][y], acc[x + 1][y], v);
+      gated_gradients<KIND>(a, v, vg[o % D], vu[o % D], dg, du);
+      if (r < it.r_end && c < a.cols) {
+        const int64_t at = (int64_t)r * a.cols + c;
+        store16<G::STREAM>(og + at, dg);
+        store16<G::STREAM>(ou + at, du);
+      }
+      if (o + D < N) fetch(o + D);
+      acc[x][y] = acc[x + 1][y] = f32x4_t{};
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
+template <int KIND, int NS, int WR, int WC, int WA, int WB>
+__device__ __forceinline__ void ffn_workgroup(const FfnTileArgs& a, uint8_t* smem, FfnGroups& groups, int block,
+                                              int blocks) {
+  using G = ProductGeom<NS, WR, WC, WA, WB>;
+  load_groups<KIND>(groups, a, G::TB);
+  FfnJob<KIND, G> job(a, groups, block, blocks);
+  if (job.n_items > 0)
+    tile_stream<ffn_over_rows(KIND), KIND != kGateUp, NS, WR, WC, WA, WB>(job, job.ldp(), job.ldq(), smem);
+}
+
+template <int KIND, int NS, int WR, int WC, int WA, int WB>
+__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_tiles_kernel(const FfnTileArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
+  __shared__ FfnGroups groups;
+  ffn_workgroup<KIND, NS, WR, WC, WA, WB>(a, smem, groups, blockIdx.x, gridDim.x);
+}
+
+// Sums the partial tiles of the cut tail tiles in contraction order and applies the
+// epilogue.  One workgroup per (XCD, tail tile, ROWS rows of it), 8 columns (kGateUp:
+// channels, 16 columns) of a row to a lane; four partials are in flight at a time.
+template <int KIND, int TA> constexpr int kFfnJoinRows = (KIND == kGateUp ? 512 : 256) * 8 / TA;
+
+template <int KIND, int TA, int TB>
+__device__ __forceinline__ void ffn_join_workgroup(const FfnTileArgs& a, FfnGroups& groups, int slots, int block) {
+  constexpr int ROWS = kFfnJoinRows<KIND, TA>, RG = TB / ROWS, LANES = 256 / ROWS;
+  load_groups<KIND>(groups, a, TB);
+  const int rg = block % RG, xcd = (block / RG) & 7, j = block / RG >> 3;
+  const FfnShare sp = FfnShare::of<KIND>(a, groups, xcd, slots, TA * TB);
+  if (sp.P == 0 || j >= sp.tail) return;
+  const int t = sp.begin + sp.R * slots + j;
+  int rt, ct, r0, r_end, half = 0;
+  if constexpr (ffn_over_rows(KIND)) {                       // (one group: several are never cut)
+    const int per_half = a.row_tiles * a.col_tiles;
+    half = t >= per_half ? 1 : 0;
+    tile_at(t - half * per_half, a.row_tiles, a.col_tiles, rt, ct);
+    r0 = rt * TB;
+    r_end = a.rows;
+  } else {
+    const int e = groups.of(t / a.col_tiles, a.groups), before = groups.before(e);
+    tile_at(t - before * a.col_tiles, groups.before(e + 1) - before, a.col_tiles, rt, ct);
+    r0 = groups.first(e) + rt * TB;
+    r_end = groups.first(e + 1);
+  }
+  const int s_lo = j * sp.KT / sp.P, s_hi = min(((j + 1) * sp.KT - 1) / sp.P, slots - 1);
+  const int rl = rg * ROWS + threadIdx.x / LANES, cl = threadIdx.x % LANES * 8;
+  const int r = r0 + rl, c = ct * (KIND == kGateUp ? TA / 2 : TA) + cl;
+  if (r >= r_end || c >= a.cols) return;
+  const int64_t at = (int64_t)r * a.cols + c;
+  auto sum = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
+    const float* base = a.partials + (int64_t)(xcd * 2 * slots + j) * (TA * TB) + rl * TA + col;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+    for (int s = s_lo; s <= s_hi; s += 4) {
+      float p[4][8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) load8f(base + (int64_t)min(s + q, s_hi) * (TA * TB), p[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += s + q <= s_hi ? p[q][k] : 0.0f;
+    }
+  };
+  float v[8];
+  if constexpr (KIND == kGateUp) {
+    float w[8];
+    const int col = cl / 16 * 32 + cl % 16;
+    sum(col, v);
+    sum(col + 16, w);
+    if (a.o1 != nullptr) {
+      store16<false>(a.o1 + at, pack8(v));
+      store16<false>(a.o2 + at, pack8(w));
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = act_value<false>(v[k], a.act) * w[k];
+    store16<false>(a.o0 + at, pack8(v));
+  } else if constexpr (KIND == kDh) {
+    const uint4 g = *reinterpret_cast<const uint4*>(a.g + at), u = *reinterpret_cast<const uint4*>(a.u + at);
+    sum(cl, v);
+    uint4 dg, du;
+    gated_gradients<KIND>(a, v, g, u, dg, du);
+    store16<false>(a.o0 + at, dg);
+    store16<false>(a.o1 + at, du);
+  } else {
+    sum(cl, v);
+    store16<false>((half != 0 ? a.o1 : a.o0) + at, pack8(v));
+  }
+}
+
+template <int KIND, int TA, int TB>
+__global__ __launch_bounds__(256) void ffn_join_kernel(const FfnTileArgs a, int slots) {
+  __shared__ FfnGroups groups;
+  ffn_join_workgroup<KIND, TA, TB>(a, groups, slots, blockIdx.x);
+}
+
+}  // namespace moe

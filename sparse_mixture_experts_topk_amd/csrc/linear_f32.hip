@@ -71,8 +71,8 @@ __global__ __launch_bounds__(256) void linear_f32_kernel(const ArgsF32 a) {
   for (int x = 0; x < B; ++x)
 #pragma unroll
     for (int y = 0; y < B; ++y) acc[x][y] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  SliceF32<float, PSLOW, T> p;
-  SliceF32<float, QSLOW, T> q;
+  SliceF32<PSLOW, T> p;
+  SliceF32<QSLOW, T> q;
   p.load(a.P, a.ldp, r0, a.rows, t0, end);
   q.load(a.Q, a.ldq, c0, a.cols, t0, end);
   int stage = 0;

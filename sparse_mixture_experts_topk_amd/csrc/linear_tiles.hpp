@@ -128,6 +128,13 @@ struct LoadMap {
     return (wave * RPI + lane / CPR) * rowbytes + chunk(wave, lane, j) * 16;   // + j * step
   }
   __device__ static __forceinline__ int step(int rowbytes) { return NW * RPI * rowbytes; }
+  // Of two operands in turn, 16 rows of each: LDS rows (NW j + wave) 8 .. are rows 32 j +
+  // 16 (wave / 4) + 8 (wave % 2) .. of operand wave / 2 % 2.
+  __device__ static __forceinline__ int pair_offset(int wave, int lane, int rowbytes) {
+    static_assert(SLOW || (NW == 8 && RPI == 8 && PERIOD == 1), "a wavefront's rows are all from one operand");
+    return ((wave >> 2) * 16 + (wave & 1) * 8 + lane / CPR) * rowbytes + chunk(wave, lane, 0) * 16;
+  }
+  __device__ static __forceinline__ int pair_step(int rowbytes) { return 32 * rowbytes; }
 };
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -178,9 +185,21 @@ __device__ __forceinline__ void join_blocks(f32x4_t a, f32x4_t b, float (&v)[8])
   }
 }
 
-// Workgroup `block` of the `blocks` (a multiple of 8) that share the product.
-template <bool PSLOW, bool QSLOW, int ACT, int NS, int WR, int WC, int WA, int WB>
-__device__ __forceinline__ void product_workgroup(const ProductArgs& a, uint8_t* smem, int block, int blocks) {
+// The stream of one workgroup's tiles.  The job says which they are, where their
+// operands' slices lie and what becomes of the products:
+//   n_items                 tiles, or runs of slices of one, of this workgroup
+//   load_item(i), tile_item(i)   item i, slices [kb, ke), ke > kb: the first for the loads,
+//                           the second for the products, each called with ascending i
+//   descs(item, kt, first, dq, dp)   operands at slice kt of the item: a [t][r] operand's
+//                           descriptor is of that slice (its rows may lie more than 2^31
+//                           bytes apart), a [r][t] operand's of the tile (or a half of
+//                           it, if the contraction has halves) and set when that begins
+//   row_slice(kt), row_terms()   slice kt's place in a [r][t] operand's row, and the row's length
+//   kPair                   Q is 16 rows of one operand and 16 of another in turn, both [r][t]
+//                           (descs gives the one that this wavefront loads)
+//   epilogue(item, acc, wr, wc, lane)   stores a tile's products and clears them
+template <bool PSLOW, bool QSLOW, int NS, int WR, int WC, int WA, int WB, class Job>
+__device__ __forceinline__ void tile_stream(Job& job, int64_t ldp, int64_t ldq, uint8_t* smem) {
   using G = ProductGeom<NS, WR, WC, WA, WB>;
   using MA = LoadMap<QSLOW, G::TA, G::NW>;
   using MB = LoadMap<PSLOW, G::TB, G::NW>;
@@ -188,72 +207,29 @@ __device__ __forceinline__ void product_workgroup(const ProductArgs& a, uint8_t*
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WC, wc = wave % WC;
-  const int KT = (a.len + BK - 1) / BK;
-  const int slots = blocks >> 3, xcd = block & 7, slot = block >> 3;
-  const TileShare sp = TileShare::of(a.row_tiles * a.col_tiles, xcd, slots, KT, a.split);
-  const int n_whole = sp.R + (!a.split && slot < sp.tail ? 1 : 0);
-  const int run0 = slot * sp.P, run1 = min(run0 + sp.P, sp.tail * KT);
-  const int n_runs = run0 < run1 ? (run1 - 1) / KT - run0 / KT + 1 : 0;
-  const int n_items = n_whole + n_runs;
-  if (n_items == 0) return;
-
-  // Item i: a whole tile, or a run [kb, ke) of slices of tail tile j (partial tile slot + j of the XCD's).
-  struct Item { int r0, c0, kb, ke, part; };
-  auto item = [&](int i) __attribute__((always_inline)) -> Item {
-    Item it{0, 0, 0, KT, -1};
-    int t;
-    if (i < n_whole) {
-      t = sp.begin + slot + i * slots;
-    } else {
-      const int j = run0 / KT + (i - n_whole);
-      t = sp.begin + sp.R * slots + j;
-      it.kb = max(run0 - j * KT, 0);
-      it.ke = min(run1 - j * KT, KT);
-      it.part = xcd * 2 * slots + slot + j;
-    }
-    int rt, ct;
-    tile_at(t, a.row_tiles, a.col_tiles, rt, ct);
-    it.r0 = __builtin_amdgcn_readfirstlane(rt * G::TB);
-    it.c0 = __builtin_amdgcn_readfirstlane(ct * G::TA);
-    it.kb = __builtin_amdgcn_readfirstlane(it.kb);
-    it.ke = __builtin_amdgcn_readfirstlane(it.ke);
-    it.part = __builtin_amdgcn_readfirstlane(it.part);
-    return it;
-  };
 
   // ---- loads ----
-  // Load cursor: slice lkt of item li.  A [r][t] operand keeps its tile's
-  // descriptor and moves along its rows by the scalar offset; a [t][r] one gets
-  // a descriptor per slice (its rows may lie more than 2^31 bytes apart).
+  // Load cursor: slice lkt of item li.  A [r][t] operand moves along its rows by the scalar offset.
   const uint32_t lds_base = (uint32_t)(uintptr_t)smem;
-  const int qrow = (int)a.ldq * 2, prow = (int)a.ldp * 2;          // bytes
-  int li = 0, lkt = 0, lke = 0, lr0 = 0, lc0 = 0;
+  const int qrow = (int)ldq * 2, prow = (int)ldp * 2;          // bytes
+  int li = 0, lkt = 0;
+  typename Job::Item lit{};
   i32x4_t dq, dp;
-  auto slice_descs = [&](bool first) __attribute__((always_inline)) {
-    const int64_t t0 = (int64_t)lkt * BK;
-    if constexpr (QSLOW) dq = make_desc(a.Q + t0 * a.ldq + lc0, ((a.len - t0) * a.ldq - lc0) * 2);
-    else if (first) dq = make_desc(a.Q + lc0 * a.ldq, min(G::TA, a.cols - lc0) * a.ldq * 2);
-    if constexpr (PSLOW) dp = make_desc(a.P + t0 * a.ldp + lr0, ((a.len - t0) * a.ldp - lr0) * 2);
-    else if (first) dp = make_desc(a.P + lr0 * a.ldp, min(G::TB, a.rows - lr0) * a.ldp * 2);
-  };
   auto load_item = [&]() __attribute__((always_inline)) {
-    if (li < n_items) {
-      const Item it = item(li);
-      lkt = it.kb;
-      lke = it.ke;
-      lr0 = it.r0;
-      lc0 = it.c0;
-      slice_descs(true);
+    if (li < job.n_items) {
+      lit = job.load_item(li);
+      lkt = lit.kb;
+      job.descs(lit, lkt, true, dq, dp);
     } else {                                       // past the last slice nothing is in range: zeros, no memory read
-      dq = make_desc(a.Q, 0);
-      dp = make_desc(a.P, 0);
-      lke = 0x7fffffff;
+      dq = make_desc(job.base(), 0);
+      dp = make_desc(job.base(), 0);
+      lit.ke = 0x7fffffff;
     }
   };
   int qoff[MA::PERIOD], poff[MB::PERIOD], qch[MA::PERIOD], pch[MB::PERIOD];
 #pragma unroll
   for (int j = 0; j < MA::PERIOD; ++j) {
-    qoff[j] = MA::offset(wave, lane, j, qrow);
+    qoff[j] = Job::kPair ? MA::pair_offset(wave, lane, qrow) : MA::offset(wave, lane, j, qrow);
     qch[j] = MA::chunk(wave, lane, j) * 8;
   }
 #pragma unroll
@@ -261,29 +237,31 @@ __device__ __forceinline__ void product_workgroup(const ProductArgs& a, uint8_t*
     poff[j] = MB::offset(wave, lane, j, prow);
     pch[j] = MB::chunk(wave, lane, j) * 8;
   }
+  const int qstep = Job::kPair ? MA::pair_step(qrow) : MA::step(qrow);
   // a chunk of a [r][t] row past the contraction's end goes out of range
   constexpr int kPast = (int)0x80000000u;
   auto load = [&](int ls, int j) __attribute__((always_inline)) {
     const uint32_t sb = lds_base + (uint32_t)((ls % NS) * G::STAGE);
+    const int k0 = job.row_slice(lkt) * BK;
     if (j < G::JA) {
       int off = qoff[j % MA::PERIOD];
-      if constexpr (!QSLOW) off = lkt * BK + qch[j % MA::PERIOD] >= a.len ? kPast : off;
-      dma_to_lds(dq, off + j * MA::step(qrow), QSLOW ? 0 : lkt * (BK * 2),
+      if constexpr (!QSLOW) off = k0 + qch[j % MA::PERIOD] >= job.row_terms() ? kPast : off;
+      dma_to_lds(dq, off + j * qstep, QSLOW ? 0 : k0 * 2,
                  __builtin_amdgcn_readfirstlane(sb + (G::NW * j + wave) * 1024));
     } else {
       const int q = j - G::JA;
       int off = poff[q % MB::PERIOD];
-      if constexpr (!PSLOW) off = lkt * BK + pch[q % MB::PERIOD] >= a.len ? kPast : off;
-      dma_to_lds(dp, off + q * MB::step(prow), PSLOW ? 0 : lkt * (BK * 2),
+      if constexpr (!PSLOW) off = k0 + pch[q % MB::PERIOD] >= job.row_terms() ? kPast : off;
+      dma_to_lds(dp, off + q * MB::step(prow), PSLOW ? 0 : k0 * 2,
                  __builtin_amdgcn_readfirstlane(sb + G::A_BYTES + (G::NW * q + wave) * 1024));
     }
   };
   auto advance = [&]() __attribute__((always_inline)) {
-    if (++lkt >= lke) {
+    if (++lkt >= lit.ke) {
       ++li;
       load_item();
-    } else if (li < n_items) {
-      slice_descs(false);
+    } else if (li < job.n_items) {
+      job.descs(lit, lkt, false, dq, dp);
     }
   };
 
@@ -324,28 +302,6 @@ __device__ __forceinline__ void product_workgroup(const ProductArgs& a, uint8_t*
     __builtin_amdgcn_s_setprio(0);
   };
 
-  auto epilogue = [&](const Item& it) __attribute__((always_inline)) {
-    int i = lane & 15, g = lane >> 4;
-    float* part = it.part >= 0 ? a.partials + (int64_t)it.part * G::PARTIAL : nullptr;
-    Epilogue ep = a.ep;
-#pragma unroll
-    for (int o = 0; o < WA * WB / 2; ++o) {
-      const int x = o % (WA / 2) * 2, y = o / (WA / 2);          // a row's 64-byte pieces one after the other
-      // Addresses are formed here and the choices made anew for every piece: kept in
-      // registers, or followed through one copy of the epilogue per combination,
-      // they would cost the product loop registers (spills: 0.7 -> 2.8 ms).
-      asm volatile("" : "+v"(i), "+v"(g), "+s"(part), "+s"(ep.bias), "+s"(ep.residual), "+s"(ep.pre), "+s"(ep.f32));
-      const int cl = (wr * WA + x) * 16 + 8 * g, c = it.c0 + cl;
-      const int rl = (wc * WB + y) * 16 + i, r = it.r0 + rl;
-      float v[8];
-      join_blocks(acc[x][y], acc[x + 1][y], v);
-      if (part != nullptr) store8f(part + rl * G::TA + cl, v);
-      else if (r < a.rows && c < a.cols) ep.template store8<ACT, G::STREAM>(r, c, a.cols, v);
-      acc[x][y] = acc[x + 1][y] = f32x4_t{};          // the next item starts from zero
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-
   // Slice g of the stream lives in stage g % NS.  Its first half reads the second
   // half's fragments; then this wavefront's loads of slice g + 1 are in, its LDS
   // reads done, barrier: slice g + 1 is whole and stage g % NS is no longer read.
@@ -365,8 +321,8 @@ __device__ __forceinline__ void product_workgroup(const ProductArgs& a, uint8_t*
 #pragma unroll
     for (int y = 0; y < WB; ++y) acc[x][y] = f32x4_t{};
   int g = 0;
-  for (int ci = 0; ci < n_items; ++ci) {
-    const Item it = item(ci);
+  for (int ci = 0; ci < job.n_items; ++ci) {
+    const typename Job::Item it = job.tile_item(ci);
     // (read again after the last item's read ahead: no fragment lives through the epilogue)
 #pragma unroll
     for (int x = 0; x < WA; ++x) fa[0][x] = read_a(g, 0, x);
@@ -382,9 +338,93 @@ __device__ __forceinline__ void product_workgroup(const ProductArgs& a, uint8_t*
       half(1, g + 1, 0, true, g + NS);
       advance();
     }
-    epilogue(it);
+    job.epilogue(it, acc, wr, wc, lane);
   }
   wait_vmcnt<0>();   // the zero loads past the end land before the workgroup's LDS is released
+}
+
+// The job of workgroup `block` of the `blocks` (a multiple of 8) that share a dense product.
+template <bool PSLOW, bool QSLOW, int ACT, class G>
+struct DenseJob {
+  static constexpr bool kPair = false;
+  struct Item { int r0, c0, kb, ke, part; };
+  const ProductArgs& a;
+  TileShare sp;
+  int KT, slots, xcd, slot, n_whole, run0, run1, n_items;
+
+  __device__ __forceinline__ DenseJob(const ProductArgs& args, int block, int blocks) : a(args) {
+    KT = (a.len + G::BK - 1) / G::BK;
+    slots = blocks >> 3;
+    xcd = block & 7;
+    slot = block >> 3;
+    sp = TileShare::of(a.row_tiles * a.col_tiles, xcd, slots, KT, a.split);
+    n_whole = sp.R + (!a.split && slot < sp.tail ? 1 : 0);
+    run0 = slot * sp.P;
+    run1 = min(run0 + sp.P, sp.tail * KT);
+    n_items = n_whole + (run0 < run1 ? (run1 - 1) / KT - run0 / KT + 1 : 0);
+  }
+  // Item i: a whole tile, or a run [kb, ke) of slices of tail tile j (partial tile slot + j of the XCD's).
+  __device__ __forceinline__ Item item(int i) const {
+    Item it{0, 0, 0, KT, -1};
+    int t;
+    if (i < n_whole) {
+      t = sp.begin + slot + i * slots;
+    } else {
+      const int j = run0 / KT + (i - n_whole);
+      t = sp.begin + sp.R * slots + j;
+      it.kb = max(run0 - j * KT, 0);
+      it.ke = min(run1 - j * KT, KT);
+      it.part = xcd * 2 * slots + slot + j;
+    }
+    int rt, ct;
+    tile_at(t, a.row_tiles, a.col_tiles, rt, ct);
+    it.r0 = __builtin_amdgcn_readfirstlane(rt * G::TB);
+    it.c0 = __builtin_amdgcn_readfirstlane(ct * G::TA);
+    it.kb = __builtin_amdgcn_readfirstlane(it.kb);
+    it.ke = __builtin_amdgcn_readfirstlane(it.ke);
+    it.part = __builtin_amdgcn_readfirstlane(it.part);
+    return it;
+  }
+  __device__ __forceinline__ Item load_item(int i) const { return item(i); }
+  __device__ __forceinline__ Item tile_item(int i) const { return item(i); }
+  __device__ __forceinline__ const void* base() const { return a.Q; }
+  __device__ __forceinline__ int row_slice(int kt) const { return kt; }
+  __device__ __forceinline__ int row_terms() const { return a.len; }
+  __device__ __forceinline__ void descs(const Item& it, int kt, bool first, i32x4_t& dq, i32x4_t& dp) const {
+    const int64_t t0 = (int64_t)kt * G::BK;
+    if constexpr (QSLOW) dq = make_desc(a.Q + t0 * a.ldq + it.c0, ((a.len - t0) * a.ldq - it.c0) * 2);
+    else if (first) dq = make_desc(a.Q + it.c0 * a.ldq, min(G::TA, a.cols - it.c0) * a.ldq * 2);
+    if constexpr (PSLOW) dp = make_desc(a.P + t0 * a.ldp + it.r0, ((a.len - t0) * a.ldp - it.r0) * 2);
+    else if (first) dp = make_desc(a.P + it.r0 * a.ldp, min(G::TB, a.rows - it.r0) * a.ldp * 2);
+  }
+  template <int WA, int WB>
+  __device__ __forceinline__ void epilogue(const Item& it, f32x4_t (&acc)[WA][WB], int wr, int wc, int lane) const {
+    int i = lane & 15, g = lane >> 4;
+    float* part = it.part >= 0 ? a.partials + (int64_t)it.part * G::PARTIAL : nullptr;
+    Epilogue ep = a.ep;
+#pragma unroll
+    for (int o = 0; o < WA * WB / 2; ++o) {
+      const int x = o % (WA / 2) * 2, y = o / (WA / 2);          // a row's 64-byte pieces one after the other
+      // Addresses are formed here and the choices made anew for every piece: kept in
+      // registers, or followed through one copy of the epilogue per combination,
+      // they would cost the product loop registers (spills: 0.7 -> 2.8 ms).
+      asm volatile("" : "+v"(i), "+v"(g), "+s"(part), "+s"(ep.bias), "+s"(ep.residual), "+s"(ep.pre), "+s"(ep.f32));
+      const int cl = (wr * WA + x) * 16 + 8 * g, c = it.c0 + cl;
+      const int rl = (wc * WB + y) * 16 + i, r = it.r0 + rl;
+      float v[8];
+      join_blocks(acc[x][y], acc[x + 1][y], v);
+      if (part != nullptr) store8f(part + rl * G::TA + cl, v);
+      else if (r < a.rows && c < a.cols) ep.template store8<ACT, G::STREAM>(r, c, a.cols, v);
+      acc[x][y] = acc[x + 1][y] = f32x4_t{};          // the next item starts from zero
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
+template <bool PSLOW, bool QSLOW, int ACT, int NS, int WR, int WC, int WA, int WB>
+__device__ __forceinline__ void product_workgroup(const ProductArgs& a, uint8_t* smem, int block, int blocks) {
+  DenseJob<PSLOW, QSLOW, ACT, ProductGeom<NS, WR, WC, WA, WB>> job(a, block, blocks);
+  if (job.n_items > 0) tile_stream<PSLOW, QSLOW, NS, WR, WC, WA, WB>(job, a.ldp, a.ldq, smem);
 }
 
 template <bool PSLOW, bool QSLOW, int ACT, int NS, int WR, int WC, int WA, int WB>
