@@ -106,7 +106,64 @@ struct FfnShare {
   }
 };
 
-// Stores of 8 columns from c of row r.
+// Four values as bf16.
+template <class V>
+__device__ __forceinline__ u32x2_t pack4(const V& v) {
+  return u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
+// A product leaves lane (i, g) with 4 columns of row i from each block; a store wants
+// neighbouring lanes on neighbouring columns, for memory takes whole 128-byte lines far
+// better than 64 scattered pieces of 16 bytes (the weight gradients of 8 groups of 1024
+// rows, 4096 x 14336: 2 x 1875 us against 2120, 935 against 1010).  A row block goes
+// through 1 KiB of LDS of the wavefront's own: one wavefront's LDS operations execute in
+// order, so nothing waits but the reads' results.
+//
+// `Columns` = 64: 8 rows of 128 bytes at a time, 8 lanes a row; 32: 16 rows of 64 bytes, 4
+// lanes a row.  The 16-byte chunks are swizzled by row.
+template <int Columns>
+struct RowStore {
+  static constexpr int ROWS = 512 / Columns, LANES = Columns / 8, TIMES = 16 / ROWS;
+  static_assert(Columns == 64 || Columns == 32, "a wavefront's columns");
+  __device__ static __forceinline__ int key(int row) { return Columns == 64 ? row : row >> 2; }
+  // This lane's row and first column in time 0.
+  __device__ static __forceinline__ int row(int lane) { return lane / LANES; }
+  __device__ static __forceinline__ int column(int lane) { return lane % LANES * 8; }
+  // w: 4 columns of each 16-column block of row i; v[n]: 8 columns of row n ROWS + row(lane).
+  __device__ static __forceinline__ void turn(uint8_t* lds, const u32x2_t (&w)[Columns / 16], int lane,
+                                              u32x4_t (&v)[TIMES]) {
+    const int i = lane & 15, g = lane >> 4, r = i % ROWS;
+    uint8_t* to = lds + r * (Columns * 2) + (g & 1) * 8;
+    const uint8_t* from = lds + row(lane) * (Columns * 2) + ((lane % LANES ^ key(row(lane))) << 4);
+#pragma unroll
+    for (int n = 0; n < TIMES; ++n) {
+      if (TIMES == 1 || i / ROWS == n) {
+#pragma unroll
+        for (int x = 0; x < Columns / 16; ++x)
+          *reinterpret_cast<u32x2_t*>(to + ((2 * x + (g >> 1)) ^ key(r)) * 16) = w[x];
+      }
+      asm volatile("" ::: "memory");             // (every lane's part, before any lane's read)
+      v[n] = *reinterpret_cast<const u32x4_t*>(from);
+      asm volatile("" ::: "memory");
+    }
+  }
+};
+
+// A tile's part of a bf16 output: a store outside the tile's rows or columns is dropped.
+struct TileOut {
+  __amdgpu_buffer_rsrc_t desc;
+  // rows, cols: what there is from the tile's first row r0 and column c0 on
+  __device__ __forceinline__ TileOut(uint16_t* out, int64_t ld, int r0, int c0, int rows, int cols)
+      : desc(__builtin_amdgcn_make_buffer_rsrc(out + r0 * ld + c0, 0, (int)(((rows - 1) * ld + cols) * 2), kRawBufferFlags)) {}
+  template <bool STREAM>
+  __device__ __forceinline__ void store(int off, u32x4_t v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, desc, off, 0, STREAM ? 2 : 0);      // 2: non-temporal
+  }
+  __device__ __forceinline__ void store(int off, u32x2_t v) const {
+    __builtin_amdgcn_raw_buffer_store_b64(v, desc, off, 0, 0);
+  }
+};
+
 template <int KIND>
 __device__ __forceinline__ void gated_gradients(const FfnTileArgs& a, const float (&dh)[8], uint4 g, uint4 u, uint4& dg,
                                                 uint4& du) {
@@ -124,22 +181,29 @@ __device__ __forceinline__ void gated_gradients(const FfnTileArgs& a, const floa
   du = pack8(vu);
 }
 
+struct FfnLds {
+  __attribute__((aligned(16))) uint8_t turned[8][1024];
+  FfnGroups groups;
+};
+
 // The job of workgroup `block` of `blocks` (a multiple of 8).
 template <int KIND, class G>
 struct FfnJob {
   static constexpr bool kOverRows = ffn_over_rows(KIND), kPair = KIND == kGateUp;
-  static constexpr bool PSLOW = kOverRows, QSLOW = KIND != kGateUp;
+  static constexpr bool kNt = G::STREAM && (KIND == kDw13 || KIND == kDw2);
+  static constexpr int kStores = kPair ? G::WB : KIND == kDh ? G::WA * G::WB : G::WA * G::WB / 2;
   // e: group; r0, r_end: rows (of the weight for its gradients); first, terms: kDw13, kDw2,
   // the group's rows; half: kDw13, of w3
   struct Item { int e, r0, r_end, c0, first, terms, half, kb, ke, part; };
   const FfnTileArgs& a;
   const FfnGroups& groups;
+  uint8_t* turned;                        // 1 KiB of LDS of this wavefront's
   FfnShare sp;
   int slots, xcd, slot, n_whole, run0, run1, n_items, wave, half_slices;
   int load_e = 0, tile_e = 0;             // groups of the two cursors
 
-  __device__ __forceinline__ FfnJob(const FfnTileArgs& args, const FfnGroups& gr, int block, int blocks)
-      : a(args), groups(gr) {
+  __device__ __forceinline__ FfnJob(const FfnTileArgs& args, FfnLds& lds, int block, int blocks)
+      : a(args), groups(lds.groups), turned(lds.turned[__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)]) {
     slots = blocks >> 3;
     xcd = block & 7;
     slot = block >> 3;
@@ -191,7 +255,7 @@ struct FfnJob {
     it.c0 = ct * (kPair ? G::TA / 2 : G::TA);
     it.e = __builtin_amdgcn_readfirstlane(it.e);
     it.r0 = __builtin_amdgcn_readfirstlane(it.r0);
-    it.r_end = __builtin_amdgcn_readfirstlane(it.r_end);
+    if constexpr (!kOverRows) it.r_end = __builtin_amdgcn_readfirstlane(it.r_end);
     it.c0 = __builtin_amdgcn_readfirstlane(it.c0);
     it.half = __builtin_amdgcn_readfirstlane(it.half);
     it.kb = __builtin_amdgcn_readfirstlane(it.kb);
@@ -228,6 +292,7 @@ struct FfnJob {
 
   template <int WA, int WB>
   __device__ __forceinline__ void epilogue(const Item& it, f32x4_t (&acc)[WA][WB], int wr, int wc, int lane) const {
+    asm volatile("" : "+v"(lane));          // (places in rows are formed here: kept, they would cost the product loop registers)
     int i = lane & 15, g = lane >> 4;
     float* part = it.part >= 0 ? a.partials + (int64_t)it.part * G::PARTIAL : nullptr;
     if (part != nullptr) {
@@ -241,74 +306,79 @@ struct FfnJob {
       }
       return;
     }
+    // Offsets from the tile's corner: one per pair of column blocks, out of range where
+    // there is no such column; a row block adds `step`.
+    const int rows = min(it.r_end - it.r0, G::TB), cols = a.cols - it.c0, step = 16 * a.cols * 2;
+    constexpr int kPast = (int)0x80000000u;
     if constexpr (kPair) {
-      store_gate_up(it, acc, wr, wc, i, g);
+      // Blocks 2 n and 2 n + 1 of a wavefront are g and u of the same 16 channels.
+      const TileOut h(a.o0, a.cols, it.r0, it.c0, rows, cols);
+      const bool keep = a.o1 != nullptr;
+      const TileOut pg(keep ? a.o1 : a.o0, a.cols, it.r0, it.c0, rows, cols);
+      const TileOut pu(keep ? a.o2 : a.o0, a.cols, it.r0, it.c0, rows, cols);
+      using Rows = RowStore<32>;
+      const int c = WA == 4 ? wr * 32 + Rows::column(lane) : wr * 16 + 4 * g, r = WA == 4 ? Rows::row(lane) : i;
+      int off = c < cols ? ((wc * WB * 16 + r) * a.cols + c) * 2 : kPast;
+#pragma unroll
+      for (int y = 0; y < WB; ++y) {
+        asm volatile("" : "+v"(off));             // (or the row blocks' offsets are all formed at once)
+        u32x2_t wh[WA / 2], wg[WA / 2], wu[WA / 2];
+#pragma unroll
+        for (int n = 0; n < WA / 2; ++n) {
+          const f32x4_t vg = acc[2 * n][y], vu = acc[2 * n + 1][y];
+          float vh[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) vh[k] = act_value<false>(vg[k], a.act) * vu[k];
+          wh[n] = pack4(vh);
+          wg[n] = pack4(vg);
+          wu[n] = pack4(vu);
+        }
+        if constexpr (WA == 4) {
+          u32x4_t v[1];
+          Rows::turn(turned, wh, lane, v);
+          h.template store<kNt>(off, v[0]);
+          if (keep) {
+            Rows::turn(turned, wg, lane, v);
+            pg.template store<kNt>(off, v[0]);
+            Rows::turn(turned, wu, lane, v);
+            pu.template store<kNt>(off, v[0]);
+          }
+        } else {
+          static_assert(WA == 2, "one pair of blocks, or two");
+          h.store(off, wh[0]);
+          if (keep) {
+            pg.store(off, wg[0]);
+            pu.store(off, wu[0]);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < WA; ++x) acc[x][y] = f32x4_t{};
+        off += step;
+        __builtin_amdgcn_sched_barrier(0);
+      }
     } else if constexpr (KIND == kDh) {
       store_gradients(it, acc, wr, wc, i, g);
     } else {
-      uint16_t* out = it.half != 0 ? a.o1 : a.o0;
-      if constexpr (kOverRows) out += (int64_t)it.e * a.rows * a.cols;
-#pragma unroll
-      for (int o = 0; o < WA * WB / 2; ++o) {
-        const int x = o % (WA / 2) * 2, y = o / (WA / 2);
-        // (addresses are formed anew for every piece: kept, they would cost the product loop registers)
-        asm volatile("" : "+v"(i), "+v"(g), "+s"(out));
-        const int c = it.c0 + (wr * WA + x) * 16 + 8 * g, r = it.r0 + (wc * WB + y) * 16 + i;
-        float v[8];
-        join_blocks(acc[x][y], acc[x + 1][y], v);
-        if (r < it.r_end && c < a.cols) store16<G::STREAM>(out + (int64_t)r * a.cols + c, pack8(v));
-        acc[x][y] = acc[x + 1][y] = f32x4_t{};
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-  }
-
-  // Blocks 2 n and 2 n + 1 of a wavefront are g and u of the same 16 channels.
-  template <int WA, int WB>
-  __device__ __forceinline__ void store_gate_up(const Item& it, f32x4_t (&acc)[WA][WB], int wr, int wc, int i, int g) const {
-    uint16_t *h = a.o0, *pg = a.o1, *pu = a.o2;
-    int act = a.act;
-    if constexpr (WA == 4) {
+      using Rows = RowStore<16 * WA>;
+      uint16_t* to = it.half != 0 ? a.o1 : a.o0;
+      if constexpr (kOverRows) to += (int64_t)it.e * a.rows * a.cols;
+      const TileOut out(to, a.cols, it.r0, it.c0, rows, cols);
+      const int c = wr * WA * 16 + Rows::column(lane), time = Rows::ROWS * a.cols * 2;
+      int off = c < cols ? ((wc * WB * 16 + Rows::row(lane)) * a.cols + c) * 2 : kPast;
 #pragma unroll
       for (int y = 0; y < WB; ++y) {
-        asm volatile("" : "+v"(i), "+v"(g), "+s"(h), "+s"(pg), "+s"(pu), "+s"(act));
-        const int c = it.c0 + wr * 32 + 8 * g, r = it.r0 + (wc * WB + y) * 16 + i;
-        float vg[8], vu[8];
-        join_blocks(acc[0][y], acc[2][y], vg);
-        join_blocks(acc[1][y], acc[3][y], vu);
-        if (r < it.r_end && c < a.cols) {
-          const int64_t at = (int64_t)r * a.cols + c;
-          if (pg != nullptr) {
-            store16<G::STREAM>(pg + at, pack8(vg));
-            store16<G::STREAM>(pu + at, pack8(vu));
-          }
+        asm volatile("" : "+v"(off));
+        u32x2_t w[WA];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) vg[k] = act_value<false>(vg[k], act) * vu[k];
-          store16<G::STREAM>(h + at, pack8(vg));
+        for (int x = 0; x < WA; ++x) {
+          w[x] = pack4(acc[x][y]);
+          acc[x][y] = f32x4_t{};
         }
+        u32x4_t v[Rows::TIMES];
+        Rows::turn(turned, w, lane, v);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) acc[x][y] = f32x4_t{};
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    } else {
-      static_assert(WA == 2, "one pair of blocks");
-#pragma unroll
-      for (int y = 0; y < WB; ++y) {
-        asm volatile("" : "+v"(i), "+v"(g), "+s"(h), "+s"(pg), "+s"(pu), "+s"(act));
-        const int c = it.c0 + wr * 16 + 4 * g, r = it.r0 + (wc * WB + y) * 16 + i;
-        const f32x4_t vg = acc[0][y], vu = acc[1][y];
-        if (r < it.r_end && c < a.cols) {
-          const int64_t at = (int64_t)r * a.cols + c;
-          if (pg != nullptr) {
-            *reinterpret_cast<uint2*>(pg + at) = make_uint2(pack_bf16x2(vg[0], vg[1]), pack_bf16x2(vg[2], vg[3]));
-            *reinterpret_cast<uint2*>(pu + at) = make_uint2(pack_bf16x2(vu[0], vu[1]), pack_bf16x2(vu[2], vu[3]));
-          }
-          float v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = act_value<false>(vg[k], act) * vu[k];
-          *reinterpret_cast<uint2*>(h + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        }
-        acc[0][y] = acc[1][y] = f32x4_t{};
+        for (int n = 0; n < Rows::TIMES; ++n) out.template store<kNt>(off + n * time, v[n]);
+        off += step;
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -317,51 +387,50 @@ struct FfnJob {
   // dg and du: g and u of D pieces (8 channels of a row per lane) are on their way.
   template <int WA, int WB>
   __device__ __forceinline__ void store_gradients(const Item& it, f32x4_t (&acc)[WA][WB], int wr, int wc, int i, int g) const {
-    constexpr int N = WA * WB / 2, D = N < 4 ? N : 4;
-    const uint16_t *pg = a.g, *pu = a.u;
-    uint16_t *og = a.o0, *ou = a.o1;
-    uint4 vg[D], vu[D];
-    auto place = [&](int o, int& r, int& c) __attribute__((always_inline)) {
-      c = it.c0 + (wr * WA + o % (WA / 2) * 2) * 16 + 8 * g;
-      r = it.r0 + (wc * WB + o / (WA / 2)) * 16 + i;
-    };
+    constexpr int NB = WA / 2, N = NB * WB, D = N < 4 ? N : 4;
+    const int rows = min(it.r_end - it.r0, G::TB), cols = a.cols - it.c0, step = 16 * a.cols * 2;
+    const TileOut og(a.o0, a.cols, it.r0, it.c0, rows, cols), ou(a.o1, a.cols, it.r0, it.c0, rows, cols);
+    // (what is out of range loads as zero)
+    const TileOut pg(const_cast<uint16_t*>(a.g), a.cols, it.r0, it.c0, rows, cols);
+    const TileOut pu(const_cast<uint16_t*>(a.u), a.cols, it.r0, it.c0, rows, cols);
+    u32x4_t vg[D], vu[D];
+    int off[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int c = (wr * WA + 2 * n) * 16 + 8 * g;
+      off[n] = c < cols ? ((wc * WB * 16 + i) * a.cols + c) * 2 : (int)0x80000000u;
+    }
     auto fetch = [&](int o) __attribute__((always_inline)) {
-      int r, c;
-      place(o, r, c);
-      const int64_t at = (int64_t)min(r, it.r_end - 1) * a.cols + min(c, a.cols - 8);
-      vg[o % D] = load_stream16(pg + at);
-      vu[o % D] = load_stream16(pu + at);
+      const int at = off[o % NB] + (o / NB) * step;
+      vg[o % D] = __builtin_amdgcn_raw_buffer_load_b128(pg.desc, at, 0, 2);
+      vu[o % D] = __builtin_amdgcn_raw_buffer_load_b128(pu.desc, at, 0, 2);
     };
 #pragma unroll
     for (int o = 0; o < D; ++o) fetch(o);
 #pragma unroll
     for (int o = 0; o < N; ++o) {
-      const int x = o % (WA / 2) * 2, y = o / (WA / 2);
-      asm volatile("" : "+v"(i), "+v"(g), "+s"(pg), "+s"(pu), "+s"(og), "+s"(ou));
-      int r, c;
-      place(o, r, c);
+      const int n = o % NB, y = o / NB;
+      asm volatile("" : "+v"(off[n]));
       float v[8];
       uint4 dg, du;
-      join_blocks(acc[x][y], acc[x + 1][y], v);
-      gated_gradients<KIND>(a, v, vg[o % D], vu[o % D], dg, du);
-      if (r < it.r_end && c < a.cols) {
-        const int64_t at = (int64_t)r * a.cols + c;
-        store16<G::STREAM>(og + at, dg);
-        store16<G::STREAM>(ou + at, du);
-      }
+      join_blocks(acc[2 * n][y], acc[2 * n + 1][y], v);
+      gated_gradients<KIND>(a, v, __builtin_bit_cast(uint4, vg[o % D]), __builtin_bit_cast(uint4, vu[o % D]), dg, du);
+      const int at = off[n] + y * step;
+      og.template store<kNt>(at, __builtin_bit_cast(u32x4_t, dg));
+      ou.template store<kNt>(at, __builtin_bit_cast(u32x4_t, du));
       if (o + D < N) fetch(o + D);
-      acc[x][y] = acc[x + 1][y] = f32x4_t{};
+      acc[2 * n][y] = acc[2 * n + 1][y] = f32x4_t{};
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
 
 template <int KIND, int NS, int WR, int WC, int WA, int WB>
-__device__ __forceinline__ void ffn_workgroup(const FfnTileArgs& a, uint8_t* smem, FfnGroups& groups, int block,
+__device__ __forceinline__ void ffn_workgroup(const FfnTileArgs& a, uint8_t* smem, FfnLds& lds, int block,
                                               int blocks) {
   using G = ProductGeom<NS, WR, WC, WA, WB>;
-  load_groups<KIND>(groups, a, G::TB);
-  FfnJob<KIND, G> job(a, groups, block, blocks);
+  load_groups<KIND>(lds.groups, a, G::TB);
+  FfnJob<KIND, G> job(a, lds, block, blocks);
   if (job.n_items > 0)
     tile_stream<ffn_over_rows(KIND), KIND != kGateUp, NS, WR, WC, WA, WB>(job, job.ldp(), job.ldq(), smem);
 }
@@ -369,8 +438,8 @@ __device__ __forceinline__ void ffn_workgroup(const FfnTileArgs& a, uint8_t* sme
 template <int KIND, int NS, int WR, int WC, int WA, int WB>
 __global__ __launch_bounds__(64 * WR * WC, 1) void ffn_tiles_kernel(const FfnTileArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
-  __shared__ FfnGroups groups;
-  ffn_workgroup<KIND, NS, WR, WC, WA, WB>(a, smem, groups, blockIdx.x, gridDim.x);
+  __shared__ FfnLds lds;
+  ffn_workgroup<KIND, NS, WR, WC, WA, WB>(a, smem, lds, blockIdx.x, gridDim.x);
 }
 
 // Sums the partial tiles of the cut tail tiles in contraction order and applies the

@@ -85,9 +85,9 @@ __device__ __forceinline__ void tile_at(int t, int row_tiles, int col_tiles, int
 }
 
 // WR x WC wavefronts (c x r), each with WA x WB blocks of 16 x 16.
-template <int NS, int WR, int WC, int WA, int WB>
+template <int NS, int WR, int WC, int WA_, int WB_>
 struct ProductGeom {
-  static constexpr int BK = 64;
+  static constexpr int BK = 64, WA = WA_, WB = WB_;
   static constexpr int NW = WR * WC, THREADS = 64 * NW;
   static constexpr int TA = 16 * WR * WA, TB = 16 * WC * WB;
   static constexpr int A_BYTES = TA * BK * 2, B_BYTES = TB * BK * 2, STAGE = A_BYTES + B_BYTES;
@@ -197,7 +197,8 @@ __device__ __forceinline__ void join_blocks(f32x4_t a, f32x4_t b, float (&v)[8])
 //   row_slice(kt), row_terms()   slice kt's place in a [r][t] operand's row, and the row's length
 //   kPair                   Q is 16 rows of one operand and 16 of another in turn, both [r][t]
 //                           (descs gives the one that this wavefront loads)
-//   epilogue(item, acc, wr, wc, lane)   stores a tile's products and clears them
+//   epilogue(item, acc, wr, wc, lane)   stores a tile's products and clears them, by
+//                           kStores vector-memory instructions at least of every wavefront
 template <bool PSLOW, bool QSLOW, int NS, int WR, int WC, int WA, int WB, class Job>
 __device__ __forceinline__ void tile_stream(Job& job, int64_t ldp, int64_t ldq, uint8_t* smem) {
   using G = ProductGeom<NS, WR, WC, WA, WB>;
@@ -320,7 +321,9 @@ __device__ __forceinline__ void tile_stream(Job& job, int64_t ldp, int64_t ldq, 
   for (int x = 0; x < WA; ++x)
 #pragma unroll
     for (int y = 0; y < WB; ++y) acc[x][y] = f32x4_t{};
-  int g = 0;
+  // The wait is for the loads of slice g + 1 alone.  In the NS - 1 slices after an
+  // epilogue these lie before its stores, which then may stay on their way.
+  int g = 0, stored = -NS;
   for (int ci = 0; ci < job.n_items; ++ci) {
     const typename Job::Item it = job.tile_item(ci);
     // (read again after the last item's read ahead: no fragment lives through the epilogue)
@@ -331,7 +334,8 @@ __device__ __forceinline__ void tile_stream(Job& job, int64_t ldp, int64_t ldq, 
     for (int kt = it.kb; kt < it.ke; ++kt, ++g) {
       __builtin_amdgcn_sched_barrier(0);
       half(0, g, 1, false, 0);
-      wait_vmcnt<G::LOADS * (NS - 2)>();
+      if (Job::kStores > 0 && g - stored < NS - 1) wait_vmcnt<G::LOADS * (NS - 2) + Job::kStores>();
+      else wait_vmcnt<G::LOADS * (NS - 2)>();
       wait_lgkmcnt0();
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
@@ -339,6 +343,7 @@ __device__ __forceinline__ void tile_stream(Job& job, int64_t ldp, int64_t ldq, 
       advance();
     }
     job.epilogue(it, acc, wr, wc, lane);
+    stored = g;
   }
   wait_vmcnt<0>();   // the zero loads past the end land before the workgroup's LDS is released
 }
@@ -347,6 +352,7 @@ __device__ __forceinline__ void tile_stream(Job& job, int64_t ldp, int64_t ldq, 
 template <bool PSLOW, bool QSLOW, int ACT, class G>
 struct DenseJob {
   static constexpr bool kPair = false;
+  static constexpr int kStores = 0;      // (a wavefront without rows stores nothing)
   struct Item { int r0, c0, kb, ke, part; };
   const ProductArgs& a;
   TileShare sp;
