@@ -31,19 +31,25 @@ struct FfnArgsF32 {
   int act;
 };
 
+template <int B>
+struct FfnLdsF32 {
+  float ps[2][32 * B * kTerms];
+  float qs[2][32 * B * kTerms];
+  FfnGroups groups;
+};
+
 template <int KIND, int B, bool JOIN>
-__global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32 a) {
+__device__ __forceinline__ void ffn_f32_workgroup(const FfnArgsF32& a, FfnLdsF32<B>& lds, int block) {
   constexpr int T = 32 * B;
   constexpr bool OVER_ROWS = ffn_over_rows(KIND), PAIR = KIND == kGateUp, TWO = KIND == kDx;
   constexpr bool PSLOW = OVER_ROWS, QSLOW = KIND != kGateUp;
-  __shared__ __attribute__((aligned(16))) float ps[2][T * kTerms];
-  __shared__ __attribute__((aligned(16))) float qs[2][T * kTerms];
-  __shared__ FfnGroups groups;
+  auto &ps = lds.ps, &qs = lds.qs;
+  FfnGroups& groups = lds.groups;
   groups.load(a.offsets, a.groups, a.M, [](int rows) { return (rows + T - 1) / T; });
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, g = lane >> 4;
-  const int64_t tile = JOIN ? blockIdx.x : blockIdx.x / a.runs;
-  const int run = JOIN ? 0 : blockIdx.x % a.runs;
+  const int64_t tile = JOIN ? block : block / a.runs;
+  const int run = JOIN ? 0 : block % a.runs;
 
   // the tile's group, first row and column, rows' end, and the operands there
   int e, r0, r_end, c0, len = a.len;
@@ -184,8 +190,18 @@ __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32 a) {
   }
 }
 
+// A's product (or join) on the first a_blocks workgroups, B's (another kind) on the others.
+template <int KA, int KB, int B, bool JOIN>
+__global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32 a, const FfnArgsF32 b, int a_blocks) {
+  __shared__ __attribute__((aligned(16))) FfnLdsF32<B> lds;
+  const int i = blockIdx.x;
+  if (KA == KB || i < a_blocks) ffn_f32_workgroup<KA, B, JOIN>(a, lds, i);
+  else ffn_f32_workgroup<KB, B, JOIN>(b, lds, i - a_blocks);
+}
+
 // 128 x 128 tiles where they give every CU one, 64 x 64 otherwise; the contraction in
-// as many runs as give each CU two workgroups, of 4 slices at least.
+// as many runs as give each CU two workgroups, of 16 slices at least (a join is a
+// launch more).
 struct FfnPlanF32 {
   int T, col_tiles, runs;
   int64_t tiles, group_tiles;      // tiles: all that any offsets can give
@@ -203,16 +219,14 @@ struct FfnPlanF32 {
       const int64_t row_tiles = (f.M + p.T - 1) / p.T + f.groups - 1;
       p.tiles = over_rows ? p.group_tiles * f.groups : std::min<int64_t>(row_tiles, f.M) * p.col_tiles;
       const int64_t usual = over_rows ? p.tiles : std::max<int64_t>(p.tiles - (int64_t)(f.groups - 1) / 2 * p.col_tiles, 1);
-      p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({64, 2 * cus / usual, len / (4 * kTerms)}));
+      p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({64, 2 * cus / usual, len / (16 * kTerms)}));
       if (usual >= cus || p.T == 64) return p;
     }
   }
   size_t workspace() const { return runs > 1 ? (size_t)tiles * runs * T * T * 4 : 0; }
 };
 
-template <int KIND>
-hipError_t launch(const moe_ffn_t& f, FfnArgsF32 a, void* partials, hipStream_t st) {
-  const FfnPlanF32 p = FfnPlanF32::of(f, KIND);
+FfnArgsF32 planned(const moe_ffn_t& f, const FfnPlanF32& p, FfnArgsF32 a, void* partials) {
   a.M = f.M;
   a.groups = f.groups;
   a.act = f.act;
@@ -220,15 +234,32 @@ hipError_t launch(const moe_ffn_t& f, FfnArgsF32 a, void* partials, hipStream_t 
   a.runs = p.runs;
   a.group_tiles = p.group_tiles;
   a.partials = static_cast<float*>(partials);
+  return a;
+}
+
+// Two products that need nothing of each other: one launch where they have one tile
+// size.  (A product alone: has_b false; KB is then not run.)
+template <int KA, int KB>
+hipError_t launch_pair(const moe_ffn_t& f, const FfnArgsF32& args_a, const FfnArgsF32& args_b, bool has_a, bool has_b,
+                       void* partials, hipStream_t st) {
+  const FfnPlanF32 pa = FfnPlanF32::of(f, KA), pb = FfnPlanF32::of(f, KB);
+  if (has_a && has_b && pa.T != pb.T) {
+    const hipError_t e = launch_pair<KA, KB>(f, args_a, args_b, true, false, partials, st);
+    return e != hipSuccess ? e : launch_pair<KA, KB>(f, args_a, args_b, false, true, partials, st);
+  }
+  const FfnArgsF32 a = planned(f, pa, args_a, partials);
+  const FfnArgsF32 b = planned(f, pb, args_b, static_cast<uint8_t*>(partials) + (has_a ? pa.workspace() : 0));
   auto run = [&](auto product, auto join) {
-    hipLaunchKernelGGL(product, dim3((unsigned)(p.tiles * p.runs)), dim3(256), 0, st, a);
+    const int64_t na = has_a ? pa.tiles * pa.runs : 0, nb = has_b ? pb.tiles * pb.runs : 0;
+    hipLaunchKernelGGL(product, dim3((unsigned)(na + nb)), dim3(256), 0, st, a, b, (int)na);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.runs == 1) return e;
-    hipLaunchKernelGGL(join, dim3((unsigned)p.tiles), dim3(256), 0, st, a);
+    const int64_t ja = has_a && pa.runs > 1 ? pa.tiles : 0, jb = has_b && pb.runs > 1 ? pb.tiles : 0;
+    if (e != hipSuccess || ja + jb == 0) return e;
+    hipLaunchKernelGGL(join, dim3((unsigned)(ja + jb)), dim3(256), 0, st, a, b, (int)ja);
     return hipGetLastError();
   };
-  if (p.T == 128) return run(ffn_f32_kernel<KIND, 4, false>, ffn_f32_kernel<KIND, 4, true>);
-  return run(ffn_f32_kernel<KIND, 2, false>, ffn_f32_kernel<KIND, 2, true>);
+  if ((has_a ? pa : pb).T == 128) return run(ffn_f32_kernel<KA, KB, 4, false>, ffn_f32_kernel<KA, KB, 4, true>);
+  return run(ffn_f32_kernel<KA, KB, 2, false>, ffn_f32_kernel<KA, KB, 2, true>);
 }
 
 }  // namespace
@@ -236,37 +267,30 @@ hipError_t launch(const moe_ffn_t& f, FfnArgsF32 a, void* partials, hipStream_t 
 size_t ffn_gate_up_bytes_f32(const moe_ffn_t& f) { return FfnPlanF32::of(f, kGateUp).workspace(); }
 
 size_t ffn_backward_product_bytes_f32(const moe_ffn_t& f) {
-  size_t most = 0;
-  for (int kind : {kDh, kDx, kDw13, kDw2}) most = std::max(most, FfnPlanF32::of(f, kind).workspace());
-  return most;
+  auto of = [&](int kind) { return FfnPlanF32::of(f, kind).workspace(); };
+  return std::max(of(kDh) + of(kDw2), of(kDx) + of(kDw13));
 }
 
 hipError_t launch_ffn_gate_up_f32(const moe_ffn_t& f, const FfnTensors<float>& t, void* workspace, hipStream_t st) {
   FfnArgsF32 a{};
   a.P0 = t.x; a.Q0 = t.w1; a.Q1 = t.w3; a.offsets = t.offsets; a.cols = f.d_ff; a.len = f.d_model;
   a.o0 = t.h_out; a.o1 = t.g_out; a.o2 = t.u_out;
-  return launch<kGateUp>(f, a, workspace, st);
+  return launch_pair<kGateUp, kGateUp>(f, a, a, true, false, workspace, st);
 }
 
+// dh and dw2, which need nothing of each other, then dx and dw1, dw3, which need dh's dg and du.
 hipError_t launch_ffn_backward_f32(const moe_ffn_t& f, const FfnTensors<float>& t, void* partials, hipStream_t st) {
-  hipError_t e = hipSuccess;
-  FfnArgsF32 a{};
-  a.offsets = t.offsets;
-  if (t.dw2 != nullptr) {
-    a.P0 = t.dy; a.Q0 = t.h; a.rows = f.d_model; a.cols = f.d_ff; a.o0 = t.dw2;
-    if ((e = launch<kDw2>(f, a, partials, st)) != hipSuccess) return e;
-  }
-  if (t.dx == nullptr && t.dw1 == nullptr) return e;
-  a.P0 = t.dy; a.Q0 = t.w2; a.cols = f.d_ff; a.len = f.d_model; a.g = t.g; a.u = t.u; a.o0 = t.dg; a.o1 = t.du;
-  if ((e = launch<kDh>(f, a, partials, st)) != hipSuccess) return e;
-  a.P0 = t.dg; a.P1 = t.du;
-  if (t.dx != nullptr) {
-    a.Q0 = t.w1; a.Q1 = t.w3; a.cols = f.d_model; a.len = f.d_ff; a.o0 = t.dx;
-    if ((e = launch<kDx>(f, a, partials, st)) != hipSuccess) return e;
-  }
-  if (t.dw1 == nullptr) return e;
-  a.Q0 = t.x; a.rows = f.d_ff; a.cols = f.d_model; a.o0 = t.dw1; a.o1 = t.dw3;
-  return launch<kDw13>(f, a, partials, st);
+  FfnArgsF32 dh{}, dw2{}, dx{}, dw13{};
+  dh.offsets = dw2.offsets = dx.offsets = dw13.offsets = t.offsets;
+  dh.P0 = t.dy; dh.Q0 = t.w2; dh.cols = f.d_ff; dh.len = f.d_model; dh.g = t.g; dh.u = t.u; dh.o0 = t.dg; dh.o1 = t.du;
+  dw2.P0 = t.dy; dw2.Q0 = t.h; dw2.rows = f.d_model; dw2.cols = f.d_ff; dw2.o0 = t.dw2;
+  dx.P0 = t.dg; dx.P1 = t.du; dx.Q0 = t.w1; dx.Q1 = t.w3; dx.cols = f.d_model; dx.len = f.d_ff; dx.o0 = t.dx;
+  dw13.P0 = t.dg; dw13.P1 = t.du; dw13.Q0 = t.x; dw13.rows = f.d_ff; dw13.cols = f.d_model; dw13.o0 = t.dw1;
+  dw13.o1 = t.dw3;
+  const bool inner = t.dx != nullptr || t.dw1 != nullptr;
+  const hipError_t e = launch_pair<kDh, kDw2>(f, dh, dw2, inner, t.dw2 != nullptr, partials, st);
+  if (e != hipSuccess || !inner) return e;
+  return launch_pair<kDx, kDw13>(f, dx, dw13, t.dx != nullptr, t.dw1 != nullptr, partials, st);
 }
 
 }  // namespace moe

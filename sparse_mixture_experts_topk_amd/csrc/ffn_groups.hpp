@@ -2,6 +2,7 @@
 #pragma once
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "linear_epilogue.hpp"
 
 namespace moe {
 
@@ -89,8 +90,10 @@ struct FfnTensors {
 size_t ffn_gate_up_bytes_bf16(const moe_ffn_t& f);
 size_t ffn_backward_product_bytes_bf16(const moe_ffn_t& f);
 hipError_t launch_ffn_gate_up_bf16(const moe_ffn_t& f, const FfnTensors<uint16_t>& t, void* workspace, hipStream_t st);
-hipError_t launch_ffn_dh_bf16(const moe_ffn_t& f, const FfnTensors<uint16_t>& t, void* partials, hipStream_t st);
 hipError_t launch_ffn_backward_bf16(const moe_ffn_t& f, const FfnTensors<uint16_t>& t, void* partials, hipStream_t st);
+
+// ... gate/up of up to kLinearDecodeRows rows of one group with streamed weights (ffn_decode.hip).
+hipError_t launch_ffn_decode(const moe_ffn_t& f, const DecodeBlock& b, const FfnTensors<uint16_t>& t, hipStream_t st);
 
 // fp32 operands (ffn_f32.hip).
 size_t ffn_gate_up_bytes_f32(const moe_ffn_t& f);

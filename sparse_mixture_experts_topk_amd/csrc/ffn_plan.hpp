@@ -11,7 +11,6 @@ namespace moe {
 // even, each group half a tile short of its last.
 struct FfnPlan {
   double cost = 1e30;      // us
-  int shape = 0;           // tile, as with_tile counts them
   int row_tiles = 0, col_tiles = 0, grid = 0, split_ns = 0;
   size_t workspace = 0;
 
@@ -19,10 +18,9 @@ struct FfnPlan {
   static constexpr int kNoTail = 24;
 
   template <class C>
-  static FfnPlan of_tile(const moe_ffn_t& f, int kind, int shape, int64_t cus) {
+  static FfnPlan of_tile(const moe_ffn_t& f, int kind, int64_t cus) {
     using G = GeomOf<C>;
     FfnPlan p;
-    p.shape = shape;
     const bool over_rows = ffn_over_rows(kind);
     const int slow = kind == kGateUp ? 0 : over_rows ? 2 : 1;
     const int cols = kind == kGateUp ? 2 * f.d_ff : kind == kDh || kind == kDw2 ? f.d_ff : f.d_model;
@@ -63,15 +61,6 @@ struct FfnPlan {
     }
     return p;
   }
-  static FfnPlan of(const moe_ffn_t& f, int kind) {
-    const int64_t cus = plan_cus(device_cu_count());
-    const FfnPlan s[4] = {of_tile<Tile256x256>(f, kind, 0, cus), of_tile<Tile256x128>(f, kind, 1, cus),
-                          of_tile<Tile128x128>(f, kind, 2, cus), of_tile<Tile128x64>(f, kind, 3, cus)};
-    int best = 0;
-    for (int i = 1; i < 4; ++i)
-      if (s[i].cost < s[best].cost) best = i;
-    return s[best];
-  }
   // Whether a join has work to do, where the rows are known: one group of all M.
   template <class C>
   bool cuts(const moe_ffn_t& f, int kind) const {
@@ -86,9 +75,47 @@ struct FfnPlan {
   }
 };
 
-template <int KIND>
-hipError_t launch_ffn_tiles(const moe_ffn_t& f, FfnTileArgs a, void* partials, hipStream_t st) {
-  const FfnPlan p = FfnPlan::of(f, KIND);
+// A product's plan in each of the four shapes, and the cheapest.
+struct FfnPlans {
+  FfnPlan p[4];
+  int best = 0;
+
+  static FfnPlans of(const moe_ffn_t& f, int kind) {
+    const int64_t cus = plan_cus(device_cu_count());
+    FfnPlans s{{FfnPlan::of_tile<Tile256x256>(f, kind, cus), FfnPlan::of_tile<Tile256x128>(f, kind, cus),
+                FfnPlan::of_tile<Tile128x128>(f, kind, cus), FfnPlan::of_tile<Tile128x64>(f, kind, cus)}};
+    for (int i = 1; i < 4; ++i)
+      if (s.p[i].cost < s.p[s.best].cost) s.best = i;
+    return s;
+  }
+  const FfnPlan& least() const { return p[best]; }
+};
+
+// Two products in one launch, with one tile shape: the second's workgroups fill the
+// CUs that the first's last round leaves, and a launch is saved.  Worth kFfnOneLaunch
+// us against each in its best shape.
+constexpr double kFfnOneLaunch = 2.5;
+struct FfnPairPlan {
+  FfnPlans a, b;
+  int tile = 0;                      // the shape for both
+  bool one;
+
+  static FfnPairPlan of(const moe_ffn_t& f, int kind_a, int kind_b) {
+    FfnPairPlan p{FfnPlans::of(f, kind_a), FfnPlans::of(f, kind_b)};
+    for (int i = 1; i < 4; ++i)
+      if (p.cost(i) < p.cost(p.tile)) p.tile = i;
+    p.one = p.cost(p.tile) <= p.a.least().cost + p.b.least().cost + kFfnOneLaunch;
+    return p;
+  }
+  double cost(int i) const { return a.p[i].cost + b.p[i].cost; }
+  // partial tiles: both products', or those of one at a time
+  size_t workspace() const {
+    const size_t each = std::max(a.least().workspace, b.least().workspace);
+    return one ? std::max(each, a.p[tile].workspace + b.p[tile].workspace) : each;
+  }
+};
+
+inline FfnTileArgs planned(const moe_ffn_t& f, const FfnPlan& p, FfnTileArgs a, void* partials) {
   a.M = f.M;
   a.groups = f.groups;
   a.act = f.act;
@@ -96,16 +123,53 @@ hipError_t launch_ffn_tiles(const moe_ffn_t& f, FfnTileArgs a, void* partials, h
   a.col_tiles = p.col_tiles;
   a.split_ns = p.split_ns;
   a.partials = static_cast<float*>(partials);
-  return with_tile(p.shape, [&](auto tile) {
+  return a;
+}
+// Workgroups of a product's join: every tail tile there may be (fewer than the slots of an XCD).
+template <int KIND, class C>
+unsigned ffn_join_blocks(const moe_ffn_t& f, const FfnPlan& p, const int32_t* offsets) {
+  if (p.split_ns == 0 || (offsets == nullptr && !p.cuts<C>(f, KIND))) return 0;
+  return (unsigned)(p.grid * (GeomOf<C>::TB / kFfnJoinRows<KIND, GeomOf<C>::TA>));
+}
+
+template <int KIND>
+hipError_t launch_ffn_tiles(const moe_ffn_t& f, const FfnPlans& plans, const FfnTileArgs& args, void* partials,
+                            hipStream_t st) {
+  const FfnPlan& p = plans.least();
+  const FfnTileArgs a = planned(f, p, args, partials);
+  return with_tile(plans.best, [&](auto tile) {
     using C = decltype(tile);
     using G = GeomOf<C>;
     hipLaunchKernelGGL((ffn_tiles_kernel<KIND, C::NS, C::WR, C::WC, C::WA, C::WB>), dim3((unsigned)p.grid),
                        dim3(G::THREADS), 0, st, a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.split_ns == 0 || (a.offsets == nullptr && !p.template cuts<C>(f, KIND))) return e;
-    constexpr int per_tile = G::TB / kFfnJoinRows<KIND, G::TA>;
-    hipLaunchKernelGGL((ffn_join_kernel<KIND, G::TA, G::TB>), dim3((unsigned)(p.grid * per_tile)), dim3(256), 0, st, a,
-                       p.grid / 8);
+    const unsigned joins = ffn_join_blocks<KIND, C>(f, p, a.offsets);
+    if (e != hipSuccess || joins == 0) return e;
+    hipLaunchKernelGGL((ffn_join_kernel<KIND, G::TA, G::TB>), dim3(joins), dim3(256), 0, st, a, p.grid / 8);
+    return hipGetLastError();
+  });
+}
+
+template <int KA, int KB>
+hipError_t launch_ffn_pair(const moe_ffn_t& f, const FfnPairPlan& plan, const FfnTileArgs& args_a,
+                           const FfnTileArgs& args_b, void* partials, hipStream_t st) {
+  if (!plan.one) {
+    const hipError_t e = launch_ffn_tiles<KA>(f, plan.a, args_a, partials, st);
+    return e != hipSuccess ? e : launch_ffn_tiles<KB>(f, plan.b, args_b, partials, st);
+  }
+  const FfnPlan &pa = plan.a.p[plan.tile], &pb = plan.b.p[plan.tile];
+  const FfnTileArgs a = planned(f, pa, args_a, partials);
+  const FfnTileArgs b = planned(f, pb, args_b, static_cast<uint8_t*>(partials) + pa.workspace);
+  return with_tile(plan.tile, [&](auto tile) {
+    using C = decltype(tile);
+    using G = GeomOf<C>;
+    hipLaunchKernelGGL((ffn_pair_kernel<KA, KB, C::NS, C::WR, C::WC, C::WA, C::WB>), dim3((unsigned)(pa.grid + pb.grid)),
+                       dim3(G::THREADS), 0, st, a, b, pa.grid);
+    const hipError_t e = hipGetLastError();
+    const unsigned ja = ffn_join_blocks<KA, C>(f, pa, a.offsets), jb = ffn_join_blocks<KB, C>(f, pb, b.offsets);
+    if (e != hipSuccess || ja + jb == 0) return e;
+    hipLaunchKernelGGL((ffn_pair_join_kernel<KA, KB, G::TA, G::TB>), dim3(ja + jb), dim3(256), 0, st, a, b, pa.grid / 8,
+                       pb.grid / 8, (int)ja);
     return hipGetLastError();
   });
 }

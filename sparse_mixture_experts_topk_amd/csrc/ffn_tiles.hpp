@@ -513,6 +513,25 @@ __device__ __forceinline__ void ffn_join_workgroup(const FfnTileArgs& a, FfnGrou
   }
 }
 
+// A's product on the first a_blocks workgroups, B's on the others.
+template <int KA, int KB, int NS, int WR, int WC, int WA, int WB>
+__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_pair_kernel(const FfnTileArgs a, const FfnTileArgs b, int a_blocks) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
+  __shared__ FfnLds lds;
+  const int i = blockIdx.x;
+  if (i < a_blocks) ffn_workgroup<KA, NS, WR, WC, WA, WB>(a, smem, lds, i, a_blocks);
+  else ffn_workgroup<KB, NS, WR, WC, WA, WB>(b, smem, lds, i - a_blocks, gridDim.x - a_blocks);
+}
+
+template <int KA, int KB, int TA, int TB>
+__global__ __launch_bounds__(256) void ffn_pair_join_kernel(const FfnTileArgs a, const FfnTileArgs b, int a_slots,
+                                                            int b_slots, int a_blocks) {
+  __shared__ FfnGroups groups;
+  const int i = blockIdx.x;
+  if (i < a_blocks) ffn_join_workgroup<KA, TA, TB>(a, groups, a_slots, i);
+  else ffn_join_workgroup<KB, TA, TB>(b, groups, b_slots, i - a_blocks);
+}
+
 template <int KIND, int TA, int TB>
 __global__ __launch_bounds__(256) void ffn_join_kernel(const FfnTileArgs a, int slots) {
   __shared__ FfnGroups groups;

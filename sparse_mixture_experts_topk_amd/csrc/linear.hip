@@ -18,13 +18,6 @@
 
 namespace moe {
 
-// Streaming keeps a block of channels on one CU, which takes in 45-65 KB per us: its
-// weights and, again for each block, the rows of x.  Where the blocks leave CUs
-// idle and that is longer than the tiles' runs and their join (kTilesStart us more
-// than a stream to get going), tiles it is.  MI355X, us, stream / tiles: 32 x 2048 x
-// 14336 27.5 / 19.8, 16 x 2048 x 14336 22.1 / 19.9; 32 x 4096 x 4096 11.1 / 15.6, 16 x
-// 4096 x 14336 24.8 / 28.9, 31 x 368 x 9120 9.8 / 13.2.
-constexpr double kCuBytesPerUs = 55e3, kTilesStart = 3;
 namespace {
 struct LinearPlan {
   bool stream = true;
