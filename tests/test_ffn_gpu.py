@@ -767,3 +767,88 @@ def test_clip_of_a_tensor_of_more_than_2_31_elements():
     for got, was in ((a[-1000:], tail), (a[:1000], head)):
         w = f64(was) / math.sqrt(want)
         close(f64(got), w, BF16 * 1.001 * np.abs(w), "scaled")
+
+
+# ---- every tile shape and schedule, whole, against fp64 products on the device ----
+
+def large_case(M, d, F, G, offsets, act="silu", dtype="bf16"):
+    """Sizes at which the plans differ: tiles of each shape, cut and whole, groups' ends apart.  Relative to the
+    Frobenius norm, each output is off by its own half step and those of its operands (dg, du: from dh and an
+    activation of some ten fp32 roundings), and by the roundings of its sums: after m of n independent terms a sum
+    has sqrt(m / n) of its final size, so n additions, each rounding by half a step of fp32 (products alike), leave
+    2 n of these half steps at most; n counts the terms of every sum on the way."""
+    say(f"large {dtype} M={M} d={d} F={F} G={G}")
+    dt = DT[dtype]
+    x, dy = device_normal(1, M, d, dtype=dt), device_normal(2, M, d, dtype=dt)
+    w1, w3 = (device_normal(3 + i, G, F, d, std=d ** -0.5, dtype=dt) for i in range(2))
+    w2 = device_normal(5, G, d, F, std=F ** -0.5, dtype=dt)
+    f = moe.make_ffn(M, d, F, G, dtype, act)
+    ws = [workspace(moe.moe_ffn_workspace_bytes(f, c)) for c in (moe.MOE_CALL_FFN_GATE_UP, moe.MOE_CALL_FFN_BACKWARD)]
+    h, p1, p3 = (torch.full((M + 1, F), -7.0, dtype=dt, device=DEV) for _ in range(3))
+    dx = torch.full((M + 1, d), -7.0, dtype=dt, device=DEV)
+    dw1, dw3, dw2 = torch.full((G + 1, F, d), -7.0, dtype=dt, device=DEV), torch.full((G + 1, F, d), -7.0, dtype=dt, device=DEV), \
+        torch.full((G + 1, d, F), -7.0, dtype=dt, device=DEV)
+    o = off(offsets)
+    moe.moe_ffn_gate_up(f, x, o, w1, w3, h, p1, p3, ws[0].t if ws[0] else None)
+    moe.moe_ffn_backward(f, dy, o, x, p1, p3, h, w1, w3, w2, dx, dw1, dw3, dw2, ws[1].t)
+    torch.cuda.synchronize()
+    for w in ws:
+        if w:
+            w.np()
+    for t in (h, p1, p3, dx, dw1, dw3, dw2):
+        assert (t[-1] == -7).all(), "written past the end"
+    away = torch.from_numpy(outside(M, offsets)).to(DEV)
+    for t in (h, p1, p3, dx):
+        assert (t[:M][away] == -7).all(), "rows of no group"
+    step = steps(dtype)[0]
+
+    def near(got, want, halves, n, what):
+        tol = halves * step + (2 * n + 10) * F32
+        err = torch.linalg.vector_norm(got.double() - want) / torch.linalg.vector_norm(want).clamp(min=1e-30)
+        assert err <= tol, (what, float(err) / step)
+        big = (got.double() - want).abs().amax() / want.abs().amax()       # no element far off
+        assert big <= 4 * tol, (what, float(big) / step)
+
+    with_rows = {e: (a, b) for e, a, b in ref.spans(offsets, G, M)}
+    for e in range(G):
+        if e not in with_rows:
+            assert not dw1[e].any() and not dw3[e].any() and not dw2[e].any()
+            continue
+        a, b = with_rows[e]
+        xs, ys, a1, a3, a2 = x[a:b].double(), dy[a:b].double(), w1[e].double(), w3[e].double(), w2[e].double()
+        g, u = xs @ a1.t().contiguous(), xs @ a3.t().contiguous()
+        value = g * torch.sigmoid(g)
+        near(h[a:b], value * u, 1.0, d, f"h {e}")
+        near(p1[a:b], g, 1.0, d, f"g {e}")
+        near(p3[a:b], u, 1.0, d, f"u {e}")
+        g, u, hs = p1[a:b].double(), p3[a:b].double(), h[a:b].double()
+        sg = torch.sigmoid(g)
+        dh = ys @ a2
+        dg, du = dh * u * (sg + g * sg * (1 - sg)), dh * g * sg
+        near(dx[a:b], dg @ a1 + du @ a3, 2.0, d + 2 * F, f"dx {e}")
+        near(dw1[e], dg.t().contiguous() @ xs, 2.0, d + b - a, f"dw1 {e}")
+        near(dw3[e], du.t().contiguous() @ xs, 2.0, d + b - a, f"dw3 {e}")
+        near(dw2[e], ys.t().contiguous() @ hs, 1.0, b - a, f"dw2 {e}")
+
+
+@pytest.mark.parametrize("case", [
+    # ends of groups apart: of 128 rows and fewer, of more, of none, groups smaller than an end, empty ones
+    (4500, 256, 8192, 3, [0, 1152, 2944, 4500]), (5000, 136, 8200, 6, [0, 1, 1, 1537, 3202, 3330, 4990]),
+    (3000, 264, 12296, 4, [5, 5, 1100, 1229, 2995]), (2048, 4096, 8192, 2, [0, 1025, 2048]),
+    # one group: whole and cut tiles of every shape
+    (4096, 4096, 1024, 1, None), (2000, 2048, 2048, 1, None), (1024, 1024, 2048, 1, None), (300, 4096, 4096, 1, None),
+    (700, 512, 512, 1, [0, 690]), (96, 2048, 1024, 1, None), (33, 8192, 264, 1, None), (40, 264, 8192, 1, None),
+    (16, 8192, 64, 1, None), (32, 1024, 14336, 1, None), (24, 4096, 2048, 1, [3, 24]), (4, 512, 512, 1, None),
+    (12, 2048, 512, 1, None), (8192, 512, 256, 1, None), (2500, 136, 72, 1, None),
+    # several: few rounds, cut
+    (600, 2048, 512, 4, [0, 100, 300, 301, 600]), (1500, 1024, 2048, 8, [0, 100, 300, 600, 900, 900, 1100, 1480, 1500]),
+    (900, 4096, 264, 2, [0, 450, 900]), (8000, 64, 64, 32, [250 * i for i in range(33)]),
+])
+def test_block_in_every_tile_shape(case):
+    large_case(*case)
+
+
+@pytest.mark.parametrize("case", [(700, 1024, 512, 1, None), (64, 4096, 512, 1, None), (3000, 256, 1024, 3, [0, 1000, 1001, 2990]),
+                                  (20, 2048, 64, 2, [0, 11, 20])])
+def test_block_in_fp32_in_every_schedule(case):
+    large_case(*case, dtype="f32")
