@@ -129,16 +129,19 @@ __device__ __forceinline__ void ffn_f32_workgroup(const FfnArgsF32& a, FfnLdsF32
       return;
     }
   } else {
-#pragma unroll
-    for (int y = 0; y < B; ++y)
+    for (int r = 0; r < a.runs; ++r) {
+      f32x4_t v[B][B];
 #pragma unroll
       for (int x = 0; x < B; ++x)
-#pragma unroll 4
-        for (int r = 0; r < a.runs; ++r) {
-          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(partial(r, x, y));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[x][y][k] += v[k];
-        }
+        for (int y = 0; y < B; ++y) v[x][y] = *reinterpret_cast<const f32x4_t*>(partial(r, x, y));
+#pragma unroll
+      for (int x = 0; x < B; ++x)
+#pragma unroll
+        for (int y = 0; y < B; ++y)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[x][y][k] += v[x][y][k];
+    }
   }
 
   // lane (i, g): row y 16 + i, columns x 16 + 4 g .. + 3
@@ -199,7 +202,9 @@ __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32 a, const 
   else ffn_f32_workgroup<KB, B, JOIN>(b, lds, i - a_blocks);
 }
 
-// 128 x 128 tiles where they give every CU one, 64 x 64 otherwise; the contraction in
+// 128 x 128 tiles where they give every CU one and the groups fill their rows, 64 x 64
+// otherwise (257 groups of 4 rows, 2936 x 248, gate/up: 853 us in the large, FIGURE in the
+// small); the contraction in
 // as many runs as give each CU two workgroups, of 16 slices at least (a join is a
 // launch more).
 struct FfnPlanF32 {
@@ -220,7 +225,7 @@ struct FfnPlanF32 {
       p.tiles = over_rows ? p.group_tiles * f.groups : std::min<int64_t>(row_tiles, f.M) * p.col_tiles;
       const int64_t usual = over_rows ? p.tiles : std::max<int64_t>(p.tiles - (int64_t)(f.groups - 1) / 2 * p.col_tiles, 1);
       p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({64, 2 * cus / usual, len / (16 * kTerms)}));
-      if (usual >= cus || p.T == 64) return p;
+      if ((usual >= cus && (over_rows || f.M > 64 * (int64_t)f.groups)) || p.T == 64) return p;
     }
   }
   size_t workspace() const { return runs > 1 ? (size_t)tiles * runs * T * T * 4 : 0; }

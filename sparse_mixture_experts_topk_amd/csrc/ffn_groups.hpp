@@ -21,18 +21,19 @@ constexpr bool ffn_over_rows(int kind) { return kind == kDw13 || kind == kDw2; }
 constexpr int kMaxFfnGroups = kMaxExpertGroups;
 
 // Row offsets of the groups, in LDS: bounded to the buffers' rows and ascending,
-// whatever the array holds (NULL: one group of all rows); and a running sum over the
-// groups before each of units(rows of the group).
+// whatever the array holds (NULL: one group of all rows); and running sums over the
+// groups before each: of units(rows of the group), and of the groups that have rows.
 struct FfnGroups {
   int32_t off[kMaxFfnGroups + 1];
   int32_t pre[kMaxFfnGroups + 1];
+  int16_t full[kMaxFfnGroups + 1];
 
   // By the first wavefront; then a barrier.
   template <class Units>
   __device__ __forceinline__ void load(const int32_t* offsets, int groups, int M, Units&& units) {
     if (threadIdx.x < kWave) {
       const int lane = threadIdx.x;
-      int high = 0, carry = 0;
+      int high = 0, carry = 0, count = 0;
       for (int base = 0; base <= groups; base += kWave) {
         const int e = base + lane;
         int o = 0;
@@ -44,7 +45,9 @@ struct FfnGroups {
         }
         o = max(o, high);
         const int above = __shfl_up(o, 1), before = lane == 0 ? high : above;
-        int sum = e == 0 || e > groups ? 0 : units(o - before);       // of group e - 1
+        const bool there = e != 0 && e <= groups && o > before;       // group e - 1 has rows
+        int sum = there ? units(o - before) : 0;
+        const uint64_t rows = __ballot(there);
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
           const int v = __shfl_up(sum, d);
@@ -54,9 +57,11 @@ struct FfnGroups {
         if (e <= groups) {
           off[e] = o;
           pre[e] = sum;
+          full[e] = (int16_t)(count + __popcll(rows & (~0ull >> (kWave - 1 - lane))));
         }
         high = __shfl(o, kWave - 1);
         carry = __shfl(sum, kWave - 1);
+        count += __popcll(rows);
       }
     }
     __syncthreads();
@@ -64,12 +69,27 @@ struct FfnGroups {
   // (uniform values)
   __device__ __forceinline__ int first(int e) const { return __builtin_amdgcn_readfirstlane(off[e]); }
   __device__ __forceinline__ int before(int e) const { return __builtin_amdgcn_readfirstlane(pre[e]); }
+  __device__ __forceinline__ int full_before(int e) const { return __builtin_amdgcn_readfirstlane(full[e]); }
   // The last group with before(group) <= v: one that has units, if v is below their sum.
   __device__ __forceinline__ int of(int v, int groups) const {
+    return last(groups, [&](int e) { return before(e) <= v; });
+  }
+  // The v-th of the groups that have rows.
+  __device__ __forceinline__ int full_of(int v, int groups) const {
+    return last(groups, [&](int e) { return full_before(e) <= v; });
+  }
+  // The v-th of those that have none.
+  __device__ __forceinline__ int empty_of(int v, int groups) const {
+    return last(groups, [&](int e) { return e - full_before(e) <= v; });
+  }
+
+ private:
+  template <class Below>
+  __device__ static __forceinline__ int last(int groups, Below&& below) {
     int lo = 0, hi = groups;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (before(mid) <= v) lo = mid;
+      if (below(mid)) lo = mid;
       else hi = mid;
     }
     return lo;

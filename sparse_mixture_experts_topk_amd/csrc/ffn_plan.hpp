@@ -34,8 +34,8 @@ struct FfnPlan {
     if (over_rows) {
       p.row_tiles = (rows + G::TB - 1) / G::TB;
       most = (int64_t)f.groups * halves * p.row_tiles * p.col_tiles;
-      tiles = (double)most;
-      KT = std::max(slices_of((f.M + f.groups - 1) / f.groups), 1);
+      tiles = (double)touched * halves * p.row_tiles * p.col_tiles;
+      KT = slices_of((f.M + touched - 1) / touched);
     } else {
       most = std::min<int64_t>(row_tiles + touched - 1, f.M) * p.col_tiles;
       tiles = (std::max<double>((double)f.M / G::TB + 0.5 * (touched - 1), f.groups == 1 ? row_tiles : 1)) * p.col_tiles;
@@ -132,6 +132,11 @@ unsigned ffn_join_blocks(const moe_ffn_t& f, const FfnPlan& p, const int32_t* of
   return (unsigned)(p.grid * (GeomOf<C>::TB / kFfnJoinRows<KIND, GeomOf<C>::TA>));
 }
 
+// Workgroups that clear the weight gradients of groups without rows.
+inline int clear_blocks(const moe_ffn_t& f, int kind) {
+  return ffn_over_rows(kind) && f.groups > 1 ? (int)plan_cus(device_cu_count()) : 0;
+}
+
 template <int KIND>
 hipError_t launch_ffn_tiles(const moe_ffn_t& f, const FfnPlans& plans, const FfnTileArgs& args, void* partials,
                             hipStream_t st) {
@@ -140,8 +145,8 @@ hipError_t launch_ffn_tiles(const moe_ffn_t& f, const FfnPlans& plans, const Ffn
   return with_tile(plans.best, [&](auto tile) {
     using C = decltype(tile);
     using G = GeomOf<C>;
-    hipLaunchKernelGGL((ffn_tiles_kernel<KIND, C::NS, C::WR, C::WC, C::WA, C::WB>), dim3((unsigned)p.grid),
-                       dim3(G::THREADS), 0, st, a);
+    hipLaunchKernelGGL((ffn_tiles_kernel<KIND, C::NS, C::WR, C::WC, C::WA, C::WB>),
+                       dim3((unsigned)(p.grid + clear_blocks(f, KIND))), dim3(G::THREADS), 0, st, a, p.grid);
     const hipError_t e = hipGetLastError();
     const unsigned joins = ffn_join_blocks<KIND, C>(f, p, a.offsets);
     if (e != hipSuccess || joins == 0) return e;
@@ -163,8 +168,9 @@ hipError_t launch_ffn_pair(const moe_ffn_t& f, const FfnPairPlan& plan, const Ff
   return with_tile(plan.tile, [&](auto tile) {
     using C = decltype(tile);
     using G = GeomOf<C>;
-    hipLaunchKernelGGL((ffn_pair_kernel<KA, KB, C::NS, C::WR, C::WC, C::WA, C::WB>), dim3((unsigned)(pa.grid + pb.grid)),
-                       dim3(G::THREADS), 0, st, a, b, pa.grid);
+    hipLaunchKernelGGL((ffn_pair_kernel<KA, KB, C::NS, C::WR, C::WC, C::WA, C::WB>),
+                       dim3((unsigned)(pa.grid + pb.grid + clear_blocks(f, KB))), dim3(G::THREADS), 0, st, a, b, pa.grid,
+                       pb.grid);
     const hipError_t e = hipGetLastError();
     const unsigned ja = ffn_join_blocks<KA, C>(f, pa, a.offsets), jb = ffn_join_blocks<KB, C>(f, pb, b.offsets);
     if (e != hipSuccess || ja + jb == 0) return e;

@@ -15,7 +15,8 @@
 // contraction where that is shorter by the plan's costs (FfnShare), its partial tiles
 // joined in order by a second kernel; weight gradients of several groups have tiles of
 // as many slices as their group has rows, so there the shares are even by slices,
-// and no tile is cut.
+// and no tile is cut; groups without rows have no tiles, and other workgroups of the
+// launch clear their gradients (33 rows in 256 groups of 424 x 776: FIGURE).
 #pragma once
 #include "device_common.hpp"
 #include "ffn_groups.hpp"
@@ -49,7 +50,7 @@ template <int KIND>
 __device__ __forceinline__ void load_groups(FfnGroups& groups, const FfnTileArgs& a, int rows_per_tile) {
   // rows: tiles; weights: slices and the epilogue of one tile
   if constexpr (ffn_over_rows(KIND))
-    groups.load(a.offsets, a.groups, a.M, [](int rows) { return max(slices_of(rows), 1) + kFfnTileSlices; });
+    groups.load(a.offsets, a.groups, a.M, [](int rows) { return slices_of(rows) + kFfnTileSlices; });
   else
     groups.load(a.offsets, a.groups, a.M, [=](int rows) { return (rows + rows_per_tile - 1) / rows_per_tile; });
 }
@@ -95,14 +96,16 @@ struct FfnShare {
   }
 
  private:
-  // First tile of XCD x's share: an eighth of all slices each, to a tile.
+  // First tile of XCD x's share, tiles counted over the groups that have rows: an eighth
+  // of all slices each, to a tile.
   __device__ static int bound(const FfnGroups& groups, int n, int per_group, int x) {
-    if (x == 8) return n * per_group;
+    if (groups.full_before(n) == 0) return 0;
+    if (x == 8) return groups.full_before(n) * per_group;
     const int64_t to = (int64_t)x * per_group * groups.before(n) / 8;      // slices before it
     const int e = groups.of((int)(to / per_group), n);
     const int w = groups.before(e + 1) - groups.before(e);
     const int in = (int)((to - (int64_t)per_group * groups.before(e) + w - 1) / w);
-    return e * per_group + min(in, per_group);
+    return groups.full_before(e) * per_group + min(in, per_group);
   }
 };
 
@@ -214,6 +217,8 @@ struct FfnJob {
     run0 = slot * sp.P;
     run1 = min(run0 + sp.P, sp.tail * sp.KT);
     n_items = n_whole + (run0 < run1 ? (run1 - 1) / sp.KT - run0 / sp.KT + 1 : 0);
+    if (kOverRows && a.groups > 1 && n_items > 0)
+      load_e = tile_e = groups.full_of((sp.begin + slot) / ((KIND == kDw13 ? 2 : 1) * a.row_tiles * a.col_tiles), a.groups);
   }
   __device__ __forceinline__ Item item(int i, int& e) const {
     Item it{};
@@ -232,8 +237,10 @@ struct FfnJob {
     int rt, ct;
     if constexpr (kOverRows) {
       const int per_half = a.row_tiles * a.col_tiles, per_group = (KIND == kDw13 ? 2 : 1) * per_half;
-      e = t / per_group;
-      int in = t - e * per_group;
+      const int n = t / per_group;                             // of the groups that have rows
+      int in = t - n * per_group;
+      if (a.groups > 1)
+        while (groups.full_before(e + 1) <= n) ++e;            // tiles ascend
       if (KIND == kDw13 && in >= per_half) {
         in -= per_half;
         it.half = 1;
@@ -241,7 +248,7 @@ struct FfnJob {
       tile_at(in, a.row_tiles, a.col_tiles, rt, ct);
       it.first = groups.first(e);
       it.terms = groups.first(e + 1) - it.first;
-      if (sp.KT == 0) it.ke = max(slices_of(it.terms), 1);     // an empty group: one slice of nothing
+      if (sp.KT == 0) it.ke = slices_of(it.terms);
       it.r0 = rt * G::TB;
       it.r_end = a.rows;
     } else {
@@ -435,11 +442,29 @@ __device__ __forceinline__ void ffn_workgroup(const FfnTileArgs& a, uint8_t* sme
     tile_stream<ffn_over_rows(KIND), KIND != kGateUp, NS, WR, WC, WA, WB>(job, job.ldp(), job.ldq(), smem);
 }
 
+// Clears the gradients of groups without rows, of several: workgroup `block` of `blocks`.
+template <int KIND, int THREADS>
+__device__ __forceinline__ void clear_workgroup(const FfnTileArgs& a, FfnGroups& groups, int block, int blocks) {
+  load_groups<KIND>(groups, a, 0);
+  const int halves = KIND == kDw13 ? 2 : 1, empty = (a.groups - groups.full_before(a.groups)) * halves;
+  constexpr int PART = THREADS * 8;                                  // 16-byte parts of a piece
+  const int64_t n = (int64_t)a.rows * a.cols / 8;                    // (columns are a multiple of 8)
+  const int64_t pieces = (n + PART - 1) / PART;
+  for (int64_t i = block; i < empty * pieces; i += blocks) {
+    const int q = (int)(i / pieces), e = groups.empty_of(q / halves, a.groups);
+    const int64_t v0 = i % pieces * PART, v1 = v0 + PART < n ? v0 + PART : n;
+    uint4* to = reinterpret_cast<uint4*>((q % halves != 0 ? a.o1 : a.o0) + (int64_t)e * a.rows * a.cols);
+    for (int64_t v = v0 + threadIdx.x; v < v1; v += THREADS) store16<true>(to + v, make_uint4(0, 0, 0, 0));
+  }
+}
+
 template <int KIND, int NS, int WR, int WC, int WA, int WB>
-__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_tiles_kernel(const FfnTileArgs a) {
+__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_tiles_kernel(const FfnTileArgs a, int a_blocks) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
   __shared__ FfnLds lds;
-  ffn_workgroup<KIND, NS, WR, WC, WA, WB>(a, smem, lds, blockIdx.x, gridDim.x);
+  const int i = blockIdx.x;
+  if (!ffn_over_rows(KIND) || i < a_blocks) ffn_workgroup<KIND, NS, WR, WC, WA, WB>(a, smem, lds, i, a_blocks);
+  else clear_workgroup<KIND, 64 * WR * WC>(a, lds.groups, i - a_blocks, gridDim.x - a_blocks);
 }
 
 // Sums the partial tiles of the cut tail tiles in contraction order and applies the
@@ -513,14 +538,21 @@ __device__ __forceinline__ void ffn_join_workgroup(const FfnTileArgs& a, FfnGrou
   }
 }
 
-// A's product on the first a_blocks workgroups, B's on the others.
+// A's product on the first a_blocks workgroups, B's (a weight gradient) on the next
+// b_blocks; the others clear.
 template <int KA, int KB, int NS, int WR, int WC, int WA, int WB>
-__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_pair_kernel(const FfnTileArgs a, const FfnTileArgs b, int a_blocks) {
+__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_pair_kernel(const FfnTileArgs a, const FfnTileArgs b, int a_blocks,
+                                                                   int b_blocks) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
   __shared__ FfnLds lds;
-  const int i = blockIdx.x;
-  if (i < a_blocks) ffn_workgroup<KA, NS, WR, WC, WA, WB>(a, smem, lds, i, a_blocks);
-  else ffn_workgroup<KB, NS, WR, WC, WA, WB>(b, smem, lds, i - a_blocks, gridDim.x - a_blocks);
+  int i = blockIdx.x;
+  if (i < a_blocks) {
+    ffn_workgroup<KA, NS, WR, WC, WA, WB>(a, smem, lds, i, a_blocks);
+  } else if ((i -= a_blocks) < b_blocks) {
+    ffn_workgroup<KB, NS, WR, WC, WA, WB>(b, smem, lds, i, b_blocks);
+  } else {
+    clear_workgroup<KB, 64 * WR * WC>(b, lds.groups, i - b_blocks, gridDim.x - a_blocks - b_blocks);
+  }
 }
 
 template <int KA, int KB, int TA, int TB>

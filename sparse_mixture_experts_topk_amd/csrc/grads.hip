@@ -143,12 +143,22 @@ __device__ __forceinline__ double workgroup_sum(double v, double (&part)[THREADS
   return s;
 }
 
-__global__ __launch_bounds__(kThreads) void norm_chunks_kernel(const List l, double* __restrict__ part) {
+__device__ __forceinline__ void store_norm(double sum, double* sum_squares, float* norm) {
+  *sum_squares = sum;
+  if (norm != nullptr) *norm = (float)sqrt(sum);
+}
+
+// A list of one chunk ends here: sum_squares and norm are given.
+__global__ __launch_bounds__(kThreads) void norm_chunks_kernel(const List l, double* __restrict__ part,
+                                                               double* __restrict__ sum_squares,
+                                                               float* __restrict__ norm) {
   __shared__ double waves[kThreads / kWave];
   const Span s = span_of(l, blockIdx.x);
   const double v = s.f32 ? chunk_sum<true>(s) : chunk_sum<false>(s);
   const double sum = workgroup_sum<kThreads>(v, waves);
-  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+  if (threadIdx.x != 0) return;
+  if (sum_squares != nullptr) store_norm(sum, sum_squares, norm);
+  else part[blockIdx.x] = sum;
 }
 
 constexpr int kJoinThreads = 1024;
@@ -159,9 +169,7 @@ __global__ __launch_bounds__(kJoinThreads) void norm_join_kernel(const double* _
   double v = 0.0;
   for (int i = threadIdx.x; i < chunks; i += kJoinThreads) v += part[i];
   const double sum = workgroup_sum<kJoinThreads>(v, waves);
-  if (threadIdx.x != 0) return;
-  *sum_squares = sum;
-  if (norm != nullptr) *norm = (float)sqrt(sum);
+  if (threadIdx.x == 0) store_norm(sum, sum_squares, norm);
 }
 
 // x scale: in fp64, so that the one rounding is the result's.
@@ -224,7 +232,8 @@ __device__ __forceinline__ double clip_scale(double sum_squares, float max_norm)
 __global__ __launch_bounds__(kThreads) void clip_kernel(const List l, const double* __restrict__ sum_squares,
                                                         float max_norm) {
   const double scale = clip_scale(*sum_squares, max_norm);
-  const Span s = span_of(l, blockIdx.x);
+  // from the end: what the norm's pass read last may still be in the memory-side cache
+  const Span s = span_of(l, gridDim.x - 1 - blockIdx.x);
   const void* p = l.t[s.tensor].p;
   void* o = l.t[s.tensor].o;
   if (scale == 1.0 && p == o) return;
@@ -287,13 +296,15 @@ size_t grad_norm_workspace_bytes(const moe_tensor_t* tensors, int count) {
 hipError_t launch_grad_norm(const moe_tensor_t* tensors, int count, double* sum_squares, float* norm, void* workspace,
                             hipStream_t st) {
   double* part = static_cast<double*>(workspace);
+  const bool one = total_chunks(tensors, count) == 1;
   int chunks = 0;
   hipError_t e = each_list(tensors, nullptr, count, [&](const List& l, int n) {
-    hipLaunchKernelGGL(norm_chunks_kernel, dim3((unsigned)n), dim3(kThreads), 0, st, l, part + chunks);
+    hipLaunchKernelGGL(norm_chunks_kernel, dim3((unsigned)n), dim3(kThreads), 0, st, l, part + chunks,
+                       one ? sum_squares : nullptr, norm);
     chunks += n;
     return hipGetLastError();
   });
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || one) return e;
   hipLaunchKernelGGL(norm_join_kernel, dim3(1), dim3(kJoinThreads), 0, st, part, chunks, sum_squares, norm);
   return hipGetLastError();
 }
