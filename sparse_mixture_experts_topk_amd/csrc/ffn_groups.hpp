@@ -31,7 +31,16 @@ struct FfnGroups {
   // By the first wavefront; then a barrier.
   template <class Units>
   __device__ __forceinline__ void load(const int32_t* offsets, int groups, int M, Units&& units) {
-    if (threadIdx.x < kWave) {
+    if (groups == 1) {
+      if (threadIdx.x == 0) {
+        off[0] = offsets != nullptr ? min(max(offsets[0], 0), M) : 0;
+        off[1] = offsets != nullptr ? max(min(offsets[1], M), off[0]) : M;
+        const int rows = off[1] - off[0];
+        pre[0] = full[0] = 0;
+        pre[1] = rows > 0 ? units(rows) : 0;
+        full[1] = rows > 0;
+      }
+    } else if (threadIdx.x < kWave) {
       const int lane = threadIdx.x;
       int high = 0, carry = 0, count = 0;
       for (int base = 0; base <= groups; base += kWave) {
@@ -73,6 +82,14 @@ struct FfnGroups {
   // The last group with before(group) <= v: one that has units, if v is below their sum.
   __device__ __forceinline__ int of(int v, int groups) const {
     return last(groups, [&](int e) { return before(e) <= v; });
+  }
+  // The same for ascending v, from the last one's e.
+  __device__ __forceinline__ int next(int e, int v, int groups) const {
+    for (int i = 0; i < 2; ++i) {
+      if (before(e + 1) > v) return e;
+      ++e;
+    }
+    return before(e + 1) > v ? e : of(v, groups);
   }
   // The v-th of the groups that have rows.
   __device__ __forceinline__ int full_of(int v, int groups) const {

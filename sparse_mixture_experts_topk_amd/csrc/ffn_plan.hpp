@@ -11,7 +11,7 @@ namespace moe {
 // even, each group half a tile short of its last.
 struct FfnPlan {
   double cost = 1e30;      // us
-  int row_tiles = 0, col_tiles = 0, grid = 0, split_ns = 0;
+  int row_tiles = 0, col_tiles = 0, grid = 0, split_ns = 0, cuts = 1;
   size_t workspace = 0;
 
   // Rounds of tiles from which on a tail is not worth a join's launch.
@@ -42,6 +42,10 @@ struct FfnPlan {
       KT = (kind == kDx ? 2 : 1) * slices_of(kind == kDx ? f.d_ff : f.d_model);
     }
     const bool may_split = (!over_rows || f.groups == 1) && KT > kFfnMinSlices && tiles < (double)kNoTail * cus;
+    if (over_rows && f.groups > 1) {             // few tiles: parts of them that fill the CUs once
+      p.cuts = (int)std::max<int64_t>(1, std::min<int64_t>(cus / (int64_t)tiles, KT / kFfnMinSlices));
+      most *= p.cuts;
+    }
     const int64_t per_xcd = (most + 7) / 8;
     p.grid = (int)std::max<int64_t>(8, std::min<int64_t>(cus, 8 * (may_split ? per_xcd * KT / kFfnMinSlices : per_xcd)));
     const int slots = p.grid / 8;
@@ -50,6 +54,10 @@ struct FfnPlan {
       const FfnShare s = FfnShare::even((int)tiles, KT, 0, slots, ns, G::PARTIAL);      // the largest share
       p.cost = ((double)s.R * KT + (s.P > 0 ? s.P : s.tail > 0 ? KT : 0)) * slice + (s.R + (s.tail > 0 ? 1 : 0)) * tile;
       if (s.P > 0) p.cost += (kFfnJoinNs + 8.0 * (slots + s.tail) * G::PARTIAL / 256 * kFfnJoinNsPer100KiB / 100) * 1e-3;
+    } else if (p.cuts > 1) {
+      const double bytes = tiles * p.cuts * G::PARTIAL * 4;
+      p.cost = (double)((KT + p.cuts - 1) / p.cuts) * slice + tile + kFfnJoinNs * 1e-3 + bytes / 1024 / 100 * kFfnJoinNsPer100KiB * 1e-3;
+      p.workspace = (size_t)bytes;
     } else {
       const double rounds = tiles / p.grid;
       p.cost = may_split && rounds < 4 ? std::max(rounds, 0.25) * (KT * slice + tile) + 8
@@ -63,7 +71,7 @@ struct FfnPlan {
   }
   // Whether a join has work to do, where the rows are known: one group of all M.
   template <class C>
-  bool cuts(const moe_ffn_t& f, int kind) const {
+  bool has_tail(const moe_ffn_t& f, int kind) const {
     const bool over_rows = ffn_over_rows(kind);
     const int64_t total = over_rows ? (int64_t)(kind == kDw13 ? 2 : 1) * row_tiles * col_tiles
                                     : (int64_t)((f.M + GeomOf<C>::TB - 1) / GeomOf<C>::TB) * col_tiles;
@@ -122,14 +130,17 @@ inline FfnTileArgs planned(const moe_ffn_t& f, const FfnPlan& p, FfnTileArgs a, 
   a.row_tiles = p.row_tiles;
   a.col_tiles = p.col_tiles;
   a.split_ns = p.split_ns;
+  a.cuts = p.cuts;
   a.partials = static_cast<float*>(partials);
   return a;
 }
 // Workgroups of a product's join: every tail tile there may be (fewer than the slots of an XCD).
 template <int KIND, class C>
 unsigned ffn_join_blocks(const moe_ffn_t& f, const FfnPlan& p, const int32_t* offsets) {
-  if (p.split_ns == 0 || (offsets == nullptr && !p.cuts<C>(f, KIND))) return 0;
-  return (unsigned)(p.grid * (GeomOf<C>::TB / kFfnJoinRows<KIND, GeomOf<C>::TA>));
+  constexpr int per_tile = GeomOf<C>::TB / kFfnJoinRows<KIND, GeomOf<C>::TA>;
+  if (p.cuts > 1) return (unsigned)((KIND == kDw13 ? 2 : 1) * std::min(f.groups, f.M) * p.row_tiles * p.col_tiles * per_tile);
+  if (p.split_ns == 0 || (offsets == nullptr && !p.has_tail<C>(f, KIND))) return 0;
+  return (unsigned)(p.grid * per_tile);
 }
 
 // Workgroups that clear the weight gradients of groups without rows.

@@ -14,8 +14,9 @@
 // workgroups take full rounds of them.  The last, partial round is cut along the
 // contraction where that is shorter by the plan's costs (FfnShare), its partial tiles
 // joined in order by a second kernel; weight gradients of several groups have tiles of
-// as many slices as their group has rows, so there the shares are even by slices,
-// and no tile is cut; groups without rows have no tiles, and other workgroups of the
+// as many slices as their group has rows, so there the shares are even by slices, and
+// where there are few tiles each is cut into as many parts (7080 rows in 2 groups of 1352
+// x 280, all gradients: 227 -> FIGURE us); groups without rows have no tiles, and other workgroups of the
 // launch clear their gradients (33 rows in 256 groups of 424 x 776: FIGURE).
 #pragma once
 #include "device_common.hpp"
@@ -38,6 +39,7 @@ struct FfnTileArgs {
   int rows, cols, len;                    // kDw13, kDw2: rows of the weight; columns (kGateUp: channels); terms of a half
   int row_tiles, col_tiles;               // row_tiles: kDw13, kDw2, of a half
   int split_ns;                           // a slice, where there is room for partial tiles; else 0
+  int cuts;                               // kDw13, kDw2 of several groups: parts of each contraction
   float* partials;
   const uint16_t *g, *u;                  // kDh
   uint16_t *o0, *o1, *o2;
@@ -88,8 +90,8 @@ struct FfnShare {
       return even(per_group, max(slices_of(groups.first(1) - groups.first(0)), 1), xcd, slots, a.split_ns, tile_floats);
     FfnShare s;
     s.KT = s.P = 0;
-    s.begin = bound(groups, a.groups, per_group, xcd);
-    const int len = bound(groups, a.groups, per_group, xcd + 1) - s.begin;
+    s.begin = bound(groups, a.groups, per_group * a.cuts, xcd);
+    const int len = bound(groups, a.groups, per_group * a.cuts, xcd + 1) - s.begin;
     s.R = len / slots;
     s.tail = len - s.R * slots;
     return s;
@@ -218,7 +220,7 @@ struct FfnJob {
     run1 = min(run0 + sp.P, sp.tail * sp.KT);
     n_items = n_whole + (run0 < run1 ? (run1 - 1) / sp.KT - run0 / sp.KT + 1 : 0);
     if (kOverRows && a.groups > 1 && n_items > 0)
-      load_e = tile_e = groups.full_of((sp.begin + slot) / ((KIND == kDw13 ? 2 : 1) * a.row_tiles * a.col_tiles), a.groups);
+      load_e = tile_e = groups.full_of((sp.begin + slot) / ((KIND == kDw13 ? 2 : 1) * a.row_tiles * a.col_tiles * a.cuts), a.groups);
   }
   __device__ __forceinline__ Item item(int i, int& e) const {
     Item it{};
@@ -237,6 +239,13 @@ struct FfnJob {
     int rt, ct;
     if constexpr (kOverRows) {
       const int per_half = a.row_tiles * a.col_tiles, per_group = (KIND == kDw13 ? 2 : 1) * per_half;
+      const bool cut = a.groups > 1 && a.cuts > 1;
+      int c = 0;
+      if (cut) {
+        it.part = t;
+        c = t % a.cuts;
+        t /= a.cuts;
+      }
       const int n = t / per_group;                             // of the groups that have rows
       int in = t - n * per_group;
       if (a.groups > 1)
@@ -248,11 +257,20 @@ struct FfnJob {
       tile_at(in, a.row_tiles, a.col_tiles, rt, ct);
       it.first = groups.first(e);
       it.terms = groups.first(e + 1) - it.first;
-      if (sp.KT == 0) it.ke = slices_of(it.terms);
+      if (sp.KT == 0) {
+        const int KT = slices_of(it.terms);
+        it.kb = cut ? (int)((int64_t)KT * c / a.cuts) : 0;
+        it.ke = cut ? (int)((int64_t)KT * (c + 1) / a.cuts) : KT;
+        if (it.kb == it.ke) {                                  // fewer slices than parts: one slice of nothing
+          it.terms = 0;
+          it.kb = 0;
+          it.ke = 1;
+        }
+      }
       it.r0 = rt * G::TB;
       it.r_end = a.rows;
     } else {
-      while (groups.before(e + 1) * a.col_tiles <= t) ++e;     // tiles ascend
+      if (a.groups > 1) e = groups.next(e, t / a.col_tiles, a.groups);      // tiles ascend
       const int before = groups.before(e);
       tile_at(t - before * a.col_tiles, groups.before(e + 1) - before, a.col_tiles, rt, ct);
       it.r0 = groups.first(e) + rt * G::TB;
@@ -467,8 +485,8 @@ __global__ __launch_bounds__(64 * WR * WC, 1) void ffn_tiles_kernel(const FfnTil
   else clear_workgroup<KIND, 64 * WR * WC>(a, lds.groups, i - a_blocks, gridDim.x - a_blocks);
 }
 
-// Sums the partial tiles of the cut tail tiles in contraction order and applies the
-// epilogue.  One workgroup per (XCD, tail tile, ROWS rows of it), 8 columns (kGateUp:
+// Sums the partial tiles of the cut tiles in contraction order and applies the epilogue.
+// One workgroup per (XCD, tail tile, ROWS rows of it), or, if all are cut, (tile, ROWS rows), 8 columns (kGateUp:
 // channels, 16 columns) of a row to a lane; four partials are in flight at a time.
 template <int KIND, int TA> constexpr int kFfnJoinRows = (KIND == kGateUp ? 512 : 256) * 8 / TA;
 
@@ -476,40 +494,59 @@ template <int KIND, int TA, int TB>
 __device__ __forceinline__ void ffn_join_workgroup(const FfnTileArgs& a, FfnGroups& groups, int slots, int block) {
   constexpr int ROWS = kFfnJoinRows<KIND, TA>, RG = TB / ROWS, LANES = 256 / ROWS;
   load_groups<KIND>(groups, a, TB);
-  const int rg = block % RG, xcd = (block / RG) & 7, j = block / RG >> 3;
-  const FfnShare sp = FfnShare::of<KIND>(a, groups, xcd, slots, TA * TB);
-  if (sp.P == 0 || j >= sp.tail) return;
-  const int t = sp.begin + sp.R * slots + j;
-  int rt, ct, r0, r_end, half = 0;
-  if constexpr (ffn_over_rows(KIND)) {                       // (one group: several are never cut)
-    const int per_half = a.row_tiles * a.col_tiles;
+  const int rg = block % RG;
+  int t, first, parts;                       // the tile, and where its partial tiles lie
+  bool cut = false;
+  if constexpr (ffn_over_rows(KIND)) cut = a.groups > 1;
+  if (cut) {
+    t = block / RG;
+    first = t * a.cuts;
+    parts = a.cuts;
+  } else {
+    const int xcd = (block / RG) & 7, j = block / RG >> 3;
+    const FfnShare sp = FfnShare::of<KIND>(a, groups, xcd, slots, TA * TB);
+    if (sp.P == 0 || j >= sp.tail) return;
+    t = sp.begin + sp.R * slots + j;
+    const int s_lo = j * sp.KT / sp.P, s_hi = min(((j + 1) * sp.KT - 1) / sp.P, slots - 1);
+    first = xcd * 2 * slots + j + s_lo;
+    parts = s_hi - s_lo + 1;
+  }
+  int rt, ct, r0, r_end, half = 0, e = 0;
+  if constexpr (ffn_over_rows(KIND)) {
+    const int per_half = a.row_tiles * a.col_tiles, per_group = (KIND == kDw13 ? 2 : 1) * per_half;
+    if (cut) {
+      const int n = t / per_group;
+      if (n >= groups.full_before(a.groups)) return;
+      e = groups.full_of(n, a.groups);
+      t -= n * per_group;
+    }
     half = t >= per_half ? 1 : 0;
     tile_at(t - half * per_half, a.row_tiles, a.col_tiles, rt, ct);
     r0 = rt * TB;
     r_end = a.rows;
   } else {
-    const int e = groups.of(t / a.col_tiles, a.groups), before = groups.before(e);
+    e = groups.of(t / a.col_tiles, a.groups);
+    const int before = groups.before(e);
     tile_at(t - before * a.col_tiles, groups.before(e + 1) - before, a.col_tiles, rt, ct);
     r0 = groups.first(e) + rt * TB;
     r_end = groups.first(e + 1);
   }
-  const int s_lo = j * sp.KT / sp.P, s_hi = min(((j + 1) * sp.KT - 1) / sp.P, slots - 1);
   const int rl = rg * ROWS + threadIdx.x / LANES, cl = threadIdx.x % LANES * 8;
   const int r = r0 + rl, c = ct * (KIND == kGateUp ? TA / 2 : TA) + cl;
   if (r >= r_end || c >= a.cols) return;
   const int64_t at = (int64_t)r * a.cols + c;
   auto sum = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
-    const float* base = a.partials + (int64_t)(xcd * 2 * slots + j) * (TA * TB) + rl * TA + col;
+    const float* base = a.partials + (int64_t)first * (TA * TB) + rl * TA + col;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-    for (int s = s_lo; s <= s_hi; s += 4) {
+    for (int s = 0; s < parts; s += 4) {
       float p[4][8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) load8f(base + (int64_t)min(s + q, s_hi) * (TA * TB), p[q]);
+      for (int q = 0; q < 4; ++q) load8f(base + (int64_t)min(s + q, parts - 1) * (TA * TB), p[q]);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += s + q <= s_hi ? p[q][k] : 0.0f;
+        for (int k = 0; k < 8; ++k) v[k] += s + q < parts ? p[q][k] : 0.0f;
     }
   };
   float v[8];
@@ -534,7 +571,7 @@ __device__ __forceinline__ void ffn_join_workgroup(const FfnTileArgs& a, FfnGrou
     store16<false>(a.o1 + at, du);
   } else {
     sum(cl, v);
-    store16<false>((half != 0 ? a.o1 : a.o0) + at, pack8(v));
+    store16<false>((half != 0 ? a.o1 : a.o0) + (ffn_over_rows(KIND) ? (int64_t)e * a.rows * a.cols : 0) + at, pack8(v));
   }
 }
 

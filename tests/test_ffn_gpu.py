@@ -843,6 +843,9 @@ def large_case(M, d, F, G, offsets, act="silu", dtype="bf16"):
     # several: few rounds, cut
     (600, 2048, 512, 4, [0, 100, 300, 301, 600]), (1500, 1024, 2048, 8, [0, 100, 300, 600, 900, 900, 1100, 1480, 1500]),
     (900, 4096, 264, 2, [0, 450, 900]), (8000, 64, 64, 32, [250 * i for i in range(33)]),
+    # few weight tiles over long contractions, cut: groups of all rows, of few, of none
+    (7080, 1352, 280, 2, [0, 3200, 7080]), (6000, 72, 136, 3, [0, 5990, 5990, 6000]), (5000, 520, 264, 5, [7, 7, 2000, 2001, 4000, 4900]),
+    (2, 216, 248, 256, [0] * 100 + [1] * 100 + [2] * 57), (40, 64, 136, 257, [0] * 3 + [7] * 200 + [20] * 50 + [40] * 5),
 ])
 def test_block_in_every_tile_shape(case):
     large_case(*case)
