@@ -203,7 +203,7 @@ __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32 a, const 
 }
 
 // 128 x 128 tiles where they give every CU one and the groups fill their rows, 64 x 64
-// otherwise (257 groups of 4 rows, 2936 x 248, gate/up: 853 us in the large, FIGURE in the
+// otherwise (257 groups of 4 rows, 2936 x 248, gate/up: 853 us in the large, 427 in the
 // small); the contraction in
 // as many runs as give each CU two workgroups, of 16 slices at least (a join is a
 // launch more).

@@ -342,6 +342,32 @@ def test_offsets_out_of_range_are_bounded():
         assert np.array_equal(a.np(), b.np())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_group_with_bounds(dtype):
+    """Given bounds of the one group: few rows (streamed) and more, none at all."""
+    for M, offsets in ((20, [4, 15]), (20, [0, 0]), (20, [20, 20]), (32, [0, 32]), (200, [7, 180]), (200, [100, 100]),
+                       (1, [0, 1]), (1, [1, 1])):
+        gate_up_case(M, 136, 264, 1, offsets, dtype=dtype)
+        backward_case(M, 136, 264, 1, offsets, dtype=dtype)
+
+
+@pytest.mark.parametrize("d,F", [(1 << 18, 8), (8, 1 << 18)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_widest_channels(d, F, dtype):
+    for M, G, offsets in ((5, 1, None), (40, 2, [0, 3, 40])):
+        gate_up_case(M, d, F, G, offsets, dtype=dtype)
+        backward_case(M, d, F, G, offsets, dtype=dtype)
+
+
+@pytest.mark.parametrize("dims", [(33, 4096, 512, 1), (500, 392, 264, 4), (3000, 264, 136, 2), (90, 104, 1008, 200), (7, 512, 64, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_block_repeats_bit_for_bit(dims, dtype):
+    a, b = (gate_up_case(*dims, off_list, dtype=dtype) for off_list in [uneven(dims[0], dims[3], 5)] * 2)
+    assert all(np.array_equal(a[n], b[n]) for n in a)
+    a, b = (backward_case(*dims, off_list, dtype=dtype) for off_list in [uneven(dims[0], dims[3], 5)] * 2)
+    assert all(np.array_equal(a[n], b[n]) for n in a)
+
+
 # ---- gradient of the permutation ----
 
 def rows_of(T, k, S, drop, seed):
@@ -736,6 +762,24 @@ def test_ffn_of_more_than_2_31_elements(d, F):
     b = ref.backward(*(f64(t[cut:]) for t in (dy, x, p1, p3, h)), f64(w1[1]), f64(w3[1]), f64(w2[1]), "silu")
     for got, want in ((dw1, b["dw1"]), (dw3, b["dw3"]), (dw2, b["dw2"])):
         assert np.abs(f64(got[1]) - want).max() <= 4 * BF16 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_block_of_the_most_rows(dtype):
+    M, d, F, G = 1 << 24, 8, 8, 257
+    say(f"block {dtype} M={M} d={d} F={F} G={G}")
+    offsets = [M // 300 * e for e in range(G)] + [M - 1]
+    x = device_normal(1, M, d, dtype=DT[dtype])
+    w1, w3 = device_normal(2, G, F, d, dtype=DT[dtype]), device_normal(3, G, F, d, dtype=DT[dtype])
+    f = moe.make_ffn(M, d, F, G, dtype)
+    h = torch.full((M, F), -7.0, dtype=DT[dtype], device=DEV)
+    moe.moe_ffn_gate_up(f, x, off(offsets), w1, w3, h, None, None, runner._bytes(moe.moe_ffn_workspace_bytes(f), DEV))
+    torch.cuda.synchronize()
+    assert (h[-1] == -7).all()
+    for e in (0, 1, 100, 255, 256):
+        for r in (offsets[e], offsets[e] + 1000, offsets[e + 1] - 1):
+            want = ref.gate_up(f64(x[r:r + 1]), f64(w1[e]), f64(w3[e]), "silu")[0]
+            assert np.abs(f64(h[r]) - want).max() <= 2 * steps(dtype)[0] * np.abs(want).max() + 1e-4, (e, r)
 
 
 def test_permute_backward_of_the_most_tokens():
