@@ -153,9 +153,9 @@ def scored_routing(di: DeviceInputs, router, balance_bias=None, stream=None, out
 @_on_its_device
 def gate_backward(di: DeviceInputs, st: dict, router, dy: torch.Tensor, dscores=None, stream=None) -> dict:
     """Gradients of the gate from the gradient ``dy`` at y: ``st`` is the result of ``staged`` with
-    the same router.  dy_perm is the gradient at the experts' rows, for the caller's own backward pass
-    of the experts (the library has none); dx and dw_gate, dbias are those of the router's product
-    alone (the path through the gate weights)."""
+    the same router.  dy_perm is the gradient at the experts' rows (layer_backward takes it on
+    through the experts); dx and dw_gate, dbias are those of the router's product alone (the path
+    through the gate weights)."""
     cfg, dev = di.cfg, di.x.device
     T, d, E, k = cfg.T, cfg.d_model, cfg.n_experts, cfg.top_k
     W = (E + 7) // 8 * 8          # moe_linear_backward has widths of multiples of 8: zero rows behind the experts'
