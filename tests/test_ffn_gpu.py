@@ -603,7 +603,7 @@ def layer(T=96, E=8, k=2, shared=0, **kw):
 
 
 F32S = dict(act_dtype="f32", w_dtype="f32")
-LAYERS = [dict(), dict(shared=1, E=32, k=4), dict(T=1), dict(T=700), dict(capacity=20), dict(E=12, k=3),
+LAYERS = [dict(), dict(shared=1, E=32, k=4), dict(T=1), dict(T=700), dict(capacity=20), dict(capacity=0), dict(capacity=0, shared=1), dict(E=12, k=3),
           dict(T=200, capacity=40, overflow="next_best"), dict(T=64, **F32S), dict(T=90, shared=1, k=3, **F32S)]
 
 
