@@ -854,29 +854,51 @@ def large_case(M, d, F, G, offsets, act="silu", dtype="bf16"):
         assert big <= 4 * tol, (what, float(big) / step)
 
     with_rows = {e: (a, b) for e, a, b in ref.spans(offsets, G, M)}
-    for e in range(G):
-        if e not in with_rows:
-            assert not dw1[e].any() and not dw3[e].any() and not dw2[e].any()
-            continue
-        a, b = with_rows[e]
-        xs, ys, a1, a3, a2 = x[a:b].double(), dy[a:b].double(), w1[e].double(), w3[e].double(), w2[e].double()
-        g, u = xs @ a1.t().contiguous(), xs @ a3.t().contiguous()
-        value = g * torch.sigmoid(g)
-        near(h[a:b], value * u, 1.0, d, f"h {e}")
+
+    def check_gradients(outputs):
+        for e in range(G):
+            if e not in with_rows:
+                assert not any(t[e].any() for n, ts in (("dw13", (dw1, dw3)), ("dw2", (dw2,))) if n in outputs for t in ts)
+                continue
+            a, b = with_rows[e]
+            xs, ys, a1, a3, a2 = x[a:b].double(), dy[a:b].double(), w1[e].double(), w3[e].double(), w2[e].double()
+            g, u, hs = p1[a:b].double(), p3[a:b].double(), h[a:b].double()
+            sg = torch.sigmoid(g)
+            if "dw2" in outputs:
+                near(dw2[e], ys.t().contiguous() @ hs, 1.0, b - a, f"dw2 {e}")
+            if outputs == "dw2":
+                continue
+            dh = ys @ a2
+            dg, du = dh * u * (sg + g * sg * (1 - sg)), dh * g * sg
+            if "dx" in outputs:
+                near(dx[a:b], dg @ a1 + du @ a3, 2.0, d + 2 * F, f"dx {e}")
+            if "dw13" in outputs:
+                near(dw1[e], dg.t().contiguous() @ xs, 2.0, d + b - a, f"dw1 {e}")
+                near(dw3[e], du.t().contiguous() @ xs, 2.0, d + b - a, f"dw3 {e}")
+
+    for e, (a, b) in with_rows.items():
+        xs = x[a:b].double()
+        g, u = xs @ w1[e].double().t().contiguous(), xs @ w3[e].double().t().contiguous()
+        near(h[a:b], g * torch.sigmoid(g) * u, 1.0, d, f"h {e}")
         near(p1[a:b], g, 1.0, d, f"g {e}")
         near(p3[a:b], u, 1.0, d, f"u {e}")
-        g, u, hs = p1[a:b].double(), p3[a:b].double(), h[a:b].double()
-        sg = torch.sigmoid(g)
-        dh = ys @ a2
-        dg, du = dh * u * (sg + g * sg * (1 - sg)), dh * g * sg
-        near(dx[a:b], dg @ a1 + du @ a3, 2.0, d + 2 * F, f"dx {e}")
-        near(dw1[e], dg.t().contiguous() @ xs, 2.0, d + b - a, f"dw1 {e}")
-        near(dw3[e], du.t().contiguous() @ xs, 2.0, d + b - a, f"dw3 {e}")
-        near(dw2[e], ys.t().contiguous() @ hs, 1.0, b - a, f"dw2 {e}")
+    check_gradients("dx dw13 dw2")
+    for outputs in ("dx", "dw13", "dw2"):                    # alone: launches of their own
+        for t in (dx, dw1, dw3, dw2):
+            t.fill_(-7.0)
+        ws[1].t.fill_(0xFF)
+        has = [outputs == n for n in ("dx", "dw13", "dw2")]
+        moe.moe_ffn_backward(f, dy, o, x, p1, p3, h, w1, w3, w2, dx if has[0] else None, dw1 if has[1] else None,
+                             dw3 if has[1] else None, dw2 if has[2] else None, ws[1].t)
+        torch.cuda.synchronize()
+        ws[1].np()
+        check_gradients(outputs)
+        for t, there in ((dx, has[0]), (dw1, has[1]), (dw3, has[1]), (dw2, has[2])):
+            assert (t[-1] == -7).all() and (there or (t == -7).all()), "written past the end, or not asked for"
 
 
 @pytest.mark.parametrize("case", [
-    # ends of groups apart: of 128 rows and fewer, of more, of none, groups smaller than an end, empty ones
+    # many rounds of large tiles: groups that end in a few rows of one, in many, at its border, groups of one row, of none
     (4500, 256, 8192, 3, [0, 1152, 2944, 4500]), (5000, 136, 8200, 6, [0, 1, 1, 1537, 3202, 3330, 4990]),
     (3000, 264, 12296, 4, [5, 5, 1100, 1229, 2995]), (2048, 4096, 8192, 2, [0, 1025, 2048]),
     # one group: whole and cut tiles of every shape
@@ -884,6 +906,9 @@ def large_case(M, d, F, G, offsets, act="silu", dtype="bf16"):
     (700, 512, 512, 1, [0, 690]), (96, 2048, 1024, 1, None), (33, 8192, 264, 1, None), (40, 264, 8192, 1, None),
     (16, 8192, 64, 1, None), (32, 1024, 14336, 1, None), (24, 4096, 2048, 1, [3, 24]), (4, 512, 512, 1, None),
     (12, 2048, 512, 1, None), (8192, 512, 256, 1, None), (2500, 136, 72, 1, None),
+    (8192, 2048, 1024, 1, None), (6000, 1024, 1024, 1, None), (16000, 512, 512, 1, None), (5000, 136, 264, 1, [1, 4999]),
+    (1100, 4096, 2048, 1, None), (520, 2048, 4096, 1, None), (2100, 1024, 4096, 1, None), (2048, 4096, 4352, 1, None),
+    (1792, 4352, 8192, 1, None),
     # several: few rounds, cut
     (600, 2048, 512, 4, [0, 100, 300, 301, 600]), (1500, 1024, 2048, 8, [0, 100, 300, 600, 900, 900, 1100, 1480, 1500]),
     (900, 4096, 264, 2, [0, 450, 900]), (8000, 64, 64, 32, [250 * i for i in range(33)]),
@@ -896,6 +921,7 @@ def test_block_in_every_tile_shape(case):
 
 
 @pytest.mark.parametrize("case", [(700, 1024, 512, 1, None), (64, 4096, 512, 1, None), (3000, 256, 1024, 3, [0, 1000, 1001, 2990]),
-                                  (20, 2048, 64, 2, [0, 11, 20])])
+                                  (20, 2048, 64, 2, [0, 11, 20]), (2048, 512, 1024, 1, None), (2048, 2048, 512, 1, None),
+                                  (2048, 512, 2048, 1, None)])
 def test_block_in_fp32_in_every_schedule(case):
     large_case(*case, dtype="f32")
