@@ -47,12 +47,18 @@ struct Span {
   bool f32;
 };
 __device__ __forceinline__ Span span_of(const List& l, int b) {
-  int lo = 0, hi = l.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (l.first[mid] <= b) lo = mid;
-    else hi = mid;
-  }
+  // How many tensors begin at b or before: every lane looks at one of each 64, for a search
+  // step by step waits for the arguments' memory at each (norm and clipping replayed from a
+  // graph, 1000 tensors of 4096: 52.3 -> 47.0 us in bf16, 74.1 -> 60.0 in fp32).
+  constexpr int N = (kListed + kWave - 1) / kWave;
+  int32_t first[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) first[i] = l.first[min(i * kWave + (int)(threadIdx.x & 63), kListed)];
+  int lo = -1;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    lo += __popcll(__ballot(i * kWave + (int)(threadIdx.x & 63) < l.count && first[i] <= b));
+  lo = __builtin_amdgcn_readfirstlane(lo);
   Span s;
   s.tensor = lo;
   s.f32 = l.t[lo].n2 & 1;
