@@ -143,11 +143,6 @@ unsigned ffn_join_blocks(const moe_ffn_t& f, const FfnPlan& p, const int32_t* of
   return (unsigned)(p.grid * per_tile);
 }
 
-// Workgroups that clear the weight gradients of groups without rows.
-inline int clear_blocks(const moe_ffn_t& f, int kind) {
-  return ffn_over_rows(kind) && f.groups > 1 ? (int)plan_cus(device_cu_count()) : 0;
-}
-
 template <int KIND>
 hipError_t launch_ffn_tiles(const moe_ffn_t& f, const FfnPlans& plans, const FfnTileArgs& args, void* partials,
                             hipStream_t st) {
@@ -157,7 +152,7 @@ hipError_t launch_ffn_tiles(const moe_ffn_t& f, const FfnPlans& plans, const Ffn
     using C = decltype(tile);
     using G = GeomOf<C>;
     hipLaunchKernelGGL((ffn_tiles_kernel<KIND, C::NS, C::WR, C::WC, C::WA, C::WB>),
-                       dim3((unsigned)(p.grid + clear_blocks(f, KIND))), dim3(G::THREADS), 0, st, a, p.grid);
+                       dim3((unsigned)p.grid), dim3(G::THREADS), 0, st, a);
     const hipError_t e = hipGetLastError();
     const unsigned joins = ffn_join_blocks<KIND, C>(f, p, a.offsets);
     if (e != hipSuccess || joins == 0) return e;
@@ -180,8 +175,7 @@ hipError_t launch_ffn_pair(const moe_ffn_t& f, const FfnPairPlan& plan, const Ff
     using C = decltype(tile);
     using G = GeomOf<C>;
     hipLaunchKernelGGL((ffn_pair_kernel<KA, KB, C::NS, C::WR, C::WC, C::WA, C::WB>),
-                       dim3((unsigned)(pa.grid + pb.grid + clear_blocks(f, KB))), dim3(G::THREADS), 0, st, a, b, pa.grid,
-                       pb.grid);
+                       dim3((unsigned)(pa.grid + pb.grid)), dim3(G::THREADS), 0, st, a, b, pa.grid);
     const hipError_t e = hipGetLastError();
     const unsigned ja = ffn_join_blocks<KA, C>(f, pa, a.offsets), jb = ffn_join_blocks<KB, C>(f, pb, b.offsets);
     if (e != hipSuccess || ja + jb == 0) return e;

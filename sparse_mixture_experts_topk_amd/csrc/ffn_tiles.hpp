@@ -16,8 +16,9 @@
 // joined in order by a second kernel; weight gradients of several groups have tiles of
 // as many slices as their group has rows, so there the shares are even by slices, and
 // where there are few tiles each is cut into as many parts (7080 rows in 2 groups of 1352
-// x 280, all gradients: 227 -> 141 us); groups without rows have no tiles, and other workgroups of the
-// launch clear their gradients (33 rows in 256 groups of 424 x 776, all gradients: 417 -> 183 us).
+// x 280, all gradients: 227 -> 141 us); groups without rows have no tiles, and every workgroup of
+// the launch clears a part of their gradients after its tiles (33 rows in 256 groups of 424 x 776, all gradients:
+// 417 us as tiles of zeros, 184 by workgroups of their own, 178).
 #pragma once
 #include "device_common.hpp"
 #include "ffn_groups.hpp"
@@ -460,11 +461,12 @@ __device__ __forceinline__ void ffn_workgroup(const FfnTileArgs& a, uint8_t* sme
     tile_stream<ffn_over_rows(KIND), KIND != kGateUp, NS, WR, WC, WA, WB>(job, job.ldp(), job.ldq(), smem);
 }
 
-// Clears the gradients of groups without rows, of several: workgroup `block` of `blocks`.
+// Clears the gradients of groups without rows, of several: workgroup `block` of `blocks`,
+// after its tiles (the groups are loaded).
 template <int KIND, int THREADS>
-__device__ __forceinline__ void clear_workgroup(const FfnTileArgs& a, FfnGroups& groups, int block, int blocks) {
-  load_groups<KIND>(groups, a, 0);
+__device__ __forceinline__ void clear_workgroup(const FfnTileArgs& a, const FfnGroups& groups, int block, int blocks) {
   const int halves = KIND == kDw13 ? 2 : 1, empty = (a.groups - groups.full_before(a.groups)) * halves;
+  if (a.groups == 1 || empty == 0) return;
   constexpr int PART = THREADS * 8;                                  // 16-byte parts of a piece
   const int64_t n = (int64_t)a.rows * a.cols / 8;                    // (columns are a multiple of 8)
   const int64_t pieces = (n + PART - 1) / PART;
@@ -477,12 +479,11 @@ __device__ __forceinline__ void clear_workgroup(const FfnTileArgs& a, FfnGroups&
 }
 
 template <int KIND, int NS, int WR, int WC, int WA, int WB>
-__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_tiles_kernel(const FfnTileArgs a, int a_blocks) {
+__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_tiles_kernel(const FfnTileArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
   __shared__ FfnLds lds;
-  const int i = blockIdx.x;
-  if (!ffn_over_rows(KIND) || i < a_blocks) ffn_workgroup<KIND, NS, WR, WC, WA, WB>(a, smem, lds, i, a_blocks);
-  else clear_workgroup<KIND, 64 * WR * WC>(a, lds.groups, i - a_blocks, gridDim.x - a_blocks);
+  ffn_workgroup<KIND, NS, WR, WC, WA, WB>(a, smem, lds, blockIdx.x, gridDim.x);
+  if constexpr (ffn_over_rows(KIND)) clear_workgroup<KIND, 64 * WR * WC>(a, lds.groups, blockIdx.x, gridDim.x);
 }
 
 // Sums the partial tiles of the cut tiles in contraction order and applies the epilogue.
@@ -575,21 +576,15 @@ __device__ __forceinline__ void ffn_join_workgroup(const FfnTileArgs& a, FfnGrou
   }
 }
 
-// A's product on the first a_blocks workgroups, B's (a weight gradient) on the next
-// b_blocks; the others clear.
+// A's product on the first a_blocks workgroups, B's (a weight gradient) on the others; all clear.
 template <int KA, int KB, int NS, int WR, int WC, int WA, int WB>
-__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_pair_kernel(const FfnTileArgs a, const FfnTileArgs b, int a_blocks,
-                                                                   int b_blocks) {
+__global__ __launch_bounds__(64 * WR * WC, 1) void ffn_pair_kernel(const FfnTileArgs a, const FfnTileArgs b, int a_blocks) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * ProductGeom<NS, WR, WC, WA, WB>::STAGE];
   __shared__ FfnLds lds;
-  int i = blockIdx.x;
-  if (i < a_blocks) {
-    ffn_workgroup<KA, NS, WR, WC, WA, WB>(a, smem, lds, i, a_blocks);
-  } else if ((i -= a_blocks) < b_blocks) {
-    ffn_workgroup<KB, NS, WR, WC, WA, WB>(b, smem, lds, i, b_blocks);
-  } else {
-    clear_workgroup<KB, 64 * WR * WC>(b, lds.groups, i - b_blocks, gridDim.x - a_blocks - b_blocks);
-  }
+  const int i = blockIdx.x;
+  if (i < a_blocks) ffn_workgroup<KA, NS, WR, WC, WA, WB>(a, smem, lds, i, a_blocks);
+  else ffn_workgroup<KB, NS, WR, WC, WA, WB>(b, smem, lds, i - a_blocks, gridDim.x - a_blocks);
+  clear_workgroup<KB, 64 * WR * WC>(b, lds.groups, i, gridDim.x);
 }
 
 template <int KA, int KB, int TA, int TB>
