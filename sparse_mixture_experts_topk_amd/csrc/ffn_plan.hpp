@@ -103,6 +103,14 @@ struct FfnPlans {
 // CUs that the first's last round leaves, and a launch is saved.  Worth kFfnOneLaunch
 // us against each in its best shape.
 constexpr double kFfnOneLaunch = 2.5;
+// Its small tiles have two stages, so that a CU holds a workgroup of each product and one's
+// start and epilogue fall under the other's products, which saves a share of short products' time, at most
+// kPairSaves us.  All gradients, us, deep stages / two / two and this in the choice: 2108 x
+// 1736 x 704 102 / 81 / 80; 509 x 4096 x 2048 108 / 107 / 101; 33 rows in 256 groups of 424 x 776
+// 178 / 168 / 145; 3000 rows in 4 groups of 1024 x 1408 151 / 149 / 131.  (The share without a bound: 7351 rows in 256
+// groups of 4096 x 2048 4590 -> 6310.)
+constexpr double kPairOverlap = 0.28, kPairSaves = 25;
+template <class C> constexpr int kPairStages = GeomOf<C>::TA * GeomOf<C>::TB <= 128 * 128 ? 2 : C::NS;
 struct FfnPairPlan {
   FfnPlans a, b;
   int tile = 0;                      // the shape for both
@@ -115,7 +123,10 @@ struct FfnPairPlan {
     p.one = p.cost(p.tile) <= p.a.least().cost + p.b.least().cost + kFfnOneLaunch;
     return p;
   }
-  double cost(int i) const { return a.p[i].cost + b.p[i].cost; }
+  double cost(int i) const {
+    const double each = a.p[i].cost + b.p[i].cost;
+    return i >= 2 ? each - std::min(kPairOverlap * each, kPairSaves) : each;
+  }
   // partial tiles: both products', or those of one at a time
   size_t workspace() const {
     const size_t each = std::max(a.least().workspace, b.least().workspace);
@@ -174,7 +185,7 @@ hipError_t launch_ffn_pair(const moe_ffn_t& f, const FfnPairPlan& plan, const Ff
   return with_tile(plan.tile, [&](auto tile) {
     using C = decltype(tile);
     using G = GeomOf<C>;
-    hipLaunchKernelGGL((ffn_pair_kernel<KA, KB, C::NS, C::WR, C::WC, C::WA, C::WB>),
+    hipLaunchKernelGGL((ffn_pair_kernel<KA, KB, kPairStages<C>, C::WR, C::WC, C::WA, C::WB>),
                        dim3((unsigned)(pa.grid + pb.grid)), dim3(G::THREADS), 0, st, a, b, pa.grid);
     const hipError_t e = hipGetLastError();
     const unsigned ja = ffn_join_blocks<KA, C>(f, pa, a.offsets), jb = ffn_join_blocks<KB, C>(f, pb, b.offsets);
