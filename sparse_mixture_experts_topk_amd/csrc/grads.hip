@@ -178,6 +178,10 @@ __global__ __launch_bounds__(kJoinThreads) void norm_join_kernel(const double* _
   if (threadIdx.x == 0) store_norm(sum, sum_squares, norm);
 }
 
+// An fp64 product in bf16, rounded once: over fp32 one next to the middle between two bf16
+// values would land on it and go to the even one, whichever side it was on.
+__device__ __forceinline__ uint16_t to_bf16(double v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
 // x scale: in fp64, so that the one rounding is the result's.
 template <bool F32>
 __device__ __forceinline__ uint4 scaled(uint4 u, double scale) {
@@ -185,7 +189,7 @@ __device__ __forceinline__ uint4 scaled(uint4 u, double scale) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (F32) w[i] = __float_as_uint((float)(__uint_as_float(w[i]) * scale));
-    else w[i] = pack_bf16x2((float)(bf16_lo(w[i]) * scale), (float)(bf16_hi(w[i]) * scale));
+    else w[i] = to_bf16(bf16_lo(w[i]) * scale) | (uint32_t)to_bf16(bf16_hi(w[i]) * scale) << 16;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -195,7 +199,7 @@ template <bool F32>
 __device__ __forceinline__ void clip_elements(const void* p, void* o, int64_t first, int64_t end, double scale) {
   for (int64_t e = first + threadIdx.x; e < end; e += kThreads) {
     if constexpr (F32) static_cast<float*>(o)[e] = (float)(static_cast<const float*>(p)[e] * scale);
-    else static_cast<uint16_t*>(o)[e] = f32_to_bf16_bits((float)(bf16_bits_to_f32(static_cast<const uint16_t*>(p)[e]) * scale));
+    else static_cast<uint16_t*>(o)[e] = to_bf16(bf16_bits_to_f32(static_cast<const uint16_t*>(p)[e]) * scale);
   }
 }
 
