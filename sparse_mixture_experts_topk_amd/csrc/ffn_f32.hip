@@ -7,7 +7,18 @@
 // holds g and u of the same elements; kDx walks dg, w1 and then du, w3.
 // Where the tiles leave CUs idle the contraction is cut into runs whose results
 // are summed in order by a second kernel, which has the same lanes and epilogue.
+//
+// A matrix core adds its terms to an fp32 sum one after the other, and what is added
+// to a sum 2^n times as large loses n bits: of 2^20 rows of one sign dw2 lost 2.6e-4, of
+// 2^24 3.3e-2.  LONG: results that may be sums of more than kLong terms are taken in
+// chains of kChain, each joined to the sum of those before it in memory, where the
+// result goes, which costs the loop no registers (2.4e-7 and 9e-7 are left).  All
+// gradients, ms, without / with: 40000 rows of 4096 x 1024 22.7 / 19.8, 2^17 rows in 3
+// groups of 1024 x 2048 39.5 / 38.4, 2^20 in one of 257 groups of 64 x 64 4.6 / 4.5,
+// 40000 rows in 64 groups of 1024 x 1024, none of them long, 4.83 / 5.20 (two
+// workgroups on a CU for three).
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "f32_tiles.hpp"
@@ -17,6 +28,10 @@
 
 namespace moe {
 namespace {
+
+constexpr int kChain = 1 << 12, kLong = 1 << 15;
+// Kinds whose sums are results themselves: over rows, and the two halves of kDx.
+constexpr bool ffn_long_sums(int kind) { return ffn_over_rows(kind) || kind == kDx; }
 
 struct FfnArgsF32 {
   const float *P0, *P1, *Q0, *Q1;      // P1, Q1: the second half where there are two
@@ -38,11 +53,11 @@ struct FfnLdsF32 {
   FfnGroups groups;
 };
 
-template <int KIND, int B, bool JOIN>
+template <int KIND, int B, bool JOIN, bool LONG>
 __device__ __forceinline__ void ffn_f32_workgroup(const FfnArgsF32& a, FfnLdsF32<B>& lds, int block) {
   constexpr int T = 32 * B;
   constexpr bool OVER_ROWS = ffn_over_rows(KIND), PAIR = KIND == kGateUp, TWO = KIND == kDx;
-  constexpr bool PSLOW = OVER_ROWS, QSLOW = KIND != kGateUp;
+  constexpr bool PSLOW = OVER_ROWS, QSLOW = KIND != kGateUp, CHAINS = LONG && ffn_long_sums(KIND);
   auto &ps = lds.ps, &qs = lds.qs;
   FfnGroups& groups = lds.groups;
   groups.load(a.offsets, a.groups, a.M, [](int rows) { return (rows + T - 1) / T; });
@@ -113,13 +128,33 @@ __device__ __forceinline__ void ffn_f32_workgroup(const FfnArgsF32& a, FfnLdsF32
       if constexpr (PAIR) q.load_pair(Q0, Q1, ldq, c0, a.cols, t, len);
       else q.load(second ? Q1 : Q0, ldq, c0, a.cols, t, len);
     };
-    if (s0 < s1) load(s0);
-    for (int s = s0, stage = 0; s < s1; ++s, stage ^= 1) {
-      p.store(ps[stage]);
-      q.store(qs[stage]);
-      __syncthreads();      // (the other stage's readers were past it at the last barrier)
-      if (s + 1 < s1) load(s + 1);
-      multiply_f32<B>(ps[stage], qs[stage], wr, wc, i, g, acc);
+    for (int s = s0, stage = 0;;) {
+      const bool more = s != s0;
+      const int end = CHAINS ? min(s1, s + kChain / kTerms) : s1;
+      if (s < end) load(s);
+      for (; s < end; ++s, stage ^= 1) {
+        p.store(ps[stage]);
+        q.store(qs[stage]);
+        __syncthreads();      // (the other stage's readers were past it at the last barrier)
+        if (s + 1 < end) load(s + 1);
+        multiply_f32<B>(ps[stage], qs[stage], wr, wc, i, g, acc);
+      }
+      if constexpr (!CHAINS) break;
+#pragma unroll
+      for (int y = 0; y < B; ++y)
+#pragma unroll
+        for (int x = 0; x < B; ++x) {
+          const int r = r0 + wr + y * 16 + i, c = c0 + wc + x * 16 + 4 * g;
+          f32x4_t* at = reinterpret_cast<f32x4_t*>(a.runs > 1 ? partial(run, x, y) : o0 + (int64_t)r * a.cols + c);
+          if (a.runs > 1 || (r < r_end && c < a.cols)) {
+            f32x4_t v = acc[x][y];
+            if (more) v += *at;
+            *at = v;
+          }
+          acc[x][y] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      if (s >= s1) return;
     }
     if (a.runs > 1) {
 #pragma unroll
@@ -194,12 +229,12 @@ __device__ __forceinline__ void ffn_f32_workgroup(const FfnArgsF32& a, FfnLdsF32
 }
 
 // A's product (or join) on the first a_blocks workgroups, B's (another kind) on the others.
-template <int KA, int KB, int B, bool JOIN>
+template <int KA, int KB, int B, bool JOIN, bool LONG>
 __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32 a, const FfnArgsF32 b, int a_blocks) {
   __shared__ __attribute__((aligned(16))) FfnLdsF32<B> lds;
   const int i = blockIdx.x;
-  if (KA == KB || i < a_blocks) ffn_f32_workgroup<KA, B, JOIN>(a, lds, i);
-  else ffn_f32_workgroup<KB, B, JOIN>(b, lds, i - a_blocks);
+  if (KA == KB || i < a_blocks) ffn_f32_workgroup<KA, B, JOIN, LONG>(a, lds, i);
+  else ffn_f32_workgroup<KB, B, JOIN, LONG>(b, lds, i - a_blocks);
 }
 
 // 128 x 128 tiles where they give every CU one and the groups fill their rows, 64 x 64
@@ -210,6 +245,7 @@ __global__ __launch_bounds__(256) void ffn_f32_kernel(const FfnArgsF32 a, const 
 struct FfnPlanF32 {
   int T, col_tiles, runs;
   int64_t tiles, group_tiles;      // tiles: all that any offsets can give
+  bool is_long;                    // a run may have sums of more than kLong terms (any group all rows)
   static FfnPlanF32 of(const moe_ffn_t& f, int kind) {
     FfnPlanF32 p{};
     const int64_t cus = device_cu_count();
@@ -218,6 +254,7 @@ struct FfnPlanF32 {
     const int cols = kind == kGateUp ? 2 * f.d_ff : kind == kDh || kind == kDw2 ? f.d_ff : f.d_model;
     const int64_t len = over_rows ? (f.M + f.groups - 1) / f.groups
                         : kind == kDx ? 2 * (int64_t)f.d_ff : f.d_model;
+    const int64_t most = over_rows ? f.M : len;
     for (p.T = 128;; p.T = 64) {
       p.col_tiles = (cols + p.T - 1) / p.T;
       p.group_tiles = over_rows ? (int64_t)halves * ((rows + p.T - 1) / p.T) * p.col_tiles : 0;
@@ -225,6 +262,7 @@ struct FfnPlanF32 {
       p.tiles = over_rows ? p.group_tiles * f.groups : std::min<int64_t>(row_tiles, f.M) * p.col_tiles;
       const int64_t usual = over_rows ? p.tiles : std::max<int64_t>(p.tiles - (int64_t)(f.groups - 1) / 2 * p.col_tiles, 1);
       p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({64, 2 * cus / usual, len / (16 * kTerms)}));
+      p.is_long = ffn_long_sums(kind) && most > (int64_t)kLong * p.runs;
       if ((usual >= cus && (over_rows || f.M > 64 * (int64_t)f.groups)) || p.T == 64) return p;
     }
   }
@@ -263,8 +301,14 @@ hipError_t launch_pair(const moe_ffn_t& f, const FfnArgsF32& args_a, const FfnAr
     hipLaunchKernelGGL(join, dim3((unsigned)(ja + jb)), dim3(256), 0, st, a, b, (int)ja);
     return hipGetLastError();
   };
-  if ((has_a ? pa : pb).T == 128) return run(ffn_f32_kernel<KA, KB, 4, false>, ffn_f32_kernel<KA, KB, 4, true>);
-  return run(ffn_f32_kernel<KA, KB, 2, false>, ffn_f32_kernel<KA, KB, 2, true>);
+  const auto with = [&](auto b) {
+    constexpr int B = decltype(b)::value;
+    const auto join = ffn_f32_kernel<KA, KB, B, true, false>;
+    if constexpr (ffn_long_sums(KA) || ffn_long_sums(KB))
+      if ((has_a && pa.is_long) || (has_b && pb.is_long)) return run(ffn_f32_kernel<KA, KB, B, false, true>, join);
+    return run(ffn_f32_kernel<KA, KB, B, false, false>, join);
+  };
+  return (has_a ? pa : pb).T == 128 ? with(std::integral_constant<int, 4>{}) : with(std::integral_constant<int, 2>{});
 }
 
 }  // namespace

@@ -1,5 +1,6 @@
 """The feed-forward block's gradients, clipping and the runner's training pass at their edges: roundings, long sums,
 norms that leave fp32, lists whose memory moves."""
+import math
 import sys
 
 import numpy as np
@@ -7,6 +8,7 @@ import pytest
 import torch
 
 import sparse_mixture_experts_topk_amd as moe
+from sparse_mixture_experts_topk_amd import runner
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +61,107 @@ def test_clipped_bf16_is_rounded_once(scale, offset, in_place):
     every = every[np.isfinite(every)].astype(np.float64)
     got, want = clip_by(every, scale, offset, in_place)
     assert np.array_equal(got, want), [(every[i], got[i], want[i]) for i in np.nonzero(got != want)[0][:4]]
+
+
+# ---- weight gradients over many rows ----
+
+def device_values(seed, *shape, std=1.0, dtype=torch.float32, positive=False):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    t = torch.empty(*shape, device=DEV, dtype=dtype).normal_(0, std, generator=g)
+    return t.abs_() if positive else t
+
+
+def weight_gradients(M, d, F, offsets, dtype, positive):
+    """Every group's dw1, dw3, dw2 (no activation: dg = dh u, du = dh g) and fp64 sums of the same products."""
+    G, dt = len(offsets) - 1, DT[dtype]
+    say(f"weight gradients {dtype} M={M} d={d} F={F} G={G} positive={positive}")
+    val = lambda seed, *s, std=1.0: device_values(seed, *s, std=std, dtype=dt, positive=positive)      # noqa: E731
+    x, dy, p1, p3, h = val(1, M, d), val(2, M, d, std=0.01), val(3, M, F), val(4, M, F), val(5, M, F)
+    w2 = val(6, G, d, F, std=F ** -0.5)
+    f = moe.make_ffn(M, d, F, G, dtype, "none")
+    dw1, dw3, dw2 = (torch.full(s, -7.0, dtype=dt, device=DEV) for s in ((G, F, d), (G, F, d), (G, d, F)))
+    ws = runner._bytes(moe.moe_ffn_workspace_bytes(f, moe.MOE_CALL_FFN_BACKWARD), DEV)
+    moe.moe_ffn_backward(f, dy, torch.tensor(offsets, dtype=torch.int32, device=DEV), x, p1, p3, h, None, None, w2, None,
+                         dw1, dw3, dw2, ws)
+    torch.cuda.synchronize()
+    for e in range(G):
+        a, b = offsets[e], offsets[e + 1]
+        if a == b:
+            assert not (dw1[e].any() or dw3[e].any() or dw2[e].any()), e
+            continue
+        want = [torch.zeros(s, dtype=torch.float64, device=DEV) for s in ((F, d), (F, d), (d, F))]
+        for r in range(a, b, 1 << 18):
+            rows = slice(r, min(b, r + (1 << 18)))
+            ys, xs = dy[rows].double(), x[rows].double()
+            dh = ys @ w2[e].double()
+            want[0] += (dh * p3[rows].double()).t().contiguous() @ xs
+            want[1] += (dh * p1[rows].double()).t().contiguous() @ xs
+            want[2] += ys.t().contiguous() @ h[rows].double()
+        for got, w, what in zip((dw1[e], dw3[e], dw2[e]), want, ("dw1", "dw3", "dw2")):
+            yield e, b - a, what, got.double(), w
+
+
+@pytest.mark.parametrize("M,d,F,offsets", [
+    ((1 << 20) + 5, 64, 64, [0, (1 << 20) + 2] + [(1 << 20) + 5] * 256),           # all rows but three in one of many groups
+    (1 << 24, 64, 64, [0, (1 << 24) - 7] + [1 << 24] * 256),
+    ((1 << 20) + 77, 136, 72, [0, (1 << 20) + 77]), (1 << 24, 64, 64, [0, (1 << 24)]),
+    ((1 << 17) + 3, 1032, 2048, [0, 70000, 70001, (1 << 17) + 3]), (40000, 4096, 1024, [0, 40000]),
+])
+def test_fp32_weight_gradients_over_many_rows_of_one_sign(M, d, F, offsets):
+    """An addition rounds by half a step (2^-24) of the sum so far at most.  m terms of one sign: on average of half
+    the sum, so m / 2 half steps of it.  Terms are added up to 2^15 in a row, or 2^12 where there are more; then N chains
+    are (up to 64 runs of them, and they among themselves); dg and du are off by the additions of their d terms, every
+    product by a half step: the bound of an element.  The roundings are independent, uniform within the half step and, as
+    long as a step of the sum stays far below a term, of either sign: a chain's standard deviation is sqrt(m / 9) of
+    its half steps, and the whole is within twice that, relative to the Frobenius norm."""
+    for e, n, what, got, want in weight_gradients(M, d, F, offsets, "f32", True):
+        m, N = min(n, 1 << 15), n / (1 << 12) + 64
+        worst = ((got - want).abs() / want.abs()).amax().item()
+        whole = (torch.linalg.vector_norm(got - want) / torch.linalg.vector_norm(want)).item()
+        print(f"{e} {what} n={n}: worst {worst:.3e} whole {whole:.3e}")
+        assert worst <= (m / 2 + N / 2 + d / 2 + 8) * 2.0 ** -24, (e, what, worst)
+        assert whole <= 2 * (math.sqrt(m / 9) + math.sqrt(N / 9) + math.sqrt(d / 9) + 4) * 2.0 ** -24, (e, what, whole)
+
+
+@pytest.mark.parametrize("positive", [True, False])
+@pytest.mark.parametrize("M,d,F,offsets", [
+    ((1 << 21) + 77, 8, 1032, [0, (1 << 21) - 923, (1 << 21) + 77]), ((1 << 21) + 77, 1032, 8, [0, (1 << 21) - 923, (1 << 21) + 77]),
+    ((1 << 21) + 77, 136, 200, [5, (1 << 21) + 77]), ((1 << 20) + 9, 64, 64, [0, 0, (1 << 20) + 2] + [(1 << 20) + 9] * 254),
+])
+def test_bf16_weight_gradients_over_many_rows(M, d, F, offsets, positive):
+    """Off by their own half step (2^-8) and, dg and du, by one of each term's; by the roundings of fp32 sums, of 32
+    terms an instruction, which may round four times: n / 8 additions.  Of one sign: half steps of half the sum.  Of
+    either sign the sum grows as the square root of its terms: relative to the Frobenius norm n / 8 additions leave
+    sqrt(n / 8 / 2) half steps if they are independent, doubled."""
+    for e, n, what, got, want in weight_gradients(M, d, F, offsets, "bf16", positive):
+        own = 2.0 ** -8 * (1 if what == "dw2" else 2)
+        whole = (torch.linalg.vector_norm(got - want) / torch.linalg.vector_norm(want)).item()
+        print(f"{e} {what} n={n}: whole {whole:.3e}")
+        assert whole <= own + (2 * math.sqrt(n / 16) + d / 2) * 2.0 ** -24, (e, what, whole)
+        if positive:
+            worst = ((got - want).abs() / want.abs()).amax().item()
+            assert worst <= own * 1.01 + (n / 16 + d / 2) * 2.0 ** -24, (e, what, worst)
+
+
+@pytest.mark.parametrize("M,d,F", [(4097, 512, 20000), (8192, 1024, 16392), (300, 72, 20000)])
+def test_fp32_input_gradient_over_many_channels_of_one_sign(M, d, F):
+    """dx sums 2 F terms: bounds as for the weight gradients, with n = 2 F."""
+    say(f"input gradient M={M} d={d} F={F}")
+    val = lambda seed, *s, std=1.0: device_values(seed, *s, std=std, positive=True)      # noqa: E731
+    dy, p1, p3 = val(1, M, d, std=0.01), val(2, M, F), val(3, M, F)
+    w1, w3, w2 = val(4, F, d), val(5, F, d), val(6, d, F)
+    f = moe.make_ffn(M, d, F, 1, "f32", "none")
+    dx = torch.full((M + 1, d), -7.0, device=DEV)
+    ws = runner._bytes(moe.moe_ffn_workspace_bytes(f, moe.MOE_CALL_FFN_BACKWARD), DEV)
+    moe.moe_ffn_backward(f, dy, None, None, p1, p3, None, w1, w3, w2, dx, None, None, None, ws)
+    torch.cuda.synchronize()
+    assert (dx[M] == -7).all()
+    dh = dy.double() @ w2.double()
+    want = (dh * p3.double()) @ w1.double() + (dh * p1.double()) @ w3.double()
+    got, n = dx[:M].double(), 2 * F
+    m, N = min(n, 1 << 15), n / (1 << 12) + 64
+    worst = ((got - want).abs() / want.abs()).amax().item()
+    whole = (torch.linalg.vector_norm(got - want) / torch.linalg.vector_norm(want)).item()
+    print(f"worst {worst:.3e} whole {whole:.3e}")
+    assert worst <= (m / 2 + N / 2 + d / 2 + 8) * 2.0 ** -24
+    assert whole <= 2 * (math.sqrt(m / 9) + math.sqrt(N / 9) + math.sqrt(d / 9) + 4) * 2.0 ** -24
