@@ -547,13 +547,14 @@ moe_status_t moe_grad_norm_workspace_bytes(const moe_tensor_t* tensors, int32_t 
  *   sum_squares  [1] fp64 out: the sum of the squares of all elements, in fp64, in an
  *                order that depends on the list's sizes and alignments alone.  (Ranks that
  *                hold parts of a model add theirs before moe_grad_clip.)
- *   norm         [1] fp32 out or NULL: its square root
+ *   norm         [1] fp32 out or NULL: its square root (infinite above FLT_MAX)
  * An infinite or NaN element makes both so. */
 moe_status_t moe_grad_norm(const moe_tensor_t* tensors, int32_t count, double* sum_squares, float* norm,
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* Scales the list to a norm of at most max_norm: out = in * min(1, max_norm / sqrt(*sum_squares)),
- * one rounding.  A sum that is not finite scales nothing: the caller sees it in the norm.
+ * one rounding.  A norm that is not finite in fp32, as moe_grad_norm stores it (the sum may be:
+ * a norm above FLT_MAX), scales nothing: the caller sees it there.
  *   tensors, outs  host arrays of `count` tensors each; outs[i] has tensors[i]'s n and dtype
  *                and may be its memory.  outs NULL: in place.  Nothing else may overlap an
  *                output (MOE_ERR_INVALID_ARG).

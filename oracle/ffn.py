@@ -50,8 +50,9 @@ def permute_backward(dx_perm, slot_to_row, addend, T, top_k, n_shared):
 
 
 def clip(grads, max_norm):
-    """(sum of squares, norm, scaled gradients) in fp64."""
+    """(sum of squares, norm, scaled gradients) in fp64; nothing is scaled by a norm that fp32 does not hold."""
     total = math.fsum(float(np.dot(g.ravel(), g.ravel())) for g in grads)
     norm = math.sqrt(total)
-    scale = max_norm / norm if norm > max_norm and math.isfinite(norm) else 1.0
+    fits = norm < 2.0 ** 128 - 2.0 ** 103                     # rounds to FLT_MAX or less
+    scale = max_norm / norm if norm > max_norm and fits else 1.0
     return total, norm, [g * scale for g in grads]

@@ -233,10 +233,11 @@ __device__ __forceinline__ void clip_chunk(const Span& s, const void* p, void* o
   clip_elements<F32>(p, o, i1 * V - s.head, e1, scale);
 }
 
-// The factor: 1 for a norm within the bound, and for one that is not finite.
+// The factor: 1 for a norm within the bound, and for one that is not finite as store_norm
+// gives it to the caller, in fp32 (fp32 and bf16 elements near 1e38 have one that leaves it).
 __device__ __forceinline__ double clip_scale(double sum_squares, float max_norm) {
   const double norm = sqrt(sum_squares);
-  return norm > (double)max_norm && norm < INFINITY ? (double)max_norm / norm : 1.0;
+  return norm > (double)max_norm && (float)norm < INFINITY ? (double)max_norm / norm : 1.0;
 }
 
 __global__ __launch_bounds__(kThreads) void clip_kernel(const List l, const double* __restrict__ sum_squares,
