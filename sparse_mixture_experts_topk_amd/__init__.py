@@ -367,25 +367,39 @@ def moe_permute_backward(shape, dx_perm, slot_to_row, addend, dx, stream=None):
 
 class MoeTensors:
     """A list of tensors (fp32 or bf16, contiguous, on one device) for moe_grad_norm and moe_grad_clip, and
-    their descriptors; it keeps the tensors alive."""
+    their descriptors.  A call that finds a tensor in other memory than it was listed with (``t.data = ...``)
+    lists all of them anew; another size or type in the same memory (``resize_``) needs a new list.  The list
+    keeps the tensors alive, and that memory, so that nothing else can come to lie there unnoticed."""
     _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
-        self.device = _device(*self.tensors)
         self.array = (MoeTensor * max(1, len(self.tensors)))()
+        self._at = None
+        self.refresh()
+
+    def refresh(self):
+        at = [t.data_ptr() for t in self.tensors]
+        if at == self._at:
+            return
+        self._at, self.device = None, _device(*self.tensors)
         for i, t in enumerate(self.tensors):
             code = self._CODES.get(t.dtype)
             if code is None:
                 raise ValueError(f"make_tensors: tensor {i} must be torch.float32 or torch.bfloat16, got {t.dtype}")
             self.array[i] = (_ptr("make_tensors", f"tensor {i}", t, t.dtype, 0, self.device) or None, t.numel(), code)
+        self._memory = [t.detach() for t in self.tensors]
+        self._at = at
 
     def __len__(self):
         return len(self.tensors)
 
 
 def make_tensors(tensors) -> MoeTensors:
-    return tensors if isinstance(tensors, MoeTensors) else MoeTensors(tensors)
+    if not isinstance(tensors, MoeTensors):
+        return MoeTensors(tensors)
+    tensors.refresh()
+    return tensors
 
 
 def moe_grad_norm_workspace_bytes(tensors) -> int:

@@ -88,6 +88,39 @@ def test_a_norm_that_is_not_finite_in_fp32_scales_nothing(values, clipped, dtype
     assert (np.abs(t.cpu().double().numpy() - want[0]) <= step * 1.001 * np.abs(want[0])).all()
 
 
+# ---- lists whose tensors' memory moves ----
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_a_list_follows_its_tensors(in_place):
+    """Gradients that get other memory between steps (bucketed ones, say): the new values are read and scaled, the
+    old memory is left alone."""
+    sizes, g = (1000, 3, 4097), torch.Generator().manual_seed(31)
+    fresh = lambda: [torch.randn(n, generator=g).to(dt).to(DEV)                                   # noqa: E731
+                     for n, dt in zip(sizes, (torch.float32, torch.bfloat16, torch.bfloat16))]
+    grads, outs = fresh(), fresh()
+    lst, to = moe.make_tensors(grads), None if in_place else moe.make_tensors(outs)
+    total, norm = torch.zeros(1, dtype=torch.float64, device=DEV), torch.zeros(1, device=DEV)
+    ws = torch.empty(moe.moe_grad_norm_workspace_bytes(lst), dtype=torch.uint8, device=DEV)
+    old, left = None, None
+    for step in range(3):
+        if step:
+            old = [t.data for t in grads]
+            left = [t.clone() for t in old]
+            for t, v in zip(grads, fresh()):
+                t.data = v
+            outs[1].data = torch.zeros_like(outs[1])
+        _, n, want = ref.clip([t.cpu().double().numpy() for t in grads], 2.0)
+        moe.moe_grad_norm(lst, total, norm, ws)
+        moe.moe_grad_clip(lst, to, total, 2.0)
+        torch.cuda.synchronize()
+        assert abs(norm.item() - n) <= 2.0 ** -22 * n
+        for t, w in zip(grads if in_place else outs, want):
+            step_of = 2.0 ** -8 if t.dtype is torch.bfloat16 else 2.0 ** -24
+            assert (np.abs(t.cpu().double().numpy() - w) <= 1.001 * step_of * np.abs(w)).all()
+        if old is not None:
+            assert all(torch.equal(a, b) for a, b in zip(old, left))
+
+
 # ---- weight gradients over many rows ----
 
 def device_values(seed, *shape, std=1.0, dtype=torch.float32, positive=False):
