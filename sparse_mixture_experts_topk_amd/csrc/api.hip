@@ -7,7 +7,6 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <new>
 
 #include "../../include/moe.h"
 #include "launch.hpp"
@@ -241,31 +240,48 @@ moe_status_t validate_tensors(const moe_tensor_t* t, int32_t count) {
 
 struct Range {
   uintptr_t begin, end;
-  bool out;
+  uint32_t id;           // 2 i: output i, 2 i + 1: its input
+  bool operator<(const Range& o) const { return begin != o.begin ? begin < o.begin : id < o.id; }
 };
 
-// Whether an output overlaps anything but its own input (which it then is exactly).
+// Whether an output overlaps anything but its own input (which it then is exactly): the
+// ranges in ascending order, as many at a time as there is room for (nothing is allocated).
+// A longer list is gone through again for the next ones (on a host core, 300 tensors out of
+// place 40 us, 2^16 64 ms; sorted whole in allocated memory 40 us and 20 ms).
 moe_status_t check_overlap(const moe_tensor_t* in, const moe_tensor_t* out, int32_t count) {
-  Range* r = new (std::nothrow) Range[2 * (size_t)count + 1];
-  if (r == nullptr) return MOE_ERR_INVALID_ARG;
-  size_t n = 0;
-  for (int32_t i = 0; i < count; ++i) {
-    if (in[i].n == 0) continue;
-    const uintptr_t bytes = (uintptr_t)in[i].n * act_bytes(in[i].dtype);
-    const uintptr_t a = reinterpret_cast<uintptr_t>(in[i].data), b = reinterpret_cast<uintptr_t>(out[i].data);
-    r[n++] = {b, b + bytes, true};
-    if (a != b) r[n++] = {a, a + bytes, false};
-  }
-  std::sort(r, r + n, [](const Range& x, const Range& y) { return x.begin < y.begin; });
+  constexpr int kKept = 2048;
+  Range r[2 * kKept], last{};
   uintptr_t any = 0, outs = 0;           // ends so far
-  bool bad = false;
-  for (size_t i = 0; i < n && !bad; ++i) {
-    bad = r[i].begin < (r[i].out ? any : outs);
-    any = std::max(any, r[i].end);
-    if (r[i].out) outs = std::max(outs, r[i].end);
+  for (bool first = true;; first = false) {
+    int n = 0;                           // the smallest behind `last`, below `bound`
+    bool bounded = false;
+    Range bound{};
+    auto take = [&](const Range& x) {
+      if ((!first && !(last < x)) || (bounded && !(x < bound))) return;
+      r[n++] = x;
+      if (n < 2 * kKept) return;
+      n = kKept;
+      std::nth_element(r, r + n, r + 2 * kKept);
+      bound = r[n];
+      bounded = true;
+    };
+    for (int32_t i = 0; i < count; ++i) {
+      if (in[i].n == 0) continue;
+      const uintptr_t bytes = (uintptr_t)in[i].n * act_bytes(in[i].dtype);
+      const uintptr_t a = reinterpret_cast<uintptr_t>(in[i].data), b = reinterpret_cast<uintptr_t>(out[i].data);
+      take({b, b + bytes, 2 * (uint32_t)i});
+      if (a != b) take({a, a + bytes, 2 * (uint32_t)i + 1});
+    }
+    std::sort(r, r + n);
+    for (int i = 0; i < n; ++i) {
+      const bool is_out = (r[i].id & 1) == 0;
+      if (r[i].begin < (is_out ? any : outs)) return MOE_ERR_INVALID_ARG;
+      any = std::max(any, r[i].end);
+      if (is_out) outs = std::max(outs, r[i].end);
+    }
+    if (!bounded) return MOE_OK;
+    last = r[n - 1];
   }
-  delete[] r;
-  return bad ? MOE_ERR_INVALID_ARG : MOE_OK;
 }
 
 template <typename T>

@@ -1,4 +1,9 @@
 """CPU checks of lists of tensors and of clipping's refusals at their edges."""
+import ctypes
+import random
+import shutil
+import subprocess
+
 import pytest
 import torch
 
@@ -87,3 +92,57 @@ def test_a_list_whose_tensor_became_another_type_is_refused_until_it_is_mended(m
     a.address, a.dtype = 0x1000, torch.float32
     moe.moe_grad_norm(lst, 0x100)
     assert calls.lists == [[(0x1000, 4, moe.MOE_F32)]]
+
+
+# ---- clipping's refusals ----
+
+INVALID = 1
+TOTAL = 1 << 44                 # an aligned address that no refused call reads
+
+
+def tensors(entries):
+    return (_lib.MoeTensor * len(entries))(*[(a, n, t) for a, n, t in entries])
+
+
+def clip(ins, outs):
+    """Refused calls only: an accepted one would read its tensors."""
+    return _lib.load().moe_grad_clip(tensors(ins), None if outs is None else tensors(outs), len(ins),
+                                     ctypes.c_void_p(TOTAL), ctypes.c_float(1.0), None)
+
+
+def lists(count, seed, in_place):
+    """Tensors of 1 to 16 fp32 or bf16 elements in slots of 64 bytes, in any order: none overlap."""
+    rng = random.Random(seed)
+    slots = list(range(2 * count))
+    rng.shuffle(slots)
+    ins = [(0x100000 + 64 * slots[i], rng.randint(1, 16), rng.choice((moe.MOE_F32, moe.MOE_BF16))) for i in range(count)]
+    outs = None if in_place else [(0x100000 + 64 * slots[count + i], n, t) for i, (_, n, t) in enumerate(ins)]
+    return rng, ins, outs
+
+
+@pytest.mark.parametrize("count", [2, 40, 1023, 2048, 4100, 20000])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_clip_refuses_one_overlap_among_many_tensors(count, in_place):
+    for seed in range(6):
+        rng, ins, outs = lists(count, seed, in_place)
+        i, j = rng.sample(range(count), 2)
+        if in_place:                                        # the last element of i is the first of j
+            a, n, t = ins[j]
+            ins[i] = (a, n, t) if seed % 2 else (a - 4 * ins[i][1] + 4, ins[i][1], moe.MOE_F32)
+        elif seed % 2:                                      # an output on another's input
+            outs[i] = (ins[j][0], *ins[i][1:])
+        else:                                               # on another output's last element
+            a, n, t = outs[j]
+            outs[i] = (a + (n - 1) * (4 if t == moe.MOE_F32 else 2) // 4 * 4, *ins[i][1:])
+        assert clip(ins, outs) == INVALID, (seed, i, j)
+
+
+def test_the_library_asks_for_no_host_memory():
+    nm = shutil.which("nm")
+    if nm is None:
+        pytest.skip("no nm here")
+    _lib.load()
+    names = subprocess.run([nm, "-D", "--undefined-only", _lib.LIB_PATH], capture_output=True, text=True, check=True).stdout.split()
+    asks = [n for n in names if n.split("@")[0] in ("malloc", "calloc", "realloc", "aligned_alloc", "posix_memalign")
+            or n.startswith(("_Znw", "_Zna"))]              # operator new, new[]
+    assert not asks, asks

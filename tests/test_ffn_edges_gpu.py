@@ -1,6 +1,7 @@
 """The feed-forward block's gradients, clipping and the runner's training pass at their edges: roundings, long sums,
 norms that leave fp32, lists whose memory moves."""
 import math
+import random
 import sys
 
 import numpy as np
@@ -119,6 +120,24 @@ def test_a_list_follows_its_tensors(in_place):
             assert (np.abs(t.cpu().double().numpy() - w) <= 1.001 * step_of * np.abs(w)).all()
         if old is not None:
             assert all(torch.equal(a, b) for a, b in zip(old, left))
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("count", [3, 1500, 9000])
+def test_clip_of_many_neighbours(count, in_place):
+    """Tensors that touch one another in memory, in any order, overlap nowhere: accepted and scaled, each once."""
+    say(f"clip of {count} neighbours in place={in_place}")
+    rng = random.Random(count)
+    sizes = [rng.randint(0, 9) for _ in range(count)]
+    src = torch.randn(sum(sizes), generator=torch.Generator().manual_seed(count)).to(DEV)
+    dst = torch.zeros_like(src)
+    pairs = list(zip(src.split(sizes), (src if in_place else dst).split(sizes)))
+    rng.shuffle(pairs)
+    total = torch.full((1,), 4.0, dtype=torch.float64, device=DEV)
+    want = src * 0.5
+    moe.moe_grad_clip([a for a, _ in pairs], None if in_place else [b for _, b in pairs], total, 1.0)
+    torch.cuda.synchronize()
+    assert torch.equal(src if in_place else dst, want)
 
 
 # ---- weight gradients over many rows ----
