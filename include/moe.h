@@ -558,7 +558,7 @@ moe_status_t moe_grad_norm(const moe_tensor_t* tensors, int32_t count, double* s
  *   tensors, outs  host arrays of `count` tensors each; outs[i] has tensors[i]'s n and dtype
  *                and may be its memory.  outs NULL: in place.  Nothing else may overlap an
  *                output (MOE_ERR_INVALID_ARG).
- *   sum_squares  [1] fp64 (device), read by the kernel;  max_norm >= 0 */
+ *   sum_squares  [1] fp64 (device), read by the kernels, in no output's memory;  max_norm >= 0 */
 moe_status_t moe_grad_clip(const moe_tensor_t* tensors, const moe_tensor_t* outs, int32_t count,
                            const double* sum_squares, float max_norm, void* stream);
 

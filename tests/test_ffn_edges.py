@@ -104,10 +104,10 @@ def tensors(entries):
     return (_lib.MoeTensor * len(entries))(*[(a, n, t) for a, n, t in entries])
 
 
-def clip(ins, outs):
+def clip(ins, outs, total=TOTAL):
     """Refused calls only: an accepted one would read its tensors."""
     return _lib.load().moe_grad_clip(tensors(ins), None if outs is None else tensors(outs), len(ins),
-                                     ctypes.c_void_p(TOTAL), ctypes.c_float(1.0), None)
+                                     ctypes.c_void_p(total), ctypes.c_float(1.0), None)
 
 
 def lists(count, seed, in_place):
@@ -135,6 +135,16 @@ def test_clip_refuses_one_overlap_among_many_tensors(count, in_place):
             a, n, t = outs[j]
             outs[i] = (a + (n - 1) * (4 if t == moe.MOE_F32 else 2) // 4 * 4, *ins[i][1:])
         assert clip(ins, outs) == INVALID, (seed, i, j)
+
+
+@pytest.mark.parametrize("at", [0x1000, 0x1010, 0x1020])
+def test_clip_refuses_a_sum_that_an_output_would_overwrite(at):
+    """Every workgroup reads the sum while others already write."""
+    f32, bf16 = moe.MOE_F32, moe.MOE_BF16
+    before = (0x1ff0, 4, f32)
+    for mine in ((0x1000, 9, f32), (0x1000, 17, bf16), (0x0ffe, 18, bf16)):     # up to 0x1024, 0x1022, 0x1022
+        assert clip([before, mine], None, total=at) == INVALID
+        assert clip([before, (0x4000, *mine[1:])], [(0x5000, *before[1:]), mine], total=at) == INVALID
 
 
 def test_the_library_asks_for_no_host_memory():
