@@ -5,7 +5,8 @@
 // in fp32 in slot order (the shared expert's row last, the addend first), rounded
 // once.  A gather, so there are no atomics and the result repeats.  One workgroup per
 // token, 16 bytes of every row to a lane, all rows in flight together (a dropped slot
-// reads row 0, there whenever there is a token, and is selected away).  HBM-bound.
+// reads row 0, there whenever there is a token, and is selected away).  addend and dx may
+// be the same memory: a lane reads its 16 bytes before it writes them.  HBM-bound.
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "linear_epilogue.hpp"
@@ -28,8 +29,7 @@ __device__ __forceinline__ void unpack(uint4 u, float (&v)[kVec<BF16>]) {
 template <bool BF16, int K, int S>
 __global__ __launch_bounds__(256) void permute_backward_kernel(const void* __restrict__ dx_perm,
                                                                const int32_t* __restrict__ slot_to_row,
-                                                               const void* __restrict__ addend, int d, int T, int first,
-                                                               void* __restrict__ dx) {
+                                                               const void* addend, int d, int T, int first, void* dx) {
   constexpr int N = K + S, V = kVec<BF16>;
   const int t = first + blockIdx.x;
   const int64_t row_bytes = (int64_t)d * (BF16 ? 2 : 4);

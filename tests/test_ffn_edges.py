@@ -1,6 +1,8 @@
 """CPU checks of lists of tensors and of clipping's refusals at their edges."""
 import ctypes
+import os
 import random
+import re
 import shutil
 import subprocess
 
@@ -156,3 +158,13 @@ def test_the_library_asks_for_no_host_memory():
     asks = [n for n in names if n.split("@")[0] in ("malloc", "calloc", "realloc", "aligned_alloc", "posix_memalign")
             or n.startswith(("_Znw", "_Zna"))]              # operator new, new[]
     assert not asks, asks
+
+
+def test_the_permutations_gradient_promises_nothing_about_addend_and_dx():
+    """The two may be the same memory, so the kernel's declaration keeps __restrict__ off both."""
+    source = os.path.join(os.path.dirname(_lib.LIB_PATH), "csrc", "permute_backward.hip")
+    with open(source) as f:
+        declared = re.search(r"void permute_backward_kernel\(([^)]*)\)", f.read()).group(1)
+    args = {a.split()[-1]: a for a in declared.split(",")}
+    assert "__restrict__" in args["dx_perm"]
+    assert "__restrict__" not in args["addend"] and "__restrict__" not in args["dx"]
