@@ -212,13 +212,12 @@ def layer_backward(di: DeviceInputs, st: dict, dy: torch.Tensor, router=None, ds
 
 def clip_gradients(grads, max_norm: float, stream=None) -> torch.Tensor:
     """Scales the tensors ``grads`` in place to a norm of at most ``max_norm`` (not where the norm is not
-    finite); returns the norm they had, [1] fp32 on the device."""
+    finite); returns the norm they had, [1] fp32 on their device (on the current one for no tensors)."""
     t = make_tensors(grads)
-    if t.device is None:
-        return torch.zeros(1)
-    with torch.cuda.device(t.device), _on(stream, t.device):
-        total, norm = torch.empty(1, dtype=torch.float64, device=t.device), torch.empty(1, device=t.device)
-        ws = _bytes(moe_grad_norm_workspace_bytes(t), t.device)
+    dev = torch.cuda.current_device() if t.device is None else t.device
+    with torch.cuda.device(dev), _on(stream, dev):
+        total, norm = torch.empty(1, dtype=torch.float64, device=dev), torch.empty(1, device=dev)
+        ws = _bytes(moe_grad_norm_workspace_bytes(t), dev)
         moe_grad_norm(t, total, norm, ws, stream)
         moe_grad_clip(t, None, total, max_norm, stream)
     return norm

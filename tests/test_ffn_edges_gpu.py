@@ -82,11 +82,19 @@ def test_a_norm_that_is_not_finite_in_fp32_scales_nothing(values, clipped, dtype
     torch.cuda.synchronize()
     assert math.isfinite(got.item()) == clipped
     if not clipped:
-        assert torch.equal(t.view(torch.uint8), was.view(torch.uint8)) and (math.isnan(norm) or np.isinf(np.float32(norm)))
+        assert torch.equal(t.view(torch.uint8), was.view(torch.uint8)) and not norm <= torch.finfo(torch.float32).max
         return
     assert abs(got.item() - norm) <= 2.0 ** -23 * norm
     step = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
     assert (np.abs(t.cpu().double().numpy() - want[0]) <= step * 1.001 * np.abs(want[0])).all()
+
+
+@pytest.mark.parametrize("on_stream", [False, True])
+def test_the_norm_of_no_gradients_is_on_the_device(on_stream):
+    for grads in ([], [torch.empty(0, device=DEV)]):
+        norm = runner.clip_gradients(grads, 1.0, torch.cuda.Stream() if on_stream else None)
+        torch.cuda.synchronize()
+        assert norm.device.type == "cuda" and norm.shape == (1,) and norm.dtype is torch.float32 and norm.item() == 0
 
 
 # ---- lists whose tensors' memory moves ----
