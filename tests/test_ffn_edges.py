@@ -1,4 +1,4 @@
-"""CPU checks of lists of tensors and of clipping's refusals at their edges."""
+"""CPU checks of lists of tensors, of clipping's refusals and of the difference test at their edges."""
 import ctypes
 import os
 import random
@@ -6,10 +6,13 @@ import re
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 import torch
 
 import sparse_mixture_experts_topk_amd as moe
+from differences import SHARE, STEP, slope_along
+from oracle import ffn as ref
 from sparse_mixture_experts_topk_amd import _lib
 
 
@@ -168,3 +171,38 @@ def test_the_permutations_gradient_promises_nothing_about_addend_and_dx():
     args = {a.split()[-1]: a for a in declared.split(",")}
     assert "__restrict__" in args["dx_perm"]
     assert "__restrict__" not in args["addend"] and "__restrict__" not in args["dx"]
+
+
+# ---- differences along the gradient: the reference's gradients pass, planted mistakes do not ----
+
+@pytest.mark.parametrize("mistake", [None, "sign", "other", "swapped", "no slope"])
+def test_differences_along_the_gradient_tell_mistakes(mistake):
+    rng = np.random.default_rng(21)
+    M, d, f = 24, 40, 56
+    w = {"x": rng.normal(size=(M, d)), "w1": rng.normal(size=(f, d)) * d ** -0.5, "w3": rng.normal(size=(f, d)) * d ** -0.5,
+         "w2": rng.normal(size=(d, f)) * f ** -0.5}
+    dy = rng.normal(size=(M, d))
+
+    def loss(**kw):
+        a = {**w, **kw}
+        return float(((ref.gate_up(a["x"], a["w1"], a["w3"], "silu")[0] @ a["w2"].T) * dy).sum())
+
+    h, g, u = ref.gate_up(w["x"], w["w1"], w["w3"], "silu")
+    grads = ref.backward(dy, w["x"], g, u, h, w["w1"], w["w3"], w["w2"], "silu")
+    none = ref.backward(dy, w["x"], g, u, h, w["w1"], w["w3"], w["w2"], "none")
+    for name in w:
+        grad = grads["d" + name]
+        if mistake == "sign":
+            grad = -grad
+        elif mistake == "other":
+            grad = rng.permutation(grad.ravel()).reshape(grad.shape)
+        elif mistake == "swapped":
+            if name not in ("w1", "w3"):
+                continue
+            grad = grads["dw3" if name == "w1" else "dw1"]
+        elif mistake == "no slope":                       # the activation taken for the identity
+            if name == "w2":
+                continue
+            grad = none["d" + name]
+        got, want = slope_along(lambda v, n=name: loss(**{n: v}), w[name], grad, STEP)
+        assert (abs(got - want) <= SHARE * want) == (mistake is None), (name, got, want)

@@ -1,5 +1,6 @@
 """The feed-forward block's gradients, clipping and the runner's training pass at their edges: roundings, long sums,
 norms that leave fp32, lists whose memory moves."""
+import dataclasses
 import math
 import random
 import sys
@@ -9,8 +10,9 @@ import pytest
 import torch
 
 import sparse_mixture_experts_topk_amd as moe
+from differences import SHARE, STEP, slope_along
 from oracle import ffn as ref
-from sparse_mixture_experts_topk_amd import runner
+from sparse_mixture_experts_topk_amd import runner, synthetic
 
 pytestmark = pytest.mark.gpu
 
@@ -250,3 +252,31 @@ def test_fp32_input_gradient_over_many_channels_of_one_sign(M, d, F):
     print(f"worst {worst:.3e} whole {whole:.3e}")
     assert worst <= (m / 2 + N / 2 + d / 2 + 8) * 2.0 ** -24
     assert whole <= 2 * (math.sqrt(m / 9) + math.sqrt(N / 9) + math.sqrt(d / 9) + 4) * 2.0 ** -24
+
+
+# ---- the whole layer's gradients against differences along themselves ----
+
+@pytest.mark.parametrize("kw", [dict(), dict(n_shared=1, top_k=3), dict(T=40, capacity=9)])
+def test_layer_gradients_against_differences_along_themselves(kw):
+    cfg = synthetic.MoEConfig(**{**dict(name="slopes", T=24, d_model=128, d_ff=192, n_experts=8, act_dtype="f32", w_dtype="f32",
+                                        wg_std=128 ** -0.5, w13_std=0.08, w2_std=0.08, seed=12), **kw})
+    say(f"differences {kw}")
+    inp = synthetic.make_inputs(cfg)
+    inp.router_bias = 0.3 * torch.randn(cfg.n_experts, generator=torch.Generator().manual_seed(70))
+    di = runner.DeviceInputs.from_host(inp)
+    dy = torch.randn(cfg.T, cfg.d_model, generator=torch.Generator().manual_seed(75)).to(DEV)
+    st = runner.staged(di, keep=True)
+    o = runner.layer_backward(di, st, dy)
+
+    def loss(name, value):
+        s = runner.staged(dataclasses.replace(di, **{name: value.float()}), keep=True)
+        assert torch.equal(s["slot_to_row"], st["slot_to_row"]), "the step changes the choice of experts"
+        return (s["y"].double() * dy.double()).sum().item()
+
+    for name, grad in (("w1", "dw1"), ("w3", "dw3"), ("w2", "dw2"), ("x", "dx"), ("w_gate", "dw_gate"), ("router_bias", "dbias")):
+        # Where logits move no token may choose other experts: shorter steps, which y's roundings allow: independent ones
+        # of 2^-21 in n = 3072 elements leave 2^-21 |y| |dy| / sqrt(n) in the loss, over 2^-13 |base| |grad| 2^-13.8 of the ratio.
+        step = STEP if name in ("w1", "w3", "w2") else 2.0 ** -13
+        got, want = slope_along(lambda v, n=name: loss(n, v), getattr(di, name).double(), o[grad].double(), step)
+        print(f"{name}: {got:.6e} {want:.6e} {abs(got - want) / want:.2e}")
+        assert abs(got - want) <= SHARE * want, name
