@@ -512,8 +512,9 @@ moe_status_t moe_ffn_gate_up(const moe_ffn_t* ffn, const void* x, const int32_t*
  *   pre1, pre3 [M, d_ff] as written by moe_ffn_gate_up, w2 [groups, d_model, d_ff]:
  *            required for dx, dw1 and dw3
  * dg and du are rounded to dtype for the products, their matrix-core operands (MOE_F32:
- * kept whole); sums in fp32, in an order that is the same from call to call.  relu'(0) =
- * 0.  Weight gradients are fully written, zero for a group without rows (M = 0 too).
+ * kept whole); sums in fp32, in an order that is the same from call to call (MOE_F32: dx
+ * and weight gradients in parts of 2^15 terms at most).  relu'(0) = 0.  Weight gradients
+ * are fully written, zero for a group without rows (M = 0 too).
  * Outputs overlap no input.  At least one output must be given where M > 0. */
 moe_status_t moe_ffn_backward(const moe_ffn_t* ffn, const void* dy, const int32_t* offsets, const void* x,
                               const void* pre1, const void* pre3, const void* h, const void* w1,

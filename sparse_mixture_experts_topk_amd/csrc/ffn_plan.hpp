@@ -8,13 +8,22 @@
 namespace moe {
 
 // How the rows of the groups fall is known to the device alone: the plan takes them as
-// even, each group half a tile short of its last.
+// even, each group half a tile short of its last.  For several groups the last round is
+// therefore priced by fractions: where it may be cut and there are few rounds, by its part of a round
+// (a quarter at least) and a join of 8 us; elsewhere few rounds are taken as half a
+// round longer.  All gradients, us, so / by the rounds alone: 7080 rows of 2 groups of 1352 x
+// 280 148 / 168, 600 of 4 of 2048 x 512 53 / 56, 1024 of 8 of 4096 x 2048 289 / 271; gate/up,
+// 3000 of 4 of 1024 x 1408 39 / 41, 1024 of 8 of 4096 x 2048 81 / 87; 21 other cases the same.
 struct FfnPlan {
   double cost = 1e30;      // us
   int row_tiles = 0, col_tiles = 0, grid = 0, split_ns = 0, cuts = 1;
   size_t workspace = 0;
 
-  // Rounds of tiles from which on a tail is not worth a join's launch.
+  // Rounds of tiles from which on a tail is not worth a join's launch: what it saves, half a
+  // round on average, is under 2%.  (All gradients, us, this / always a join / never: 8192 rows of
+  // 8 groups of 4096 x 4096 1653 / 1655 / 1895, 4096 of 8 of 2048 x 4096 575 / 573 / 646, 509 x 4096 x
+  // 2048 100 / 98 / 113.  Rows of several groups have a join launched that may find nothing to do:
+  // 3000 of 4 of 1024 x 1408 126 / 126 / 117, gate/up of 2000 of 32 of 768 x 1024 40 / 40 / 27.)
   static constexpr int kNoTail = 24;
 
   template <class C>
@@ -108,7 +117,9 @@ constexpr double kFfnOneLaunch = 2.5;
 // kPairSaves us.  All gradients, us, deep stages / two / two and this in the choice: 2108 x
 // 1736 x 704 102 / 81 / 80; 509 x 4096 x 2048 108 / 107 / 101; 33 rows in 256 groups of 424 x 776
 // 178 / 168 / 145; 3000 rows in 4 groups of 1024 x 1408 151 / 149 / 131.  (The share without a bound: 7351 rows in 256
-// groups of 4096 x 2048 4590 -> 6310.)
+// groups of 4096 x 2048 4590 -> 6310.)  Also where both products together leave every workgroup a CU of
+// its own two stages are the faster, deep / two: 64 x 512 x 512 26.2 / 24.2, 300 x 1024 x 1024 42.0 / 34.1,
+// 128 rows in 8 groups of 256 x 512 30.1 / 28.0.
 constexpr double kPairOverlap = 0.28, kPairSaves = 25;
 template <class C> constexpr int kPairStages = GeomOf<C>::TA * GeomOf<C>::TB <= 128 * 128 ? 2 : C::NS;
 struct FfnPairPlan {

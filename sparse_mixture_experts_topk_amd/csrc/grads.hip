@@ -5,7 +5,7 @@
 // Squares and sums are fp64: bf16 and fp32 gradients reach 1e38 and 1e-38, whose
 // squares leave fp32, and a sum of 10^9 terms loses digits there; the products hide
 // under the reads.  Workgroup b sums one chunk of one tensor; a second kernel adds
-// the chunks' sums in a fixed order, so S depends on the list's sizes and values alone.
+// the chunks' sums in a fixed order, so S depends on the list's sizes, alignments and values alone.
 // Both passes are HBM-bound: the norm has to be known before the first element is
 // written, so the list is read twice and written once.
 //

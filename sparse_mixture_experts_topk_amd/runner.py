@@ -196,7 +196,8 @@ def _ffn_of(cfg):
 def layer_backward(di: DeviceInputs, st: dict, dy: torch.Tensor, router=None, dscores=None, stream=None) -> dict:
     """Gradients of the whole layer from the gradient ``dy`` at y: ``st`` is the result of
     ``staged(..., keep=True)`` with the same router (None: the library's own, a softmax over the kept
-    logits).  dx, dw_gate, dbias (with a router bias), dw1, dw3, dw2, beside what gate_backward gives."""
+    logits).  dx, dw_gate, dbias (with a router bias), dw1, dw3, dw2, beside what gate_backward gives.  Between the
+    calls the gradients at the experts' rows (dy_perm, dx_perm) and the router's part of dx are in the activations' type."""
     cfg, dev = di.cfg, di.x.device
     ffn = _ffn_of(cfg)
     o = gate_backward(di, st, make_router() if router is None else router, dy, dscores, stream)
@@ -247,7 +248,7 @@ def forward(di: DeviceInputs, buf: Optional[ForwardBuffers] = None, stream=None,
 def staged(di: DeviceInputs, stream=None, router=None, balance_bias=None, keep: bool = False) -> dict:
     """The five boundary calls in sequence (with a router: scored_routing in place of
     moe_route_topk); returns every intermediate buffer.  ``keep``: for layer_backward, the
-    experts' pre-activations too, by moe_ffn_gate_up (bf16 or fp32 experts)."""
+    experts' pre-activations too, by moe_ffn_gate_up (bf16 or fp32 experts, up to 2^24 slots of all tokens)."""
     cfg = di.cfg
     dev = di.x.device
     T, d, F, E, k, S = cfg.T, cfg.d_model, cfg.d_ff, cfg.n_experts, cfg.top_k, cfg.n_shared
