@@ -275,7 +275,8 @@ def test_layer_gradients_against_differences_along_themselves(kw):
 
     for name, grad in (("w1", "dw1"), ("w3", "dw3"), ("w2", "dw2"), ("x", "dx"), ("w_gate", "dw_gate"), ("router_bias", "dbias")):
         # Where logits move no token may choose other experts: shorter steps, which y's roundings allow: independent ones
-        # of 2^-21 in n = 3072 elements leave 2^-21 |y| |dy| / sqrt(n) in the loss, over 2^-13 |base| |grad| 2^-13.8 of the ratio.
+        # of 2^-21 in the n = T d elements leave 2^-21 |y| |dy| / sqrt(n) in the loss, sqrt(n) > 2^5; over 2^-13 |base|
+        # |grad| that is 2^-13 of the ratio.
         step = STEP if name in ("w1", "w3", "w2") else 2.0 ** -13
         got, want = slope_along(lambda v, n=name: loss(n, v), getattr(di, name).double(), o[grad].double(), step)
         print(f"{name}: {got:.6e} {want:.6e} {abs(got - want) / want:.2e}")
